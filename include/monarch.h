@@ -56,7 +56,7 @@
 extern "C" {
 #endif
 
-#define MONARCH_ABI_VERSION 4
+#define MONARCH_ABI_VERSION 5
 
 typedef enum {
   MONARCH_OK = 0,
@@ -66,7 +66,8 @@ typedef enum {
   MONARCH_ERR_ALIGN = -4,
   MONARCH_ERR_WORKSPACE = -5,
   MONARCH_ERR_HIP = -6,
-  MONARCH_ERR_SCRATCH = -7   /* monarch_bwd_noalloc: problem too large for its scratch */
+  MONARCH_ERR_SCRATCH = -7,  /* monarch_bwd_noalloc: problem too large for its scratch */
+  MONARCH_ERR_VALUE = -8     /* a scalar argument out of its range or not finite */
 } monarch_status;
 
 typedef enum { MONARCH_F32 = 0, MONARCH_BF16 = 1 } monarch_dtype;
@@ -305,6 +306,64 @@ int monarch_dyad_bwd(const void* dy, const void* x, const void* w_a, const void*
 
 int monarch_dyad_describe(int direction, int64_t in_features, int64_t out_features,
                           int64_t nblocks, int64_t batch, int dtype, char* buf, size_t buf_len);
+
+/* ---------------------------------------------------------------------------
+ * Sandwich norm: what stands between two blocks of a model whose dense layers
+ * are Monarch layers. One call takes a block's output y through the norm
+ * after the block, the gate and the residual join, and the result through the
+ * norm before the next block:
+ *   u     = norm_post(y) * post_w + post_b
+ *   h_out = skip_scale * h + branch_scale * gate * u
+ *   n     = norm_pre(h_out) * pre_w + pre_b        (of h_out before rounding)
+ * norm(v) = (v - mu) / sqrt(mean((v - mu)^2) + eps) over the features of a row,
+ * mu = mean(v) for MONARCH_NORM_LAYER and 0 for MONARCH_NORM_RMS;
+ * MONARCH_NORM_NONE leaves v (as norm_post) or writes no n (as norm_pre; pre_w,
+ * pre_b and n are then not used).
+ *   h, y, h_out, n  [rows, features]       post_w, post_b, pre_w, pre_b [features]
+ *   gate [gates, features]: row i of h takes gate row i / (rows/gates), so gates =
+ *   1 is one gate for every row, gates = rows one for each; gates = 0 is none.
+ *   Any of post_w, post_b, pre_w, pre_b may be NULL (1, or 0 for a bias).
+ *   y NULL: the norm before the first block. h_out is h (h_out is not
+ *   written and may be NULL; skip_scale, the gate and post_* are not used).
+ *   stats: fp32 [rows, 4], written by the forward pass for the backward pass
+ *   (mean and reciprocal root of y's row, then of h_out's).
+ * features <= 16384, gates divides rows. All sums are fp32; each result is
+ * rounded once. Outputs must not alias inputs, except that h_out may be h and
+ * n may be y. eps < 0 or a scale that is not finite gives MONARCH_ERR_VALUE,
+ * a norm out of range MONARCH_ERR_DTYPE; otherwise errors as for monarch_fwd.
+ * rows == 0 returns MONARCH_OK. */
+typedef enum { MONARCH_NORM_NONE = 0, MONARCH_NORM_RMS = 1, MONARCH_NORM_LAYER = 2 } monarch_norm;
+
+int monarch_sandwich_fwd(const void* h, const void* y, const void* post_w, const void* post_b,
+                         const void* gate, const void* pre_w, const void* pre_b, void* h_out,
+                         void* n, void* stats, int64_t rows, int64_t features, int64_t gates,
+                         int post_norm, int pre_norm, float skip_scale, float branch_scale,
+                         float eps, int dtype, void* stream, void* const* events, int n_events);
+
+/* Workspace bytes of monarch_sandwich_bwd (with_bias: post_b or pre_b is given). */
+size_t monarch_sandwich_bwd_workspace_bytes(int64_t rows, int64_t features, int64_t gates,
+                                            int with_bias, int dtype);
+
+/* Backward pass from dh_out (NULL: zero) and dn (with a norm_pre): dh and dy
+ * [rows, features], and the gradients of the parameters, each of which may be
+ * NULL when it is not wanted. h_out, y, stats and the parameters are those of the
+ * forward call. Without norm_pre, dn and h_out are not used and dh_out is
+ * needed. With y NULL only dh, dpre_w and dpre_b are computed (dh with
+ * skip_scale). Everything is overwritten; sums over rows run in a fixed order.
+ * dh may be dh_out or dn. rows == 0 zeroes the parameters' gradients. */
+int monarch_sandwich_bwd(const void* dh_out, const void* dn, const void* h_out, const void* y,
+                         const void* stats, const void* post_w, const void* post_b,
+                         const void* gate, const void* pre_w, const void* pre_b, void* dh, void* dy,
+                         void* dpost_w, void* dpost_b, void* dgate, void* dpre_w, void* dpre_b,
+                         void* workspace, size_t workspace_bytes, int64_t rows, int64_t features,
+                         int64_t gates, int post_norm, int pre_norm, float skip_scale,
+                         float branch_scale, int dtype, void* stream, void* const* events,
+                         int n_events);
+
+/* Kernel names of monarch_sandwich_fwd (direction 0) / _bwd (1, with parameter
+ * gradients wanted). */
+int monarch_sandwich_describe(int direction, int64_t rows, int64_t features, int64_t gates,
+                              int dtype, char* buf, size_t buf_len);
 
 /* ---------------------------------------------------------------------------
  * Stream copy: copies `bytes` bytes from src to dst (device buffers, 16-byte

@@ -25,6 +25,7 @@ MONARCH_ERR_ALIGN = -4
 MONARCH_ERR_WORKSPACE = -5
 MONARCH_ERR_HIP = -6
 MONARCH_ERR_SCRATCH = -7
+MONARCH_ERR_VALUE = -8
 # static scratch of monarch_bwd_noalloc per GPU (MONARCH_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 256 << 20
 
@@ -32,6 +33,9 @@ F32 = 0
 BF16 = 1
 ACT_NONE = 0
 ACT_RELU = 1
+NORM_NONE = 0
+NORM_RMS = 1
+NORM_LAYER = 2
 
 EXPORTED = (
     "monarch_fwd", "monarch_bwd", "monarch_bwd_workspace_bytes", "monarch_fwd_traced",
@@ -42,6 +46,8 @@ EXPORTED = (
     "monarch_hyper_describe", "monarch_dyad_fwd_workspace_bytes", "monarch_dyad_fwd",
     "monarch_dyad_bwd_workspace_bytes",
     "monarch_dyad_bwd", "monarch_dyad_describe", "monarch_bwd_noalloc", "monarch_stream_copy",
+    "monarch_sandwich_fwd", "monarch_sandwich_bwd_workspace_bytes", "monarch_sandwich_bwd",
+    "monarch_sandwich_describe",
 )
 
 _lib = None
@@ -122,6 +128,17 @@ def load_library():
     lib.monarch_dyad_bwd.restype = c_int
     lib.monarch_dyad_describe.argtypes = [c_int] + [i64] * 4 + [c_int, ctypes.c_char_p, sz]
     lib.monarch_dyad_describe.restype = c_int
+    c_float = ctypes.c_float
+    lib.monarch_sandwich_fwd.argtypes = ([vp] * 10 + [i64] * 3 + [c_int] * 2 + [c_float] * 3 +
+                                         [c_int, vp] + ev)
+    lib.monarch_sandwich_fwd.restype = c_int
+    lib.monarch_sandwich_bwd_workspace_bytes.argtypes = [i64] * 3 + [c_int] * 2
+    lib.monarch_sandwich_bwd_workspace_bytes.restype = sz
+    lib.monarch_sandwich_bwd.argtypes = ([vp] * 18 + [sz] + [i64] * 3 + [c_int] * 2 +
+                                         [c_float] * 2 + [c_int, vp] + ev)
+    lib.monarch_sandwich_bwd.restype = c_int
+    lib.monarch_sandwich_describe.argtypes = [c_int] + [i64] * 3 + [c_int, ctypes.c_char_p, sz]
+    lib.monarch_sandwich_describe.restype = c_int
     _lib = lib
     return lib
 
@@ -363,6 +380,45 @@ def monarch_dyad_describe(direction, in_features, out_features, nblocks, batch, 
     buf = ctypes.create_string_buffer(1024)
     n = lib.monarch_dyad_describe(direction, in_features, out_features, nblocks, batch, dtype, buf,
                                   len(buf))
+    if n < 0:
+        raise MonarchError(n, monarch_status_string(n))
+    return buf.value.decode().split(";") if n else []
+
+
+def monarch_sandwich_fwd(h, y, post_w, post_b, gate, pre_w, pre_b, h_out, n, stats, rows, features,
+                         gates, post_norm, pre_norm, skip_scale, branch_scale, eps, dtype,
+                         stream=None, events=None) -> None:
+    lib = load_library()
+    arr, ne = _events(events)
+    _check(lib.monarch_sandwich_fwd(_ptr(h), _ptr(y), _ptr(post_w), _ptr(post_b), _ptr(gate),
+                                    _ptr(pre_w), _ptr(pre_b), _ptr(h_out), _ptr(n), _ptr(stats),
+                                    rows, features, gates, post_norm, pre_norm, skip_scale,
+                                    branch_scale, eps, dtype, _stream(stream), arr, ne))
+
+
+def monarch_sandwich_bwd_workspace_bytes(rows, features, gates, with_bias, dtype) -> int:
+    return load_library().monarch_sandwich_bwd_workspace_bytes(rows, features, gates,
+                                                               1 if with_bias else 0, dtype)
+
+
+def monarch_sandwich_bwd(dh_out, dn, h_out, y, stats, post_w, post_b, gate, pre_w, pre_b, dh, dy,
+                         dpost_w, dpost_b, dgate, dpre_w, dpre_b, workspace, workspace_bytes, rows,
+                         features, gates, post_norm, pre_norm, skip_scale, branch_scale, dtype,
+                         stream=None, events=None) -> None:
+    lib = load_library()
+    arr, ne = _events(events)
+    _check(lib.monarch_sandwich_bwd(
+        _ptr(dh_out), _ptr(dn), _ptr(h_out), _ptr(y), _ptr(stats), _ptr(post_w), _ptr(post_b),
+        _ptr(gate), _ptr(pre_w), _ptr(pre_b), _ptr(dh), _ptr(dy), _ptr(dpost_w), _ptr(dpost_b),
+        _ptr(dgate), _ptr(dpre_w), _ptr(dpre_b), _ptr(workspace), workspace_bytes, rows, features,
+        gates, post_norm, pre_norm, skip_scale, branch_scale, dtype, _stream(stream), arr, ne))
+
+
+def monarch_sandwich_describe(direction, rows, features, gates, dtype):
+    """Kernel names monarch_sandwich_fwd (0) / monarch_sandwich_bwd (1) launches."""
+    lib = load_library()
+    buf = ctypes.create_string_buffer(1024)
+    n = lib.monarch_sandwich_describe(direction, rows, features, gates, dtype, buf, len(buf))
     if n < 0:
         raise MonarchError(n, monarch_status_string(n))
     return buf.value.decode().split(";") if n else []

@@ -28,21 +28,6 @@ int record_hip(hipError_t e) {
 
 namespace {
 
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
-struct Tracer {
-  void* const* ev;
-  int n;
-  int idx = 0;
-  hipStream_t s;
-  hipError_t mark() {
-    hipError_t e = hipSuccess;
-    if (ev && idx < n && ev[idx]) e = hipEventRecord(static_cast<hipEvent_t>(ev[idx]), s);
-    ++idx;
-    return e;
-  }
-};
-
 int run_plan(const Plan& plan, const Problem& pr, const Buffers& b, hipStream_t s,
              void* const* events, int n_events) {
   Tracer tr{events, n_events, 0, s};
@@ -87,23 +72,6 @@ int run_seq(const SeqStep* steps, int n, bool bf16, hipStream_t s, void* const* 
   return record_hip(tr.mark());
 }
 
-int write_names(const char* const* names, int n, char* buf, size_t buf_len) {
-  if (buf && buf_len) {
-    buf[0] = '\0';
-    size_t used = 0;
-    for (int i = 0; i < n; ++i) {
-      int w = snprintf(buf + used, buf_len - used, "%s%s", i ? ";" : "", names[i]);
-      if (w < 0) break;
-      used += static_cast<size_t>(w);
-      if (used >= buf_len) {
-        buf[buf_len - 1] = '\0';
-        break;
-      }
-    }
-  }
-  return n;
-}
-
 int describe_plan(const Problem& pr, int direction, char* buf, size_t buf_len) {
   if (direction != 0 && direction != 1) return MONARCH_ERR_DTYPE;
   Plan plan;
@@ -129,6 +97,23 @@ int describe_plan(const Problem& pr, int direction, char* buf, size_t buf_len) {
 }
 
 }  // namespace
+
+int write_names(const char* const* names, int n, char* buf, size_t buf_len) {
+  if (buf && buf_len) {
+    buf[0] = '\0';
+    size_t used = 0;
+    for (int i = 0; i < n; ++i) {
+      int w = snprintf(buf + used, buf_len - used, "%s%s", i ? ";" : "", names[i]);
+      if (w < 0) break;
+      used += static_cast<size_t>(w);
+      if (used >= buf_len) {
+        buf[buf_len - 1] = '\0';
+        break;
+      }
+    }
+  }
+  return n;
+}
 
 int bwd_check(const Problem& pr, const void* dy, const void* x, const void* w1, const void* w2,
               const void* z, const void* y, const void* dx, const void* dw1, const void* dw2,
@@ -481,6 +466,7 @@ const char* monarch_status_string(int status) {
     case MONARCH_ERR_HIP: return g_hip_error;
     case MONARCH_ERR_SCRATCH:
       return "problem needs more than MONARCH_NOALLOC_SCRATCH_BYTES of scratch (use monarch_bwd)";
+    case MONARCH_ERR_VALUE: return "a scalar argument is out of its range or not finite";
     default: return "unknown status";
   }
 }

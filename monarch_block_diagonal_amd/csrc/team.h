@@ -1,0 +1,160 @@
+// Row teams: a row of a matrix is held by TEAM threads in 16-byte pieces
+// (gfx950). Shared by the row-wise kernels (norms, distillation loss).
+#pragma once
+
+#include "common.h"
+
+namespace monarch {
+
+// A 16-byte access whose address is a multiple of the element size only: rows
+// of odd widths start anywhere. The compiler lowers it to one 16-byte access
+// (global accesses on this target may be unaligned).
+typedef u32x4 __attribute__((aligned(2), may_alias)) u32x4_at2;
+typedef u32x4 __attribute__((aligned(4), may_alias)) u32x4_at4;
+
+template <typename T> struct PieceOf;
+template <> struct PieceOf<float> {
+  static constexpr int N = 4;   // elements of 16 bytes
+  typedef u32x4_at4 Raw;
+  static __device__ __forceinline__ void unpack(const u32x4& r, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+  }
+  static __device__ __forceinline__ u32x4 pack(const float (&v)[4]) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(v[i]);
+    return r;
+  }
+};
+template <> struct PieceOf<uint16_t> {
+  static constexpr int N = 8;
+  typedef u32x4_at2 Raw;
+  static __device__ __forceinline__ void unpack(const u32x4& r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(r[i] << 16);
+      v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ u32x4 pack(const float (&v)[8]) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    return r;
+  }
+};
+
+// Elements [at, at + N) of a row of d elements; those past the row are 0.
+template <typename T>
+__device__ __forceinline__ u32x4 load_piece(const T* row, int at, int d) {
+  constexpr int N = PieceOf<T>::N;
+  if (at + N <= d) return *reinterpret_cast<const typename PieceOf<T>::Raw*>(row + at);
+  u32x4 r = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (at + i < d) {
+      if constexpr (N == 4)
+        r[i] = __float_as_uint(row[at + i]);
+      else
+        r[i / 2] |= static_cast<uint32_t>(row[at + i]) << (16 * (i % 2));
+    }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_piece(T* row, int at, int d, const u32x4& r) {
+  constexpr int N = PieceOf<T>::N;
+  if (at + N <= d) {
+    *reinterpret_cast<typename PieceOf<T>::Raw*>(row + at) = r;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (at + i < d) {
+      if constexpr (N == 4)
+        row[at + i] = __uint_as_float(r[i]);
+      else
+        row[at + i] = static_cast<uint16_t>(r[i / 2] >> (16 * (i % 2)));
+    }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_read(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+struct SumOp {
+  static __device__ __forceinline__ float of(float a, float b) { return a + b; }
+};
+struct MaxOp {
+  static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
+};
+
+// Reduction over aligned groups of W lanes (16, 32 or 64), the result in every
+// lane, in the register file alone: two quad permutations, the half-row and
+// row mirrors, then the row and half-wave swaps. The order is fixed.
+template <class Op, int W>
+__device__ __forceinline__ float lanes_reduce(float v) {
+  v = Op::of(v, dpp_read<0xb1>(v));    // quad_perm [1,0,3,2]
+  v = Op::of(v, dpp_read<0x4e>(v));    // quad_perm [2,3,0,1]
+  v = Op::of(v, dpp_read<0x141>(v));   // row_half_mirror
+  v = Op::of(v, dpp_read<0x140>(v));   // row_mirror
+  if constexpr (W >= 32) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    v = Op::of(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  }
+  if constexpr (W >= 64) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    v = Op::of(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  }
+  return v;
+}
+
+// Reductions over a team of TEAM threads (16 .. 1024, a power of two; a team of
+// more than a wave is the whole workgroup), in a fixed order. Several values
+// go through one exchange. Two LDS slots are used in turn, so one barrier an
+// exchange is enough: a wave that writes a slot again has passed the barrier
+// of the exchange between, which every reader of the slot reached first.
+template <int TEAM>
+struct Team {
+  static constexpr int WAVES = TEAM > 64 ? TEAM / 64 : 1;
+  static constexpr int MAXV = 2;   // values an exchange
+  struct Lds {
+    float slot[2][MAXV][WAVES];
+  };
+  Lds* lds;
+  int turn = 0;
+  __device__ __forceinline__ explicit Team(Lds* l) : lds(l) {}
+
+  template <class Op, int K>
+  __device__ __forceinline__ void reduce(float (&v)[K]) {
+    static_assert(K <= MAXV, "");
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = lanes_reduce<Op, (TEAM < 64 ? TEAM : 64)>(v[k]);
+    if constexpr (TEAM > 64) {
+      const int wave = threadIdx.x / 64;
+      if (threadIdx.x % 64 == 0)
+#pragma unroll
+        for (int k = 0; k < K; ++k) lds->slot[turn][k][wave] = v[k];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float s = lds->slot[turn][k][0];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) s = Op::of(s, lds->slot[turn][k][w]);
+        v[k] = s;
+      }
+      turn ^= 1;
+    }
+  }
+  __device__ __forceinline__ float sum(float x) {
+    float v[1] = {x};
+    reduce<SumOp, 1>(v);
+    return v[0];
+  }
+};
+
+}  // namespace monarch

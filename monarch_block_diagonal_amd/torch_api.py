@@ -11,6 +11,8 @@ explicit intermediate width, optional bias).
 """
 from __future__ import annotations
 
+from typing import NamedTuple, Optional
+
 import torch
 
 from . import binding as B
@@ -324,3 +326,96 @@ def dyad_backward(dy, x, wa, wb, stream=None):
     B.monarch_dyad_bwd(dy, x, wa, wb, dx, dwa, dwb, ws, need, x.shape[1], nb * qo, nb, b, code,
                        stream)
     return dx, dwa, dwb
+
+
+class SandwichGrads(NamedTuple):
+    """Gradients of sandwich_forward's inputs; None where there is no such input."""
+    dh: torch.Tensor
+    dy: Optional[torch.Tensor]
+    dpost_weight: Optional[torch.Tensor]
+    dpost_bias: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dpre_weight: Optional[torch.Tensor]
+    dpre_bias: Optional[torch.Tensor]
+
+
+def _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias, pre_norm, skip_scale):
+    """(rows, features, gates) after checking every tensor against h [rows, features]."""
+    if h.dim() != 2:
+        raise ValueError("h must be [rows, features]")
+    rows, d = (int(v) for v in h.shape)
+    _expect(y, (rows, d), "y")
+    for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
+                    (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
+        _expect(t, (d,), name)
+    gates = 0
+    if gate is not None:
+        if gate.dim() != 2 or gate.shape[1] != d or gate.shape[0] == 0:
+            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected (gates, {d})")
+        gates = int(gate.shape[0])
+        if rows % gates or (rows and gates > rows):
+            raise ValueError(f"{gates} gate rows do not divide {rows} rows")
+    if y is None and (post_weight is not None or post_bias is not None or gate is not None or
+                      skip_scale != 1.0):
+        raise ValueError("without y there is nothing to scale, gate or norm after the block")
+    if pre_norm == B.NORM_NONE and (pre_weight is not None or pre_bias is not None):
+        raise ValueError("pre_weight and pre_bias need a pre_norm")
+    _check(h, y, post_weight, post_bias, gate, pre_weight, pre_bias)
+    return rows, d, gates
+
+
+def sandwich_forward(h, y=None, post_weight=None, post_bias=None, gate=None, pre_weight=None,
+                     pre_bias=None, *, post_norm: int = B.NORM_RMS, pre_norm: int = B.NORM_RMS,
+                     skip_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-5,
+                     stream=None):
+    """(h_out, n, stats) of the residual stream h and a block's output y:
+
+        h_out = skip_scale * h + branch_scale * gate * (norm_post(y) * post_weight + post_bias)
+        n     = norm_pre(h_out) * pre_weight + pre_bias
+
+    gate [gates, features] holds one row for rows/gates consecutive rows. Without
+    y, h_out is h itself (the norm before the first block); with pre_norm
+    NORM_NONE, n is None. stats [rows, 4] goes to sandwich_backward."""
+    rows, d, gates = _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias,
+                                      pre_norm, skip_scale)
+    h_out = torch.empty_like(h) if y is not None else h
+    n = torch.empty_like(h) if pre_norm != B.NORM_NONE else None
+    stats = torch.empty((rows, 4), dtype=torch.float32, device=h.device)
+    B.monarch_sandwich_fwd(h, y, post_weight, post_bias, gate, pre_weight, pre_bias,
+                           h_out if y is not None else None, n, stats, rows, d, gates, post_norm,
+                           pre_norm, skip_scale, branch_scale, eps, dtype_code(h), stream)
+    return h_out, n, stats
+
+
+def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=None, gate=None,
+                      pre_weight=None, pre_bias=None, *, post_norm: int = B.NORM_RMS,
+                      pre_norm: int = B.NORM_RMS, skip_scale: float = 1.0,
+                      branch_scale: float = 1.0, stream=None, eps: float | None = None):
+    """SandwichGrads from the gradients dh_out (None: zero) and dn of the
+    forward's results. h_out and stats are the forward's (eps is in stats; it is
+    accepted so that both calls take the same keywords)."""
+    ref = h_out if h_out is not None else dh_out
+    rows, d, gates = _sandwich_shapes(ref, y, post_weight, post_bias, gate, pre_weight, pre_bias,
+                                      pre_norm, skip_scale)
+    _expect(dh_out, (rows, d), "dh_out")
+    _expect(dn, (rows, d), "dn")
+    _expect(stats, (rows, 4), "stats")
+    if pre_norm != B.NORM_NONE and (dn is None or h_out is None):
+        raise ValueError("the backward of a pre_norm needs dn and h_out")
+    if pre_norm == B.NORM_NONE and dh_out is None:
+        raise ValueError("without a pre_norm the backward needs dh_out")
+    _check(ref, dh_out, dn)
+    if stats.dtype != torch.float32 or not stats.is_contiguous() or stats.device != ref.device:
+        raise ValueError("stats must be the contiguous fp32 tensor the forward returned")
+    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+    g = SandwichGrads(torch.empty_like(ref), like(y), like(post_weight), like(post_bias), like(gate),
+                      like(pre_weight), like(pre_bias))
+    code = dtype_code(ref)
+    need = B.monarch_sandwich_bwd_workspace_bytes(
+        rows, d, gates, post_bias is not None or pre_bias is not None, code)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=ref.device)
+    B.monarch_sandwich_bwd(dh_out, dn, h_out, y, stats, post_weight, post_bias, gate, pre_weight,
+                           pre_bias, g.dh, g.dy, g.dpost_weight, g.dpost_bias, g.dgate,
+                           g.dpre_weight, g.dpre_bias, ws, need, rows, d, gates, post_norm,
+                           pre_norm, skip_scale, branch_scale, code, stream)
+    return g
