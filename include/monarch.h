@@ -366,6 +366,51 @@ int monarch_sandwich_describe(int direction, int64_t rows, int64_t features, int
                               int dtype, char* buf, size_t buf_len);
 
 /* ---------------------------------------------------------------------------
+ * Distillation from a teacher's top logits, for a student whose dense layers
+ * became Monarch layers (monarch_project) and which is trained against the
+ * dense model. For row i with student logits z [vocab], teacher entries
+ * (id_k, t_k), k < top, and a label c:
+ *   p_k = softmax of t_k / temperature over the row's valid entries
+ *   q = softmax(z / temperature), s = softmax(z)          over the vocabulary
+ *   loss[i] = mix * temperature^2 * sum_k p_k (log p_k - log q[id_k])
+ *             - (1 - mix) * log s[c]
+ * An entry is valid when 0 <= id_k < vocab and t_k > -inf (pad shorter lists with
+ * id -1), a label when 0 <= c < vocab (mark ignored rows with any other value, as
+ * -100). Entries that name the same id add up. Without a valid entry the first
+ * term is 0, without a label the second. A row with neither has loss 0 and
+ * gradient 0 whatever its logits hold; so has a row whose logits are -inf
+ * throughout. p_k = 0 adds nothing, also where q is 0.
+ *   logits [rows, ld]: row i's vocab logits start at i*ld (ld >= vocab, in
+ *   elements); fp32 or bf16 (`dtype`), aligned to their element size only.
+ *   dlogits likewise with dld; columns past vocab are neither read nor written.
+ *   teacher fp32 [rows, top] and ids int64 [rows, top], top <=
+ *   MONARCH_DISTILL_MAX_TOP; labels int64 [rows] or NULL; loss fp32 [rows].
+ * 1e-6 <= temperature <= 1e6 and 0 <= mix <= 1, or MONARCH_ERR_VALUE. Sums are
+ * fp32, dlogits is rounded once. rows == 0 returns MONARCH_OK.
+ *
+ * monarch_distill_fwd: the loss, and stats (fp32 [rows, 4], 16-byte aligned, for
+ * the backward pass; may be NULL).
+ * monarch_distill_bwd: dlogits = dloss[i] * d loss[i] / d logits from the same inputs.
+ * monarch_distill_step: the loss and dlogits for row_weight (fp32 [rows], NULL:
+ * 1) in dloss's place in one call, which reads the logits from memory once
+ * where a row fits on the chip. In both, dlogits may be the logits' memory
+ * (dld == ld). */
+#define MONARCH_DISTILL_MAX_TOP 512
+
+int monarch_distill_fwd(const void* logits, int64_t ld, const void* teacher, const void* ids,
+                        const void* labels, void* loss, void* stats, int64_t rows, int64_t vocab,
+                        int64_t top, float temperature, float mix, int dtype, void* stream,
+                        void* const* events, int n_events);
+int monarch_distill_bwd(const void* dloss, const void* logits, int64_t ld, const void* teacher,
+                        const void* ids, const void* labels, const void* stats, void* dlogits,
+                        int64_t dld, int64_t rows, int64_t vocab, int64_t top, float temperature,
+                        float mix, int dtype, void* stream, void* const* events, int n_events);
+int monarch_distill_step(const void* logits, int64_t ld, const void* teacher, const void* ids,
+                         const void* labels, const void* row_weight, void* loss, void* dlogits,
+                         int64_t dld, int64_t rows, int64_t vocab, int64_t top, float temperature,
+                         float mix, int dtype, void* stream, void* const* events, int n_events);
+
+/* ---------------------------------------------------------------------------
  * Stream copy: copies `bytes` bytes from src to dst (device buffers, 16-byte
  * aligned, not overlapping), reading and writing each byte once with 16-byte
  * non-temporal accesses. Not part of the Monarch operator: it is the

@@ -33,6 +33,7 @@ F32 = 0
 BF16 = 1
 ACT_NONE = 0
 ACT_RELU = 1
+DISTILL_MAX_TOP = 512     # MONARCH_DISTILL_MAX_TOP
 NORM_NONE = 0
 NORM_RMS = 1
 NORM_LAYER = 2
@@ -47,7 +48,8 @@ EXPORTED = (
     "monarch_dyad_bwd_workspace_bytes",
     "monarch_dyad_bwd", "monarch_dyad_describe", "monarch_bwd_noalloc", "monarch_stream_copy",
     "monarch_sandwich_fwd", "monarch_sandwich_bwd_workspace_bytes", "monarch_sandwich_bwd",
-    "monarch_sandwich_describe",
+    "monarch_sandwich_describe", "monarch_distill_fwd", "monarch_distill_bwd",
+    "monarch_distill_step",
 )
 
 _lib = None
@@ -139,6 +141,15 @@ def load_library():
     lib.monarch_sandwich_bwd.restype = c_int
     lib.monarch_sandwich_describe.argtypes = [c_int] + [i64] * 3 + [c_int, ctypes.c_char_p, sz]
     lib.monarch_sandwich_describe.restype = c_int
+    lib.monarch_distill_fwd.argtypes = ([vp, i64] + [vp] * 5 + [i64] * 3 + [c_float] * 2 +
+                                        [c_int, vp] + ev)
+    lib.monarch_distill_fwd.restype = c_int
+    lib.monarch_distill_bwd.argtypes = ([vp, vp, i64] + [vp] * 5 + [i64] * 4 + [c_float] * 2 +
+                                        [c_int, vp] + ev)
+    lib.monarch_distill_bwd.restype = c_int
+    lib.monarch_distill_step.argtypes = ([vp, i64] + [vp] * 6 + [i64] * 4 + [c_float] * 2 +
+                                         [c_int, vp] + ev)
+    lib.monarch_distill_step.restype = c_int
     _lib = lib
     return lib
 
@@ -422,3 +433,30 @@ def monarch_sandwich_describe(direction, rows, features, gates, dtype):
     if n < 0:
         raise MonarchError(n, monarch_status_string(n))
     return buf.value.decode().split(";") if n else []
+
+
+def monarch_distill_fwd(logits, ld, teacher, ids, labels, loss, stats, rows, vocab, top,
+                        temperature, mix, dtype, stream=None, events=None) -> None:
+    lib = load_library()
+    arr, n = _events(events)
+    _check(lib.monarch_distill_fwd(_ptr(logits), ld, _ptr(teacher), _ptr(ids), _ptr(labels),
+                                   _ptr(loss), _ptr(stats), rows, vocab, top, temperature, mix,
+                                   dtype, _stream(stream), arr, n))
+
+
+def monarch_distill_bwd(dloss, logits, ld, teacher, ids, labels, stats, dlogits, dld, rows, vocab,
+                        top, temperature, mix, dtype, stream=None, events=None) -> None:
+    lib = load_library()
+    arr, n = _events(events)
+    _check(lib.monarch_distill_bwd(_ptr(dloss), _ptr(logits), ld, _ptr(teacher), _ptr(ids),
+                                   _ptr(labels), _ptr(stats), _ptr(dlogits), dld, rows, vocab, top,
+                                   temperature, mix, dtype, _stream(stream), arr, n))
+
+
+def monarch_distill_step(logits, ld, teacher, ids, labels, row_weight, loss, dlogits, dld, rows,
+                         vocab, top, temperature, mix, dtype, stream=None, events=None) -> None:
+    lib = load_library()
+    arr, n = _events(events)
+    _check(lib.monarch_distill_step(_ptr(logits), ld, _ptr(teacher), _ptr(ids), _ptr(labels),
+                                    _ptr(row_weight), _ptr(loss), _ptr(dlogits), dld, rows, vocab,
+                                    top, temperature, mix, dtype, _stream(stream), arr, n))

@@ -121,7 +121,7 @@ __device__ __forceinline__ float lanes_reduce(float v) {
 template <int TEAM>
 struct Team {
   static constexpr int WAVES = TEAM > 64 ? TEAM / 64 : 1;
-  static constexpr int MAXV = 2;   // values an exchange
+  static constexpr int MAXV = 3;   // values an exchange
   struct Lds {
     float slot[2][MAXV][WAVES];
   };

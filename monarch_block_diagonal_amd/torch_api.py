@@ -419,3 +419,93 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
                            g.dpre_weight, g.dpre_bias, ws, need, rows, d, gates, post_norm,
                            pre_norm, skip_scale, branch_scale, code, stream)
     return g
+
+
+def _distill_shapes(logits, teacher, ids, labels, per_row, name):
+    """(rows, vocab, top, ld) after checking logits [rows, vocab] (rows may lie
+    apart, columns may not), teacher and ids [rows, top], labels and per_row [rows]."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    rows, vocab = (int(v) for v in logits.shape)
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("a row's logits must lie side by side")
+    ld = int(logits.stride(0)) if rows > 1 else vocab
+    if ld < vocab:
+        raise ValueError("the rows of logits must not overlap")
+    if teacher.dim() != 2:
+        raise ValueError("the teacher's logits must be [rows, top]")
+    top = int(teacher.shape[1])
+    if top > B.DISTILL_MAX_TOP:
+        raise ValueError(f"at most {B.DISTILL_MAX_TOP} teacher entries a row, got {top}")
+    _expect(teacher, (rows, top), "the teacher's logits")
+    _expect(ids, (rows, top), "ids")
+    _expect(labels, (rows,), "labels")
+    _expect(per_row, (rows,), name)
+    for t, want, what in ((teacher, torch.float32, "the teacher's logits"), (ids, torch.int64, "ids"),
+                          (labels, torch.int64, "labels"), (per_row, torch.float32, name)):
+        if t is None:
+            continue
+        if t.dtype != want:
+            raise TypeError(f"{what} must be {want}")
+        if not t.is_contiguous() or t.device != logits.device:
+            raise ValueError(f"{what} must be contiguous and live beside the logits")
+    if logits.device.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    return rows, vocab, top, ld
+
+
+def _distill_out(logits, rows, vocab, ld, out):
+    """dlogits in the logits' own layout, or `out` after checking it."""
+    if out is None:
+        return torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
+    _expect(out, (rows, vocab), "out")
+    if out.dtype != logits.dtype or out.device != logits.device:
+        raise ValueError("out must have the logits' dtype and device")
+    if (vocab > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < vocab):
+        raise ValueError("out must have rows of side by side columns that do not overlap")
+    return out
+
+
+def distill_forward(logits, teacher, ids, labels=None, *, temperature: float = 1.0,
+                    mix: float = 1.0, stream=None):
+    """(loss [rows], stats) of distillation from a teacher's top logits:
+
+        loss = mix * temperature^2 * KL(p || softmax(logits / temperature)) + (1 - mix) * CE(labels)
+
+    p = softmax(teacher / temperature) over the row's entries, which sit at the
+    columns `ids` (int64; -1 pads). labels (int64) outside the vocabulary are ignored.
+    stats goes to distill_backward."""
+    rows, vocab, top, ld = _distill_shapes(logits, teacher, ids, labels, None, "")
+    loss = torch.empty((rows,), dtype=torch.float32, device=logits.device)
+    stats = torch.empty((rows, 4), dtype=torch.float32, device=logits.device)
+    B.monarch_distill_fwd(logits, ld, teacher, ids, labels, loss, stats, rows, vocab, top,
+                          temperature, mix, dtype_code(logits), stream)
+    return loss, stats
+
+
+def distill_backward(dloss, logits, teacher, ids, labels, stats, *, temperature: float = 1.0,
+                     mix: float = 1.0, out=None, stream=None):
+    """dlogits for dloss [rows]; out may be logits itself."""
+    rows, vocab, top, ld = _distill_shapes(logits, teacher, ids, labels, dloss, "dloss")
+    _expect(stats, (rows, 4), "stats")
+    if stats.dtype != torch.float32 or not stats.is_contiguous() or stats.device != logits.device:
+        raise ValueError("stats must be the contiguous fp32 tensor the forward returned")
+    dz = _distill_out(logits, rows, vocab, ld, out)
+    B.monarch_distill_bwd(dloss, logits, ld, teacher, ids, labels, stats, dz,
+                          int(dz.stride(0)) if rows > 1 else vocab, rows, vocab, top, temperature,
+                          mix, dtype_code(logits), stream)
+    return dz
+
+
+def distill_step(logits, teacher, ids, labels=None, row_weight=None, *, temperature: float = 1.0,
+                 mix: float = 1.0, out=None, stream=None):
+    """(loss [rows], dlogits) in one pass: dlogits is the gradient of
+    sum(row_weight * loss) (row_weight None: 1 for every row). out may be
+    logits itself, which saves a tensor of their size."""
+    rows, vocab, top, ld = _distill_shapes(logits, teacher, ids, labels, row_weight, "row_weight")
+    loss = torch.empty((rows,), dtype=torch.float32, device=logits.device)
+    dz = _distill_out(logits, rows, vocab, ld, out)
+    B.monarch_distill_step(logits, ld, teacher, ids, labels, row_weight, loss, dz,
+                           int(dz.stride(0)) if rows > 1 else vocab, rows, vocab, top, temperature,
+                           mix, dtype_code(logits), stream)
+    return loss, dz

@@ -14,3 +14,4 @@ from . import monarch_linear  # noqa: F401,E402
 from . import monarch_hypercube  # noqa: F401,E402
 from . import dyad  # noqa: F401,E402
 from . import sandwich  # noqa: F401,E402
+from . import distill  # noqa: F401,E402
