@@ -110,7 +110,7 @@ __global__ __launch_bounds__(TEAM) void distill_kernel(Distill a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int at = base + (u * TEAM + tid) * N;
-          if (at < a.vocab) raw[u] = load_piece<T>(z, at, a.vocab);
+          if (at < a.vocab) raw[u] = load_piece<T, true>(z, at, a.vocab);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(TEAM) void distill_kernel(Distill a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int at = base + (u * TEAM + tid) * N;
-          if (at < a.vocab) raw[u] = load_piece<T>(z, at, a.vocab);
+          if (at < a.vocab) raw[u] = load_piece<T, true>(z, at, a.vocab);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(TEAM) void distill_kernel(Distill a) {
             PieceOf<T>::unpack(raw[u], v);
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = nothing ? 0.0f : grad(v[i]);
-            store_piece<T>(dz, at, a.vocab, PieceOf<T>::pack(v));
+            store_piece<T, true>(dz, at, a.vocab, PieceOf<T>::pack(v));
           }
         }
       }

@@ -41,22 +41,34 @@ struct SandwichFwd {
   float skip, branch, eps;
 };
 
-template <typename T, int N>
-__device__ __forceinline__ void load_or(const void* p, int64_t off, int at, int d, float fill,
-                                        float (&v)[N]) {
-  if (p) {
-    PieceOf<T>::unpack(load_piece<T>(static_cast<const T*>(p) + off, at, d), v);
-  } else {
+// A piece of an optional row (weights, biases, a gate row): without one, ones or
+// zeros, so that the arithmetic is the same.
+template <typename T, bool CUT>
+__device__ __forceinline__ u32x4 par_piece(const void* p, int64_t off, int at, int d, float fill) {
+  if (p) return load_piece<T, CUT>(static_cast<const T*>(p) + off, at, d);
+  const uint32_t w = sizeof(T) == 2 ? (__float_as_uint(fill) >> 16) * 0x10001u : __float_as_uint(fill);
+  return u32x4{w, w, w, w};
+}
+
+// Keeps the compiler from carrying what it unpacked from r to the next use of
+// r: unpacking again is cheaper than the registers.
+__device__ __forceinline__ void forget(u32x4& r) { asm volatile("" : "+v"(r)); }
+
+// The elements of a piece at `at` that lie past the row, set to 0.
+template <bool CUT, int N>
+__device__ __forceinline__ void zero_past(float (&v)[N], int at, int d) {
+  if (at + (CUT ? N - 1 : 0) >= d)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = fill;
-  }
+    for (int i = 0; i < N; ++i)
+      if (!CUT || at + i >= d) v[i] = 0.0f;
 }
 
 // mean and 1/sqrt(mean square about it + eps) of the team's row (zero past d)
-template <int TEAM, int P, int N>
+template <bool CUT, int TEAM, int P, int N>
 __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][N], int lane, int d,
                                           int kind, float eps, float& mu, float& rho) {
   mu = 0.0f;
+  float q = 0.0f;
   if (kind == MONARCH_NORM_LAYER) {
     float s = 0.0f;
 #pragma unroll
@@ -64,94 +76,101 @@ __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][
 #pragma unroll
       for (int i = 0; i < N; ++i) s += v[p][i];
     mu = team.sum(s) / static_cast<float>(d);
-  }
-  float s = 0.0f;
 #pragma unroll
-  for (int p = 0; p < P; ++p)
+    for (int p = 0; p < P; ++p) {
+      float c[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float c = (p * TEAM + lane) * N + i < d ? v[p][i] - mu : 0.0f;
-      s = fmaf(c, c, s);
+      for (int i = 0; i < N; ++i) c[i] = v[p][i] - mu;
+      zero_past<CUT, N>(c, (p * TEAM + lane) * N, d);
+#pragma unroll
+      for (int i = 0; i < N; ++i) q = fmaf(c[i], c[i], q);
     }
-  rho = 1.0f / sqrtf(team.sum(s) / static_cast<float>(d) + eps);
+  } else {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < N; ++i) q = fmaf(v[p][i], v[p][i], q);
+  }
+  rho = 1.0f / sqrtf(team.sum(q) / static_cast<float>(d) + eps);
 }
 
-template <typename T, int TEAM, int P>
-__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void sandwich_fwd_kernel(SandwichFwd a) {
-  constexpr int N = PieceOf<T>::N, TEAMS = TEAM > 256 ? 1 : 256 / TEAM;
+template <typename T, int TEAM, int P, bool CUT>
+__global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3) void sandwich_fwd_kernel(SandwichFwd a) {
+  constexpr int N = PieceOf<T>::N, TEAMS = TEAM > 64 ? 1 : 256 / TEAM;
   __shared__ typename Team<TEAM>::Lds lds;
   Team<TEAM> team(&lds);
   const int lane = threadIdx.x % TEAM;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM; row < a.rows;
        row += static_cast<int64_t>(gridDim.x) * TEAMS) {
-    const int64_t off = row * a.d;
+    const int d = anew(a.d);
+    const int64_t off = row * d;
     const T* h = static_cast<const T*>(a.h) + off;
     u32x4 hr[P], yr[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      hr[p] = load_piece<T>(h, (p * TEAM + lane) * N, a.d);
+      hr[p] = load_piece<T, CUT>(h, (p * TEAM + lane) * N, d);
       if (a.y)
-        yr[p] = load_piece<T>(static_cast<const T*>(a.y) + off, (p * TEAM + lane) * N, a.d);
+        yr[p] = load_piece<T, CUT>(static_cast<const T*>(a.y) + off, (p * TEAM + lane) * N, d);
     }
     float v[P][N];
-    f32x4 st = {0.0f, 1.0f, 0.0f, 1.0f};
+    float mu_y = 0.0f, rho_y = 1.0f, mu_h = 0.0f, rho_h = 1.0f;
     if (a.y) {
+      if (a.post != MONARCH_NORM_NONE) {
 #pragma unroll
-      for (int p = 0; p < P; ++p) PieceOf<T>::unpack(yr[p], v[p]);
-      float mu = 0.0f, rho = 1.0f;
-      if (a.post != MONARCH_NORM_NONE)
-        row_stats<TEAM, P, N>(team, v, lane, a.d, a.post, a.eps, mu, rho);
-      st[0] = mu, st[1] = rho;
-      const int64_t goff = a.gate ? row / a.rows_per_gate * a.d : 0;
+        for (int p = 0; p < P; ++p) PieceOf<T>::unpack(yr[p], v[p]);
+        row_stats<CUT, TEAM, P, N>(team, v, lane, d, a.post, a.eps, mu_y, rho_y);
+      }
+      const int64_t goff = a.gate ? row / a.rows_per_gate * d : 0;
+      const float mean = mu_y * rho_y;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
-        float w[N], b[N], g[N], hv[N];
-        load_or<T, N>(a.post_w, 0, at, a.d, 1.0f, w);
-        load_or<T, N>(a.post_b, 0, at, a.d, 0.0f, b);
-        load_or<T, N>(a.gate, goff, at, a.d, 1.0f, g);
-        PieceOf<T>::unpack(hr[p], hv);
+        float t[N];
+        forget(yr[p]);
+        PieceOf<T>::unpack(yr[p], v[p]);
+        float w[N], b[N], g[N];
+        PieceOf<T>::unpack(par_piece<T, CUT>(a.post_w, 0, at, d, 1.0f), w);
+        PieceOf<T>::unpack(par_piece<T, CUT>(a.post_b, 0, at, d, 0.0f), b);
+        PieceOf<T>::unpack(par_piece<T, CUT>(a.gate, goff, at, d, 1.0f), g);
+        PieceOf<T>::unpack(hr[p], t);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float u = fmaf((v[p][i] - mu) * rho, w[i], b[i]);
-          v[p][i] = fmaf(a.skip, hv[i], a.branch * g[i] * u);
-          if (at + i >= a.d) v[p][i] = 0.0f;
+          const float u = fmaf(fmaf(v[p][i], rho_y, -mean), w[i], b[i]);
+          v[p][i] = fmaf(a.skip, t[i], a.branch * g[i] * u);
         }
-        if (at < a.d)
-          store_piece<T>(static_cast<T*>(a.h_out) + off, at, a.d, PieceOf<T>::pack(v[p]));
+        store_piece<T, CUT>(static_cast<T*>(a.h_out) + off, at, d, PieceOf<T>::pack(v[p]));
+        zero_past<CUT, N>(v[p], at, d);
       }
     } else {
 #pragma unroll
       for (int p = 0; p < P; ++p) PieceOf<T>::unpack(hr[p], v[p]);
     }
     if (a.pre != MONARCH_NORM_NONE) {
-      float mu, rho;
-      row_stats<TEAM, P, N>(team, v, lane, a.d, a.pre, a.eps, mu, rho);
-      st[2] = mu, st[3] = rho;
+      row_stats<CUT, TEAM, P, N>(team, v, lane, d, a.pre, a.eps, mu_h, rho_h);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
-        if (at < a.d) {
-          float w[N], b[N], n[N];
-          load_or<T, N>(a.pre_w, 0, at, a.d, 1.0f, w);
-          load_or<T, N>(a.pre_b, 0, at, a.d, 0.0f, b);
+        float w[N], b[N];
+        PieceOf<T>::unpack(par_piece<T, CUT>(a.pre_w, 0, at, d, 1.0f), w);
+        PieceOf<T>::unpack(par_piece<T, CUT>(a.pre_b, 0, at, d, 0.0f), b);
 #pragma unroll
-          for (int i = 0; i < N; ++i) n[i] = fmaf((v[p][i] - mu) * rho, w[i], b[i]);
-          store_piece<T>(static_cast<T*>(a.n_out) + off, at, a.d, PieceOf<T>::pack(n));
-        }
+        for (int i = 0; i < N; ++i) v[p][i] = fmaf((v[p][i] - mu_h) * rho_h, w[i], b[i]);
+        store_piece<T, CUT>(static_cast<T*>(a.n_out) + off, at, d, PieceOf<T>::pack(v[p]));
       }
     }
-    if (lane == 0) *reinterpret_cast<f32x4*>(a.stats + row * 4) = st;
+    if (lane == 0) *reinterpret_cast<f32x4*>(a.stats + row * 4) = f32x4{mu_y, rho_y, mu_h, rho_h};
   }
 }
 
 // ------------------------------------------------------------------ backward
 
-// How the rows of a backward call are cut. CHUNK: chunk c holds rows of one
+// How the rows of a backward call are cut (GATE). CHUNK: chunk c holds rows of one
 // gate row only (chunk / cpg), and its sums are of D alone; the gate and the
-// branch scale are applied when the chunks are joined. UNIT: many short gate
-// runs (down to one row each); each is summed by one team, which stores its
-// dgate row itself, and the chunk's sums are of g * D.
+// branch scale are applied when the chunks are joined. RUN: many short gate runs;
+// each is summed by one team, which stores its dgate row itself, and the
+// chunk's sums are of g * D. TOKEN: RUN with one row a run.
+enum { CHUNK = 0, RUN = 1, TOKEN = 2 };
+
 struct SandwichBwd {
   const void *dh_out, *dn, *h_out, *y;
   const float* stats;
@@ -164,27 +183,69 @@ struct SandwichBwd {
   float skip, branch;
 };
 
-template <typename T, int TEAM, int P, bool UNIT, bool BIAS>
-__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void sandwich_bwd_kernel(SandwichBwd a) {
-  constexpr int N = PieceOf<T>::N, WG = TEAM > 256 ? TEAM : 256, TEAMS = WG / TEAM;
+// A thread's sums over rows for its own columns: in registers, or (wide rows,
+// whose columns would not leave registers for the row itself) in LDS, 16 bytes a
+// lane side by side.
+template <int TEAM, int P, int N, bool IN_LDS>
+struct Sums {
+  float v[IN_LDS ? 1 : P][N];
+  f32x4* lds;
+  __device__ __forceinline__ void clear(f32x4* l) {
+    lds = l;
+    if constexpr (IN_LDS) {
+#pragma unroll
+      for (int k = 0; k < P * N / 4; ++k) lds[k * TEAM + threadIdx.x] = f32x4{0, 0, 0, 0};
+    } else {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[p][i] = 0.0f;
+    }
+  }
+  // adds x[i] to the sums of piece p
+  __device__ __forceinline__ void add(int p, const float (&x)[N]) {
+    if constexpr (IN_LDS) {
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        f32x4& s = lds[(p * (N / 4) + k) * TEAM + threadIdx.x];
+        f32x4 t = s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] += x[4 * k + i];
+        s = t;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[p][i] += x[i];
+    }
+  }
+  __device__ __forceinline__ float get(int p, int i) const {
+    if constexpr (IN_LDS)
+      return lds[(p * (N / 4) + i / 4) * TEAM + threadIdx.x][i % 4];
+    else
+      return v[p][i];
+  }
+};
+
+template <typename T, int TEAM, int P, int GATE, bool BIAS, bool CUT>
+__global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(SandwichBwd a) {
+  constexpr int N = PieceOf<T>::N, WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
   constexpr int COLS = TEAM * P * N;
+  constexpr bool WIDE = TEAM > 256;   // sums in LDS, parameters read again for every row
   __shared__ typename Team<TEAM>::Lds lds;
-  __shared__ float join[TEAMS > 1 ? TEAMS * COLS : 1];
+  __shared__ f32x4 shared[WIDE ? 2 * COLS / 4 : TEAMS > 1 ? TEAMS * COLS / 4 : 1];
   Team<TEAM> team(&lds);
   const int lane = threadIdx.x % TEAM, tm = threadIdx.x / TEAM;
   const float inv_d = 1.0f / static_cast<float>(a.d);
   // rows [first, last) of this team, taken every `step`
-  int64_t first, last;
-  int step;
-  int64_t group = 0;
-  if constexpr (UNIT) {
+  int64_t first, last, group = 0;
+  int step = 1;
+  if constexpr (GATE != CHUNK) {
     // chunk_rows counts whole gate runs here: this team's own range of them
     const int64_t units = a.rows / a.rows_per_gate;
-    const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * TEAMS + tm) * a.chunk_rows;
-    const int64_t u1 = u0 + a.chunk_rows < units ? u0 + a.chunk_rows : units;
-    first = u0 * a.rows_per_gate;
+    group = (static_cast<int64_t>(blockIdx.x) * TEAMS + tm) * a.chunk_rows;
+    const int64_t u1 = group + a.chunk_rows < units ? group + a.chunk_rows : units;
+    first = group * a.rows_per_gate;
     last = u1 * a.rows_per_gate;
-    step = 1;
   } else {
     group = blockIdx.x / a.cpg;
     const int64_t c = blockIdx.x - group * a.cpg;
@@ -194,126 +255,191 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void sandwich_bwd_kernel(S
     first += tm;
     step = TEAMS;
   }
-  float post_w[P][N], pre_w[P][N], gate[P][N], post_b[BIAS ? P : 1][N];
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int at = (p * TEAM + lane) * N;
-    load_or<T, N>(a.post_w, 0, at, a.d, 1.0f, post_w[p]);
-    load_or<T, N>(a.pre_w, 0, at, a.d, 1.0f, pre_w[p]);
-    if constexpr (BIAS) load_or<T, N>(a.post_b, 0, at, a.d, 0.0f, post_b[p]);
-    if constexpr (!UNIT) load_or<T, N>(a.gate, group * a.d, at, a.d, 1.0f, gate[p]);
-  }
-  float s_post[P][N] = {}, s_pre[P][N] = {}, s_gate[UNIT ? P : 1][N] = {};
-  float s_postb[BIAS ? P : 1][N] = {}, s_preb[BIAS ? P : 1][N] = {};
-  int64_t left = a.rows_per_gate;   // UNIT: rows of the gate run still to come
-  for (int64_t row = first; row < last; row += step) {
-    const int64_t off = row * a.d;
-    const f32x4 st = *reinterpret_cast<const f32x4*>(a.stats + row * 4);
-    u32x4 dhr[P], dnr[P], hr[P], yr[P], gr[UNIT ? P : 1];
+  const u32x4 zero = {0, 0, 0, 0};
+  u32x4 post_wr[P], pre_wr[P], gr[P];
+  auto load_pars = [&]() {
+    const int d = anew(a.d);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
-      const u32x4 zero = {0, 0, 0, 0};
-      dhr[p] = dnr[p] = hr[p] = yr[p] = zero;
+      post_wr[p] = par_piece<T, CUT>(a.post_w, 0, at, d, 1.0f);
+      pre_wr[p] = par_piece<T, CUT>(a.pre_w, 0, at, d, 1.0f);
+      if constexpr (GATE == CHUNK) gr[p] = par_piece<T, CUT>(a.gate, group * d, at, d, 1.0f);
+    }
+  };
+  if constexpr (!WIDE) load_pars();
+  Sums<TEAM, P, N, WIDE> s_post, s_pre;
+  Sums<TEAM, BIAS ? P : 1, N, false> s_postb, s_preb;
+  Sums<TEAM, GATE == RUN ? P : 1, N, false> s_gate;
+  s_post.clear(shared);
+  s_pre.clear(shared + (WIDE ? COLS / 4 : 0));
+  s_postb.clear(nullptr);
+  s_preb.clear(nullptr);
+  s_gate.clear(nullptr);
+  int64_t left = a.rows_per_gate;   // RUN: rows of the gate run still to come
+
+  u32x4 dnr[P], hr[P];
+  auto load_pre = [&](int64_t row) {
+    const int d = anew(a.d);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int at = (p * TEAM + lane) * N;
+      dnr[p] = hr[p] = zero;
       if (a.pre != MONARCH_NORM_NONE) {
-        dnr[p] = load_piece<T>(static_cast<const T*>(a.dn) + off, at, a.d);
-        hr[p] = load_piece<T>(static_cast<const T*>(a.h_out) + off, at, a.d);
+        dnr[p] = load_piece<T, CUT>(static_cast<const T*>(a.dn) + row * d, at, d);
+        hr[p] = load_piece<T, CUT>(static_cast<const T*>(a.h_out) + row * d, at, d);
       }
-      if (a.dh_out) dhr[p] = load_piece<T>(static_cast<const T*>(a.dh_out) + off, at, a.d);
-      if (a.y) yr[p] = load_piece<T>(static_cast<const T*>(a.y) + off, at, a.d);
-      if constexpr (UNIT)
-        gr[p] = load_piece<T>(static_cast<const T*>(a.gate) + row / a.rows_per_gate * a.d, at, a.d);
     }
+  };
+  if (WIDE && first < last) load_pre(first);
+  for (int64_t row = first; row < last; row += step) {
+    const int d = anew(a.d);
+    const int64_t off = row * d;
+    const f32x4 st = *reinterpret_cast<const f32x4*>(a.stats + row * 4);
+    if constexpr (!WIDE) load_pre(row);
+    u32x4 yr[P];
     float D[P][N];
+    {
+      u32x4 dhr[P];
+      auto load_rest = [&]() {
 #pragma unroll
-    for (int p = 0; p < P; ++p) PieceOf<T>::unpack(dhr[p], D[p]);
-    if (a.pre != MONARCH_NORM_NONE) {
-      float s[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        float dn[N], h[N];
-        PieceOf<T>::unpack(dnr[p], dn);
-        PieceOf<T>::unpack(hr[p], h);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float hat = (h[i] - st[2]) * st[3], q = dn[i] * pre_w[p][i];
-          s[0] = fmaf(q, hat, s[0]);
-          s[1] += q;
-          s_pre[p][i] = fmaf(dn[i], hat, s_pre[p][i]);
-          if constexpr (BIAS) s_preb[p][i] += dn[i];
+        for (int p = 0; p < P; ++p) {
+          const int at = (p * TEAM + lane) * N;
+          dhr[p] = yr[p] = zero;
+          if (a.dh_out) dhr[p] = load_piece<T, CUT>(static_cast<const T*>(a.dh_out) + off, at, d);
+          if (a.y) yr[p] = load_piece<T, CUT>(static_cast<const T*>(a.y) + off, at, d);
+          if constexpr (GATE != CHUNK)
+            gr[p] = load_piece<T, CUT>(static_cast<const T*>(a.gate) + group * d, at, d);
         }
-      }
-      team.template reduce<SumOp, 2>(s);
-      const float c1 = s[0] * inv_d, c2 = a.pre == MONARCH_NORM_LAYER ? s[1] * inv_d : 0.0f;
+      };
+      if constexpr (WIDE)
+        load_pars();
+      else
+        load_rest();
+      float c1 = 0.0f, c2 = 0.0f;
+      if (a.pre != MONARCH_NORM_NONE) {
+        const float mean = st[2] * st[3];
+        float s[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        float dn[N], h[N];
-        PieceOf<T>::unpack(dnr[p], dn);
-        PieceOf<T>::unpack(hr[p], h);
+        for (int p = 0; p < P; ++p) {
+          float dn[N], h[N], w[N];
+          PieceOf<T>::unpack(dnr[p], dn);
+          PieceOf<T>::unpack(hr[p], h);
+          if constexpr (BIAS) s_preb.add(p, dn);
+          forget(pre_wr[p]);
+          PieceOf<T>::unpack(pre_wr[p], w);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float hat = (h[i] - st[2]) * st[3], q = dn[i] * pre_w[p][i];
-          D[p][i] = fmaf(st[3], q - fmaf(hat, c1, c2), D[p][i]);
+          for (int i = 0; i < N; ++i) {
+            h[i] = fmaf(h[i], st[3], -mean) * dn[i];   // dn hhat
+            s[0] = fmaf(h[i], w[i], s[0]);
+            s[1] = fmaf(dn[i], w[i], s[1]);
+          }
+          s_pre.add(p, h);
         }
+        if constexpr (WIDE) load_rest();
+        team.template reduce<SumOp, 2>(s);
+        // D = dh' + rho (q - hhat c1 - c2) with hhat = h rho - mean
+        c1 = s[0] * inv_d;
+        c2 = a.pre == MONARCH_NORM_LAYER ? s[1] * inv_d : 0.0f;
+        const float k1 = c1 * st[3] * st[3], k0 = st[3] * (c2 - c1 * mean);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const int at = (p * TEAM + lane) * N;
+          float dn[N], h[N], w[N];
+          forget(dnr[p]);
+          forget(hr[p]);
+          forget(pre_wr[p]);
+          PieceOf<T>::unpack(dnr[p], dn);
+          PieceOf<T>::unpack(hr[p], h);
+          PieceOf<T>::unpack(dhr[p], D[p]);
+          PieceOf<T>::unpack(pre_wr[p], w);
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            D[p][i] += fmaf(st[3] * dn[i], w[i], -fmaf(h[i], k1, k0));
+          zero_past<CUT, N>(D[p], at, d);
+        }
+      } else {
+        if constexpr (WIDE) load_rest();
+#pragma unroll
+        for (int p = 0; p < P; ++p) PieceOf<T>::unpack(dhr[p], D[p]);
       }
     }
+    if (WIDE && row + step < last) load_pre(row + step);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
-      if (at < a.d) {
+      if (at < d) {
         float o[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = a.skip * D[p][i];
-        store_piece<T>(static_cast<T*>(a.dh) + off, at, a.d, PieceOf<T>::pack(o));
+        store_piece<T, CUT>(static_cast<T*>(a.dh) + off, at, d, PieceOf<T>::pack(o));
       }
     }
     if (a.y) {
+      const float mean = st[0] * st[1];
       float s[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        float y[N], g[N];
+        const int at = (p * TEAM + lane) * N;
+        float y[N], w[N], g[N], o[N];
         PieceOf<T>::unpack(yr[p], y);
-        if constexpr (UNIT) PieceOf<T>::unpack(gr[p], g);
+        forget(post_wr[p]);
+        forget(gr[p]);
+        PieceOf<T>::unpack(post_wr[p], w);
+        PieceOf<T>::unpack(gr[p], g);
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = fmaf(y[i], st[1], -mean);   // yhat
+        if constexpr (GATE != CHUNK) {
+          // dgate = branch D u
+          float b[N];
+          if constexpr (BIAS) PieceOf<T>::unpack(par_piece<T, CUT>(a.post_b, 0, at, d, 0.0f), b);
+#pragma unroll
+          for (int i = 0; i < N; ++i) o[i] = D[p][i] * (BIAS ? fmaf(y[i], w[i], b[i]) : y[i] * w[i]);
+          if constexpr (GATE == RUN) {
+            s_gate.add(p, o);
+          } else if (a.dgate) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) o[i] *= a.branch;
+            store_piece<T, CUT>(static_cast<T*>(a.dgate) + group * d, at, d, PieceOf<T>::pack(o));
+          }
+          // e / branch = g D, which D becomes
+#pragma unroll
+          for (int i = 0; i < N; ++i) D[p][i] *= g[i];
+        }
+        if constexpr (BIAS) s_postb.add(p, D[p]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = D[p][i] * y[i];
+        s_post.add(p, o);
+        // D becomes q2 = branch g D w
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float hat = (y[i] - st[0]) * st[1];
-          const float gv = UNIT ? g[i] : gate[p][i];
-          const float q2 = a.branch * gv * D[p][i] * post_w[p][i];
-          s[0] = fmaf(q2, hat, s[0]);
-          s[1] += q2;
-          if constexpr (UNIT) {
-            const float u = BIAS ? fmaf(hat, post_w[p][i], post_b[p][i]) : hat * post_w[p][i];
-            s_gate[p][i] = fmaf(D[p][i], u, s_gate[p][i]);
-            s_post[p][i] = fmaf(gv * D[p][i], hat, s_post[p][i]);
-            if constexpr (BIAS) s_postb[p][i] = fmaf(gv, D[p][i], s_postb[p][i]);
-          } else {
-            s_post[p][i] = fmaf(D[p][i], hat, s_post[p][i]);
-            if constexpr (BIAS) s_postb[p][i] += D[p][i];
-          }
+          if constexpr (GATE == CHUNK) D[p][i] *= g[i];
+          D[p][i] *= a.branch * w[i];
+          s[0] = fmaf(D[p][i], y[i], s[0]);
+          s[1] += D[p][i];
         }
       }
-      float c1 = 0.0f, c2 = 0.0f;
+      float k1 = 0.0f, k0 = 0.0f;
       if (a.post != MONARCH_NORM_NONE) {
         team.template reduce<SumOp, 2>(s);
-        c1 = s[0] * inv_d;
-        c2 = a.post == MONARCH_NORM_LAYER ? s[1] * inv_d : 0.0f;
+        // dy = rho (q2 - yhat c1 - c2) with yhat = y rho - mean
+        const float c1 = s[0] * inv_d, c2 = a.post == MONARCH_NORM_LAYER ? s[1] * inv_d : 0.0f;
+        k1 = c1 * st[1] * st[1];
+        k0 = st[1] * (c2 - c1 * mean);
       }
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
-        float y[N], g[N], o[N];
+        float y[N];
+        forget(yr[p]);
         PieceOf<T>::unpack(yr[p], y);
-        if constexpr (UNIT) PieceOf<T>::unpack(gr[p], g);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float hat = (y[i] - st[0]) * st[1];
-          const float gv = UNIT ? g[i] : gate[p][i];
-          o[i] = st[1] * (a.branch * gv * D[p][i] * post_w[p][i] - fmaf(hat, c1, c2));
-        }
-        if (at < a.d) store_piece<T>(static_cast<T*>(a.dy) + off, at, a.d, PieceOf<T>::pack(o));
+        for (int i = 0; i < N; ++i) y[i] = fmaf(st[1], D[p][i], -fmaf(y[i], k1, k0));
+        store_piece<T, CUT>(static_cast<T*>(a.dy) + off, at, d, PieceOf<T>::pack(y));
       }
     }
-    if constexpr (UNIT) {
+    if constexpr (GATE == TOKEN) ++group;
+    if constexpr (GATE == RUN) {
       if (--left == 0) {
         left = a.rows_per_gate;
 #pragma unroll
@@ -321,20 +447,18 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void sandwich_bwd_kernel(S
           const int at = (p * TEAM + lane) * N;
           float o[N];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            o[i] = a.branch * s_gate[p][i];
-            s_gate[p][i] = 0.0f;
-          }
-          if (a.dgate && at < a.d)
-            store_piece<T>(static_cast<T*>(a.dgate) + row / a.rows_per_gate * a.d, at, a.d,
-                           PieceOf<T>::pack(o));
+          for (int i = 0; i < N; ++i) o[i] = a.branch * s_gate.get(p, i);
+          if (a.dgate)
+            store_piece<T, CUT>(static_cast<T*>(a.dgate) + group * d, at, d, PieceOf<T>::pack(o));
         }
+        s_gate.clear(nullptr);
+        ++group;
       }
     }
   }
   // this chunk's sums: the teams' are added in team order
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.sums * a.d;
-  auto put = [&](int which, const float(&s)[P][N]) {
+  auto put = [&](int which, const auto& s) {
     if (which < 0) return;
     float* out = part + static_cast<int64_t>(which) * a.d;
     if constexpr (TEAMS == 1) {
@@ -343,14 +467,15 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void sandwich_bwd_kernel(S
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int at = (p * TEAM + lane) * N + i;
-          if (at < a.d) out[at] = s[p][i];
+          if (at < a.d) out[at] = s.get(p, i);
         }
     } else {
+      float* join = reinterpret_cast<float*>(shared);
       __syncthreads();
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int i = 0; i < N; ++i) join[tm * COLS + (p * TEAM + lane) * N + i] = s[p][i];
+        for (int i = 0; i < N; ++i) join[tm * COLS + (p * TEAM + lane) * N + i] = s.get(p, i);
       __syncthreads();
       for (int at = threadIdx.x; at < a.d; at += WG) {
         float t = join[at];
@@ -370,18 +495,17 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void sandwich_bwd_kernel(S
 
 // Joins the chunks' sums. A job is one output row: the weight gradients (sums
 // over every chunk, weighted by the chunk's gate row) and, when chunks hold
-// sums of D alone, one dgate row each. A workgroup takes 64 columns; 16 slices
-// of 64 threads sum contiguous chunk ranges, and the slices are added in order.
+// sums of D alone, one dgate row each. A workgroup takes 32 columns; 32 slices
+// of 32 threads sum contiguous chunk ranges, and the slices are added in order.
 struct SandwichJoin {
   const float* part;
   const void *gate, *post_w, *post_b;   // gate: null where the sums hold it already
   void *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
-  int64_t chunks, cpg;
-  int d, sums, s_post, s_postb, s_pre, s_preb;
+  int chunks, cpg, d, sums, s_post, s_postb, s_pre, s_preb;
   float branch;
 };
 
-constexpr int JC = 64, JS = 16;
+constexpr int JC = 32, JS = 32;
 constexpr int kWeightJobs = 4;   // post_w, post_b, pre_w, pre_b; then one job a gate row
 
 template <typename T>
@@ -391,7 +515,7 @@ __global__ __launch_bounds__(JC* JS) void sandwich_join_kernel(SandwichJoin a) {
   const int at = blockIdx.y * JC + col;
   const int64_t job = blockIdx.x;
   int which, which2 = -1;
-  int64_t c0 = 0, c1 = a.chunks;
+  int c0 = 0, c1 = a.chunks;
   bool gated = false;
   void* out;
   if (job < kWeightJobs) {
@@ -401,24 +525,36 @@ __global__ __launch_bounds__(JC* JS) void sandwich_join_kernel(SandwichJoin a) {
   } else {
     which = a.s_post;
     which2 = a.post_b ? a.s_postb : -1;
-    c0 = (job - kWeightJobs) * a.cpg;
+    c0 = static_cast<int>(job - kWeightJobs) * a.cpg;
     c1 = c0 + a.cpg;
     out = static_cast<T*>(a.dgate) + (job - kWeightJobs) * a.d;
   }
   if (!out || which < 0) return;   // the whole workgroup
-  const int64_t per = (c1 - c0 + JS - 1) / JS;
-  const int64_t b = c0 + slice * per, e = b + per < c1 ? b + per : c1;
+  const int per = (c1 - c0 + JS - 1) / JS;
+  const int b = c0 + slice * per, e = min(b + per, c1);
   float s = 0.0f, s2 = 0.0f;
   if (at < a.d) {
-    const float* p = a.part + static_cast<int64_t>(which) * a.d + at;
-    const float* p2 = a.part + static_cast<int64_t>(which2 < 0 ? 0 : which2) * a.d + at;
     const int64_t stride = static_cast<int64_t>(a.sums) * a.d;
-#pragma unroll 4
-    for (int64_t c = b; c < e; ++c) {
-      float v = p[c * stride];
-      if (gated) v *= Io<T>::load(a.gate, c / a.cpg * a.d + at);
-      s += v;
-      if (which2 >= 0) s2 += p2[c * stride];
+    auto sum = [&](int w) {
+      const float* p = a.part + static_cast<int64_t>(w) * a.d + at;
+      float t = 0.0f;
+#pragma unroll 8
+      for (int c = b; c < e; ++c) t += p[c * stride];
+      return t;
+    };
+    if (!gated) {
+      s = sum(which);
+      if (which2 >= 0) s2 = sum(which2);
+    } else {
+      const float* p = a.part + static_cast<int64_t>(which) * a.d + at;
+      int c = b;
+      while (c < e) {   // the chunks of one gate row at a time
+        const int g = c / a.cpg, end = min(e, (g + 1) * a.cpg);
+        float t = 0.0f;
+#pragma unroll 8
+        for (; c < end; ++c) t += p[c * stride];
+        s = fmaf(t, Io<T>::load(a.gate, static_cast<int64_t>(g) * a.d + at), s);
+      }
     }
   }
   buf[0][slice][col] = s;
@@ -435,10 +571,7 @@ __global__ __launch_bounds__(JC* JS) void sandwich_join_kernel(SandwichJoin a) {
     if (which2 >= 0) s = fmaf(s2, Io<T>::load(a.post_b, at), s);
   }
   if (job < 2 || job >= kWeightJobs) s *= a.branch;
-  if constexpr (sizeof(T) == 2)
-    static_cast<uint16_t*>(out)[at] = f32_to_bf16(s);
-  else
-    static_cast<float*>(out)[at] = s;
+  Io<T>::store(out, at, s);
 }
 
 // ---------------------------------------------------------------- host side
@@ -447,42 +580,50 @@ struct Shape {
   int team, pieces;
 };
 
-// The smallest team (of at least `least` threads) whose threads hold at most
-// `most` pieces of a row.
-Shape shape_of(int64_t d, bool bf16, int least, int most) {
-  const int n = bf16 ? 8 : 4;
-  const int64_t pieces = (d + n - 1) / n;
-  static const int teams[] = {16, 32, 64, 256, 1024};
-  for (int t : teams)
-    if (t >= least && (pieces + t - 1) / t <= most)
-      return {t, static_cast<int>((pieces + t - 1) / t)};
-  return {1024, static_cast<int>((pieces + 1023) / 1024)};
+// The smallest team whose threads hold at most `few` (up to a wave) or `many`
+// pieces of a row; `last` for any row that is wider.
+Shape shape_of(int64_t d, bool bf16, int first, int last, int few, int many) {
+  const int per = bf16 ? 8 : 4;
+  const int64_t pieces = (d + per - 1) / per;
+  int t = first;
+  while (t < last && (pieces + t - 1) / t > (t > 64 ? many : few)) t *= 2;
+  return {t, static_cast<int>((pieces + t - 1) / t)};
+}
+
+Shape fwd_shape(int64_t d, bool bf16) {
+  return shape_of(d, bf16, 16, 1024, bf16 ? 3 : 4, bf16 ? 2 : 4);
+}
+Shape bwd_shape(int64_t d, bool bf16) {
+  return shape_of(d, bf16, 32, bf16 ? 512 : 1024, bf16 ? 3 : 4, bf16 ? 2 : 4);
 }
 
 struct BwdPlan {
   Shape shape;
-  bool unit, bias;
+  int gate;      // CHUNK, RUN or TOKEN
+  bool bias;
   int64_t chunks, chunk_rows, cpg, rows_per_gate;
   int sums, s_post, s_postb, s_pre, s_preb;
   size_t ws;
 };
 
 constexpr int64_t kChunks = 512;      // workgroups aimed at: two a CU
-constexpr int64_t kUnitRows = 32;     // gate runs up to this long are a team's own
+constexpr int64_t kRunRows = 32;     // gate runs up to this long are a team's own
 
 // Everything about a backward call that depends on sizes alone (`with`: which
 // of post_w, post_b, gate, pre_w, pre_b there are, as the sums they need).
 BwdPlan bwd_plan(int64_t rows, int64_t d, int64_t gates, bool has_y, bool post_bias, bool has_pre,
                  bool pre_bias, bool bf16) {
   BwdPlan p = {};
-  p.shape = shape_of(d, bf16, 32, bf16 ? 3 : 4);
+  p.shape = bwd_shape(d, bf16);
   p.bias = post_bias || pre_bias;
   p.rows_per_gate = gates > 0 ? rows / gates : rows;
-  p.unit = rows > 0 && gates > 1 && p.rows_per_gate <= kUnitRows;
-  const int teams = p.shape.team >= 256 ? 1 : 256 / p.shape.team;
+  p.gate = rows == 0 || gates <= 1 || p.rows_per_gate > kRunRows ? CHUNK
+           : p.rows_per_gate > 1                                   ? RUN
+                                                                   : TOKEN;
+  const int teams = p.shape.team > 64 ? 1 : 256 / p.shape.team;
   if (rows == 0) {
     p.cpg = 0;   // no chunk: every sum is empty
-  } else if (p.unit) {
+  } else if (p.gate != CHUNK) {
     const int64_t units = gates, slots = kChunks * teams;
     p.chunk_rows = (units + slots - 1) / slots;
     p.chunks = (units + p.chunk_rows * teams - 1) / (p.chunk_rows * teams);
@@ -516,105 +657,137 @@ int check_sizes(int64_t rows, int64_t d, int64_t gates, int post, int pre, int d
   return MONARCH_OK;
 }
 
+// Whether rows end inside a piece (then they start off 16-byte boundaries too).
+bool cut_rows(int64_t d, bool bf16) { return d % (bf16 ? 8 : 4) != 0; }
+
 template <typename T, int TEAM, int P>
-void fwd_launch(const SandwichFwd& a, hipStream_t s) {
-  constexpr int WG = TEAM > 256 ? TEAM : 256, TEAMS = WG / TEAM;
+void fwd_launch(const SandwichFwd& a, bool cut, hipStream_t s) {
+  constexpr int WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
   int64_t grid = (a.rows + TEAMS - 1) / TEAMS;
   if (grid > (1 << 20)) grid = 1 << 20;   // fewer than 2^32 threads; the rest by stride
-  hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P>), dim3(static_cast<unsigned>(grid)), dim3(WG),
-                     0, s, a);
+  const dim3 g(static_cast<unsigned>(grid)), block(WG);
+  if (cut)
+    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true>), g, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, false>), g, block, 0, s, a);
 }
 
 template <typename T, int TEAM, int P>
-void bwd_launch(const SandwichBwd& a, const BwdPlan& p, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.chunks)), block(TEAM > 256 ? TEAM : 256);
-  if (p.unit && p.bias)
-    hipLaunchKernelGGL((sandwich_bwd_kernel<T, TEAM, P, true, true>), grid, block, 0, s, a);
-  else if (p.unit)
-    hipLaunchKernelGGL((sandwich_bwd_kernel<T, TEAM, P, true, false>), grid, block, 0, s, a);
-  else if (p.bias)
-    hipLaunchKernelGGL((sandwich_bwd_kernel<T, TEAM, P, false, true>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((sandwich_bwd_kernel<T, TEAM, P, false, false>), grid, block, 0, s, a);
+void bwd_launch(const SandwichBwd& a, const BwdPlan& p, bool cut, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.chunks)), block(TEAM > 64 ? TEAM : 256);
+#define BWD_GO(GATE, BIAS, CUT) \
+  hipLaunchKernelGGL((sandwich_bwd_kernel<T, TEAM, P, GATE, BIAS, CUT>), grid, block, 0, s, a)
+  // odd widths take the kernels that hold for any gate run and any bias
+  if (cut) {
+    if (p.gate == CHUNK)
+      BWD_GO(CHUNK, true, true);
+    else
+      BWD_GO(RUN, true, true);
+    return;
+  }
+  switch (p.gate * 2 + (p.bias ? 1 : 0)) {
+    case CHUNK * 2: BWD_GO(CHUNK, false, false); break;
+    case CHUNK * 2 + 1: BWD_GO(CHUNK, true, false); break;
+    case RUN * 2: BWD_GO(RUN, false, false); break;
+    case RUN * 2 + 1: BWD_GO(RUN, true, false); break;
+    case TOKEN * 2: BWD_GO(TOKEN, false, false); break;
+    default: BWD_GO(TOKEN, true, false); break;
+  }
+#undef BWD_GO
 }
 
-#define MONARCH_TEAM_CASE(CALL, T, TEAM, P) \
-  case (TEAM) * 8 + (P):                    \
-    CALL(T, TEAM, P);                       \
-    break;
+#define TEAM_CASE(CALL, T, TEAM, P)                \
+  case (TEAM) * 8 + (P): CALL(T, TEAM, P); break;
 
+// The pairs (team, pieces) that fwd_shape and bwd_shape give.
 hipError_t launch_fwd(const SandwichFwd& a, bool bf16, hipStream_t s) {
-  const Shape sh = shape_of(a.d, bf16, 16, 4);
-#define FWD(T, TEAM, P) fwd_launch<T, TEAM, P>(a, s)
-#define FWD4(T, TEAM)                \
-  MONARCH_TEAM_CASE(FWD, T, TEAM, 1) \
-  MONARCH_TEAM_CASE(FWD, T, TEAM, 2) \
-  MONARCH_TEAM_CASE(FWD, T, TEAM, 3) \
-  MONARCH_TEAM_CASE(FWD, T, TEAM, 4)
+  const Shape sh = fwd_shape(a.d, bf16);
+  const bool cut = cut_rows(a.d, bf16);
+#define FWD(T, TEAM, P) fwd_launch<T, TEAM, P>(a, cut, s)
   if (bf16) {
     switch (sh.team * 8 + sh.pieces) {
-      FWD4(uint16_t, 16)
-      FWD4(uint16_t, 32)
-      FWD4(uint16_t, 64)
-      FWD4(uint16_t, 256)
-      MONARCH_TEAM_CASE(FWD, uint16_t, 1024, 2)
+      TEAM_CASE(FWD, uint16_t, 16, 1)
+      TEAM_CASE(FWD, uint16_t, 16, 2)
+      TEAM_CASE(FWD, uint16_t, 16, 3)
+      TEAM_CASE(FWD, uint16_t, 32, 2)
+      TEAM_CASE(FWD, uint16_t, 32, 3)
+      TEAM_CASE(FWD, uint16_t, 64, 2)
+      TEAM_CASE(FWD, uint16_t, 64, 3)
+      TEAM_CASE(FWD, uint16_t, 128, 2)
+      TEAM_CASE(FWD, uint16_t, 256, 2)
+      TEAM_CASE(FWD, uint16_t, 512, 2)
+      TEAM_CASE(FWD, uint16_t, 1024, 2)
       default: return hipErrorInvalidConfiguration;
     }
   } else {
     switch (sh.team * 8 + sh.pieces) {
-      FWD4(float, 16)
-      FWD4(float, 32)
-      FWD4(float, 64)
-      FWD4(float, 256)
-      MONARCH_TEAM_CASE(FWD, float, 1024, 2)
-      MONARCH_TEAM_CASE(FWD, float, 1024, 3)
-      MONARCH_TEAM_CASE(FWD, float, 1024, 4)
+      TEAM_CASE(FWD, float, 16, 1)
+      TEAM_CASE(FWD, float, 16, 2)
+      TEAM_CASE(FWD, float, 16, 3)
+      TEAM_CASE(FWD, float, 16, 4)
+      TEAM_CASE(FWD, float, 32, 3)
+      TEAM_CASE(FWD, float, 32, 4)
+      TEAM_CASE(FWD, float, 64, 3)
+      TEAM_CASE(FWD, float, 64, 4)
+      TEAM_CASE(FWD, float, 128, 3)
+      TEAM_CASE(FWD, float, 128, 4)
+      TEAM_CASE(FWD, float, 256, 3)
+      TEAM_CASE(FWD, float, 256, 4)
+      TEAM_CASE(FWD, float, 512, 3)
+      TEAM_CASE(FWD, float, 512, 4)
+      TEAM_CASE(FWD, float, 1024, 3)
+      TEAM_CASE(FWD, float, 1024, 4)
       default: return hipErrorInvalidConfiguration;
     }
   }
-#undef FWD4
 #undef FWD
   return hipGetLastError();
 }
 
 hipError_t launch_bwd(const SandwichBwd& a, const BwdPlan& p, bool bf16, hipStream_t s) {
-#define BWD(T, TEAM, P) bwd_launch<T, TEAM, P>(a, p, s)
-#define BWD3(T, TEAM)                \
-  MONARCH_TEAM_CASE(BWD, T, TEAM, 1) \
-  MONARCH_TEAM_CASE(BWD, T, TEAM, 2) \
-  MONARCH_TEAM_CASE(BWD, T, TEAM, 3)
+  const bool cut = cut_rows(a.d, bf16);
+#define BWD(T, TEAM, P) bwd_launch<T, TEAM, P>(a, p, cut, s)
   if (bf16) {
     switch (p.shape.team * 8 + p.shape.pieces) {
-      BWD3(uint16_t, 32)
-      BWD3(uint16_t, 64)
-      BWD3(uint16_t, 256)
-      MONARCH_TEAM_CASE(BWD, uint16_t, 1024, 1)
-      MONARCH_TEAM_CASE(BWD, uint16_t, 1024, 2)
+      TEAM_CASE(BWD, uint16_t, 32, 1)
+      TEAM_CASE(BWD, uint16_t, 32, 2)
+      TEAM_CASE(BWD, uint16_t, 32, 3)
+      TEAM_CASE(BWD, uint16_t, 64, 2)
+      TEAM_CASE(BWD, uint16_t, 64, 3)
+      TEAM_CASE(BWD, uint16_t, 128, 2)
+      TEAM_CASE(BWD, uint16_t, 256, 2)
+      TEAM_CASE(BWD, uint16_t, 512, 2)
+      TEAM_CASE(BWD, uint16_t, 512, 3)
+      TEAM_CASE(BWD, uint16_t, 512, 4)
       default: return hipErrorInvalidConfiguration;
     }
   } else {
     switch (p.shape.team * 8 + p.shape.pieces) {
-      BWD3(float, 32)
-      MONARCH_TEAM_CASE(BWD, float, 32, 4)
-      BWD3(float, 64)
-      MONARCH_TEAM_CASE(BWD, float, 64, 4)
-      BWD3(float, 256)
-      MONARCH_TEAM_CASE(BWD, float, 256, 4)
-      MONARCH_TEAM_CASE(BWD, float, 1024, 2)
-      MONARCH_TEAM_CASE(BWD, float, 1024, 3)
-      MONARCH_TEAM_CASE(BWD, float, 1024, 4)
+      TEAM_CASE(BWD, float, 32, 1)
+      TEAM_CASE(BWD, float, 32, 2)
+      TEAM_CASE(BWD, float, 32, 3)
+      TEAM_CASE(BWD, float, 32, 4)
+      TEAM_CASE(BWD, float, 64, 3)
+      TEAM_CASE(BWD, float, 64, 4)
+      TEAM_CASE(BWD, float, 128, 3)
+      TEAM_CASE(BWD, float, 128, 4)
+      TEAM_CASE(BWD, float, 256, 3)
+      TEAM_CASE(BWD, float, 256, 4)
+      TEAM_CASE(BWD, float, 512, 3)
+      TEAM_CASE(BWD, float, 512, 4)
+      TEAM_CASE(BWD, float, 1024, 3)
+      TEAM_CASE(BWD, float, 1024, 4)
       default: return hipErrorInvalidConfiguration;
     }
   }
-#undef BWD3
 #undef BWD
   return hipGetLastError();
 }
-#undef MONARCH_TEAM_CASE
+#undef TEAM_CASE
 
 hipError_t launch_join(const SandwichJoin& a, int64_t jobs, bool bf16, hipStream_t s) {
   // jobs < 2^21 at 1024 threads stay below 2^32 threads a launch: gate rows
-  // summed here have more than kUnitRows rows each, columns are at most 16384
+  // summed here have more than kRunRows rows each, columns are at most 16384
   const dim3 grid(static_cast<unsigned>(jobs), static_cast<unsigned>((a.d + JC - 1) / JC));
   if (bf16)
     hipLaunchKernelGGL((sandwich_join_kernel<uint16_t>), grid, dim3(JC * JS), 0, s, a);
@@ -726,14 +899,14 @@ int monarch_sandwich_bwd(const void* dh_out, const void* dn, const void* h_out, 
   if (dpost_w || dpost_b || dgate || dpre_w || dpre_b) {
     SandwichJoin j;
     j.part = static_cast<const float*>(workspace);
-    j.gate = gates > 0 && !p.unit ? gate : nullptr;
+    j.gate = gates > 0 && p.gate == CHUNK ? gate : nullptr;
     j.post_w = post_w, j.post_b = post_b;
     j.dgate = dgate, j.dpost_w = dpost_w, j.dpost_b = dpost_b, j.dpre_w = dpre_w, j.dpre_b = dpre_b;
-    j.chunks = p.chunks, j.cpg = p.cpg;
+    j.chunks = static_cast<int>(p.chunks), j.cpg = static_cast<int>(p.cpg);
     j.d = static_cast<int>(features), j.sums = p.sums;
     j.s_post = p.s_post, j.s_postb = p.s_postb, j.s_pre = p.s_pre, j.s_preb = p.s_preb;
     j.branch = branch_scale;
-    const int64_t jobs = kWeightJobs + (dgate && !p.unit ? gates : 0);
+    const int64_t jobs = kWeightJobs + (dgate && p.gate == CHUNK ? gates : 0);
     st = record_hip(tr.mark());
     if (st) return st;
     st = record_hip(launch_join(j, jobs, bf16, s));

@@ -45,38 +45,80 @@ template <> struct PieceOf<uint16_t> {
   }
 };
 
-// Elements [at, at + N) of a row of d elements; those past the row are 0.
-template <typename T>
+// Moves a piece by one element: towards element 0, or away from it with v (its
+// raw bits) as the new element 0.
+template <int N>
+__device__ __forceinline__ void drop_first(u32x4& r) {
+  if constexpr (N == 4) {
+    r = u32x4{r[1], r[2], r[3], 0u};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) r[i] = (r[i] >> 16) | (r[i + 1] << 16);
+    r[3] >>= 16;
+  }
+}
+template <int N>
+__device__ __forceinline__ void put_first(u32x4& r, uint32_t v) {
+  if constexpr (N == 4) {
+    r = u32x4{v, r[0], r[1], r[2]};
+  } else {
+#pragma unroll
+    for (int i = 3; i > 0; --i) r[i] = (r[i] << 16) | (r[i - 1] >> 16);
+    r[0] = (r[0] << 16) | v;
+  }
+}
+
+// Elements [at, at + N) of a row of d elements; those past the row are 0. With
+// CUT, d need not be a multiple of N: a piece that the row's end cuts goes element
+// by element, in a loop that is kept rolled (at most one lane of a team takes
+// it), and rows start anywhere. Without, pieces are whole and aligned.
+template <typename T, bool CUT>
 __device__ __forceinline__ u32x4 load_piece(const T* row, int at, int d) {
   constexpr int N = PieceOf<T>::N;
-  if (at + N <= d) return *reinterpret_cast<const typename PieceOf<T>::Raw*>(row + at);
   u32x4 r = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (at + i < d) {
-      if constexpr (N == 4)
-        r[i] = __float_as_uint(row[at + i]);
-      else
-        r[i / 2] |= static_cast<uint32_t>(row[at + i]) << (16 * (i % 2));
-    }
+  if constexpr (!CUT) {
+    if (at < d) r = *reinterpret_cast<const u32x4*>(row + at);
+    return r;
+  }
+  if (at + N <= d) return *reinterpret_cast<const typename PieceOf<T>::Raw*>(row + at);
+#pragma unroll 1
+  for (int i = d - 1; i >= at; --i) {
+    uint32_t v;
+    if constexpr (N == 4)
+      v = __float_as_uint(row[i]);
+    else
+      v = row[i];
+    put_first<N>(r, v);
+  }
   return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void store_piece(T* row, int at, int d, const u32x4& r) {
+template <typename T, bool CUT>
+__device__ __forceinline__ void store_piece(T* row, int at, int d, u32x4 r) {
   constexpr int N = PieceOf<T>::N;
+  if constexpr (!CUT) {
+    if (at < d) *reinterpret_cast<u32x4*>(row + at) = r;
+    return;
+  }
   if (at + N <= d) {
     *reinterpret_cast<typename PieceOf<T>::Raw*>(row + at) = r;
     return;
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (at + i < d) {
-      if constexpr (N == 4)
-        row[at + i] = __uint_as_float(r[i]);
-      else
-        row[at + i] = static_cast<uint16_t>(r[i / 2] >> (16 * (i % 2)));
-    }
+#pragma unroll 1
+  for (int i = at; i < d; ++i) {
+    if constexpr (N == 4)
+      row[i] = __uint_as_float(r[0]);
+    else
+      row[i] = static_cast<uint16_t>(r[0]);
+    drop_first<N>(r);
+  }
+}
+
+// A loop-invariant value that is to be computed with anew in every iteration:
+// offsets and conditions derived from it would otherwise be kept in registers.
+__device__ __forceinline__ int anew(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
 }
 
 template <int CTRL>
