@@ -10,9 +10,12 @@
 // valid entry the first term is absent, without a label the second. A row with
 // neither, or whose logits are -inf throughout, has loss 0 and gradient 0.
 //
-// A team of threads takes a row. Exponentials are 2^((z - m) log2(e) / T) with m
-// the row's maximum: z - m is exact or rounded once, and rows of the type's
-// lowest value (m huge) stay finite. Sums are fp32.
+// A workgroup takes a row. The row is cut at its 16-byte boundaries into whole
+// pieces, of which every thread holds up to P in registers from its sums to its
+// gradient (a row that is longer streams the rest twice), and at most 7 elements
+// before and 7 behind them, one for each of the first threads. Exponentials are
+// 2^((z - m) log2(e) / T) with m the row's maximum: z - m is exact or rounded once,
+// and rows of the type's lowest value (m huge) stay finite. Sums are fp32.
 #include <math.h>
 
 #include "api_internal.h"
@@ -43,49 +46,75 @@ enum { WITH_LOSS = 1, WITH_GRAD = 2 };   // loss and sums from z; gradient
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The second softmax of a row, that of the labels' term, beside the one at T.
+enum Second {
+  NONE = 0,     // no label term, or T = 1: one softmax
+  OWN = 1,      // its own exponentials
+  SQUARE = 2    // T = 2: e^z = (e^(z/2))^2, one product in place of an exponential
+};
+
 // Maximum and sums of exponentials of one thread's share of a row.
+template <int SECOND>
 struct Running {
   float m = -3.402823466e38f, st = 0.0f, s1 = 0.0f;
-  template <bool TWO, int N>
-  __device__ __forceinline__ void add(const float (&v)[N], float ct) {
-    float pm = v[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) pm = fmaxf(pm, v[i]);
-    if (pm > m) {
-      st *= exp2_of((m - pm) * ct);
-      if constexpr (TWO) s1 *= exp2_of((m - pm) * kLog2e);
-      m = pm;
+  __device__ __forceinline__ void raise(float to, float ct) {
+    if (to > m) {
+      const float f = exp2_of((m - to) * ct);
+      st *= f;
+      if constexpr (SECOND == OWN) s1 *= exp2_of((m - to) * kLog2e);
+      if constexpr (SECOND == SQUARE) s1 *= f * f;
+      m = to;
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      st += exp2_of((v[i] - m) * ct);
-      if constexpr (TWO) s1 += exp2_of((v[i] - m) * kLog2e);
-    }
+  }
+  __device__ __forceinline__ void add(float v, float ct) {
+    const float e = exp2_of((v - m) * ct);
+    st += e;
+    if constexpr (SECOND == OWN) s1 += exp2_of((v - m) * kLog2e);
+    if constexpr (SECOND == SQUARE) s1 = fmaf(e, e, s1);
   }
 };
 
-// a row's piece as fp32, -inf past its end
-template <typename T, int N>
-__device__ __forceinline__ void unpack_row(const u32x4& r, int at, int d, float (&v)[N]) {
-  PieceOf<T>::unpack(r, v);
-  if (at + N > d)
+template <int N>
+__device__ __forceinline__ float max_of(float m, const float (&v)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (at + i >= d) v[i] = -INFINITY;
+  for (int i = 0; i < N; i += 2) m = fmaxf(fmaxf(m, v[i]), v[i + 1]);
+  return m;
 }
 
-// TWO: a second sum at temperature 1 (a label term whose softmax is not q).
-template <typename T, int TEAM, int WHAT, bool TWO>
-__global__ __launch_bounds__(TEAM) void distill_kernel(Distill a) {
+template <typename T, int TEAM, int P, int WHAT, int SECOND>
+__global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
   constexpr int N = PieceOf<T>::N, U = 4;
+  constexpr int PR = P > 0 ? P : 1;
+  extern __shared__ float entries[];   // ids, teacher logits, their exponentials, student logits
   __shared__ typename Team<TEAM>::Lds tlds;
-  __shared__ int s_id[MONARCH_DISTILL_MAX_TOP];
-  __shared__ float s_p[MONARCH_DISTILL_MAX_TOP], s_z[MONARCH_DISTILL_MAX_TOP];
+  int* s_id = reinterpret_cast<int*>(entries);
+  float *s_t = entries + a.top, *s_e = s_t + a.top, *s_z = s_e + a.top;
   Team<TEAM> team(&tlds);
-  const int tid = threadIdx.x;
+  const unsigned lane = threadIdx.x;   // unsigned: an offset from a scalar address
+  const int tid = static_cast<int>(lane);
   const float ct = kLog2e / a.temperature;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* z = static_cast<const T*>(a.z) + row * a.ld;
+    // the row's whole pieces start `head` elements in; `extra` is this thread's
+    // element before or behind them
+    int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / int(sizeof(T));
+    if (head > a.vocab) head = a.vocab;
+    const int pieces = (a.vocab - head) / N;
+    const int extra = tid < head ? tid : tid + pieces * N;
+    const bool has_extra = tid < 2 * N && extra < a.vocab;
+    const u32x4* body = reinterpret_cast<const u32x4*>(z + head);
+
+    // pieces past the row's are -inf: they add nothing
+    constexpr uint32_t kMinusInf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    u32x4 raw[PR];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      if (p * TEAM < pieces) {
+        raw[p] = u32x4{kMinusInf, kMinusInf, kMinusInf, kMinusInf};
+        if (p * TEAM + tid < pieces) raw[p] = (body + p * TEAM)[lane];
+      }
+    const float ze = has_extra ? Io<T>::load(z, extra) : -INFINITY;
+
     // the teacher's entries and the student's logits there
     float tmax = -INFINITY;
     for (int k = tid; k < a.top; k += TEAM) {
@@ -93,7 +122,7 @@ __global__ __launch_bounds__(TEAM) void distill_kernel(Distill a) {
       const float t = a.teacher[row * a.top + k];
       const bool ok = id >= 0 && id < a.vocab && t > -INFINITY;
       s_id[k] = ok ? static_cast<int>(id) : -1;
-      s_p[k] = t;
+      s_t[k] = t;
       s_z[k] = ok ? Io<T>::load(z, id) : 0.0f;
       if (ok) tmax = fmaxf(tmax, t);
     }
@@ -101,85 +130,99 @@ __global__ __launch_bounds__(TEAM) void distill_kernel(Distill a) {
     const bool told = label >= 0 && label < a.vocab && a.mix < 1.0f;
     const float zl = told ? Io<T>::load(z, label) : 0.0f;
 
-    float red[3];
-    float m, st = 0.0f, s1 = 0.0f;
+    float m, st, s1;
+    Running<SECOND> r;
     if constexpr (WHAT & WITH_LOSS) {
-      Running r;
-      for (int base = 0; base < a.vocab; base += TEAM * N * U) {
-        u32x4 raw[U];
+      float top = fmaxf(r.m, ze);
+      // the number of pieces is read anew for every pass over them: one kernel
+      // body for each number of them costs registers
+      int np = anew(pieces);
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        if (p * TEAM < np) {
+          float v[N];
+          PieceOf<T>::unpack(raw[p], v);
+          top = max_of<N>(top, v);
+          forget(raw[p]);
+        }
+      r.m = top;
+      r.add(ze, ct);
+      np = anew(pieces);
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        if (p * TEAM < np) {
+          float v[N];
+          PieceOf<T>::unpack(raw[p], v);
+#pragma unroll
+          for (int i = 0; i < N; ++i) r.add(v[i], ct);
+          if (WHAT & WITH_GRAD) forget(raw[p]);
+        }
+      for (int base = P * TEAM; base < pieces; base += TEAM * U) {
+        u32x4 more[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int at = base + (u * TEAM + tid) * N;
-          if (at < a.vocab) raw[u] = load_piece<T, true>(z, at, a.vocab);
+          more[u] = u32x4{kMinusInf, kMinusInf, kMinusInf, kMinusInf};
+          if (base + u * TEAM + tid < pieces) more[u] = (body + (base + u * TEAM))[lane];
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int at = base + (u * TEAM + tid) * N;
-          if (at < a.vocab) {
+        for (int u = 0; u < U; ++u)
+          if (base + u * TEAM < pieces) {
             float v[N];
-            unpack_row<T, N>(raw[u], at, a.vocab, v);
-            r.template add<TWO, N>(v, ct);
+            PieceOf<T>::unpack(more[u], v);
+            r.raise(max_of<N>(v[0], v), ct);
+#pragma unroll
+            for (int i = 0; i < N; ++i) r.add(v[i], ct);
           }
-        }
       }
-      red[0] = r.m;
-      red[1] = tmax;
-      team.template reduce<MaxOp, 2>(*reinterpret_cast<float(*)[2]>(red));
-      m = red[0];
-      tmax = red[1];
-      st = r.st * exp2_of((r.m - m) * ct);
-      s1 = TWO ? r.s1 * exp2_of((r.m - m) * kLog2e) : 0.0f;
+      float top2[2] = {r.m, tmax};
+      team.template reduce<MaxOp, 2>(top2);
+      m = top2[0];
+      tmax = top2[1];
+      r.raise(m, ct);
     } else {
-      red[0] = tmax;
-      team.template reduce<MaxOp, 1>(*reinterpret_cast<float(*)[1]>(red));
-      tmax = red[0];
-      m = a.stats_in[row * 4];
+      float top1[1] = {tmax};
+      team.template reduce<MaxOp, 1>(top1);
+      tmax = top1[0];
+      const f32x4 sums = *reinterpret_cast<const f32x4*>(a.stats_in + row * 4);
+      m = sums[0];
+      r.st = sums[1];
+      r.s1 = sums[2];
     }
+    // the teacher's sum, and 2^-10 sum_k e_k ((t_k - tmax) - (z_k - m)): T times the part
+    // of sum_k p_k (log p_k - log q_k) that is not T (log st - log tsum). Neither the sum
+    // of up to 512 entries nor a quotient by a small T overflows where they name
+    // logits of the type's lowest value.
     const bool some = tmax > -INFINITY && a.mix > 0.0f;
-    float tsum = 0.0f;
-    for (int k = tid; k < a.top; k += TEAM)
+    float sums[4] = {0.0f, 0.0f, r.st, r.s1};
+    for (int k = tid; k < a.top; k += TEAM) {
+      float e = 0.0f;
       if (s_id[k] >= 0) {
-        const float e = exp2_of((s_p[k] - tmax) * ct);
-        s_p[k] = e;
-        tsum += e;
-      } else {
-        s_p[k] = 0.0f;
+        const float t = s_t[k] - tmax;
+        e = exp2_of(t * ct);
+        sums[0] += e;
+        if (!(e == 0.0f)) sums[1] = fmaf(e * 0x1p-10f, t - (s_z[k] - m), sums[1]);
       }
-    red[0] = tsum;
-    red[1] = st;
-    red[2] = s1;
-    if constexpr (WHAT & WITH_LOSS) {
-      team.template reduce<SumOp, 3>(red);
-      st = red[1];
-      s1 = TWO ? red[2] : st;
-    } else {
-      team.template reduce<SumOp, 1>(*reinterpret_cast<float(*)[1]>(red));
-      st = a.stats_in[row * 4 + 1];
-      s1 = a.stats_in[row * 4 + 2];
+      s_e[k] = e;
     }
-    const float inv_t = some ? 1.0f / red[0] : 0.0f;
+    if constexpr (WHAT & WITH_LOSS) {
+      team.template reduce<SumOp, 4>(sums);
+      st = sums[2];
+      s1 = SECOND == NONE ? st : sums[3];
+    } else {
+      float tsum[1] = {sums[0]};
+      team.template reduce<SumOp, 1>(tsum);
+      sums[0] = tsum[0];
+      st = r.st;
+      s1 = r.s1;
+    }
     const bool alive = st != 0.0f;   // NaN counts as alive: it has to come out
     if constexpr (WHAT & WITH_LOSS) {
-      // T (log p_k - log q_k) = (t_k - tmax) - (z_k - m) + T (log st - log tsum): not
-      // divided by T, so that a logit of the type's lowest value does not overflow
-      float kl = 0.0f;
-      if (some && alive) {
-        const float base = a.temperature * (logf(st) - logf(red[0]));
-        for (int k = tid; k < a.top; k += TEAM) {
-          const float p = s_p[k] * inv_t;
-          if (p > 0.0f) {
-            const float t = a.teacher[row * a.top + k];
-            kl = fmaf(p, (t - tmax) - (s_z[k] - m) + base, kl);
-          } else if (p != p) {
-            kl = p;
-          }
-        }
-      }
-      kl = team.sum(kl);
       if (tid == 0) {
-        float loss = a.mix * a.temperature * kl;
+        float loss = 0.0f;
+        if (some && alive)
+          loss = a.mix * a.temperature * 0x1p10f * (sums[1] / sums[0]) +
+                 a.mix * a.temperature * a.temperature * (logf(st) - logf(sums[0]));
         if (told && alive) loss += (1.0f - a.mix) * (logf(s1) - (zl - m));
-        if (!some && !told) loss = 0.0f;
         a.loss[row] = loss;
         if (a.stats) *reinterpret_cast<f32x4*>(a.stats + row * 4) = f32x4{m, st, s1, 0.0f};
       }
@@ -189,48 +232,58 @@ __global__ __launch_bounds__(TEAM) void distill_kernel(Distill a) {
       const float ga = some && alive ? w * a.mix * a.temperature : 0.0f;
       const float gb = told && alive ? w * (1.0f - a.mix) : 0.0f;
       // one softmax for both terms where they share it
-      const float fa = TWO ? ga / st : (ga + gb) / st, fb = TWO ? gb / s1 : 0.0f;
+      const float fa = SECOND == NONE ? (ga + gb) / st : ga / st;
+      const float fb = SECOND == NONE ? 0.0f : gb / s1;
       T* dz = static_cast<T*>(a.dz) + row * a.dld;
+      T* dbody = dz + head;
       const bool nothing = (!some && !told) || !alive;
       auto grad = [&](float v) {
-        float g = fa * exp2_of((v - m) * ct);
-        if constexpr (TWO) g = fmaf(fb, exp2_of((v - m) * kLog2e), g);
-        return g;
+        const float e = exp2_of((v - m) * ct);
+        if constexpr (SECOND == OWN) return fmaf(fb, exp2_of((v - m) * kLog2e), fa * e);
+        if constexpr (SECOND == SQUARE) return e * fmaf(fb, e, fa);
+        return fa * e;
       };
-      for (int base = 0; base < a.vocab; base += TEAM * N * U) {
-        u32x4 raw[U];
+      const int np = anew(pieces);
+      auto put = [&](int first, const u32x4& piece) {
+        if (first >= np) return;
+        float v[N];
+        PieceOf<T>::unpack(piece, v);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int at = base + (u * TEAM + tid) * N;
-          if (at < a.vocab) raw[u] = load_piece<T, true>(z, at, a.vocab);
-        }
+        for (int i = 0; i < N; ++i) v[i] = grad(v[i]);
+        u32x4 o = PieceOf<T>::pack(v);
+        if (nothing) o = u32x4{0, 0, 0, 0};
+        if (first + tid < np)
+          reinterpret_cast<typename PieceOf<T>::Raw*>(dbody + static_cast<int64_t>(first) * N)[lane] = o;
+      };
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int at = base + (u * TEAM + tid) * N;
-          if (at < a.vocab) {
-            float v[N];
-            PieceOf<T>::unpack(raw[u], v);
+      for (int p = 0; p < P; ++p)
+        put(p * TEAM, raw[p]);
+      for (int base = P * TEAM; base < pieces; base += TEAM * U) {
+        u32x4 more[U] = {};
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = nothing ? 0.0f : grad(v[i]);
-            store_piece<T, true>(dz, at, a.vocab, PieceOf<T>::pack(v));
-          }
-        }
+        for (int u = 0; u < U; ++u)
+          if (base + u * TEAM + tid < pieces) more[u] = (body + (base + u * TEAM))[lane];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          put(base + u * TEAM, more[u]);
       }
+      if (has_extra) Io<T>::store(dz, extra, nothing ? 0.0f : grad(ze));
       // the entries and the label: their elements are written again, whole
       __syncthreads();
       if (!nothing) {
+        const float inv_t = some ? 1.0f / sums[0] : 0.0f;
         for (int k = tid; k < a.top; k += TEAM) {
           const int id = s_id[k];
           if (id < 0) continue;
-          float p = 0.0f;
+          float e = 0.0f;
           bool first = true;
           for (int j = 0; j < a.top; ++j)
             if (s_id[j] == id) {
-              p += s_p[j];
+              e += s_e[j];
               first = first && j >= k;
             }
           if (!first) continue;
-          float g = grad(s_z[k]) - ga * (p * inv_t);
+          float g = grad(s_z[k]) - ga * (e * inv_t);
           if (told && id == label) g -= gb;
           Io<T>::store(dz, id, g);
         }
@@ -258,23 +311,41 @@ bool off_elements(const void* p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) != 0;
 }
 
-template <typename T, int TEAM, int WHAT>
-hipError_t launch_two(const Distill& a, bool two, hipStream_t s) {
-  const int64_t grid = a.rows < (1 << 20) ? a.rows : (1 << 20);
-  if (two)
-    hipLaunchKernelGGL((distill_kernel<T, TEAM, WHAT, true>), dim3(static_cast<unsigned>(grid)),
-                       dim3(TEAM), 0, s, a);
+template <typename T, int TEAM, int P, int WHAT>
+hipError_t launch_second(const Distill& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.rows < (1 << 20) ? a.rows : (1 << 20))), block(TEAM);
+  const size_t lds = static_cast<size_t>(a.top) * 16;
+  const bool two = a.labels && a.mix < 1.0f && a.temperature != 1.0f;
+  if (two && a.temperature == 2.0f)
+    hipLaunchKernelGGL((distill_kernel<T, TEAM, P, WHAT, SQUARE>), grid, block, lds, s, a);
+  else if (two)
+    hipLaunchKernelGGL((distill_kernel<T, TEAM, P, WHAT, OWN>), grid, block, lds, s, a);
   else
-    hipLaunchKernelGGL((distill_kernel<T, TEAM, WHAT, false>), dim3(static_cast<unsigned>(grid)),
-                       dim3(TEAM), 0, s, a);
+    hipLaunchKernelGGL((distill_kernel<T, TEAM, P, WHAT, NONE>), grid, block, lds, s, a);
   return hipGetLastError();
+}
+
+// The smallest workgroup whose registers hold the row: 4, 8 or 16 pieces a
+// thread. A gradient alone streams the row once, and needs no more than enough
+// threads.
+template <typename T, int WHAT>
+hipError_t launch_sized(const Distill& a, hipStream_t s) {
+  const int pieces = a.vocab / PieceOf<T>::N;
+  constexpr bool HOLD = WHAT & WITH_LOSS;
+  if (pieces <= 64 * 4) return launch_second<T, 64, HOLD ? 4 : 0, WHAT>(a, s);
+  if (pieces <= 256 * 4) return launch_second<T, 256, HOLD ? 4 : 0, WHAT>(a, s);
+  if constexpr (HOLD) {
+    if (pieces <= 512 * 8) return launch_second<T, 512, 8, WHAT>(a, s);
+    if (pieces <= 512 * 16) return launch_second<T, 512, 16, WHAT>(a, s);
+    return launch_second<T, 1024, 16, WHAT>(a, s);
+  } else {
+    return launch_second<T, 512, 0, WHAT>(a, s);
+  }
 }
 
 template <int WHAT>
 hipError_t launch(const Distill& a, bool bf16, hipStream_t s) {
-  const bool two = a.labels && a.mix < 1.0f && a.temperature != 1.0f;
-  if (bf16) return launch_two<uint16_t, 512, WHAT>(a, two, s);
-  return launch_two<float, 512, WHAT>(a, two, s);
+  return bf16 ? launch_sized<uint16_t, WHAT>(a, s) : launch_sized<float, WHAT>(a, s);
 }
 
 // The checks that every call shares; `what` as for the kernel.

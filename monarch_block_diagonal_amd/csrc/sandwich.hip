@@ -50,10 +50,6 @@ __device__ __forceinline__ u32x4 par_piece(const void* p, int64_t off, int at, i
   return u32x4{w, w, w, w};
 }
 
-// Keeps the compiler from carrying what it unpacked from r to the next use of
-// r: unpacking again is cheaper than the registers.
-__device__ __forceinline__ void forget(u32x4& r) { asm volatile("" : "+v"(r)); }
-
 // The elements of a piece at `at` that lie past the row, set to 0.
 template <bool CUT, int N>
 __device__ __forceinline__ void zero_past(float (&v)[N], int at, int d) {

@@ -114,6 +114,10 @@ __device__ __forceinline__ void store_piece(T* row, int at, int d, u32x4 r) {
   }
 }
 
+// Keeps the compiler from carrying what it computed from r to the next use of
+// r: unpacking again is cheaper than the registers.
+__device__ __forceinline__ void forget(u32x4& r) { asm volatile("" : "+v"(r)); }
+
 // A loop-invariant value that is to be computed with anew in every iteration:
 // offsets and conditions derived from it would otherwise be kept in registers.
 __device__ __forceinline__ int anew(int v) {
@@ -163,7 +167,7 @@ __device__ __forceinline__ float lanes_reduce(float v) {
 template <int TEAM>
 struct Team {
   static constexpr int WAVES = TEAM > 64 ? TEAM / 64 : 1;
-  static constexpr int MAXV = 3;   // values an exchange
+  static constexpr int MAXV = 4;   // values an exchange
   struct Lds {
     float slot[2][MAXV][WAVES];
   };
