@@ -42,6 +42,9 @@ struct Distill {
   float temperature, mix;
 };
 
+// LDS slots for the entries and the label, in whole 16-byte reads.
+__host__ __device__ inline int entry_slots(int top) { return (top + 4) / 4 * 4; }
+
 enum { WITH_LOSS = 1, WITH_GRAD = 2 };   // loss and sums from z; gradient
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -53,18 +56,18 @@ enum Second {
   SQUARE = 2    // T = 2: e^z = (e^(z/2))^2, one product in place of an exponential
 };
 
-// Maximum and sums of exponentials of one thread's share of a row.
+// Maximum and sums of exponentials of one thread's share of a row. The maximum
+// rises a piece at a time: one more exponential for every piece, and the sums
+// of the first pieces are under way while the last ones are loaded.
 template <int SECOND>
 struct Running {
   float m = -3.402823466e38f, st = 0.0f, s1 = 0.0f;
   __device__ __forceinline__ void raise(float to, float ct) {
-    if (to > m) {
-      const float f = exp2_of((m - to) * ct);
-      st *= f;
-      if constexpr (SECOND == OWN) s1 *= exp2_of((m - to) * kLog2e);
-      if constexpr (SECOND == SQUARE) s1 *= f * f;
-      m = to;
-    }
+    const float f = exp2_of((m - to) * ct);
+    st *= f;
+    if constexpr (SECOND == OWN) s1 *= exp2_of((m - to) * kLog2e);
+    if constexpr (SECOND == SQUARE) s1 *= f * f;
+    m = to;
   }
   __device__ __forceinline__ void add(float v, float ct) {
     const float e = exp2_of((v - m) * ct);
@@ -72,23 +75,31 @@ struct Running {
     if constexpr (SECOND == OWN) s1 += exp2_of((v - m) * kLog2e);
     if constexpr (SECOND == SQUARE) s1 = fmaf(e, e, s1);
   }
-};
-
-template <int N>
-__device__ __forceinline__ float max_of(float m, const float (&v)[N]) {
+  template <int N>
+  __device__ __forceinline__ void add_piece(const float (&v)[N], float ct) {
+    float to = m;
 #pragma unroll
-  for (int i = 0; i < N; i += 2) m = fmaxf(fmaxf(m, v[i]), v[i + 1]);
-  return m;
-}
+    for (int i = 0; i < N; i += 2) to = fmaxf(fmaxf(to, v[i]), v[i + 1]);
+    raise(to, ct);
+#pragma unroll
+    for (int i = 0; i < N; ++i) add(v[i], ct);
+  }
+};
 
 template <typename T, int TEAM, int P, int WHAT, int SECOND>
 __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
   constexpr int N = PieceOf<T>::N, U = 4;
   constexpr int PR = P > 0 ? P : 1;
-  extern __shared__ float entries[];   // ids, teacher logits, their exponentials, student logits
+  constexpr uint32_t kMinusInf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  const u32x4 nothing_more = {kMinusInf, kMinusInf, kMinusInf, kMinusInf};   // adds nothing
+  // `top` entries and the label: column (-1: none), student's logit, teacher's
+  // exponential; then the teacher's logits
+  extern __shared__ __align__(16) int s_id[];
   __shared__ typename Team<TEAM>::Lds tlds;
-  int* s_id = reinterpret_cast<int*>(entries);
-  float *s_t = entries + a.top, *s_e = s_t + a.top, *s_z = s_e + a.top;
+  const int slots = entry_slots(a.top);
+  float* s_z = reinterpret_cast<float*>(s_id + slots);
+  float* s_e = s_z + slots;
+  float* s_t = s_e + slots;
   Team<TEAM> team(&tlds);
   const unsigned lane = threadIdx.x;   // unsigned: an offset from a scalar address
   const int tid = static_cast<int>(lane);
@@ -104,64 +115,53 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
     const bool has_extra = tid < 2 * N && extra < a.vocab;
     const u32x4* body = reinterpret_cast<const u32x4*>(z + head);
 
-    // pieces past the row's are -inf: they add nothing
-    constexpr uint32_t kMinusInf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-    u32x4 raw[PR];
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-      if (p * TEAM < pieces) {
-        raw[p] = u32x4{kMinusInf, kMinusInf, kMinusInf, kMinusInf};
-        if (p * TEAM + tid < pieces) raw[p] = (body + p * TEAM)[lane];
-      }
-    const float ze = has_extra ? Io<T>::load(z, extra) : -INFINITY;
-
-    // the teacher's entries and the student's logits there
-    float tmax = -INFINITY;
-    for (int k = tid; k < a.top; k += TEAM) {
-      const int64_t id = a.ids[row * a.top + k];
-      const float t = a.teacher[row * a.top + k];
-      const bool ok = id >= 0 && id < a.vocab && t > -INFINITY;
-      s_id[k] = ok ? static_cast<int>(id) : -1;
-      s_t[k] = t;
-      s_z[k] = ok ? Io<T>::load(z, id) : 0.0f;
-      if (ok) tmax = fmaxf(tmax, t);
+    // this thread's entry, the label and the single elements first: loads return
+    // in order, and these few are wanted as soon as the pieces are here
+    int64_t id0 = -1;
+    float t0 = 0.0f;
+    if (tid < a.top) {
+      id0 = a.ids[row * a.top + tid];
+      t0 = a.teacher[row * a.top + tid];
     }
     const int64_t label = a.labels ? a.labels[row] : -1;
     const bool told = label >= 0 && label < a.vocab && a.mix < 1.0f;
-    const float zl = told ? Io<T>::load(z, label) : 0.0f;
+    const float ze = has_extra ? Io<T>::load(z, extra) : -INFINITY;
+    // P rounds of TEAM pieces, loaded without a branch between them: the last,
+    // short round is moved back to end with the row (its first threads then hold
+    // pieces of the round before, which do not count), and those past it repeat it
+    u32x4 raw[PR];
+    if (P > 0 && pieces >= TEAM) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) raw[p] = (body + min(p * TEAM, pieces - TEAM))[lane];
+    } else if (P > 0 && tid < pieces) {
+      raw[0] = body[lane];
+    }
+    // where round p starts, and whether this thread's piece in it counts
+    auto round_at = [](int p, int np) { return min(p * TEAM, max(np - TEAM, 0)); };
+    auto counts = [tid](int p, int at, int np) { return at + tid >= p * TEAM && at + tid < np; };
 
     float m, st, s1;
     Running<SECOND> r;
+    // the number of pieces is read anew for every pass over them: one kernel
+    // body for each number of them costs registers
+    int np = anew(pieces);
     if constexpr (WHAT & WITH_LOSS) {
-      float top = fmaxf(r.m, ze);
-      // the number of pieces is read anew for every pass over them: one kernel
-      // body for each number of them costs registers
-      int np = anew(pieces);
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        if (p * TEAM < np) {
-          float v[N];
-          PieceOf<T>::unpack(raw[p], v);
-          top = max_of<N>(top, v);
-          forget(raw[p]);
-        }
-      r.m = top;
+      r.raise(fmaxf(r.m, ze), ct);
       r.add(ze, ct);
-      np = anew(pieces);
 #pragma unroll
       for (int p = 0; p < P; ++p)
         if (p * TEAM < np) {
+          if (p * TEAM + TEAM > np && !counts(p, round_at(p, np), np)) raw[p] = nothing_more;
           float v[N];
           PieceOf<T>::unpack(raw[p], v);
-#pragma unroll
-          for (int i = 0; i < N; ++i) r.add(v[i], ct);
+          r.template add_piece<N>(v, ct);
           if (WHAT & WITH_GRAD) forget(raw[p]);
         }
       for (int base = P * TEAM; base < pieces; base += TEAM * U) {
         u32x4 more[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          more[u] = u32x4{kMinusInf, kMinusInf, kMinusInf, kMinusInf};
+          more[u] = nothing_more;
           if (base + u * TEAM + tid < pieces) more[u] = (body + (base + u * TEAM))[lane];
         }
 #pragma unroll
@@ -169,11 +169,30 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
           if (base + u * TEAM < pieces) {
             float v[N];
             PieceOf<T>::unpack(more[u], v);
-            r.raise(max_of<N>(v[0], v), ct);
-#pragma unroll
-            for (int i = 0; i < N; ++i) r.add(v[i], ct);
+            r.template add_piece<N>(v, ct);
           }
       }
+    }
+    // the teacher's entries and the student's logits there
+    float tmax = -INFINITY;
+    for (int k = tid; k < slots; k += TEAM) {
+      int id = -1;
+      float t = 0.0f;
+      if (k < a.top) {
+        const int64_t id64 = k == tid ? id0 : a.ids[row * a.top + k];
+        t = k == tid ? t0 : a.teacher[row * a.top + k];
+        if (id64 >= 0 && id64 < a.vocab && t > -INFINITY) {
+          id = static_cast<int>(id64);
+          tmax = fmaxf(tmax, t);
+        }
+      } else if (k == a.top && told) {
+        id = static_cast<int>(label);
+      }
+      s_id[k] = id;
+      s_t[k] = t;
+      s_z[k] = id >= 0 ? Io<T>::load(z, id) : 0.0f;
+    }
+    if constexpr (WHAT & WITH_LOSS) {
       float top2[2] = {r.m, tmax};
       team.template reduce<MaxOp, 2>(top2);
       m = top2[0];
@@ -194,9 +213,9 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
     // logits of the type's lowest value.
     const bool some = tmax > -INFINITY && a.mix > 0.0f;
     float sums[4] = {0.0f, 0.0f, r.st, r.s1};
-    for (int k = tid; k < a.top; k += TEAM) {
+    for (int k = tid; k < slots; k += TEAM) {
       float e = 0.0f;
-      if (s_id[k] >= 0) {
+      if (k < a.top && s_id[k] >= 0) {
         const float t = s_t[k] - tmax;
         e = exp2_of(t * ct);
         sums[0] += e;
@@ -204,6 +223,7 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
       }
       s_e[k] = e;
     }
+    if (TEAM <= 64) __syncthreads();   // the entries, which larger teams pass a barrier after
     if constexpr (WHAT & WITH_LOSS) {
       team.template reduce<SumOp, 4>(sums);
       st = sums[2];
@@ -222,7 +242,7 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
         if (some && alive)
           loss = a.mix * a.temperature * 0x1p10f * (sums[1] / sums[0]) +
                  a.mix * a.temperature * a.temperature * (logf(st) - logf(sums[0]));
-        if (told && alive) loss += (1.0f - a.mix) * (logf(s1) - (zl - m));
+        if (told && alive) loss += (1.0f - a.mix) * (logf(s1) - (s_z[a.top] - m));
         a.loss[row] = loss;
         if (a.stats) *reinterpret_cast<f32x4*>(a.stats + row * 4) = f32x4{m, st, s1, 0.0f};
       }
@@ -243,21 +263,20 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
         if constexpr (SECOND == SQUARE) return e * fmaf(fb, e, fa);
         return fa * e;
       };
-      const int np = anew(pieces);
-      auto put = [&](int first, const u32x4& piece) {
-        if (first >= np) return;
+      np = anew(pieces);
+      auto put = [&](int first, bool mine, const u32x4& piece) {
         float v[N];
         PieceOf<T>::unpack(piece, v);
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = grad(v[i]);
         u32x4 o = PieceOf<T>::pack(v);
         if (nothing) o = u32x4{0, 0, 0, 0};
-        if (first + tid < np)
+        if (mine)
           reinterpret_cast<typename PieceOf<T>::Raw*>(dbody + static_cast<int64_t>(first) * N)[lane] = o;
       };
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        put(p * TEAM, raw[p]);
+        if (p * TEAM < np) put(round_at(p, np), counts(p, round_at(p, np), np), raw[p]);
       for (int base = P * TEAM; base < pieces; base += TEAM * U) {
         u32x4 more[U] = {};
 #pragma unroll
@@ -265,34 +284,40 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
           if (base + u * TEAM + tid < pieces) more[u] = (body + (base + u * TEAM))[lane];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          put(base + u * TEAM, more[u]);
+          if (base + u * TEAM < pieces)
+            put(base + u * TEAM, base + u * TEAM + tid < pieces, more[u]);
       }
       if (has_extra) Io<T>::store(dz, extra, nothing ? 0.0f : grad(ze));
-      // the entries and the label: their elements are written again, whole
-      __syncthreads();
-      if (!nothing) {
-        const float inv_t = some ? 1.0f / sums[0] : 0.0f;
-        for (int k = tid; k < a.top; k += TEAM) {
-          const int id = s_id[k];
-          if (id < 0) continue;
-          float e = 0.0f;
-          bool first = true;
-          for (int j = 0; j < a.top; ++j)
-            if (s_id[j] == id) {
-              e += s_e[j];
-              first = first && j >= k;
-            }
-          if (!first) continue;
-          float g = grad(s_z[k]) - ga * (e * inv_t);
-          if (told && id == label) g -= gb;
-          Io<T>::store(dz, id, g);
+      // the entries and the label: their elements are written again, whole, by the
+      // first slot that names them, with the sum of all that do
+      const float inv_t = some ? 1.0f / sums[0] : 0.0f;
+      auto fix = [&](int k, float& g) {
+        const int id = nothing ? -1 : s_id[k];
+        float e = s_e[k];
+        int same = 0, before = 0;
+        for (int j = 0; j < slots; j += 4) {
+          const int4 other = *reinterpret_cast<const int4*>(s_id + j);
+          same += (other.x == id) + (other.y == id) + (other.z == id) + (other.w == id);
+          before += (other.x == id && j < k) + (other.y == id && j + 1 < k) +
+                    (other.z == id && j + 2 < k) + (other.w == id && j + 3 < k);
         }
-        if (told) {
-          int hit = 0;
-          for (int k = tid; k < a.top; k += TEAM) hit |= s_id[k] == label;
-          hit = __syncthreads_or(hit);
-          if (!hit && tid == 0) Io<T>::store(dz, label, grad(zl) - gb);
+        if (id < 0 || before) return -1;
+        if (same > 1) {
+          e = 0.0f;
+          for (int j = 0; j < slots; ++j)
+            if (s_id[j] == id) e += s_e[j];
         }
+        g = grad(s_z[k]) - ga * (e * inv_t);
+        if (told && id == label) g -= gb;
+        return id;
+      };
+      float g = 0.0f;
+      int id = tid < slots ? fix(tid, g) : -1;
+      __syncthreads();   // the row is written
+      if (id >= 0) Io<T>::store(dz, id, g);
+      for (int k = tid + TEAM; k < slots; k += TEAM) {
+        id = fix(k, g);
+        if (id >= 0) Io<T>::store(dz, id, g);
       }
     }
     __syncthreads();   // the next row overwrites the entries
@@ -314,7 +339,7 @@ bool off_elements(const void* p, int bytes) {
 template <typename T, int TEAM, int P, int WHAT>
 hipError_t launch_second(const Distill& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(a.rows < (1 << 20) ? a.rows : (1 << 20))), block(TEAM);
-  const size_t lds = static_cast<size_t>(a.top) * 16;
+  const size_t lds = static_cast<size_t>(entry_slots(a.top)) * 16;
   const bool two = a.labels && a.mix < 1.0f && a.temperature != 1.0f;
   if (two && a.temperature == 2.0f)
     hipLaunchKernelGGL((distill_kernel<T, TEAM, P, WHAT, SQUARE>), grid, block, lds, s, a);
@@ -325,8 +350,7 @@ hipError_t launch_second(const Distill& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The smallest workgroup whose registers hold the row: 4, 8 or 16 pieces a
-// thread. A gradient alone streams the row once, and needs no more than enough
+// The smallest workgroup whose registers hold the row, 4 or 16 pieces a thread. A gradient alone streams the row once, and needs no more than enough
 // threads.
 template <typename T, int WHAT>
 hipError_t launch_sized(const Distill& a, hipStream_t s) {
@@ -335,7 +359,7 @@ hipError_t launch_sized(const Distill& a, hipStream_t s) {
   if (pieces <= 64 * 4) return launch_second<T, 64, HOLD ? 4 : 0, WHAT>(a, s);
   if (pieces <= 256 * 4) return launch_second<T, 256, HOLD ? 4 : 0, WHAT>(a, s);
   if constexpr (HOLD) {
-    if (pieces <= 512 * 8) return launch_second<T, 512, 8, WHAT>(a, s);
+    if (pieces <= 256 * 16) return launch_second<T, 256, 16, WHAT>(a, s);
     if (pieces <= 512 * 16) return launch_second<T, 512, 16, WHAT>(a, s);
     return launch_second<T, 1024, 16, WHAT>(a, s);
   } else {
