@@ -162,13 +162,40 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None   # torch's (device index) -> hipStream_t of the current stream
+_device = None       # torch's () -> current device index
+
+
+def _torch_runtime():
+    """Binds the two functions above on first use. The calls behind
+    torch.cuda.current_stream and current_device without the Python objects they
+    build, which cost more than a kernel launch."""
+    global _raw_stream, _device
+    import torch
+    torch.cuda.current_stream()   # initialises the GPU runtime
+    _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def current_device() -> int:
+    """Index of the GPU whose current stream calls without a stream go to."""
+    if _device is None:
+        _torch_runtime()
+    return _device()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            _torch_runtime()
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _addresses(*ts):
+    """_ptr of each."""
+    return [t if t is None or t.__class__ is int else t.data_ptr() for t in ts]
 
 
 def _events(events: Optional[Sequence]):
@@ -399,12 +426,10 @@ def monarch_dyad_describe(direction, in_features, out_features, nblocks, batch, 
 def monarch_sandwich_fwd(h, y, post_w, post_b, gate, pre_w, pre_b, h_out, n, stats, rows, features,
                          gates, post_norm, pre_norm, skip_scale, branch_scale, eps, dtype,
                          stream=None, events=None) -> None:
-    lib = load_library()
     arr, ne = _events(events)
-    _check(lib.monarch_sandwich_fwd(_ptr(h), _ptr(y), _ptr(post_w), _ptr(post_b), _ptr(gate),
-                                    _ptr(pre_w), _ptr(pre_b), _ptr(h_out), _ptr(n), _ptr(stats),
-                                    rows, features, gates, post_norm, pre_norm, skip_scale,
-                                    branch_scale, eps, dtype, _stream(stream), arr, ne))
+    _check(load_library().monarch_sandwich_fwd(
+        *_addresses(h, y, post_w, post_b, gate, pre_w, pre_b, h_out, n, stats), rows, features,
+        gates, post_norm, pre_norm, skip_scale, branch_scale, eps, dtype, _stream(stream), arr, ne))
 
 
 def monarch_sandwich_bwd_workspace_bytes(rows, features, gates, with_bias, dtype) -> int:
@@ -416,12 +441,10 @@ def monarch_sandwich_bwd(dh_out, dn, h_out, y, stats, post_w, post_b, gate, pre_
                          dpost_w, dpost_b, dgate, dpre_w, dpre_b, workspace, workspace_bytes, rows,
                          features, gates, post_norm, pre_norm, skip_scale, branch_scale, dtype,
                          stream=None, events=None) -> None:
-    lib = load_library()
     arr, ne = _events(events)
-    _check(lib.monarch_sandwich_bwd(
-        _ptr(dh_out), _ptr(dn), _ptr(h_out), _ptr(y), _ptr(stats), _ptr(post_w), _ptr(post_b),
-        _ptr(gate), _ptr(pre_w), _ptr(pre_b), _ptr(dh), _ptr(dy), _ptr(dpost_w), _ptr(dpost_b),
-        _ptr(dgate), _ptr(dpre_w), _ptr(dpre_b), _ptr(workspace), workspace_bytes, rows, features,
+    _check(load_library().monarch_sandwich_bwd(
+        *_addresses(dh_out, dn, h_out, y, stats, post_w, post_b, gate, pre_w, pre_b, dh, dy, dpost_w,
+                    dpost_b, dgate, dpre_w, dpre_b, workspace), workspace_bytes, rows, features,
         gates, post_norm, pre_norm, skip_scale, branch_scale, dtype, _stream(stream), arr, ne))
 
 
@@ -437,26 +460,23 @@ def monarch_sandwich_describe(direction, rows, features, gates, dtype):
 
 def monarch_distill_fwd(logits, ld, teacher, ids, labels, loss, stats, rows, vocab, top,
                         temperature, mix, dtype, stream=None, events=None) -> None:
-    lib = load_library()
     arr, n = _events(events)
-    _check(lib.monarch_distill_fwd(_ptr(logits), ld, _ptr(teacher), _ptr(ids), _ptr(labels),
-                                   _ptr(loss), _ptr(stats), rows, vocab, top, temperature, mix,
-                                   dtype, _stream(stream), arr, n))
+    z, *rest = _addresses(logits, teacher, ids, labels, loss, stats)
+    _check(load_library().monarch_distill_fwd(z, ld, *rest, rows, vocab, top, temperature, mix, dtype,
+                                              _stream(stream), arr, n))
 
 
 def monarch_distill_bwd(dloss, logits, ld, teacher, ids, labels, stats, dlogits, dld, rows, vocab,
                         top, temperature, mix, dtype, stream=None, events=None) -> None:
-    lib = load_library()
     arr, n = _events(events)
-    _check(lib.monarch_distill_bwd(_ptr(dloss), _ptr(logits), ld, _ptr(teacher), _ptr(ids),
-                                   _ptr(labels), _ptr(stats), _ptr(dlogits), dld, rows, vocab, top,
-                                   temperature, mix, dtype, _stream(stream), arr, n))
+    g, z, *rest = _addresses(dloss, logits, teacher, ids, labels, stats, dlogits)
+    _check(load_library().monarch_distill_bwd(g, z, ld, *rest, dld, rows, vocab, top, temperature,
+                                              mix, dtype, _stream(stream), arr, n))
 
 
 def monarch_distill_step(logits, ld, teacher, ids, labels, row_weight, loss, dlogits, dld, rows,
                          vocab, top, temperature, mix, dtype, stream=None, events=None) -> None:
-    lib = load_library()
     arr, n = _events(events)
-    _check(lib.monarch_distill_step(_ptr(logits), ld, _ptr(teacher), _ptr(ids), _ptr(labels),
-                                    _ptr(row_weight), _ptr(loss), _ptr(dlogits), dld, rows, vocab,
-                                    top, temperature, mix, dtype, _stream(stream), arr, n))
+    z, *rest = _addresses(logits, teacher, ids, labels, row_weight, loss, dlogits)
+    _check(load_library().monarch_distill_step(z, ld, *rest, dld, rows, vocab, top, temperature, mix,
+                                               dtype, _stream(stream), arr, n))

@@ -339,29 +339,54 @@ class SandwichGrads(NamedTuple):
     dpre_bias: Optional[torch.Tensor]
 
 
+def _refuse(t, name, shape, dtype):
+    """Raises for the first thing that _beside found wrong with t."""
+    _expect(t, shape, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must live on the current GPU, where the call's stream is")
+
+
+def _saved(stats, rows, device):
+    """Checks what a forward call saved for its backward call."""
+    if stats.dtype is not torch.float32:
+        raise ValueError("stats must be the fp32 tensor the forward returned")
+    _beside(device, torch.float32, (rows, 4), stats, "stats")
+
+
+def _beside(device, dtype, shape, *named):
+    """Checks that each given tensor of (tensor, name, ...) has this dtype and
+    shape, is contiguous and lives on GPU `device`."""
+    for t, name in zip(named[::2], named[1::2]):
+        if t is not None and (t.shape != shape or t.dtype is not dtype or
+                              t.get_device() != device or not t.is_contiguous()):
+            _refuse(t, name, shape, dtype)
+
+
 def _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias, pre_norm, skip_scale):
-    """(rows, features, gates) after checking every tensor against h [rows, features]."""
+    """(rows, features, gates, device) after checking every tensor against h [rows, features]."""
     if h.dim() != 2:
         raise ValueError("h must be [rows, features]")
-    rows, d = (int(v) for v in h.shape)
-    _expect(y, (rows, d), "y")
-    for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
-                    (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
-        _expect(t, (d,), name)
+    rows, d = h.shape
+    dtype, device = h.dtype, B.current_device()
+    _beside(device, dtype, (rows, d), h, "h", y, "y")
+    _beside(device, dtype, (d,), post_weight, "post_weight", post_bias, "post_bias",
+            pre_weight, "pre_weight", pre_bias, "pre_bias")
     gates = 0
     if gate is not None:
-        if gate.dim() != 2 or gate.shape[1] != d or gate.shape[0] == 0:
-            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected (gates, {d})")
-        gates = int(gate.shape[0])
-        if rows % gates or (rows and gates > rows):
-            raise ValueError(f"{gates} gate rows do not divide {rows} rows")
+        gates = gate.shape[0] if gate.dim() == 2 else 0
+        if gates == 0 or rows % gates or (rows and gates > rows):
+            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected (gates, {d}) with gates "
+                             f"dividing {rows} rows")
+        _beside(device, dtype, (gates, d), gate, "gate")
     if y is None and (post_weight is not None or post_bias is not None or gate is not None or
                       skip_scale != 1.0):
         raise ValueError("without y there is nothing to scale, gate or norm after the block")
     if pre_norm == B.NORM_NONE and (pre_weight is not None or pre_bias is not None):
         raise ValueError("pre_weight and pre_bias need a pre_norm")
-    _check(h, y, post_weight, post_bias, gate, pre_weight, pre_bias)
-    return rows, d, gates
+    return rows, d, gates, device
 
 
 def sandwich_forward(h, y=None, post_weight=None, post_bias=None, gate=None, pre_weight=None,
@@ -376,8 +401,8 @@ def sandwich_forward(h, y=None, post_weight=None, post_bias=None, gate=None, pre
     gate [gates, features] holds one row for rows/gates consecutive rows. Without
     y, h_out is h itself (the norm before the first block); with pre_norm
     NORM_NONE, n is None. stats [rows, 4] goes to sandwich_backward."""
-    rows, d, gates = _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias,
-                                      pre_norm, skip_scale)
+    rows, d, gates, _ = _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias,
+                                         pre_norm, skip_scale)
     h_out = torch.empty_like(h) if y is not None else h
     n = torch.empty_like(h) if pre_norm != B.NORM_NONE else None
     stats = torch.empty((rows, 4), dtype=torch.float32, device=h.device)
@@ -394,21 +419,17 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
     """SandwichGrads from the gradients dh_out (None: zero) and dn of the
     forward's results. h_out and stats are the forward's (eps is in stats; it is
     accepted so that both calls take the same keywords)."""
-    ref = h_out if h_out is not None else dh_out
-    rows, d, gates = _sandwich_shapes(ref, y, post_weight, post_bias, gate, pre_weight, pre_bias,
-                                      pre_norm, skip_scale)
-    _expect(dh_out, (rows, d), "dh_out")
-    _expect(dn, (rows, d), "dn")
-    _expect(stats, (rows, 4), "stats")
     if pre_norm != B.NORM_NONE and (dn is None or h_out is None):
         raise ValueError("the backward of a pre_norm needs dn and h_out")
     if pre_norm == B.NORM_NONE and dh_out is None:
         raise ValueError("without a pre_norm the backward needs dh_out")
-    _check(ref, dh_out, dn)
-    if stats.dtype != torch.float32 or not stats.is_contiguous() or stats.device != ref.device:
-        raise ValueError("stats must be the contiguous fp32 tensor the forward returned")
+    ref = h_out if h_out is not None else dh_out
+    rows, d, gates, device = _sandwich_shapes(ref, y, post_weight, post_bias, gate, pre_weight,
+                                              pre_bias, pre_norm, skip_scale)
+    _beside(device, ref.dtype, (rows, d), dh_out, "dh_out", dn, "dn")
+    _saved(stats, rows, device)
     like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
-    g = SandwichGrads(torch.empty_like(ref), like(y), like(post_weight), like(post_bias), like(gate),
+    g = SandwichGrads(like(ref), like(y), like(post_weight), like(post_bias), like(gate),
                       like(pre_weight), like(pre_bias))
     code = dtype_code(ref)
     need = B.monarch_sandwich_bwd_workspace_bytes(
@@ -422,48 +443,40 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
 
 
 def _distill_shapes(logits, teacher, ids, labels, per_row, name):
-    """(rows, vocab, top, ld) after checking logits [rows, vocab] (rows may lie
+    """(rows, vocab, top, ld, device) after checking logits [rows, vocab] (rows may lie
     apart, columns may not), teacher and ids [rows, top], labels and per_row [rows]."""
-    if logits.dim() != 2:
-        raise ValueError("logits must be [rows, vocab]")
-    rows, vocab = (int(v) for v in logits.shape)
-    if vocab > 1 and logits.stride(1) != 1:
-        raise ValueError("a row's logits must lie side by side")
-    ld = int(logits.stride(0)) if rows > 1 else vocab
-    if ld < vocab:
-        raise ValueError("the rows of logits must not overlap")
-    if teacher.dim() != 2:
-        raise ValueError("the teacher's logits must be [rows, top]")
-    top = int(teacher.shape[1])
+    if logits.dim() != 2 or teacher.dim() != 2:
+        raise ValueError("logits must be [rows, vocab], the teacher's logits [rows, top]")
+    rows, vocab = logits.shape
+    top, device = teacher.shape[1], B.current_device()
     if top > B.DISTILL_MAX_TOP:
         raise ValueError(f"at most {B.DISTILL_MAX_TOP} teacher entries a row, got {top}")
-    _expect(teacher, (rows, top), "the teacher's logits")
-    _expect(ids, (rows, top), "ids")
-    _expect(labels, (rows,), "labels")
-    _expect(per_row, (rows,), name)
-    for t, want, what in ((teacher, torch.float32, "the teacher's logits"), (ids, torch.int64, "ids"),
-                          (labels, torch.int64, "labels"), (per_row, torch.float32, name)):
-        if t is None:
-            continue
-        if t.dtype != want:
-            raise TypeError(f"{what} must be {want}")
-        if not t.is_contiguous() or t.device != logits.device:
-            raise ValueError(f"{what} must be contiguous and live beside the logits")
-    if logits.device.type != "cuda":
-        raise ValueError("tensors must live on the GPU")
-    return rows, vocab, top, ld
+    _beside(device, torch.float32, (rows, top), teacher, "the teacher's logits")
+    _beside(device, torch.int64, (rows, top), ids, "ids")
+    _beside(device, torch.int64, (rows,), labels, "labels")
+    _beside(device, torch.float32, (rows,), per_row, name)
+    if logits.get_device() != device:
+        raise ValueError("logits must live on the current GPU, where the call's stream is")
+    return rows, vocab, top, _rows_apart(logits, rows, vocab, "logits"), device
 
 
-def _distill_out(logits, rows, vocab, ld, out):
-    """dlogits in the logits' own layout, or `out` after checking it."""
+def _rows_apart(t, rows, cols, name):
+    """Elements from one row of t [rows, cols] to the next."""
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name} must have rows of side by side columns that do not overlap")
+    return ld
+
+
+def _distill_out(logits, rows, vocab, ld, device, out):
+    """(dlogits, its ld): in the logits' own layout, or `out` after checking it."""
     if out is None:
-        return torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
+        out = torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)
+        return (out if ld == vocab else out[:, :vocab]), ld
     _expect(out, (rows, vocab), "out")
-    if out.dtype != logits.dtype or out.device != logits.device:
+    if out.dtype != logits.dtype or out.get_device() != device:
         raise ValueError("out must have the logits' dtype and device")
-    if (vocab > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < vocab):
-        raise ValueError("out must have rows of side by side columns that do not overlap")
-    return out
+    return out, _rows_apart(out, rows, vocab, "out")
 
 
 def distill_forward(logits, teacher, ids, labels=None, *, temperature: float = 1.0,
@@ -475,7 +488,7 @@ def distill_forward(logits, teacher, ids, labels=None, *, temperature: float = 1
     p = softmax(teacher / temperature) over the row's entries, which sit at the
     columns `ids` (int64; -1 pads). labels (int64) outside the vocabulary are ignored.
     stats goes to distill_backward."""
-    rows, vocab, top, ld = _distill_shapes(logits, teacher, ids, labels, None, "")
+    rows, vocab, top, ld, _ = _distill_shapes(logits, teacher, ids, labels, None, "")
     loss = torch.empty((rows,), dtype=torch.float32, device=logits.device)
     stats = torch.empty((rows, 4), dtype=torch.float32, device=logits.device)
     B.monarch_distill_fwd(logits, ld, teacher, ids, labels, loss, stats, rows, vocab, top,
@@ -486,14 +499,11 @@ def distill_forward(logits, teacher, ids, labels=None, *, temperature: float = 1
 def distill_backward(dloss, logits, teacher, ids, labels, stats, *, temperature: float = 1.0,
                      mix: float = 1.0, out=None, stream=None):
     """dlogits for dloss [rows]; out may be logits itself."""
-    rows, vocab, top, ld = _distill_shapes(logits, teacher, ids, labels, dloss, "dloss")
-    _expect(stats, (rows, 4), "stats")
-    if stats.dtype != torch.float32 or not stats.is_contiguous() or stats.device != logits.device:
-        raise ValueError("stats must be the contiguous fp32 tensor the forward returned")
-    dz = _distill_out(logits, rows, vocab, ld, out)
-    B.monarch_distill_bwd(dloss, logits, ld, teacher, ids, labels, stats, dz,
-                          int(dz.stride(0)) if rows > 1 else vocab, rows, vocab, top, temperature,
-                          mix, dtype_code(logits), stream)
+    rows, vocab, top, ld, device = _distill_shapes(logits, teacher, ids, labels, dloss, "dloss")
+    _saved(stats, rows, device)
+    dz, dld = _distill_out(logits, rows, vocab, ld, device, out)
+    B.monarch_distill_bwd(dloss, logits, ld, teacher, ids, labels, stats, dz, dld, rows, vocab, top,
+                          temperature, mix, dtype_code(logits), stream)
     return dz
 
 
@@ -502,10 +512,10 @@ def distill_step(logits, teacher, ids, labels=None, row_weight=None, *, temperat
     """(loss [rows], dlogits) in one pass: dlogits is the gradient of
     sum(row_weight * loss) (row_weight None: 1 for every row). out may be
     logits itself, which saves a tensor of their size."""
-    rows, vocab, top, ld = _distill_shapes(logits, teacher, ids, labels, row_weight, "row_weight")
+    rows, vocab, top, ld, device = _distill_shapes(logits, teacher, ids, labels, row_weight,
+                                                   "row_weight")
     loss = torch.empty((rows,), dtype=torch.float32, device=logits.device)
-    dz = _distill_out(logits, rows, vocab, ld, out)
-    B.monarch_distill_step(logits, ld, teacher, ids, labels, row_weight, loss, dz,
-                           int(dz.stride(0)) if rows > 1 else vocab, rows, vocab, top, temperature,
-                           mix, dtype_code(logits), stream)
+    dz, dld = _distill_out(logits, rows, vocab, ld, device, out)
+    B.monarch_distill_step(logits, ld, teacher, ids, labels, row_weight, loss, dz, dld, rows, vocab,
+                           top, temperature, mix, dtype_code(logits), stream)
     return loss, dz
