@@ -42,7 +42,7 @@ struct SandwichFwd {
 };
 
 // A piece of an optional row (weights, biases, a gate row): without one, ones or
-// zeros, so that the arithmetic is the same.
+// zeros, so that the arithmetic is the same. To be settled as any piece.
 template <typename T, bool CUT>
 __device__ __forceinline__ u32x4 par_piece(const void* p, int64_t off, int at, int d, float fill) {
   if (p) return load_piece<T, CUT>(static_cast<const T*>(p) + off, at, d);
@@ -90,30 +90,48 @@ __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][
   rho = 1.0f / sqrtf(team.sum(q) / static_cast<float>(d) + eps);
 }
 
+template <typename T, bool CUT, int N>
+__device__ __forceinline__ void unpack_settled(u32x4 r, int at, int d, float (&v)[N]) {
+  settle<CUT, N>(r, at, d);
+  PieceOf<T>::unpack(r, v);
+}
+
+// One row a team. Teams of a whole workgroup of 512 threads or more leave room
+// for one or two workgroups a CU: they take rows in turn and load the next one
+// while the present one is normed a second time.
 template <typename T, int TEAM, int P, bool CUT>
 __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3) void sandwich_fwd_kernel(SandwichFwd a) {
   constexpr int N = PieceOf<T>::N, TEAMS = TEAM > 64 ? 1 : 256 / TEAM;
+  constexpr bool AHEAD = TEAM >= 512 && P <= 3;
   __shared__ typename Team<TEAM>::Lds lds;
   Team<TEAM> team(&lds);
   const int lane = threadIdx.x % TEAM;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM; row < a.rows;
-       row += static_cast<int64_t>(gridDim.x) * TEAMS) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
+  u32x4 hr[P], yr[P];
+  auto load = [&](int64_t row) {
     const int d = anew(a.d);
-    const int64_t off = row * d;
-    const T* h = static_cast<const T*>(a.h) + off;
-    u32x4 hr[P], yr[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      hr[p] = load_piece<T, CUT>(h, (p * TEAM + lane) * N, d);
-      if (a.y)
-        yr[p] = load_piece<T, CUT>(static_cast<const T*>(a.y) + off, (p * TEAM + lane) * N, d);
+      const int at = (p * TEAM + lane) * N;
+      hr[p] = load_piece<T, CUT>(static_cast<const T*>(a.h) + row * d, at, d);
+      if (a.y) yr[p] = load_piece<T, CUT>(static_cast<const T*>(a.y) + row * d, at, d);
     }
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM;
+  if (AHEAD && row < a.rows) load(row);
+  for (; row < a.rows; row += step) {
+    const int d = anew(a.d);
+    const int64_t off = row * d;
+    if constexpr (!AHEAD) load(row);
     float v[P][N];
     float mu_y = 0.0f, rho_y = 1.0f, mu_h = 0.0f, rho_h = 1.0f;
     if (a.y) {
       if (a.post != MONARCH_NORM_NONE) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) PieceOf<T>::unpack(yr[p], v[p]);
+        for (int p = 0; p < P; ++p) {
+          settle<CUT, N>(yr[p], (p * TEAM + lane) * N, d);
+          PieceOf<T>::unpack(yr[p], v[p]);
+        }
         row_stats<CUT, TEAM, P, N>(team, v, lane, d, a.post, a.eps, mu_y, rho_y);
       }
       const int64_t goff = a.gate ? row / a.rows_per_gate * d : 0;
@@ -121,14 +139,14 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3)
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
-        float t[N];
+        float w[N], b[N], g[N], t[N];
         forget(yr[p]);
+        if (a.post == MONARCH_NORM_NONE) settle<CUT, N>(yr[p], at, d);
         PieceOf<T>::unpack(yr[p], v[p]);
-        float w[N], b[N], g[N];
-        PieceOf<T>::unpack(par_piece<T, CUT>(a.post_w, 0, at, d, 1.0f), w);
-        PieceOf<T>::unpack(par_piece<T, CUT>(a.post_b, 0, at, d, 0.0f), b);
-        PieceOf<T>::unpack(par_piece<T, CUT>(a.gate, goff, at, d, 1.0f), g);
-        PieceOf<T>::unpack(hr[p], t);
+        unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.post_w, 0, at, d, 1.0f), at, d, w);
+        unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.post_b, 0, at, d, 0.0f), at, d, b);
+        unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.gate, goff, at, d, 1.0f), at, d, g);
+        unpack_settled<T, CUT, N>(hr[p], at, d, t);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float u = fmaf(fmaf(v[p][i], rho_y, -mean), w[i], b[i]);
@@ -139,16 +157,17 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3)
       }
     } else {
 #pragma unroll
-      for (int p = 0; p < P; ++p) PieceOf<T>::unpack(hr[p], v[p]);
+      for (int p = 0; p < P; ++p) unpack_settled<T, CUT, N>(hr[p], (p * TEAM + lane) * N, d, v[p]);
     }
+    if (AHEAD && row + step < a.rows) load(row + step);
     if (a.pre != MONARCH_NORM_NONE) {
       row_stats<CUT, TEAM, P, N>(team, v, lane, d, a.pre, a.eps, mu_h, rho_h);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
         float w[N], b[N];
-        PieceOf<T>::unpack(par_piece<T, CUT>(a.pre_w, 0, at, d, 1.0f), w);
-        PieceOf<T>::unpack(par_piece<T, CUT>(a.pre_b, 0, at, d, 0.0f), b);
+        unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.pre_w, 0, at, d, 1.0f), at, d, w);
+        unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.pre_b, 0, at, d, 0.0f), at, d, b);
 #pragma unroll
         for (int i = 0; i < N; ++i) v[p][i] = fmaf((v[p][i] - mu_h) * rho_h, w[i], b[i]);
         store_piece<T, CUT>(static_cast<T*>(a.n_out) + off, at, d, PieceOf<T>::pack(v[p]));
@@ -260,7 +279,12 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
       const int at = (p * TEAM + lane) * N;
       post_wr[p] = par_piece<T, CUT>(a.post_w, 0, at, d, 1.0f);
       pre_wr[p] = par_piece<T, CUT>(a.pre_w, 0, at, d, 1.0f);
-      if constexpr (GATE == CHUNK) gr[p] = par_piece<T, CUT>(a.gate, group * d, at, d, 1.0f);
+      settle<CUT, N>(post_wr[p], at, d);
+      settle<CUT, N>(pre_wr[p], at, d);
+      if constexpr (GATE == CHUNK) {
+        gr[p] = par_piece<T, CUT>(a.gate, group * d, at, d, 1.0f);
+        settle<CUT, N>(gr[p], at, d);
+      }
     }
   };
   if constexpr (!WIDE) load_pars();
@@ -319,6 +343,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           float dn[N], h[N], w[N];
+          settle<CUT, N>(dnr[p], (p * TEAM + lane) * N, d);
+          settle<CUT, N>(hr[p], (p * TEAM + lane) * N, d);
           PieceOf<T>::unpack(dnr[p], dn);
           PieceOf<T>::unpack(hr[p], h);
           if constexpr (BIAS) s_preb.add(p, dn);
@@ -347,7 +373,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           forget(pre_wr[p]);
           PieceOf<T>::unpack(dnr[p], dn);
           PieceOf<T>::unpack(hr[p], h);
-          PieceOf<T>::unpack(dhr[p], D[p]);
+          unpack_settled<T, CUT, N>(dhr[p], at, d, D[p]);
           PieceOf<T>::unpack(pre_wr[p], w);
 #pragma unroll
           for (int i = 0; i < N; ++i)
@@ -357,7 +383,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
       } else {
         if constexpr (WIDE) load_rest();
 #pragma unroll
-        for (int p = 0; p < P; ++p) PieceOf<T>::unpack(dhr[p], D[p]);
+        for (int p = 0; p < P; ++p)
+          unpack_settled<T, CUT, N>(dhr[p], (p * TEAM + lane) * N, d, D[p]);
       }
     }
     if (WIDE && row + step < last) load_pre(row + step);
@@ -378,6 +405,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
         float y[N], w[N], g[N], o[N];
+        settle<CUT, N>(yr[p], at, d);
+        if constexpr (GATE != CHUNK) settle<CUT, N>(gr[p], at, d);
         PieceOf<T>::unpack(yr[p], y);
         forget(post_wr[p]);
         forget(gr[p]);
@@ -388,7 +417,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
         if constexpr (GATE != CHUNK) {
           // dgate = branch D u
           float b[N];
-          if constexpr (BIAS) PieceOf<T>::unpack(par_piece<T, CUT>(a.post_b, 0, at, d, 0.0f), b);
+          if constexpr (BIAS)
+            unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.post_b, 0, at, d, 0.0f), at, d, b);
 #pragma unroll
           for (int i = 0; i < N; ++i) o[i] = D[p][i] * (BIAS ? fmaf(y[i], w[i], b[i]) : y[i] * w[i]);
           if constexpr (GATE == RUN) {
@@ -602,7 +632,7 @@ struct BwdPlan {
   size_t ws;
 };
 
-constexpr int64_t kChunks = 512;      // workgroups aimed at: two a CU
+constexpr int64_t kCus = 256;
 constexpr int64_t kRunRows = 32;     // gate runs up to this long are a team's own
 
 // Everything about a backward call that depends on sizes alone (`with`: which
@@ -617,16 +647,18 @@ BwdPlan bwd_plan(int64_t rows, int64_t d, int64_t gates, bool has_y, bool post_b
            : p.rows_per_gate > 1                                   ? RUN
                                                                    : TOKEN;
   const int teams = p.shape.team > 64 ? 1 : 256 / p.shape.team;
+  // workgroups aimed at: two a CU, one where the sums of a wide row take its LDS
+  const int64_t aim = kCus * (p.shape.team * p.shape.pieces * (bf16 ? 8 : 4) > 8192 ? 1 : 2);
   if (rows == 0) {
     p.cpg = 0;   // no chunk: every sum is empty
   } else if (p.gate != CHUNK) {
-    const int64_t units = gates, slots = kChunks * teams;
+    const int64_t units = gates, slots = aim * teams;
     p.chunk_rows = (units + slots - 1) / slots;
     p.chunks = (units + p.chunk_rows * teams - 1) / (p.chunk_rows * teams);
     p.cpg = 1;
   } else {
     const int64_t g = gates > 0 ? gates : 1;
-    int64_t cpg = (kChunks + g - 1) / g;
+    int64_t cpg = (aim + g - 1) / g;
     const int64_t most = (p.rows_per_gate + teams - 1) / teams;
     if (cpg > most) cpg = most;
     p.chunk_rows = (p.rows_per_gate + cpg - 1) / cpg;
@@ -659,8 +691,11 @@ bool cut_rows(int64_t d, bool bf16) { return d % (bf16 ? 8 : 4) != 0; }
 template <typename T, int TEAM, int P>
 void fwd_launch(const SandwichFwd& a, bool cut, hipStream_t s) {
   constexpr int WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
+  // one row a team, or the workgroups that fit the chip at once where they load
+  // ahead; 2^20 workgroups are fewer than 2^32 threads
+  const int64_t most = TEAM >= 512 ? kCus * (1024 / TEAM) : 1 << 20;
   int64_t grid = (a.rows + TEAMS - 1) / TEAMS;
-  if (grid > (1 << 20)) grid = 1 << 20;   // fewer than 2^32 threads; the rest by stride
+  if (grid > most) grid = most;
   const dim3 g(static_cast<unsigned>(grid)), block(WG);
   if (cut)
     hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true>), g, block, 0, s, a);

@@ -45,8 +45,7 @@ template <> struct PieceOf<uint16_t> {
   }
 };
 
-// Moves a piece by one element: towards element 0, or away from it with v (its
-// raw bits) as the new element 0.
+// Moves a piece by one element towards its element 0.
 template <int N>
 __device__ __forceinline__ void drop_first(u32x4& r) {
   if constexpr (N == 4) {
@@ -57,21 +56,12 @@ __device__ __forceinline__ void drop_first(u32x4& r) {
     r[3] >>= 16;
   }
 }
-template <int N>
-__device__ __forceinline__ void put_first(u32x4& r, uint32_t v) {
-  if constexpr (N == 4) {
-    r = u32x4{v, r[0], r[1], r[2]};
-  } else {
-#pragma unroll
-    for (int i = 3; i > 0; --i) r[i] = (r[i] << 16) | (r[i - 1] >> 16);
-    r[0] = (r[0] << 16) | v;
-  }
-}
 
-// Elements [at, at + N) of a row of d elements; those past the row are 0. With
-// CUT, d need not be a multiple of N: a piece that the row's end cuts goes element
-// by element, in a loop that is kept rolled (at most one lane of a team takes
-// it), and rows start anywhere. Without, pieces are whole and aligned.
+// Elements [at, at + N) of a row of d elements. Without CUT, d is a multiple of N:
+// pieces are whole and aligned, and one past the row is 0. With CUT, rows start
+// and end anywhere: a piece that does not end with the row or before it is
+// loaded as the row's last N elements, so that every load is one access that
+// nothing waits for; settle() then moves them into place.
 template <typename T, bool CUT>
 __device__ __forceinline__ u32x4 load_piece(const T* row, int at, int d) {
   constexpr int N = PieceOf<T>::N;
@@ -80,17 +70,41 @@ __device__ __forceinline__ u32x4 load_piece(const T* row, int at, int d) {
     if (at < d) r = *reinterpret_cast<const u32x4*>(row + at);
     return r;
   }
-  if (at + N <= d) return *reinterpret_cast<const typename PieceOf<T>::Raw*>(row + at);
+  if (d >= N) return *reinterpret_cast<const typename PieceOf<T>::Raw*>(row + min(at, d - N));
 #pragma unroll 1
-  for (int i = d - 1; i >= at; --i) {
+  for (int i = 0; i < d; ++i) {   // a row shorter than a piece: as its last N elements too
     uint32_t v;
     if constexpr (N == 4)
       v = __float_as_uint(row[i]);
     else
       v = row[i];
-    put_first<N>(r, v);
+    drop_first<N>(r);
+    if constexpr (N == 4)
+      r[3] = v;
+    else
+      r[3] |= v << 16;
   }
   return r;
+}
+
+// Moves what load_piece loaded with CUT into place: elements past the row are 0.
+template <bool CUT, int N>
+__device__ __forceinline__ void settle(u32x4& r, int at, int d) {
+  if constexpr (CUT) {
+    const int s = at + N - d;   // elements past the row
+    if (s > 0) {
+      if (s >= N) {
+        r = u32x4{0, 0, 0, 0};
+      } else if constexpr (N == 4) {
+        if (s & 2) r = u32x4{r[2], r[3], 0u, 0u};
+        if (s & 1) drop_first<N>(r);
+      } else {
+        if (s & 4) r = u32x4{r[2], r[3], 0u, 0u};
+        if (s & 2) r = u32x4{r[1], r[2], r[3], 0u};
+        if (s & 1) drop_first<N>(r);
+      }
+    }
+  }
 }
 
 template <typename T, bool CUT>
