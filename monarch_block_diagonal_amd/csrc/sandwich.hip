@@ -21,6 +21,7 @@
 #include <math.h>
 
 #include <initializer_list>
+#include <type_traits>
 
 #include "api_internal.h"
 #include "monarch.h"
@@ -96,13 +97,13 @@ __device__ __forceinline__ void unpack_settled(u32x4 r, int at, int d, float (&v
   PieceOf<T>::unpack(r, v);
 }
 
-// One row a team. Teams of a whole workgroup of 512 threads or more leave room
-// for one or two workgroups a CU: they take rows in turn and load the next one
-// while the present one is normed a second time.
-template <typename T, int TEAM, int P, bool CUT>
+// One row a team. A team of 1024 threads leaves room for one workgroup a CU: it
+// takes rows in turn and loads the next one while the present one is normed a
+// second time.
+template <typename T, int TEAM, int P, bool BIAS, bool CUT>
 __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3) void sandwich_fwd_kernel(SandwichFwd a) {
   constexpr int N = PieceOf<T>::N, TEAMS = TEAM > 64 ? 1 : 256 / TEAM;
-  constexpr bool AHEAD = TEAM >= 512 && P <= 3;
+  constexpr bool AHEAD = TEAM == 1024 && P <= 3;
   __shared__ typename Team<TEAM>::Lds lds;
   Team<TEAM> team(&lds);
   const int lane = threadIdx.x % TEAM;
@@ -135,7 +136,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3)
         row_stats<CUT, TEAM, P, N>(team, v, lane, d, a.post, a.eps, mu_y, rho_y);
       }
       const int64_t goff = a.gate ? row / a.rows_per_gate * d : 0;
-      const float mean = mu_y * rho_y;
+      // branch * yhat, so that the scale costs nothing a value
+      const float scale = a.branch * rho_y, mean = mu_y * scale;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
@@ -144,13 +146,15 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3)
         if (a.post == MONARCH_NORM_NONE) settle<CUT, N>(yr[p], at, d);
         PieceOf<T>::unpack(yr[p], v[p]);
         unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.post_w, 0, at, d, 1.0f), at, d, w);
-        unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.post_b, 0, at, d, 0.0f), at, d, b);
+        if constexpr (BIAS)
+          unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.post_b, 0, at, d, 0.0f), at, d, b);
         unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.gate, goff, at, d, 1.0f), at, d, g);
         unpack_settled<T, CUT, N>(hr[p], at, d, t);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float u = fmaf(fmaf(v[p][i], rho_y, -mean), w[i], b[i]);
-          v[p][i] = fmaf(a.skip, t[i], a.branch * g[i] * u);
+          float u = fmaf(v[p][i], scale, -mean) * w[i];
+          if constexpr (BIAS) u = fmaf(a.branch, b[i], u);
+          v[p][i] = fmaf(a.skip, t[i], g[i] * u);
         }
         store_piece<T, CUT>(static_cast<T*>(a.h_out) + off, at, d, PieceOf<T>::pack(v[p]));
         zero_past<CUT, N>(v[p], at, d);
@@ -162,14 +166,19 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3)
     if (AHEAD && row + step < a.rows) load(row + step);
     if (a.pre != MONARCH_NORM_NONE) {
       row_stats<CUT, TEAM, P, N>(team, v, lane, d, a.pre, a.eps, mu_h, rho_h);
+      const float mean_h = mu_h * rho_h;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
         float w[N], b[N];
         unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.pre_w, 0, at, d, 1.0f), at, d, w);
-        unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.pre_b, 0, at, d, 0.0f), at, d, b);
+        if constexpr (BIAS)
+          unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.pre_b, 0, at, d, 0.0f), at, d, b);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[p][i] = fmaf((v[p][i] - mu_h) * rho_h, w[i], b[i]);
+        for (int i = 0; i < N; ++i) {
+          v[p][i] = fmaf(v[p][i], rho_h, -mean_h) * w[i];
+          if constexpr (BIAS) v[p][i] += b[i];
+        }
         store_piece<T, CUT>(static_cast<T*>(a.n_out) + off, at, d, PieceOf<T>::pack(v[p]));
       }
     }
@@ -198,10 +207,10 @@ struct SandwichBwd {
   float skip, branch;
 };
 
-// A thread's sums over rows for its own columns: in registers, or (wide rows,
-// whose columns would not leave registers for the row itself) in LDS, 16 bytes a
-// lane side by side.
-template <int TEAM, int P, int N, bool IN_LDS>
+// A thread's sums over rows for its own columns: in registers, or in LDS (WG
+// threads side by side, 16 bytes each), where they would not leave registers for
+// the row itself.
+template <int WG, int P, int N, bool IN_LDS>
 struct Sums {
   float v[IN_LDS ? 1 : P][N];
   f32x4* lds;
@@ -209,7 +218,7 @@ struct Sums {
     lds = l;
     if constexpr (IN_LDS) {
 #pragma unroll
-      for (int k = 0; k < P * N / 4; ++k) lds[k * TEAM + threadIdx.x] = f32x4{0, 0, 0, 0};
+      for (int k = 0; k < P * N / 4; ++k) lds[k * WG + threadIdx.x] = f32x4{0, 0, 0, 0};
     } else {
 #pragma unroll
       for (int p = 0; p < P; ++p)
@@ -222,7 +231,7 @@ struct Sums {
     if constexpr (IN_LDS) {
 #pragma unroll
       for (int k = 0; k < N / 4; ++k) {
-        f32x4& s = lds[(p * (N / 4) + k) * TEAM + threadIdx.x];
+        f32x4& s = lds[(p * (N / 4) + k) * WG + threadIdx.x];
         f32x4 t = s;
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] += x[4 * k + i];
@@ -233,11 +242,9 @@ struct Sums {
       for (int i = 0; i < N; ++i) v[p][i] += x[i];
     }
   }
-  __device__ __forceinline__ float get(int p, int i) const {
-    if constexpr (IN_LDS)
-      return lds[(p * (N / 4) + i / 4) * TEAM + threadIdx.x][i % 4];
-    else
-      return v[p][i];
+  // column i of piece p of a thread of the workgroup (LDS)
+  __device__ __forceinline__ float at(int p, int i, int thread) const {
+    return reinterpret_cast<const float*>(&lds[(p * (N / 4) + i / 4) * WG + thread])[i % 4];
   }
 };
 
@@ -245,9 +252,14 @@ template <typename T, int TEAM, int P, int GATE, bool BIAS, bool CUT>
 __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(SandwichBwd a) {
   constexpr int N = PieceOf<T>::N, WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
   constexpr int COLS = TEAM * P * N;
-  constexpr bool WIDE = TEAM > 256;   // sums in LDS, parameters read again for every row
+  // sums of post_w and pre_w in LDS; parameters read again for every row; the next
+  // row's first tensors loaded ahead
+  constexpr bool IN_LDS = TEAM > 64 || BIAS;
+  constexpr bool REREAD = TEAM > 256;
+  constexpr bool LATE = TEAM > 512;   // 128 registers a thread: y's side is loaded last
+  constexpr bool AHEAD = TEAM > 64 && !LATE;
   __shared__ typename Team<TEAM>::Lds lds;
-  __shared__ f32x4 shared[WIDE ? 2 * COLS / 4 : TEAMS > 1 ? TEAMS * COLS / 4 : 1];
+  __shared__ f32x4 shared[IN_LDS ? 2 * WG * P * N / 4 : TEAMS > 1 ? TEAMS * COLS / 4 : 1];
   Team<TEAM> team(&lds);
   const int lane = threadIdx.x % TEAM, tm = threadIdx.x / TEAM;
   const float inv_d = 1.0f / static_cast<float>(a.d);
@@ -272,27 +284,37 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
   }
   const u32x4 zero = {0, 0, 0, 0};
   u32x4 post_wr[P], pre_wr[P], gr[P];
-  auto load_pars = [&]() {
+  auto load_pre_pars = [&]() {
+    const int d = anew(a.d);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int at = (p * TEAM + lane) * N;
+      pre_wr[p] = par_piece<T, CUT>(a.pre_w, 0, at, d, 1.0f);
+      settle<CUT, N>(pre_wr[p], at, d);
+    }
+  };
+  auto load_post_pars = [&]() {
     const int d = anew(a.d);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
       post_wr[p] = par_piece<T, CUT>(a.post_w, 0, at, d, 1.0f);
-      pre_wr[p] = par_piece<T, CUT>(a.pre_w, 0, at, d, 1.0f);
       settle<CUT, N>(post_wr[p], at, d);
-      settle<CUT, N>(pre_wr[p], at, d);
       if constexpr (GATE == CHUNK) {
         gr[p] = par_piece<T, CUT>(a.gate, group * d, at, d, 1.0f);
         settle<CUT, N>(gr[p], at, d);
       }
     }
   };
-  if constexpr (!WIDE) load_pars();
-  Sums<TEAM, P, N, WIDE> s_post, s_pre;
-  Sums<TEAM, BIAS ? P : 1, N, false> s_postb, s_preb;
-  Sums<TEAM, GATE == RUN ? P : 1, N, false> s_gate;
+  if constexpr (!REREAD) {
+    load_pre_pars();
+    load_post_pars();
+  }
+  Sums<WG, P, N, IN_LDS> s_post, s_pre;
+  Sums<WG, BIAS ? P : 1, N, false> s_postb, s_preb;
+  Sums<WG, GATE == RUN ? P : 1, N, false> s_gate;
   s_post.clear(shared);
-  s_pre.clear(shared + (WIDE ? COLS / 4 : 0));
+  s_pre.clear(shared + (IN_LDS ? WG * P * N / 4 : 0));
   s_postb.clear(nullptr);
   s_preb.clear(nullptr);
   s_gate.clear(nullptr);
@@ -311,29 +333,38 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
       }
     }
   };
-  if (WIDE && first < last) load_pre(first);
+  if (AHEAD && first < last) load_pre(first);
   for (int64_t row = first; row < last; row += step) {
     const int d = anew(a.d);
     const int64_t off = row * d;
     const f32x4 st = *reinterpret_cast<const f32x4*>(a.stats + row * 4);
-    if constexpr (!WIDE) load_pre(row);
+    if constexpr (!AHEAD) load_pre(row);
     u32x4 yr[P];
+    auto load_y = [&]() {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int at = (p * TEAM + lane) * N;
+        yr[p] = zero;
+        if (a.y) yr[p] = load_piece<T, CUT>(static_cast<const T*>(a.y) + off, at, d);
+        if constexpr (GATE != CHUNK)
+          gr[p] = load_piece<T, CUT>(static_cast<const T*>(a.gate) + group * d, at, d);
+      }
+    };
     float D[P][N];
     {
       u32x4 dhr[P];
       auto load_rest = [&]() {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          const int at = (p * TEAM + lane) * N;
-          dhr[p] = yr[p] = zero;
-          if (a.dh_out) dhr[p] = load_piece<T, CUT>(static_cast<const T*>(a.dh_out) + off, at, d);
-          if (a.y) yr[p] = load_piece<T, CUT>(static_cast<const T*>(a.y) + off, at, d);
-          if constexpr (GATE != CHUNK)
-            gr[p] = load_piece<T, CUT>(static_cast<const T*>(a.gate) + group * d, at, d);
+          dhr[p] = zero;
+          if (a.dh_out)
+            dhr[p] = load_piece<T, CUT>(static_cast<const T*>(a.dh_out) + off,
+                                        (p * TEAM + lane) * N, d);
         }
+        if constexpr (!LATE) load_y();
       };
-      if constexpr (WIDE)
-        load_pars();
+      if constexpr (REREAD)
+        load_pre_pars();
       else
         load_rest();
       float c1 = 0.0f, c2 = 0.0f;
@@ -358,7 +389,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           }
           s_pre.add(p, h);
         }
-        if constexpr (WIDE) load_rest();
+        if constexpr (REREAD) load_rest();
         team.template reduce<SumOp, 2>(s);
         // D = dh' + rho (q - hhat c1 - c2) with hhat = h rho - mean
         c1 = s[0] * inv_d;
@@ -381,13 +412,15 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           zero_past<CUT, N>(D[p], at, d);
         }
       } else {
-        if constexpr (WIDE) load_rest();
+        if constexpr (REREAD) load_rest();
 #pragma unroll
         for (int p = 0; p < P; ++p)
           unpack_settled<T, CUT, N>(dhr[p], (p * TEAM + lane) * N, d, D[p]);
       }
     }
-    if (WIDE && row + step < last) load_pre(row + step);
+    if constexpr (LATE) load_y();
+    if constexpr (REREAD) load_post_pars();
+    if (AHEAD && row + step < last) load_pre(row + step);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
@@ -473,7 +506,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           const int at = (p * TEAM + lane) * N;
           float o[N];
 #pragma unroll
-          for (int i = 0; i < N; ++i) o[i] = a.branch * s_gate.get(p, i);
+          for (int i = 0; i < N; ++i) o[i] = a.branch * s_gate.v[p][i];
           if (a.dgate)
             store_piece<T, CUT>(static_cast<T*>(a.dgate) + group * d, at, d, PieceOf<T>::pack(o));
         }
@@ -487,13 +520,22 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
   auto put = [&](int which, const auto& s) {
     if (which < 0) return;
     float* out = part + static_cast<int64_t>(which) * a.d;
-    if constexpr (TEAMS == 1) {
+    if constexpr (std::is_same<decltype(s), const Sums<WG, P, N, true>&>::value) {
+      __syncthreads();
+      for (int at = threadIdx.x; at < a.d; at += WG) {
+        const int p = at / (TEAM * N), l = at / N % TEAM, i = at % N;
+        float t = s.at(p, i, l);
+#pragma unroll
+        for (int k = 1; k < TEAMS; ++k) t += s.at(p, i, k * TEAM + l);
+        out[at] = t;
+      }
+    } else if constexpr (TEAMS == 1) {
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int at = (p * TEAM + lane) * N + i;
-          if (at < a.d) out[at] = s.get(p, i);
+          if (at < a.d) out[at] = s.v[p][i];
         }
     } else {
       float* join = reinterpret_cast<float*>(shared);
@@ -501,7 +543,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int i = 0; i < N; ++i) join[tm * COLS + (p * TEAM + lane) * N + i] = s.get(p, i);
+        for (int i = 0; i < N; ++i) join[tm * COLS + (p * TEAM + lane) * N + i] = s.v[p][i];
       __syncthreads();
       for (int at = threadIdx.x; at < a.d; at += WG) {
         float t = join[at];
@@ -693,14 +735,16 @@ void fwd_launch(const SandwichFwd& a, bool cut, hipStream_t s) {
   constexpr int WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
   // one row a team, or the workgroups that fit the chip at once where they load
   // ahead; 2^20 workgroups are fewer than 2^32 threads
-  const int64_t most = TEAM >= 512 ? kCus * (1024 / TEAM) : 1 << 20;
+  const int64_t most = TEAM == 1024 ? kCus : 1 << 20;
   int64_t grid = (a.rows + TEAMS - 1) / TEAMS;
   if (grid > most) grid = most;
   const dim3 g(static_cast<unsigned>(grid)), block(WG);
   if (cut)
-    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true>), g, block, 0, s, a);
+    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true, true>), g, block, 0, s, a);
+  else if (a.post_b || a.pre_b)
+    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true, false>), g, block, 0, s, a);
   else
-    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, false>), g, block, 0, s, a);
+    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, false, false>), g, block, 0, s, a);
 }
 
 template <typename T, int TEAM, int P>
