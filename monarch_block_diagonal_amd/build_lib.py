@@ -7,7 +7,7 @@ include/monarch.h. Run as `python -m monarch_block_diagonal_amd.build_lib`.
 `--sanitize` builds a second copy, _build_asan/libmonarch_asan.so, whose host
 code is instrumented with AddressSanitizer and UndefinedBehaviorSanitizer
 (device code is built as usual), and `--sanitize --test` then runs the host
-ABI tests (tests/test_abi.py: argument checks, planning, descriptions; no
+ABI tests (tests/test_abi.py, tests/test_abi_rows.py: argument checks, planning, descriptions; no
 kernel launch) against it with the sanitizer runtime preloaded, failing on
 any report.
 """
@@ -91,7 +91,7 @@ def sanitizer_runtime() -> str:
 
 
 def test_sanitized() -> int:
-    """tests/test_abi.py against the sanitizer build; returns pytest's status."""
+    """tests/test_abi.py and test_abi_rows.py against the sanitizer build; returns pytest's status."""
     env = dict(os.environ)
     env["MONARCH_LIBRARY"] = LIB_ASAN
     env["LD_PRELOAD"] = sanitizer_runtime()
@@ -99,7 +99,8 @@ def test_sanitized() -> int:
     # tracked as leaks; any other report aborts the run
     env["ASAN_OPTIONS"] = "detect_leaks=0:abort_on_error=1:halt_on_error=1"
     env["UBSAN_OPTIONS"] = "print_stacktrace=1:halt_on_error=1"
-    cmd = [sys.executable, "-m", "pytest", os.path.join(ROOT, "tests", "test_abi.py"), "-q",
+    cmd = [sys.executable, "-m", "pytest", os.path.join(ROOT, "tests", "test_abi.py"),
+           os.path.join(ROOT, "tests", "test_abi_rows.py"), "-q",
            "-p", "no:cacheprovider"]
     return subprocess.run(cmd, env=env, cwd=ROOT).returncode
 

@@ -8,6 +8,11 @@ MonarchLinearFunction wraps the pair as an autograd function, so the operator
 can stand in for a dense linear layer. The *_ex helpers and the MonarchLinear
 module take the general layer (any in/out, zero-padded to whole blocks, an
 explicit intermediate width, optional bias).
+
+Around and after the layers: sandwich_forward / sandwich_backward (SandwichNorm)
+for the norms, gate and residual join between two blocks, and distill_forward /
+distill_backward / distill_step (DistillLossFunction) for training against a
+teacher's top logits.
 """
 from __future__ import annotations
 
@@ -442,6 +447,65 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
     return g
 
 
+class SandwichFunction(torch.autograd.Function):
+    """sandwich_forward's (h_out, n) with gradients; n alone without y, None for
+    the n of NORM_NONE."""
+
+    @staticmethod
+    def forward(ctx, h, y, post_weight, post_bias, gate, pre_weight, pre_bias, how):
+        affine = [None if t is None else t.contiguous()
+                  for t in (post_weight, post_bias, gate, pre_weight, pre_bias)]
+        h, y = h.contiguous(), None if y is None else y.contiguous()
+        h_out, n, stats = sandwich_forward(h, y, *affine, **how)
+        ctx.how, ctx.alone = how, y is None
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(h_out, y, stats, *affine)
+        return n if ctx.alone else (h_out, n)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        h_out, y, stats, *affine = ctx.saved_tensors
+        dh_out, dn = (None, grads[0]) if ctx.alone else grads
+        if dn is None and ctx.how["pre_norm"] != B.NORM_NONE:
+            dn = torch.zeros_like(h_out)
+        if dh_out is None and ctx.how["pre_norm"] == B.NORM_NONE:
+            dh_out = torch.zeros_like(h_out)
+        cont = lambda t: None if t is None else t.contiguous()  # noqa: E731
+        return (*sandwich_backward(cont(dh_out), cont(dn), h_out, y, stats, *affine, **ctx.how), None)
+
+
+class SandwichNorm(torch.nn.Module):
+    """What stands between two blocks: norm, gate and residual join of the first
+    one's output, norm for the second one.
+
+        h, n = SandwichNorm(features)(h, y)      # y: the output of a block that read n
+
+    pre_norm NORM_NONE ends the stream without a norm; `gated` adds a learned gate
+    row (a gate of the caller's own, [gates, features], may be passed instead)."""
+
+    def __init__(self, features: int, post_norm: int = B.NORM_RMS, pre_norm: int = B.NORM_RMS,
+                 bias: bool = False, gated: bool = False, skip_scale: float = 1.0,
+                 branch_scale: float = 1.0, eps: float = 1e-5, device=None, dtype=torch.float32):
+        super().__init__()
+        make = lambda on, v: (torch.nn.Parameter(torch.full((features,), v, device=device, dtype=dtype))  # noqa: E731
+                              if on else None)
+        self.how = dict(post_norm=post_norm, pre_norm=pre_norm, skip_scale=skip_scale,
+                        branch_scale=branch_scale, eps=eps)
+        self.post_weight, self.post_bias = make(True, 1.0), make(bias, 0.0)
+        self.pre_weight = make(pre_norm != B.NORM_NONE, 1.0)
+        self.pre_bias = make(bias and pre_norm != B.NORM_NONE, 0.0)
+        self.gate = (torch.nn.Parameter(torch.ones((1, features), device=device, dtype=dtype))
+                     if gated else None)
+
+    def forward(self, h, y, gate=None):
+        shape = h.shape
+        flat = lambda t: t.reshape(-1, shape[-1])  # noqa: E731
+        h_out, n = SandwichFunction.apply(flat(h), flat(y), self.post_weight, self.post_bias,
+                                          self.gate if gate is None else gate, self.pre_weight,
+                                          self.pre_bias, self.how)
+        return h_out.reshape(shape), None if n is None else n.reshape(shape)
+
+
 def _distill_shapes(logits, teacher, ids, labels, per_row, name):
     """(rows, vocab, top, ld, device) after checking logits [rows, vocab] (rows may lie
     apart, columns may not), teacher and ids [rows, top], labels and per_row [rows]."""
@@ -519,3 +583,20 @@ def distill_step(logits, teacher, ids, labels=None, row_weight=None, *, temperat
     B.monarch_distill_step(logits, ld, teacher, ids, labels, row_weight, loss, dz, dld, rows, vocab,
                            top, temperature, mix, dtype_code(logits), stream)
     return loss, dz
+
+
+class DistillLossFunction(torch.autograd.Function):
+    """distill_forward's loss [rows] with its gradient by the logits. Where the
+    rows' weights are known before the loss, distill_step is one pass instead of two."""
+
+    @staticmethod
+    def forward(ctx, logits, teacher, ids, labels, temperature: float = 1.0, mix: float = 1.0):
+        ctx.how = dict(temperature=temperature, mix=mix)
+        loss, stats = distill_forward(logits, teacher, ids, labels, **ctx.how)
+        ctx.save_for_backward(logits, teacher, ids, labels, stats)
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        dz = distill_backward(dloss.contiguous(), *ctx.saved_tensors, **ctx.how)
+        return dz, None, None, None, None, None
