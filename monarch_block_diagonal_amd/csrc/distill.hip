@@ -89,6 +89,10 @@ struct Running {
 template <typename T, int TEAM, int P, int WHAT, int SECOND>
 __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
   constexpr int N = PieceOf<T>::N, U = 4;
+  // rows longer than 1024 threads' registers: the next 8 rounds stay in LDS (128 KB)
+  constexpr int L = TEAM == 1024 && WHAT == (WITH_LOSS | WITH_GRAD) ? 8 : 0;
+  static_assert(L % U == 0, "");
+  __shared__ u32x4 s_held[L > 0 ? L * TEAM : 1];
   constexpr int PR = P > 0 ? P : 1;
   constexpr uint32_t kMinusInf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
   const u32x4 nothing_more = {kMinusInf, kMinusInf, kMinusInf, kMinusInf};   // adds nothing
@@ -164,6 +168,9 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
           more[u] = nothing_more;
           if (base + u * TEAM + tid < pieces) more[u] = (body + (base + u * TEAM))[lane];
         }
+        if (base < (P + L) * TEAM)
+#pragma unroll
+          for (int u = 0; u < U; ++u) s_held[base - P * TEAM + u * TEAM + tid] = more[u];
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (base + u * TEAM < pieces) {
@@ -279,9 +286,14 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
         if (p * TEAM < np) put(round_at(p, np), counts(p, round_at(p, np), np), raw[p]);
       for (int base = P * TEAM; base < pieces; base += TEAM * U) {
         u32x4 more[U] = {};
+        if (base < (P + L) * TEAM) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (base + u * TEAM + tid < pieces) more[u] = (body + (base + u * TEAM))[lane];
+          for (int u = 0; u < U; ++u) more[u] = s_held[base - P * TEAM + u * TEAM + tid];
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (base + u * TEAM + tid < pieces) more[u] = (body + (base + u * TEAM))[lane];
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (base + u * TEAM < pieces)
