@@ -16,6 +16,7 @@ teacher's top logits.
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -358,16 +359,17 @@ def _saved(stats, rows, device):
     """Checks what a forward call saved for its backward call."""
     if stats.dtype is not torch.float32:
         raise ValueError("stats must be the fp32 tensor the forward returned")
-    _beside(device, torch.float32, (rows, 4), stats, "stats")
+    _beside(device, torch.float32, (rows, 4), "stats", stats)
 
 
-def _beside(device, dtype, shape, *named):
-    """Checks that each given tensor of (tensor, name, ...) has this dtype and
-    shape, is contiguous and lives on GPU `device`."""
-    for t, name in zip(named[::2], named[1::2]):
-        if t is not None and (t.shape != shape or t.dtype is not dtype or
-                              t.get_device() != device or not t.is_contiguous()):
-            _refuse(t, name, shape, dtype)
+def _beside(device, dtype, shape, names, *tensors):
+    """Checks that each given tensor has this dtype and shape, is contiguous and
+    lives on GPU `device`; `names` (divided by spaces) are for the refusal."""
+    for t in tensors:
+        if t is not None and not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and
+                                  t.get_device() == device):
+            at = next(i for i, x in enumerate(tensors) if x is t)
+            _refuse(t, names.split()[at], shape, dtype)
 
 
 def _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias, pre_norm, skip_scale):
@@ -376,22 +378,26 @@ def _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias, p
         raise ValueError("h must be [rows, features]")
     rows, d = h.shape
     dtype, device = h.dtype, B.current_device()
-    _beside(device, dtype, (rows, d), h, "h", y, "y")
-    _beside(device, dtype, (d,), post_weight, "post_weight", post_bias, "post_bias",
-            pre_weight, "pre_weight", pre_bias, "pre_bias")
+    _beside(device, dtype, (rows, d), "h y", h, y)
+    _beside(device, dtype, (d,), "post_weight post_bias pre_weight pre_bias", post_weight, post_bias,
+            pre_weight, pre_bias)
     gates = 0
     if gate is not None:
         gates = gate.shape[0] if gate.dim() == 2 else 0
         if gates == 0 or rows % gates or (rows and gates > rows):
             raise ValueError(f"gate has shape {tuple(gate.shape)}, expected (gates, {d}) with gates "
                              f"dividing {rows} rows")
-        _beside(device, dtype, (gates, d), gate, "gate")
+        _beside(device, dtype, (gates, d), "gate", gate)
     if y is None and (post_weight is not None or post_bias is not None or gate is not None or
                       skip_scale != 1.0):
         raise ValueError("without y there is nothing to scale, gate or norm after the block")
     if pre_norm == B.NORM_NONE and (pre_weight is not None or pre_bias is not None):
         raise ValueError("pre_weight and pre_bias need a pre_norm")
     return rows, d, gates, device
+
+
+# a function of the sizes alone: asked for once for each of them
+_sandwich_workspace = functools.lru_cache(maxsize=256)(B.monarch_sandwich_bwd_workspace_bytes)
 
 
 def sandwich_forward(h, y=None, post_weight=None, post_bias=None, gate=None, pre_weight=None,
@@ -431,14 +437,13 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
     ref = h_out if h_out is not None else dh_out
     rows, d, gates, device = _sandwich_shapes(ref, y, post_weight, post_bias, gate, pre_weight,
                                               pre_bias, pre_norm, skip_scale)
-    _beside(device, ref.dtype, (rows, d), dh_out, "dh_out", dn, "dn")
+    _beside(device, ref.dtype, (rows, d), "dh_out dn", dh_out, dn)
     _saved(stats, rows, device)
     like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
     g = SandwichGrads(like(ref), like(y), like(post_weight), like(post_bias), like(gate),
                       like(pre_weight), like(pre_bias))
     code = dtype_code(ref)
-    need = B.monarch_sandwich_bwd_workspace_bytes(
-        rows, d, gates, post_bias is not None or pre_bias is not None, code)
+    need = _sandwich_workspace(rows, d, gates, post_bias is not None or pre_bias is not None, code)
     ws = torch.empty(max(need, 1), dtype=torch.uint8, device=ref.device)
     B.monarch_sandwich_bwd(dh_out, dn, h_out, y, stats, post_weight, post_bias, gate, pre_weight,
                            pre_bias, g.dh, g.dy, g.dpost_weight, g.dpost_bias, g.dgate,
@@ -515,10 +520,10 @@ def _distill_shapes(logits, teacher, ids, labels, per_row, name):
     top, device = teacher.shape[1], B.current_device()
     if top > B.DISTILL_MAX_TOP:
         raise ValueError(f"at most {B.DISTILL_MAX_TOP} teacher entries a row, got {top}")
-    _beside(device, torch.float32, (rows, top), teacher, "the teacher's logits")
-    _beside(device, torch.int64, (rows, top), ids, "ids")
-    _beside(device, torch.int64, (rows,), labels, "labels")
-    _beside(device, torch.float32, (rows,), per_row, name)
+    _beside(device, torch.float32, (rows, top), "teacher", teacher)
+    _beside(device, torch.int64, (rows, top), "ids", ids)
+    _beside(device, torch.int64, (rows,), "labels", labels)
+    _beside(device, torch.float32, (rows,), name, per_row)
     if logits.get_device() != device:
         raise ValueError("logits must live on the current GPU, where the call's stream is")
     return rows, vocab, top, _rows_apart(logits, rows, vocab, "logits"), device
