@@ -44,24 +44,24 @@ struct SandwichFwd {
 
 // A piece of an optional row (weights, biases, a gate row): without one, ones or
 // zeros, so that the arithmetic is the same. To be settled as any piece.
-template <typename T, bool CUT>
+template <typename T, Rows R>
 __device__ __forceinline__ u32x4 par_piece(const void* p, int64_t off, int at, int d, float fill) {
-  if (p) return load_piece<T, CUT>(static_cast<const T*>(p) + off, at, d);
+  if (p) return load_piece<T, R>(static_cast<const T*>(p) + off, at, d);
   const uint32_t w = sizeof(T) == 2 ? (__float_as_uint(fill) >> 16) * 0x10001u : __float_as_uint(fill);
   return u32x4{w, w, w, w};
 }
 
 // The elements of a piece at `at` that lie past the row, set to 0.
-template <bool CUT, int N>
+template <Rows R, int N>
 __device__ __forceinline__ void zero_past(float (&v)[N], int at, int d) {
-  if (at + (CUT ? N - 1 : 0) >= d)
+  if (at + (R == WHOLE ? 0 : N - 1) >= d)
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (!CUT || at + i >= d) v[i] = 0.0f;
+      if (R == WHOLE || at + i >= d) v[i] = 0.0f;
 }
 
 // mean and 1/sqrt(mean square about it + eps) of the team's row (zero past d)
-template <bool CUT, int TEAM, int P, int N>
+template <Rows R, int TEAM, int P, int N>
 __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][N], int lane, int d,
                                           int kind, float eps, float& mu, float& rho) {
   mu = 0.0f;
@@ -78,7 +78,7 @@ __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][
       float c[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) c[i] = v[p][i] - mu;
-      zero_past<CUT, N>(c, (p * TEAM + lane) * N, d);
+      zero_past<R, N>(c, (p * TEAM + lane) * N, d);
 #pragma unroll
       for (int i = 0; i < N; ++i) q = fmaf(c[i], c[i], q);
     }
@@ -91,17 +91,17 @@ __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][
   rho = 1.0f / sqrtf(team.sum(q) / static_cast<float>(d) + eps);
 }
 
-template <typename T, bool CUT, int N>
+template <typename T, Rows R, int N>
 __device__ __forceinline__ void unpack_settled(u32x4 r, int at, int d, float (&v)[N]) {
-  settle<CUT, N>(r, at, d);
+  settle<R, N>(r, at, d);
   PieceOf<T>::unpack(r, v);
 }
 
 // One row a team. A team of 1024 threads leaves room for one workgroup a CU: it
 // takes rows in turn and loads the next one while the present one is normed a
 // second time.
-template <typename T, int TEAM, int P, bool BIAS, bool CUT>
-__global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3) void sandwich_fwd_kernel(SandwichFwd a) {
+template <typename T, int TEAM, int P, bool BIAS, Rows R>
+__global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 4 : 3) void sandwich_fwd_kernel(SandwichFwd a) {
   constexpr int N = PieceOf<T>::N, TEAMS = TEAM > 64 ? 1 : 256 / TEAM;
   constexpr bool AHEAD = TEAM == 1024 && P <= 3;
   __shared__ typename Team<TEAM>::Lds lds;
@@ -114,8 +114,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3)
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
-      hr[p] = load_piece<T, CUT>(static_cast<const T*>(a.h) + row * d, at, d);
-      if (a.y) yr[p] = load_piece<T, CUT>(static_cast<const T*>(a.y) + row * d, at, d);
+      hr[p] = load_piece<T, R>(static_cast<const T*>(a.h) + row * d, at, d);
+      if (a.y) yr[p] = load_piece<T, R>(static_cast<const T*>(a.y) + row * d, at, d);
     }
   };
   int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM;
@@ -130,10 +130,10 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3)
       if (a.post != MONARCH_NORM_NONE) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          settle<CUT, N>(yr[p], (p * TEAM + lane) * N, d);
+          settle<R, N>(yr[p], (p * TEAM + lane) * N, d);
           PieceOf<T>::unpack(yr[p], v[p]);
         }
-        row_stats<CUT, TEAM, P, N>(team, v, lane, d, a.post, a.eps, mu_y, rho_y);
+        row_stats<R, TEAM, P, N>(team, v, lane, d, a.post, a.eps, mu_y, rho_y);
       }
       const int64_t goff = a.gate ? row / a.rows_per_gate * d : 0;
       // branch * yhat, so that the scale costs nothing a value
@@ -143,43 +143,43 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || !CUT ? 4 : 3)
         const int at = (p * TEAM + lane) * N;
         float w[N], b[N], g[N], t[N];
         forget(yr[p]);
-        if (a.post == MONARCH_NORM_NONE) settle<CUT, N>(yr[p], at, d);
+        if (a.post == MONARCH_NORM_NONE) settle<R, N>(yr[p], at, d);
         PieceOf<T>::unpack(yr[p], v[p]);
-        unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.post_w, 0, at, d, 1.0f), at, d, w);
+        unpack_settled<T, R, N>(par_piece<T, R>(a.post_w, 0, at, d, 1.0f), at, d, w);
         if constexpr (BIAS)
-          unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.post_b, 0, at, d, 0.0f), at, d, b);
-        unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.gate, goff, at, d, 1.0f), at, d, g);
-        unpack_settled<T, CUT, N>(hr[p], at, d, t);
+          unpack_settled<T, R, N>(par_piece<T, R>(a.post_b, 0, at, d, 0.0f), at, d, b);
+        unpack_settled<T, R, N>(par_piece<T, R>(a.gate, goff, at, d, 1.0f), at, d, g);
+        unpack_settled<T, R, N>(hr[p], at, d, t);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           float u = fmaf(v[p][i], scale, -mean) * w[i];
           if constexpr (BIAS) u = fmaf(a.branch, b[i], u);
           v[p][i] = fmaf(a.skip, t[i], g[i] * u);
         }
-        store_piece<T, CUT>(static_cast<T*>(a.h_out) + off, at, d, PieceOf<T>::pack(v[p]));
-        zero_past<CUT, N>(v[p], at, d);
+        store_piece<T, R>(static_cast<T*>(a.h_out) + off, at, d, PieceOf<T>::pack(v[p]));
+        zero_past<R, N>(v[p], at, d);
       }
     } else {
 #pragma unroll
-      for (int p = 0; p < P; ++p) unpack_settled<T, CUT, N>(hr[p], (p * TEAM + lane) * N, d, v[p]);
+      for (int p = 0; p < P; ++p) unpack_settled<T, R, N>(hr[p], (p * TEAM + lane) * N, d, v[p]);
     }
     if (AHEAD && row + step < a.rows) load(row + step);
     if (a.pre != MONARCH_NORM_NONE) {
-      row_stats<CUT, TEAM, P, N>(team, v, lane, d, a.pre, a.eps, mu_h, rho_h);
+      row_stats<R, TEAM, P, N>(team, v, lane, d, a.pre, a.eps, mu_h, rho_h);
       const float mean_h = mu_h * rho_h;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
         float w[N], b[N];
-        unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.pre_w, 0, at, d, 1.0f), at, d, w);
+        unpack_settled<T, R, N>(par_piece<T, R>(a.pre_w, 0, at, d, 1.0f), at, d, w);
         if constexpr (BIAS)
-          unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.pre_b, 0, at, d, 0.0f), at, d, b);
+          unpack_settled<T, R, N>(par_piece<T, R>(a.pre_b, 0, at, d, 0.0f), at, d, b);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           v[p][i] = fmaf(v[p][i], rho_h, -mean_h) * w[i];
           if constexpr (BIAS) v[p][i] += b[i];
         }
-        store_piece<T, CUT>(static_cast<T*>(a.n_out) + off, at, d, PieceOf<T>::pack(v[p]));
+        store_piece<T, R>(static_cast<T*>(a.n_out) + off, at, d, PieceOf<T>::pack(v[p]));
       }
     }
     if (lane == 0) *reinterpret_cast<f32x4*>(a.stats + row * 4) = f32x4{mu_y, rho_y, mu_h, rho_h};
@@ -248,7 +248,7 @@ struct Sums {
   }
 };
 
-template <typename T, int TEAM, int P, int GATE, bool BIAS, bool CUT>
+template <typename T, int TEAM, int P, int GATE, bool BIAS, Rows R>
 __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(SandwichBwd a) {
   constexpr int N = PieceOf<T>::N, WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
   constexpr int COLS = TEAM * P * N;
@@ -289,8 +289,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
-      pre_wr[p] = par_piece<T, CUT>(a.pre_w, 0, at, d, 1.0f);
-      settle<CUT, N>(pre_wr[p], at, d);
+      pre_wr[p] = par_piece<T, R>(a.pre_w, 0, at, d, 1.0f);
+      settle<R, N>(pre_wr[p], at, d);
     }
   };
   auto load_post_pars = [&]() {
@@ -298,11 +298,11 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
-      post_wr[p] = par_piece<T, CUT>(a.post_w, 0, at, d, 1.0f);
-      settle<CUT, N>(post_wr[p], at, d);
+      post_wr[p] = par_piece<T, R>(a.post_w, 0, at, d, 1.0f);
+      settle<R, N>(post_wr[p], at, d);
       if constexpr (GATE == CHUNK) {
-        gr[p] = par_piece<T, CUT>(a.gate, group * d, at, d, 1.0f);
-        settle<CUT, N>(gr[p], at, d);
+        gr[p] = par_piece<T, R>(a.gate, group * d, at, d, 1.0f);
+        settle<R, N>(gr[p], at, d);
       }
     }
   };
@@ -328,8 +328,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
       const int at = (p * TEAM + lane) * N;
       dnr[p] = hr[p] = zero;
       if (a.pre != MONARCH_NORM_NONE) {
-        dnr[p] = load_piece<T, CUT>(static_cast<const T*>(a.dn) + row * d, at, d);
-        hr[p] = load_piece<T, CUT>(static_cast<const T*>(a.h_out) + row * d, at, d);
+        dnr[p] = load_piece<T, R>(static_cast<const T*>(a.dn) + row * d, at, d);
+        hr[p] = load_piece<T, R>(static_cast<const T*>(a.h_out) + row * d, at, d);
       }
     }
   };
@@ -345,9 +345,9 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
         yr[p] = zero;
-        if (a.y) yr[p] = load_piece<T, CUT>(static_cast<const T*>(a.y) + off, at, d);
+        if (a.y) yr[p] = load_piece<T, R>(static_cast<const T*>(a.y) + off, at, d);
         if constexpr (GATE != CHUNK)
-          gr[p] = load_piece<T, CUT>(static_cast<const T*>(a.gate) + group * d, at, d);
+          gr[p] = load_piece<T, R>(static_cast<const T*>(a.gate) + group * d, at, d);
       }
     };
     float D[P][N];
@@ -358,7 +358,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
         for (int p = 0; p < P; ++p) {
           dhr[p] = zero;
           if (a.dh_out)
-            dhr[p] = load_piece<T, CUT>(static_cast<const T*>(a.dh_out) + off,
+            dhr[p] = load_piece<T, R>(static_cast<const T*>(a.dh_out) + off,
                                         (p * TEAM + lane) * N, d);
         }
         if constexpr (!LATE) load_y();
@@ -374,8 +374,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           float dn[N], h[N], w[N];
-          settle<CUT, N>(dnr[p], (p * TEAM + lane) * N, d);
-          settle<CUT, N>(hr[p], (p * TEAM + lane) * N, d);
+          settle<R, N>(dnr[p], (p * TEAM + lane) * N, d);
+          settle<R, N>(hr[p], (p * TEAM + lane) * N, d);
           PieceOf<T>::unpack(dnr[p], dn);
           PieceOf<T>::unpack(hr[p], h);
           if constexpr (BIAS) s_preb.add(p, dn);
@@ -404,18 +404,18 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           forget(pre_wr[p]);
           PieceOf<T>::unpack(dnr[p], dn);
           PieceOf<T>::unpack(hr[p], h);
-          unpack_settled<T, CUT, N>(dhr[p], at, d, D[p]);
+          unpack_settled<T, R, N>(dhr[p], at, d, D[p]);
           PieceOf<T>::unpack(pre_wr[p], w);
 #pragma unroll
           for (int i = 0; i < N; ++i)
             D[p][i] += fmaf(st[3] * dn[i], w[i], -fmaf(h[i], k1, k0));
-          zero_past<CUT, N>(D[p], at, d);
+          zero_past<R, N>(D[p], at, d);
         }
       } else {
         if constexpr (REREAD) load_rest();
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          unpack_settled<T, CUT, N>(dhr[p], (p * TEAM + lane) * N, d, D[p]);
+          unpack_settled<T, R, N>(dhr[p], (p * TEAM + lane) * N, d, D[p]);
       }
     }
     if constexpr (LATE) load_y();
@@ -428,7 +428,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
         float o[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = a.skip * D[p][i];
-        store_piece<T, CUT>(static_cast<T*>(a.dh) + off, at, d, PieceOf<T>::pack(o));
+        store_piece<T, R>(static_cast<T*>(a.dh) + off, at, d, PieceOf<T>::pack(o));
       }
     }
     if (a.y) {
@@ -438,8 +438,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
         float y[N], w[N], g[N], o[N];
-        settle<CUT, N>(yr[p], at, d);
-        if constexpr (GATE != CHUNK) settle<CUT, N>(gr[p], at, d);
+        settle<R, N>(yr[p], at, d);
+        if constexpr (GATE != CHUNK) settle<R, N>(gr[p], at, d);
         PieceOf<T>::unpack(yr[p], y);
         forget(post_wr[p]);
         forget(gr[p]);
@@ -451,7 +451,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           // dgate = branch D u
           float b[N];
           if constexpr (BIAS)
-            unpack_settled<T, CUT, N>(par_piece<T, CUT>(a.post_b, 0, at, d, 0.0f), at, d, b);
+            unpack_settled<T, R, N>(par_piece<T, R>(a.post_b, 0, at, d, 0.0f), at, d, b);
 #pragma unroll
           for (int i = 0; i < N; ++i) o[i] = D[p][i] * (BIAS ? fmaf(y[i], w[i], b[i]) : y[i] * w[i]);
           if constexpr (GATE == RUN) {
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           } else if (a.dgate) {
 #pragma unroll
             for (int i = 0; i < N; ++i) o[i] *= a.branch;
-            store_piece<T, CUT>(static_cast<T*>(a.dgate) + group * d, at, d, PieceOf<T>::pack(o));
+            store_piece<T, R>(static_cast<T*>(a.dgate) + group * d, at, d, PieceOf<T>::pack(o));
           }
           // e / branch = g D, which D becomes
 #pragma unroll
@@ -494,7 +494,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
         PieceOf<T>::unpack(yr[p], y);
 #pragma unroll
         for (int i = 0; i < N; ++i) y[i] = fmaf(st[1], D[p][i], -fmaf(y[i], k1, k0));
-        store_piece<T, CUT>(static_cast<T*>(a.dy) + off, at, d, PieceOf<T>::pack(y));
+        store_piece<T, R>(static_cast<T*>(a.dy) + off, at, d, PieceOf<T>::pack(y));
       }
     }
     if constexpr (GATE == TOKEN) ++group;
@@ -508,7 +508,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
 #pragma unroll
           for (int i = 0; i < N; ++i) o[i] = a.branch * s_gate.v[p][i];
           if (a.dgate)
-            store_piece<T, CUT>(static_cast<T*>(a.dgate) + group * d, at, d, PieceOf<T>::pack(o));
+            store_piece<T, R>(static_cast<T*>(a.dgate) + group * d, at, d, PieceOf<T>::pack(o));
         }
         s_gate.clear(nullptr);
         ++group;
@@ -727,11 +727,13 @@ int check_sizes(int64_t rows, int64_t d, int64_t gates, int post, int pre, int d
   return MONARCH_OK;
 }
 
-// Whether rows end inside a piece (then they start off 16-byte boundaries too).
-bool cut_rows(int64_t d, bool bf16) { return d % (bf16 ? 8 : 4) != 0; }
+Rows rows_of(int64_t d, bool bf16) {
+  const int n = bf16 ? 8 : 4;
+  return d % n == 0 ? WHOLE : d > n ? CUT : SHORT;
+}
 
 template <typename T, int TEAM, int P>
-void fwd_launch(const SandwichFwd& a, bool cut, hipStream_t s) {
+void fwd_launch(const SandwichFwd& a, Rows lie, hipStream_t s) {
   constexpr int WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
   // one row a team, or the workgroups that fit the chip at once where they load
   // ahead; 2^20 workgroups are fewer than 2^32 threads
@@ -739,34 +741,45 @@ void fwd_launch(const SandwichFwd& a, bool cut, hipStream_t s) {
   int64_t grid = (a.rows + TEAMS - 1) / TEAMS;
   if (grid > most) grid = most;
   const dim3 g(static_cast<unsigned>(grid)), block(WG);
-  if (cut)
-    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true, true>), g, block, 0, s, a);
-  else if (a.post_b || a.pre_b)
-    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true, false>), g, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, false, false>), g, block, 0, s, a);
+  if (lie == CUT) {
+    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true, CUT>), g, block, 0, s, a);
+  } else if (lie == SHORT) {
+    if constexpr (TEAM == 16 && P == 1)
+      hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true, SHORT>), g, block, 0, s, a);
+  } else if (a.post_b || a.pre_b) {
+    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true, WHOLE>), g, block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, false, WHOLE>), g, block, 0, s, a);
+  }
 }
 
 template <typename T, int TEAM, int P>
-void bwd_launch(const SandwichBwd& a, const BwdPlan& p, bool cut, hipStream_t s) {
+void bwd_launch(const SandwichBwd& a, const BwdPlan& p, Rows lie, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.chunks)), block(TEAM > 64 ? TEAM : 256);
-#define BWD_GO(GATE, BIAS, CUT) \
-  hipLaunchKernelGGL((sandwich_bwd_kernel<T, TEAM, P, GATE, BIAS, CUT>), grid, block, 0, s, a)
+#define BWD_GO(GATE, BIAS, ROWS) \
+  hipLaunchKernelGGL((sandwich_bwd_kernel<T, TEAM, P, GATE, BIAS, ROWS>), grid, block, 0, s, a)
   // odd widths take the kernels that hold for any gate run and any bias
-  if (cut) {
+  if (lie == CUT) {
     if (p.gate == CHUNK)
-      BWD_GO(CHUNK, true, true);
+      BWD_GO(CHUNK, true, CUT);
     else
-      BWD_GO(RUN, true, true);
-    return;
-  }
-  switch (p.gate * 2 + (p.bias ? 1 : 0)) {
-    case CHUNK * 2: BWD_GO(CHUNK, false, false); break;
-    case CHUNK * 2 + 1: BWD_GO(CHUNK, true, false); break;
-    case RUN * 2: BWD_GO(RUN, false, false); break;
-    case RUN * 2 + 1: BWD_GO(RUN, true, false); break;
-    case TOKEN * 2: BWD_GO(TOKEN, false, false); break;
-    default: BWD_GO(TOKEN, true, false); break;
+      BWD_GO(RUN, true, CUT);
+  } else if (lie == SHORT) {
+    if constexpr (TEAM == 32 && P == 1) {
+      if (p.gate == CHUNK)
+        BWD_GO(CHUNK, true, SHORT);
+      else
+        BWD_GO(RUN, true, SHORT);
+    }
+  } else {
+    switch (p.gate * 2 + (p.bias ? 1 : 0)) {
+      case CHUNK * 2: BWD_GO(CHUNK, false, WHOLE); break;
+      case CHUNK * 2 + 1: BWD_GO(CHUNK, true, WHOLE); break;
+      case RUN * 2: BWD_GO(RUN, false, WHOLE); break;
+      case RUN * 2 + 1: BWD_GO(RUN, true, WHOLE); break;
+      case TOKEN * 2: BWD_GO(TOKEN, false, WHOLE); break;
+      default: BWD_GO(TOKEN, true, WHOLE); break;
+    }
   }
 #undef BWD_GO
 }
@@ -777,8 +790,8 @@ void bwd_launch(const SandwichBwd& a, const BwdPlan& p, bool cut, hipStream_t s)
 // The pairs (team, pieces) that fwd_shape and bwd_shape give.
 hipError_t launch_fwd(const SandwichFwd& a, bool bf16, hipStream_t s) {
   const Shape sh = fwd_shape(a.d, bf16);
-  const bool cut = cut_rows(a.d, bf16);
-#define FWD(T, TEAM, P) fwd_launch<T, TEAM, P>(a, cut, s)
+  const Rows lie = rows_of(a.d, bf16);
+#define FWD(T, TEAM, P) fwd_launch<T, TEAM, P>(a, lie, s)
   if (bf16) {
     switch (sh.team * 8 + sh.pieces) {
       TEAM_CASE(FWD, uint16_t, 16, 1)
@@ -820,8 +833,8 @@ hipError_t launch_fwd(const SandwichFwd& a, bool bf16, hipStream_t s) {
 }
 
 hipError_t launch_bwd(const SandwichBwd& a, const BwdPlan& p, bool bf16, hipStream_t s) {
-  const bool cut = cut_rows(a.d, bf16);
-#define BWD(T, TEAM, P) bwd_launch<T, TEAM, P>(a, p, cut, s)
+  const Rows lie = rows_of(a.d, bf16);
+#define BWD(T, TEAM, P) bwd_launch<T, TEAM, P>(a, p, lie, s)
   if (bf16) {
     switch (p.shape.team * 8 + p.shape.pieces) {
       TEAM_CASE(BWD, uint16_t, 32, 1)

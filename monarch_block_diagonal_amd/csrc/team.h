@@ -57,40 +57,43 @@ __device__ __forceinline__ void drop_first(u32x4& r) {
   }
 }
 
-// Elements [at, at + N) of a row of d elements. Without CUT, d is a multiple of N:
-// pieces are whole and aligned, and one past the row is 0. With CUT, rows start
-// and end anywhere: a piece that does not end with the row or before it is
-// loaded as the row's last N elements, so that every load is one access that
-// nothing waits for; settle() then moves them into place.
-template <typename T, bool CUT>
+// How the rows of d elements lie in pieces of N. WHOLE: d is a multiple of N, so
+// that pieces are whole and aligned. CUT: rows start and end anywhere, d >= N.
+// SHORT: d < N.
+enum Rows { WHOLE = 0, CUT = 1, SHORT = 2 };
+
+// Elements [at, at + N) of a row of d elements. A piece past a WHOLE row is 0. A
+// piece that a CUT row's end cuts, or that lies past it, is loaded as the row's
+// last N elements, so that every load is one access that nothing waits for, and
+// settle() moves it into place. A SHORT row is loaded an element at a time, as its
+// last N elements too.
+template <typename T, Rows R>
 __device__ __forceinline__ u32x4 load_piece(const T* row, int at, int d) {
   constexpr int N = PieceOf<T>::N;
-  u32x4 r = {0, 0, 0, 0};
-  if constexpr (!CUT) {
+  if constexpr (R == WHOLE) {
+    u32x4 r = {0, 0, 0, 0};
     if (at < d) r = *reinterpret_cast<const u32x4*>(row + at);
     return r;
-  }
-  if (d >= N) return *reinterpret_cast<const typename PieceOf<T>::Raw*>(row + min(at, d - N));
+  } else if constexpr (R == CUT) {
+    return *reinterpret_cast<const typename PieceOf<T>::Raw*>(row + min(at, d - N));
+  } else {
+    u32x4 r = {0, 0, 0, 0};
 #pragma unroll 1
-  for (int i = 0; i < d; ++i) {   // a row shorter than a piece: as its last N elements too
-    uint32_t v;
-    if constexpr (N == 4)
-      v = __float_as_uint(row[i]);
-    else
-      v = row[i];
-    drop_first<N>(r);
-    if constexpr (N == 4)
-      r[3] = v;
-    else
-      r[3] |= v << 16;
+    for (int i = 0; i < d; ++i) {
+      drop_first<N>(r);
+      if constexpr (N == 4)
+        r[3] = __float_as_uint(row[i]);
+      else
+        r[3] |= static_cast<uint32_t>(row[i]) << 16;
+    }
+    return r;
   }
-  return r;
 }
 
-// Moves what load_piece loaded with CUT into place: elements past the row are 0.
-template <bool CUT, int N>
+// Moves what load_piece loaded into place: elements past the row are 0.
+template <Rows R, int N>
 __device__ __forceinline__ void settle(u32x4& r, int at, int d) {
-  if constexpr (CUT) {
+  if constexpr (R != WHOLE) {
     const int s = at + N - d;   // elements past the row
     if (s > 0) {
       if (s >= N) {
@@ -107,10 +110,10 @@ __device__ __forceinline__ void settle(u32x4& r, int at, int d) {
   }
 }
 
-template <typename T, bool CUT>
+template <typename T, Rows R>
 __device__ __forceinline__ void store_piece(T* row, int at, int d, u32x4 r) {
   constexpr int N = PieceOf<T>::N;
-  if constexpr (!CUT) {
+  if constexpr (R == WHOLE) {
     if (at < d) *reinterpret_cast<u32x4*>(row + at) = r;
     return;
   }
