@@ -43,21 +43,12 @@ struct SandwichFwd {
 };
 
 // A piece of an optional row (weights, biases, a gate row): without one, ones or
-// zeros, so that the arithmetic is the same. To be settled as any piece.
+// zeros, so that the arithmetic is the same.
 template <typename T, Rows R>
 __device__ __forceinline__ u32x4 par_piece(const void* p, int64_t off, int at, int d, float fill) {
   if (p) return load_piece<T, R>(static_cast<const T*>(p) + off, at, d);
   const uint32_t w = sizeof(T) == 2 ? (__float_as_uint(fill) >> 16) * 0x10001u : __float_as_uint(fill);
   return u32x4{w, w, w, w};
-}
-
-// The elements of a piece at `at` that lie past the row, set to 0.
-template <Rows R, int N>
-__device__ __forceinline__ void zero_past(float (&v)[N], int at, int d) {
-  if (at + (R == WHOLE ? 0 : N - 1) >= d)
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (R == WHOLE || at + i >= d) v[i] = 0.0f;
 }
 
 // mean and 1/sqrt(mean square about it + eps) of the team's row (zero past d)
@@ -78,7 +69,7 @@ __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][
       float c[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) c[i] = v[p][i] - mu;
-      zero_past<R, N>(c, (p * TEAM + lane) * N, d);
+      mask<R, N>(c, (p * TEAM + lane) * N, d);
 #pragma unroll
       for (int i = 0; i < N; ++i) q = fmaf(c[i], c[i], q);
     }
@@ -89,12 +80,6 @@ __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][
       for (int i = 0; i < N; ++i) q = fmaf(v[p][i], v[p][i], q);
   }
   rho = 1.0f / sqrtf(team.sum(q) / static_cast<float>(d) + eps);
-}
-
-template <typename T, Rows R, int N>
-__device__ __forceinline__ void unpack_settled(u32x4 r, int at, int d, float (&v)[N]) {
-  settle<R, N>(r, at, d);
-  PieceOf<T>::unpack(r, v);
 }
 
 // One row a team. A team of 1024 threads leaves room for one workgroup a CU: it
@@ -130,8 +115,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 
       if (a.post != MONARCH_NORM_NONE) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          settle<R, N>(yr[p], (p * TEAM + lane) * N, d);
           PieceOf<T>::unpack(yr[p], v[p]);
+          if constexpr (R != WHOLE) mask<R, N>(v[p], (p * TEAM + lane) * N, d);
         }
         row_stats<R, TEAM, P, N>(team, v, lane, d, a.post, a.eps, mu_y, rho_y);
       }
@@ -143,13 +128,12 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 
         const int at = (p * TEAM + lane) * N;
         float w[N], b[N], g[N], t[N];
         forget(yr[p]);
-        if (a.post == MONARCH_NORM_NONE) settle<R, N>(yr[p], at, d);
         PieceOf<T>::unpack(yr[p], v[p]);
-        unpack_settled<T, R, N>(par_piece<T, R>(a.post_w, 0, at, d, 1.0f), at, d, w);
+        PieceOf<T>::unpack(par_piece<T, R>(a.post_w, 0, at, d, 1.0f), w);
         if constexpr (BIAS)
-          unpack_settled<T, R, N>(par_piece<T, R>(a.post_b, 0, at, d, 0.0f), at, d, b);
-        unpack_settled<T, R, N>(par_piece<T, R>(a.gate, goff, at, d, 1.0f), at, d, g);
-        unpack_settled<T, R, N>(hr[p], at, d, t);
+          PieceOf<T>::unpack(par_piece<T, R>(a.post_b, 0, at, d, 0.0f), b);
+        PieceOf<T>::unpack(par_piece<T, R>(a.gate, goff, at, d, 1.0f), g);
+        PieceOf<T>::unpack(hr[p], t);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           float u = fmaf(v[p][i], scale, -mean) * w[i];
@@ -157,11 +141,14 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 
           v[p][i] = fmaf(a.skip, t[i], g[i] * u);
         }
         store_piece<T, R>(static_cast<T*>(a.h_out) + off, at, d, PieceOf<T>::pack(v[p]));
-        zero_past<R, N>(v[p], at, d);
+        mask<R, N>(v[p], at, d);
       }
     } else {
 #pragma unroll
-      for (int p = 0; p < P; ++p) unpack_settled<T, R, N>(hr[p], (p * TEAM + lane) * N, d, v[p]);
+      for (int p = 0; p < P; ++p) {
+        PieceOf<T>::unpack(hr[p], v[p]);
+        if constexpr (R != WHOLE) mask<R, N>(v[p], (p * TEAM + lane) * N, d);
+      }
     }
     if (AHEAD && row + step < a.rows) load(row + step);
     if (a.pre != MONARCH_NORM_NONE) {
@@ -171,9 +158,9 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
         float w[N], b[N];
-        unpack_settled<T, R, N>(par_piece<T, R>(a.pre_w, 0, at, d, 1.0f), at, d, w);
+        PieceOf<T>::unpack(par_piece<T, R>(a.pre_w, 0, at, d, 1.0f), w);
         if constexpr (BIAS)
-          unpack_settled<T, R, N>(par_piece<T, R>(a.pre_b, 0, at, d, 0.0f), at, d, b);
+          PieceOf<T>::unpack(par_piece<T, R>(a.pre_b, 0, at, d, 0.0f), b);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           v[p][i] = fmaf(v[p][i], rho_h, -mean_h) * w[i];
@@ -290,7 +277,6 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
       pre_wr[p] = par_piece<T, R>(a.pre_w, 0, at, d, 1.0f);
-      settle<R, N>(pre_wr[p], at, d);
     }
   };
   auto load_post_pars = [&]() {
@@ -299,10 +285,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
       post_wr[p] = par_piece<T, R>(a.post_w, 0, at, d, 1.0f);
-      settle<R, N>(post_wr[p], at, d);
       if constexpr (GATE == CHUNK) {
         gr[p] = par_piece<T, R>(a.gate, group * d, at, d, 1.0f);
-        settle<R, N>(gr[p], at, d);
       }
     }
   };
@@ -374,9 +358,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           float dn[N], h[N], w[N];
-          settle<R, N>(dnr[p], (p * TEAM + lane) * N, d);
-          settle<R, N>(hr[p], (p * TEAM + lane) * N, d);
           PieceOf<T>::unpack(dnr[p], dn);
+          if constexpr (R != WHOLE) mask<R, N>(dn, (p * TEAM + lane) * N, d);
           PieceOf<T>::unpack(hr[p], h);
           if constexpr (BIAS) s_preb.add(p, dn);
           forget(pre_wr[p]);
@@ -404,18 +387,20 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           forget(pre_wr[p]);
           PieceOf<T>::unpack(dnr[p], dn);
           PieceOf<T>::unpack(hr[p], h);
-          unpack_settled<T, R, N>(dhr[p], at, d, D[p]);
+          PieceOf<T>::unpack(dhr[p], D[p]);
           PieceOf<T>::unpack(pre_wr[p], w);
 #pragma unroll
           for (int i = 0; i < N; ++i)
             D[p][i] += fmaf(st[3] * dn[i], w[i], -fmaf(h[i], k1, k0));
-          zero_past<R, N>(D[p], at, d);
+          mask<R, N>(D[p], at, d);
         }
       } else {
         if constexpr (REREAD) load_rest();
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-          unpack_settled<T, R, N>(dhr[p], (p * TEAM + lane) * N, d, D[p]);
+        for (int p = 0; p < P; ++p) {
+          PieceOf<T>::unpack(dhr[p], D[p]);
+          if constexpr (R != WHOLE) mask<R, N>(D[p], (p * TEAM + lane) * N, d);
+        }
       }
     }
     if constexpr (LATE) load_y();
@@ -438,8 +423,6 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
         float y[N], w[N], g[N], o[N];
-        settle<R, N>(yr[p], at, d);
-        if constexpr (GATE != CHUNK) settle<R, N>(gr[p], at, d);
         PieceOf<T>::unpack(yr[p], y);
         forget(post_wr[p]);
         forget(gr[p]);
@@ -451,7 +434,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           // dgate = branch D u
           float b[N];
           if constexpr (BIAS)
-            unpack_settled<T, R, N>(par_piece<T, R>(a.post_b, 0, at, d, 0.0f), at, d, b);
+            PieceOf<T>::unpack(par_piece<T, R>(a.post_b, 0, at, d, 0.0f), b);
 #pragma unroll
           for (int i = 0; i < N; ++i) o[i] = D[p][i] * (BIAS ? fmaf(y[i], w[i], b[i]) : y[i] * w[i]);
           if constexpr (GATE == RUN) {
@@ -515,41 +498,41 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
       }
     }
   }
-  // this chunk's sums: the teams' are added in team order
+  // this chunk's sums: the teams' are added in team order. `shift` is how far a
+  // piece is moved back to end with its row (load_piece).
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.sums * a.d;
+  auto shift = [&](int at) { return R == WHOLE ? 0 : max(at + N - a.d, 0); };
   auto put = [&](int which, const auto& s) {
     if (which < 0) return;
     float* out = part + static_cast<int64_t>(which) * a.d;
     if constexpr (std::is_same<decltype(s), const Sums<WG, P, N, true>&>::value) {
       __syncthreads();
       for (int at = threadIdx.x; at < a.d; at += WG) {
-        const int p = at / (TEAM * N), l = at / N % TEAM, i = at % N;
+        const int p = at / (TEAM * N), l = at / N % TEAM, i = at % N + shift(at / N * N);
         float t = s.at(p, i, l);
 #pragma unroll
         for (int k = 1; k < TEAMS; ++k) t += s.at(p, i, k * TEAM + l);
         out[at] = t;
       }
-    } else if constexpr (TEAMS == 1) {
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int at = (p * TEAM + lane) * N + i;
-          if (at < a.d) out[at] = s.v[p][i];
-        }
     } else {
-      float* join = reinterpret_cast<float*>(shared);
-      __syncthreads();
+      float* to = TEAMS == 1 ? out : reinterpret_cast<float*>(shared) + tm * COLS;
+      if constexpr (TEAMS > 1) __syncthreads();
 #pragma unroll
-      for (int p = 0; p < P; ++p)
+      for (int p = 0; p < P; ++p) {
+        const int at = (p * TEAM + lane) * N, back = shift(at);
 #pragma unroll
-        for (int i = 0; i < N; ++i) join[tm * COLS + (p * TEAM + lane) * N + i] = s.v[p][i];
-      __syncthreads();
-      for (int at = threadIdx.x; at < a.d; at += WG) {
-        float t = join[at];
+        for (int i = 0; i < N; ++i)
+          if (at < a.d && i >= back) to[at - back + i] = s.v[p][i];
+      }
+      if constexpr (TEAMS > 1) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.d; c += WG) {
+          const float* from = reinterpret_cast<const float*>(shared) + c;
+          float t = from[0];
 #pragma unroll
-        for (int k = 1; k < TEAMS; ++k) t += join[k * COLS + at];
-        out[at] = t;
+          for (int k = 1; k < TEAMS; ++k) t += from[k * COLS];
+          out[c] = t;
+        }
       }
     }
   };

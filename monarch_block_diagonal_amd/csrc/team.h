@@ -63,10 +63,11 @@ __device__ __forceinline__ void drop_first(u32x4& r) {
 enum Rows { WHOLE = 0, CUT = 1, SHORT = 2 };
 
 // Elements [at, at + N) of a row of d elements. A piece past a WHOLE row is 0. A
-// piece that a CUT row's end cuts, or that lies past it, is loaded as the row's
-// last N elements, so that every load is one access that nothing waits for, and
-// settle() moves it into place. A SHORT row is loaded an element at a time, as its
-// last N elements too.
+// piece that a CUT row's end cuts, or that lies past it, is the row's last N
+// elements instead, so that every load is one access that nothing waits for: its
+// first at + N - d elements belong to the piece before and do not count (mask()
+// sets them to 0, store_piece() leaves them out). A SHORT row is loaded an element
+// at a time, as its last N elements too.
 template <typename T, Rows R>
 __device__ __forceinline__ u32x4 load_piece(const T* row, int at, int d) {
   constexpr int N = PieceOf<T>::N;
@@ -90,23 +91,18 @@ __device__ __forceinline__ u32x4 load_piece(const T* row, int at, int d) {
   }
 }
 
-// Moves what load_piece loaded into place: elements past the row are 0.
+// Sets the values of a piece that do not count to 0.
 template <Rows R, int N>
-__device__ __forceinline__ void settle(u32x4& r, int at, int d) {
-  if constexpr (R != WHOLE) {
-    const int s = at + N - d;   // elements past the row
-    if (s > 0) {
-      if (s >= N) {
-        r = u32x4{0, 0, 0, 0};
-      } else if constexpr (N == 4) {
-        if (s & 2) r = u32x4{r[2], r[3], 0u, 0u};
-        if (s & 1) drop_first<N>(r);
-      } else {
-        if (s & 4) r = u32x4{r[2], r[3], 0u, 0u};
-        if (s & 2) r = u32x4{r[1], r[2], r[3], 0u};
-        if (s & 1) drop_first<N>(r);
-      }
-    }
+__device__ __forceinline__ void mask(float (&v)[N], int at, int d) {
+  if constexpr (R == WHOLE) {
+    if (at >= d)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.0f;
+  } else {
+    const int s = at + N - d;
+    if (s > 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = i < s ? 0.0f : v[i];
   }
 }
 
@@ -121,8 +117,13 @@ __device__ __forceinline__ void store_piece(T* row, int at, int d, u32x4 r) {
     *reinterpret_cast<typename PieceOf<T>::Raw*>(row + at) = r;
     return;
   }
+  if (at >= d) return;
 #pragma unroll 1
-  for (int i = at; i < d; ++i) {
+  for (int i = d - N; i < d; ++i) {
+    if (i < at) {
+      drop_first<N>(r);
+      continue;
+    }
     if constexpr (N == 4)
       row[i] = __uint_as_float(r[0]);
     else
