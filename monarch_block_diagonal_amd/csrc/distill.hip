@@ -279,7 +279,8 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
         u32x4 o = PieceOf<T>::pack(v);
         if (nothing) o = u32x4{0, 0, 0, 0};
         if (mine)
-          reinterpret_cast<typename PieceOf<T>::Raw*>(dbody + static_cast<int64_t>(first) * N)[lane] = o;
+          __builtin_nontemporal_store(
+              o, reinterpret_cast<typename PieceOf<T>::Raw*>(dbody + static_cast<int64_t>(first) * N) + lane);
       };
 #pragma unroll
       for (int p = 0; p < P; ++p)

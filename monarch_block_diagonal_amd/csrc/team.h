@@ -106,15 +106,18 @@ __device__ __forceinline__ void mask(float (&v)[N], int at, int d) {
   }
 }
 
+// Rows are stored past the caches (they are too many to be read back from them,
+// and the lines they would take are those of tensors still to be read): 16384 x
+// 768 bf16 forward 20.7 -> 18.7 us.
 template <typename T, Rows R>
 __device__ __forceinline__ void store_piece(T* row, int at, int d, u32x4 r) {
   constexpr int N = PieceOf<T>::N;
   if constexpr (R == WHOLE) {
-    if (at < d) *reinterpret_cast<u32x4*>(row + at) = r;
+    if (at < d) __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(row + at));
     return;
   }
   if (at + N <= d) {
-    *reinterpret_cast<typename PieceOf<T>::Raw*>(row + at) = r;
+    __builtin_nontemporal_store(r, reinterpret_cast<typename PieceOf<T>::Raw*>(row + at));
     return;
   }
   if (at >= d) return;
