@@ -586,18 +586,18 @@ __global__ __launch_bounds__(JC* JS) void sandwich_join_kernel(SandwichJoin a) {
   float s = 0.0f, s2 = 0.0f;
   if (at < a.d) {
     const int64_t stride = static_cast<int64_t>(a.sums) * a.d;
-    auto sum = [&](int w) {
-      const float* p = a.part + static_cast<int64_t>(w) * a.d + at;
-      float t = 0.0f;
+    const float* p = a.part + static_cast<int64_t>(which) * a.d + at;
+    const float* p2 = a.part + static_cast<int64_t>(which2 < 0 ? which : which2) * a.d + at;
+    if (which2 >= 0) {
 #pragma unroll 8
-      for (int c = b; c < e; ++c) t += p[c * stride];
-      return t;
-    };
-    if (!gated) {
-      s = sum(which);
-      if (which2 >= 0) s2 = sum(which2);
+      for (int c = b; c < e; ++c) {
+        s += p[c * stride];
+        s2 += p2[c * stride];
+      }
+    } else if (!gated) {
+#pragma unroll 8
+      for (int c = b; c < e; ++c) s += p[c * stride];
     } else {
-      const float* p = a.part + static_cast<int64_t>(which) * a.d + at;
       int c = b;
       while (c < e) {   // the chunks of one gate row at a time
         const int g = c / a.cpg, end = min(e, (g + 1) * a.cpg);
