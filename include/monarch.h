@@ -383,7 +383,7 @@ int monarch_sandwich_describe(int direction, int64_t rows, int64_t features, int
  *   logits [rows, ld]: row i's vocab logits start at i*ld (ld >= vocab, in
  *   elements); fp32 or bf16 (`dtype`), aligned to their element size only.
  *   dlogits likewise with dld; columns past vocab are neither read nor written.
- *   teacher fp32 [rows, top] and ids int64 [rows, top], top <=
+ *   vocab <= 2^30. teacher fp32 [rows, top] and ids int64 [rows, top], top <=
  *   MONARCH_DISTILL_MAX_TOP; labels int64 [rows] or NULL; loss fp32 [rows].
  * 1e-6 <= temperature <= 1e6 and 0 <= mix <= 1, or MONARCH_ERR_VALUE. Sums are
  * fp32, dlogits is rounded once. rows == 0 returns MONARCH_OK.

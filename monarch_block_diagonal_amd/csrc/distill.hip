@@ -339,7 +339,8 @@ __global__ __launch_bounds__(TEAM, 4) void distill_kernel(Distill a) {
 
 int check_sizes(int64_t rows, int64_t vocab, int64_t ld, int64_t top, int dtype) {
   if (dtype != MONARCH_F32 && dtype != MONARCH_BF16) return MONARCH_ERR_DTYPE;
-  if (rows < 0 || rows >= kLimit || vocab <= 0 || vocab >= kLimit || ld < vocab || top < 0 ||
+  // columns are counted in 32 bits, up to a workgroup past the row
+  if (rows < 0 || rows >= kLimit || vocab <= 0 || vocab > kLimit / 2 || ld < vocab || top < 0 ||
       top > MONARCH_DISTILL_MAX_TOP)
     return MONARCH_ERR_SHAPE;
   return MONARCH_OK;
@@ -363,8 +364,9 @@ hipError_t launch_second(const Distill& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The smallest workgroup whose registers hold the row, 4 or 16 pieces a thread. A gradient alone streams the row once, and needs no more than enough
-// threads.
+// The smallest workgroup whose registers hold the row, 4 or 16 pieces a thread
+// (1000 x 10000 fp32 step: 256 threads x 16 24 us, 512 x 8 32 us, 1024 x 4 58 us). A
+// gradient alone streams the row once, and needs no more than enough threads.
 template <typename T, int WHAT>
 hipError_t launch_sized(const Distill& a, hipStream_t s) {
   const int pieces = a.vocab / PieceOf<T>::N;

@@ -177,8 +177,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 
 
 // How the rows of a backward call are cut (GATE). CHUNK: chunk c holds rows of one
 // gate row only (chunk / cpg), and its sums are of D alone; the gate and the
-// branch scale are applied when the chunks are joined. RUN: many short gate runs;
-// each is summed by one team, which stores its dgate row itself, and the
+// branch scale are applied when the chunks are joined. RUN: short gate runs, or
+// many; each is summed by one team, which stores its dgate row itself, and the
 // chunk's sums are of g * D. TOKEN: RUN with one row a run.
 enum { CHUNK = 0, RUN = 1, TOKEN = 2 };
 
@@ -668,12 +668,14 @@ BwdPlan bwd_plan(int64_t rows, int64_t d, int64_t gates, bool has_y, bool post_b
   p.shape = bwd_shape(d, bf16);
   p.bias = post_bias || pre_bias;
   p.rows_per_gate = gates > 0 ? rows / gates : rows;
-  p.gate = rows == 0 || gates <= 1 || p.rows_per_gate > kRunRows ? CHUNK
-           : p.rows_per_gate > 1                                   ? RUN
-                                                                   : TOKEN;
   const int teams = p.shape.team > 64 ? 1 : 256 / p.shape.team;
   // workgroups aimed at: two a CU, one where the sums of a wide row take its LDS
   const int64_t aim = kCus * (p.shape.team * p.shape.pieces * (bf16 ? 8 : 4) > 8192 ? 1 : 2);
+  // a gate run is a team's own where it is short, or where there are enough of them
+  // for every team; one run cut into chunks is joined by as many workgroups
+  p.gate = rows == 0 || gates <= 1 || (p.rows_per_gate > kRunRows && gates < aim * teams) ? CHUNK
+           : p.rows_per_gate > 1 ? RUN
+                                 : TOKEN;
   if (rows == 0) {
     p.cpg = 0;   // no chunk: every sum is empty
   } else if (p.gate != CHUNK) {
@@ -857,8 +859,7 @@ hipError_t launch_bwd(const SandwichBwd& a, const BwdPlan& p, bool bf16, hipStre
 #undef TEAM_CASE
 
 hipError_t launch_join(const SandwichJoin& a, int64_t jobs, bool bf16, hipStream_t s) {
-  // jobs < 2^21 at 1024 threads stay below 2^32 threads a launch: gate rows
-  // summed here have more than kRunRows rows each, columns are at most 16384
+  // gate rows that are joined here are fewer than the teams of a launch (bwd_plan)
   const dim3 grid(static_cast<unsigned>(jobs), static_cast<unsigned>((a.d + JC - 1) / JC));
   if (bf16)
     hipLaunchKernelGGL((sandwich_join_kernel<uint16_t>), grid, dim3(JC * JS), 0, s, a);

@@ -396,6 +396,14 @@ def _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias, p
     return rows, d, gates, device
 
 
+def _on_stream(stream, call, *args, **kw):
+    """call(*args, **kw) on a stream of the caller's: results and workspaces come
+    from that stream's memory, so that none is handed out again before its work is done."""
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                           else torch.cuda.ExternalStream(stream)):
+        return call(*args, **kw)
+
+
 # a function of the sizes alone: asked for once for each of them
 _sandwich_workspace = functools.lru_cache(maxsize=256)(B.monarch_sandwich_bwd_workspace_bytes)
 
@@ -412,6 +420,10 @@ def sandwich_forward(h, y=None, post_weight=None, post_bias=None, gate=None, pre
     gate [gates, features] holds one row for rows/gates consecutive rows. Without
     y, h_out is h itself (the norm before the first block); with pre_norm
     NORM_NONE, n is None. stats [rows, 4] goes to sandwich_backward."""
+    if stream is not None:
+        return _on_stream(stream, sandwich_forward, h, y, post_weight, post_bias, gate,
+                          pre_weight, pre_bias, post_norm=post_norm, pre_norm=pre_norm,
+                          skip_scale=skip_scale, branch_scale=branch_scale, eps=eps)
     rows, d, gates, _ = _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias,
                                          pre_norm, skip_scale)
     h_out = torch.empty_like(h) if y is not None else h
@@ -419,7 +431,7 @@ def sandwich_forward(h, y=None, post_weight=None, post_bias=None, gate=None, pre
     stats = torch.empty((rows, 4), dtype=torch.float32, device=h.device)
     B.monarch_sandwich_fwd(h, y, post_weight, post_bias, gate, pre_weight, pre_bias,
                            h_out if y is not None else None, n, stats, rows, d, gates, post_norm,
-                           pre_norm, skip_scale, branch_scale, eps, dtype_code(h), stream)
+                           pre_norm, skip_scale, branch_scale, eps, dtype_code(h))
     return h_out, n, stats
 
 
@@ -430,6 +442,10 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
     """SandwichGrads from the gradients dh_out (None: zero) and dn of the
     forward's results. h_out and stats are the forward's (eps is in stats; it is
     accepted so that both calls take the same keywords)."""
+    if stream is not None:
+        return _on_stream(stream, sandwich_backward, dh_out, dn, h_out, y, stats, post_weight,
+                          post_bias, gate, pre_weight, pre_bias, post_norm=post_norm,
+                          pre_norm=pre_norm, skip_scale=skip_scale, branch_scale=branch_scale)
     if pre_norm != B.NORM_NONE and (dn is None or h_out is None):
         raise ValueError("the backward of a pre_norm needs dn and h_out")
     if pre_norm == B.NORM_NONE and dh_out is None:
@@ -448,7 +464,7 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
     B.monarch_sandwich_bwd(dh_out, dn, h_out, y, stats, post_weight, post_bias, gate, pre_weight,
                            pre_bias, g.dh, g.dy, g.dpost_weight, g.dpost_bias, g.dgate,
                            g.dpre_weight, g.dpre_bias, ws, need, rows, d, gates, post_norm,
-                           pre_norm, skip_scale, branch_scale, code, stream)
+                           pre_norm, skip_scale, branch_scale, code)
     return g
 
 
@@ -557,22 +573,28 @@ def distill_forward(logits, teacher, ids, labels=None, *, temperature: float = 1
     p = softmax(teacher / temperature) over the row's entries, which sit at the
     columns `ids` (int64; -1 pads). labels (int64) outside the vocabulary are ignored.
     stats goes to distill_backward."""
+    if stream is not None:
+        return _on_stream(stream, distill_forward, logits, teacher, ids, labels,
+                          temperature=temperature, mix=mix)
     rows, vocab, top, ld, _ = _distill_shapes(logits, teacher, ids, labels, None, "")
     loss = torch.empty((rows,), dtype=torch.float32, device=logits.device)
     stats = torch.empty((rows, 4), dtype=torch.float32, device=logits.device)
     B.monarch_distill_fwd(logits, ld, teacher, ids, labels, loss, stats, rows, vocab, top,
-                          temperature, mix, dtype_code(logits), stream)
+                          temperature, mix, dtype_code(logits))
     return loss, stats
 
 
 def distill_backward(dloss, logits, teacher, ids, labels, stats, *, temperature: float = 1.0,
                      mix: float = 1.0, out=None, stream=None):
     """dlogits for dloss [rows]; out may be logits itself."""
+    if stream is not None:
+        return _on_stream(stream, distill_backward, dloss, logits, teacher, ids, labels, stats,
+                          temperature=temperature, mix=mix, out=out)
     rows, vocab, top, ld, device = _distill_shapes(logits, teacher, ids, labels, dloss, "dloss")
     _saved(stats, rows, device)
     dz, dld = _distill_out(logits, rows, vocab, ld, device, out)
     B.monarch_distill_bwd(dloss, logits, ld, teacher, ids, labels, stats, dz, dld, rows, vocab, top,
-                          temperature, mix, dtype_code(logits), stream)
+                          temperature, mix, dtype_code(logits))
     return dz
 
 
@@ -581,12 +603,15 @@ def distill_step(logits, teacher, ids, labels=None, row_weight=None, *, temperat
     """(loss [rows], dlogits) in one pass: dlogits is the gradient of
     sum(row_weight * loss) (row_weight None: 1 for every row). out may be
     logits itself, which saves a tensor of their size."""
+    if stream is not None:
+        return _on_stream(stream, distill_step, logits, teacher, ids, labels, row_weight,
+                          temperature=temperature, mix=mix, out=out)
     rows, vocab, top, ld, device = _distill_shapes(logits, teacher, ids, labels, row_weight,
                                                    "row_weight")
     loss = torch.empty((rows,), dtype=torch.float32, device=logits.device)
     dz, dld = _distill_out(logits, rows, vocab, ld, device, out)
     B.monarch_distill_step(logits, ld, teacher, ids, labels, row_weight, loss, dz, dld, rows, vocab,
-                           top, temperature, mix, dtype_code(logits), stream)
+                           top, temperature, mix, dtype_code(logits))
     return loss, dz
 
 

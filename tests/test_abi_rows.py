@@ -79,6 +79,7 @@ def test_sandwich_workspace():
     assert M.monarch_sandwich_bwd_workspace_bytes(10000, 768, 0, True, B.BF16) == 2 * a
     # bounded by the number of chunks or gate rows, not by the rows
     assert M.monarch_sandwich_bwd_workspace_bytes(1 << 24, 768, 0, False, B.BF16) <= 512 * 2 * 768 * 4 + 256
+    assert M.monarch_sandwich_bwd_workspace_bytes(40 << 24, 8, 1 << 24, False, B.BF16) <= 8192 * 2 * 8 * 4 + 256
 
 
 def test_sandwich_no_rows_and_description():
@@ -107,7 +108,7 @@ KINDS = ("fwd", "bwd", "step")
 def test_distill_sizes_and_values(kind):
     for dt in (-1, 2):
         assert distill(kind, dt=dt) == B.MONARCH_ERR_DTYPE
-    for kw in (dict(rows=-1), dict(rows=1 << 31), dict(vocab=0), dict(vocab=1 << 31, ld=1 << 31), dict(ld=99), dict(top=-1),
+    for kw in (dict(rows=-1), dict(rows=1 << 31), dict(vocab=0), dict(vocab=1 << 31, ld=1 << 31), dict(vocab=(1 << 30) + 1, ld=1 << 31), dict(ld=99), dict(top=-1),
                dict(top=513)):
         assert distill(kind, **kw) == B.MONARCH_ERR_SHAPE, kw
     for kw in (dict(T=0.0), dict(T=-1.0), dict(T=float("nan")), dict(T=1e7), dict(T=1e-7), dict(mix=-0.5), dict(mix=1.1),

@@ -175,6 +175,15 @@ def test_gate_runs_longer_and_shorter_than_a_chunk(api):
         compare(api, rows, 72, gates, True, "f32", "rms", "rms")
 
 
+@pytest.mark.parametrize("bias", [False, True])
+def test_many_long_gate_runs(api, bias):
+    """More runs than a launch has teams are taken whole, whatever their length; fewer are cut."""
+    compare(api, 33 * 4096, 8, 4096, bias, "f32", "rms", "rms")
+    compare(api, 33 * 4095, 8, 4095, bias, "f32", "rms", "rms")
+    compare(api, 40 * 512, 1032, 512, bias, "bf16", "rms", "layer")
+    compare(api, 40 * 1024, 129, 1024, bias, "f32", "layer", "rms")
+
+
 def test_results_do_not_change_from_run_to_run(api):
     a, dh, dn = draw(5000, 768, 5, True, "bf16")
     D = {k: dev(v, "bf16") for k, v in a.items()}

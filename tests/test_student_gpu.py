@@ -121,6 +121,37 @@ def test_graph_replays_equal_eager(api):
             assert torch.equal(a, b), (k, i)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_calls_on_a_given_stream(api, raw):
+    """Work goes to the stream that is named, and its memory comes from there."""
+    rows, d, V = 4096, 768, 2000
+    torch.manual_seed(6)
+    h, y, w = torch.randn(rows, d, device="cuda"), torch.randn(rows, d, device="cuda"), torch.rand(d, device="cuda")
+    z, t = torch.randn(rows, V, device="cuda"), torch.randn(rows, 8, device="cuda")
+    ids = torch.randint(0, V, (rows, 8), device="cuda")
+
+    def step(**on):
+        h_out, n, stats = api.sandwich_forward(h, y, w, None, None, w, None, **on)
+        grads = api.sandwich_backward(h, y, h_out, y, stats, w, None, None, w, None, **on)
+        loss, dz = api.distill_step(z, t, ids, **on)
+        loss2, saved = api.distill_forward(z, t, ids, **on)
+        return [h_out, n, *[g for g in grads if g is not None], loss, dz, api.distill_backward(loss2, z, t, ids, None, saved, **on)]
+
+    want = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        slow = [torch.randn(2048, 2048, device="cuda") @ torch.randn(2048, 2048, device="cuda") for _ in range(8)]
+    got = step(stream=side.cuda_stream if raw else side)
+    # allocations of the current stream must not take what the side stream still writes
+    other = [torch.full((rows, d), float("nan"), device="cuda") for _ in range(16)]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert len(slow) + len(other) == 24
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), i
+
+
 def test_student_learns():
     from monarch_block_diagonal_amd.distill_student import train
     _, losses = train(steps=40, rows=1024)
