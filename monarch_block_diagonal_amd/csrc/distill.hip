@@ -16,6 +16,19 @@
 // before and 7 behind them, one for each of the first threads. Exponentials are
 // 2^((z - m) log2(e) / T) with m the row's maximum: z - m is exact or rounded once,
 // and rows of the type's lowest value (m huge) stay finite. Sums are fp32.
+//
+// Loss and gradient together read and write each logit once: bound by HBM while
+// every CU has many rows to take, by the phases of a row (load, about 20 operations a
+// logit, store) where it has few. Measured: loss of 4096 x 50257 bf16 at T = 2 with
+// labels 77 us, 5.3 TB/s (its arithmetic busy 86% of the time, but no slower than T =
+// 1, which has a tenth less); both of 16384 x 50257
+// bf16 586 us a call, 5.6 TB/s, as a copy; of 1024 x 50257 bf16 (4 rows a CU) 49 us,
+// 4.2 TB/s; of 1000 x 10000 fp32 26.7 us; of 2048 x 131072 fp32, which no CU holds, 480
+// us, 4.5 TB/s. Read twice instead of held, the second took 784 us and the last 718.
+// Kept out by measurement: workgroups that load their next row into the registers
+// that a gradient frees (621 -> 672 us: the waits at a row's start then cover its
+// stores), and 2^(z c - M) as one fused operation with a second path for rows far
+// from 0 (no gain).
 #include <math.h>
 
 #include "api_internal.h"
@@ -53,7 +66,8 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 enum Second {
   NONE = 0,     // no label term, or T = 1: one softmax
   OWN = 1,      // its own exponentials
-  SQUARE = 2    // T = 2: e^z = (e^(z/2))^2, one product in place of an exponential
+  SQUARE = 2    // T = 2, the usual one: e^z = (e^(z/2))^2, a product and no second
+                // exponential (4096 x 50257 bf16, loss: 88 us with OWN, 77 us; both: 184, 171)
 };
 
 // Maximum and sums of exponentials of one thread's share of a row. The maximum
