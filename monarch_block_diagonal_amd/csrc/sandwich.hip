@@ -1,654 +1,18 @@
-// Sandwich norm: the norm after a block, its gate, the scaled residual join
-// and the norm before the next block, forward and backward.
-//
-//   u  = norm_post(y) * w_post + b_post
-//   h' = skip * h + branch * g * u
-//   n  = norm_pre(h') * w_pre + b_pre
-//
-// norm(v) = (v - mu) * rho with rho = 1/sqrt(mean((v - mu)^2) + eps), mu the mean
-// (LAYER) or 0 (RMS), and v itself without a norm. The gate g [gates, d]
-// holds one row for rows/gates consecutive rows. With q = dn * w_pre,
-// hhat = (h' - mu) rho and yhat likewise, the gradients are
-//   D  = dh' + rho (q - hhat mean(q hhat) - [LAYER] mean(q)),   dh = skip D
-//   e  = branch g D, q2 = e w_post
-//   dy = rho (q2 - yhat mean(q2 yhat) - [LAYER] mean(q2))
-//   dg = branch sum D u, dw_post = sum e yhat, db_post = sum e,
-//   dw_pre = sum dn hhat, db_pre = sum dn      (sums over rows).
-//
-// A row is held in registers by a team of threads (team.h): every tensor is
-// read once and written once, which is what bounds both passes (about 10
-// operations a value forward, 35 backward). All arithmetic and all sums are
-// fp32; results are rounded once, at their store. n is computed from h' before
-// its rounding. The backward pass reads h' as it was stored: in bf16 its results
-// carry that rounding besides their own (2.4e-3 off the formula's where one
-// rounding is 1.7e-3), for a pass that needs neither h nor the gated branch again.
+// Sandwich norm: planning and C entries. The formulas and the kernels are in
+// sandwich_kernels.h.
+#include "sandwich.h"
+
 #include <math.h>
 
 #include <initializer_list>
-#include <type_traits>
 
 #include "api_internal.h"
 #include "monarch.h"
-#include "team.h"
 
 namespace monarch {
 namespace {
 
 constexpr int64_t kLimit = int64_t(1) << 31;
-constexpr int kMaxFeatures = 16384;   // 1024 threads x 4 pieces of 4 fp32 elements
-
-struct SandwichFwd {
-  const void *h, *y, *post_w, *post_b, *gate, *pre_w, *pre_b;
-  void *h_out, *n_out;
-  float* stats;
-  int64_t rows, rows_per_gate;
-  int d, post, pre;
-  float skip, branch, eps;
-};
-
-// A piece of an optional row (weights, biases, a gate row): without one, ones or
-// zeros, so that the arithmetic is the same.
-template <typename T, Rows R>
-__device__ __forceinline__ u32x4 par_piece(const void* p, int64_t off, int at, int d, float fill) {
-  if (p) return load_piece<T, R>(static_cast<const T*>(p) + off, at, d);
-  const uint32_t w = sizeof(T) == 2 ? (__float_as_uint(fill) >> 16) * 0x10001u : __float_as_uint(fill);
-  return u32x4{w, w, w, w};
-}
-
-// mean and 1/sqrt(mean square about it + eps) of the team's row (zero past d)
-template <Rows R, int TEAM, int P, int N>
-__device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][N], int lane, int d,
-                                          int kind, float eps, float& mu, float& rho) {
-  mu = 0.0f;
-  float q = 0.0f;
-  if (kind == MONARCH_NORM_LAYER) {
-    float s = 0.0f;
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int i = 0; i < N; ++i) s += v[p][i];
-    mu = team.sum(s) / static_cast<float>(d);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float c[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) c[i] = v[p][i] - mu;
-      mask<R, N>(c, (p * TEAM + lane) * N, d);
-#pragma unroll
-      for (int i = 0; i < N; ++i) q = fmaf(c[i], c[i], q);
-    }
-  } else {
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int i = 0; i < N; ++i) q = fmaf(v[p][i], v[p][i], q);
-  }
-  rho = 1.0f / sqrtf(team.sum(q) / static_cast<float>(d) + eps);
-}
-
-// One row a team. A team of 1024 threads leaves room for one workgroup a CU: it
-// takes rows in turn and loads the next one while the present one is normed a
-// second time. Measured (every tensor once): 16384 x 768 bf16 18.7 us, 5.4 TB/s;
-// 10000 x 625 fp32 20.2 us, 5.0 TB/s; 8192 x 16384 bf16 with a gate a row 240 us,
-// 5.6 TB/s, which is what a copy of that size reaches; one row of 768 4.2 us, the
-// launch. Small teams of 32 lanes x 3 pieces beat 64 x 2 for 768 features (20.3
-// against 21.1 us): every lane holds whole pieces.
-template <typename T, int TEAM, int P, bool BIAS, Rows R>
-__global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 4 : 3) void sandwich_fwd_kernel(SandwichFwd a) {
-  constexpr int N = PieceOf<T>::N, TEAMS = TEAM > 64 ? 1 : 256 / TEAM;
-  constexpr bool AHEAD = TEAM == 1024 && P <= 3;
-  __shared__ typename Team<TEAM>::Lds lds;
-  Team<TEAM> team(&lds);
-  const int lane = threadIdx.x % TEAM;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
-  u32x4 hr[P], yr[P];
-  auto load = [&](int64_t row) {
-    const int d = anew(a.d);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int at = (p * TEAM + lane) * N;
-      hr[p] = load_piece<T, R>(static_cast<const T*>(a.h) + row * d, at, d);
-      if (a.y) yr[p] = load_piece<T, R>(static_cast<const T*>(a.y) + row * d, at, d);
-    }
-  };
-  int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM;
-  if (AHEAD && row < a.rows) load(row);
-  for (; row < a.rows; row += step) {
-    const int d = anew(a.d);
-    const int64_t off = row * d;
-    if constexpr (!AHEAD) load(row);
-    float v[P][N];
-    float mu_y = 0.0f, rho_y = 1.0f, mu_h = 0.0f, rho_h = 1.0f;
-    if (a.y) {
-      if (a.post != MONARCH_NORM_NONE) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          PieceOf<T>::unpack(yr[p], v[p]);
-          if constexpr (R != WHOLE) mask<R, N>(v[p], (p * TEAM + lane) * N, d);
-        }
-        row_stats<R, TEAM, P, N>(team, v, lane, d, a.post, a.eps, mu_y, rho_y);
-      }
-      const int64_t goff = a.gate ? row / a.rows_per_gate * d : 0;
-      // branch * yhat, so that the scale costs nothing a value
-      const float scale = a.branch * rho_y, mean = mu_y * scale;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int at = (p * TEAM + lane) * N;
-        float w[N], b[N], g[N], t[N];
-        forget(yr[p]);
-        PieceOf<T>::unpack(yr[p], v[p]);
-        PieceOf<T>::unpack(par_piece<T, R>(a.post_w, 0, at, d, 1.0f), w);
-        if constexpr (BIAS)
-          PieceOf<T>::unpack(par_piece<T, R>(a.post_b, 0, at, d, 0.0f), b);
-        PieceOf<T>::unpack(par_piece<T, R>(a.gate, goff, at, d, 1.0f), g);
-        PieceOf<T>::unpack(hr[p], t);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          float u = fmaf(v[p][i], scale, -mean) * w[i];
-          if constexpr (BIAS) u = fmaf(a.branch, b[i], u);
-          v[p][i] = fmaf(a.skip, t[i], g[i] * u);
-        }
-        store_piece<T, R>(static_cast<T*>(a.h_out) + off, at, d, PieceOf<T>::pack(v[p]));
-        mask<R, N>(v[p], at, d);
-      }
-    } else {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        PieceOf<T>::unpack(hr[p], v[p]);
-        if constexpr (R != WHOLE) mask<R, N>(v[p], (p * TEAM + lane) * N, d);
-      }
-    }
-    if (AHEAD && row + step < a.rows) load(row + step);
-    if (a.pre != MONARCH_NORM_NONE) {
-      row_stats<R, TEAM, P, N>(team, v, lane, d, a.pre, a.eps, mu_h, rho_h);
-      const float mean_h = mu_h * rho_h;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int at = (p * TEAM + lane) * N;
-        float w[N], b[N];
-        PieceOf<T>::unpack(par_piece<T, R>(a.pre_w, 0, at, d, 1.0f), w);
-        if constexpr (BIAS)
-          PieceOf<T>::unpack(par_piece<T, R>(a.pre_b, 0, at, d, 0.0f), b);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          v[p][i] = fmaf(v[p][i], rho_h, -mean_h) * w[i];
-          if constexpr (BIAS) v[p][i] += b[i];
-        }
-        store_piece<T, R>(static_cast<T*>(a.n_out) + off, at, d, PieceOf<T>::pack(v[p]));
-      }
-    }
-    if (lane == 0) *reinterpret_cast<f32x4*>(a.stats + row * 4) = f32x4{mu_y, rho_y, mu_h, rho_h};
-  }
-}
-
-// ------------------------------------------------------------------ backward
-
-// How the rows of a backward call are cut (GATE). CHUNK: chunk c holds rows of one
-// gate row only (chunk / cpg), and its sums are of D alone; the gate and the
-// branch scale are applied when the chunks are joined. RUN: short gate runs, or
-// many; each is summed by one team, which stores its dgate row itself, and the
-// chunk's sums are of g * D. TOKEN: RUN with one row a run.
-enum { CHUNK = 0, RUN = 1, TOKEN = 2 };
-
-struct SandwichBwd {
-  const void *dh_out, *dn, *h_out, *y;
-  const float* stats;
-  const void *post_w, *post_b, *gate, *pre_w, *pre_b;
-  void *dh, *dy, *dgate;
-  float* part;          // [chunks][sums][d]
-  int64_t rows, rows_per_gate, chunk_rows, cpg;
-  int d, post, pre, sums;
-  int s_post, s_postb, s_pre, s_preb;   // index of each sum in a chunk, -1: not taken
-  float skip, branch;
-};
-
-// A thread's sums over rows for its own columns: in registers, or in LDS (WG
-// threads side by side, 16 bytes each), where they would not leave registers for
-// the row itself.
-template <int WG, int P, int N, bool IN_LDS>
-struct Sums {
-  float v[IN_LDS ? 1 : P][N];
-  f32x4* lds;
-  __device__ __forceinline__ void clear(f32x4* l) {
-    lds = l;
-    if constexpr (IN_LDS) {
-#pragma unroll
-      for (int k = 0; k < P * N / 4; ++k) lds[k * WG + threadIdx.x] = f32x4{0, 0, 0, 0};
-    } else {
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[p][i] = 0.0f;
-    }
-  }
-  // adds x[i] to the sums of piece p
-  __device__ __forceinline__ void add(int p, const float (&x)[N]) {
-    if constexpr (IN_LDS) {
-#pragma unroll
-      for (int k = 0; k < N / 4; ++k) {
-        f32x4& s = lds[(p * (N / 4) + k) * WG + threadIdx.x];
-        f32x4 t = s;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] += x[4 * k + i];
-        s = t;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[p][i] += x[i];
-    }
-  }
-  // column i of piece p of a thread of the workgroup (LDS)
-  __device__ __forceinline__ float at(int p, int i, int thread) const {
-    return reinterpret_cast<const float*>(&lds[(p * (N / 4) + i / 4) * WG + thread])[i % 4];
-  }
-};
-
-// Each team takes the rows of its chunk in turn and keeps its columns' sums over
-// them, so that the parameters' gradients cost a partial row a chunk: two chunks
-// a CU (three made the partial rows cost more than they hid: 30 -> 37 us for 16384
-// x 768 bf16). Wide rows leave no registers for the sums: they lie in LDS (131 KB
-// for 16384 columns; in registers the kernel spilled, 1208 -> 488 us), parameters
-// are read again from the caches, and the next row's dn and h' are under way during
-// the second half of a row. Measured: 16384 x 768 bf16 with 16 gates 29.4 us, 5.1
-// TB/s; 10000 x 625 fp32 with biases 30.4 us, 4.9 TB/s; 8192 x 16384 bf16 with a gate
-// a row 417 us, 5.1 TB/s.
-template <typename T, int TEAM, int P, int GATE, bool BIAS, Rows R>
-__global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(SandwichBwd a) {
-  constexpr int N = PieceOf<T>::N, WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
-  constexpr int COLS = TEAM * P * N;
-  // sums of post_w and pre_w in LDS; parameters read again for every row; the next
-  // row's first tensors loaded ahead
-  constexpr bool IN_LDS = TEAM > 64 || BIAS;
-  constexpr bool REREAD = TEAM > 256;
-  constexpr bool LATE = TEAM > 512;   // 128 registers a thread: y's side is loaded last
-  constexpr bool AHEAD = TEAM > 64 && !LATE;
-  __shared__ typename Team<TEAM>::Lds lds;
-  __shared__ f32x4 shared[IN_LDS ? 2 * WG * P * N / 4 : TEAMS > 1 ? TEAMS * COLS / 4 : 1];
-  Team<TEAM> team(&lds);
-  const int lane = threadIdx.x % TEAM, tm = threadIdx.x / TEAM;
-  const float inv_d = 1.0f / static_cast<float>(a.d);
-  // rows [first, last) of this team, taken every `step`
-  int64_t first, last, group = 0;
-  int step = 1;
-  if constexpr (GATE != CHUNK) {
-    // chunk_rows counts whole gate runs here: this team's own range of them
-    const int64_t units = a.rows / a.rows_per_gate;
-    group = (static_cast<int64_t>(blockIdx.x) * TEAMS + tm) * a.chunk_rows;
-    const int64_t u1 = group + a.chunk_rows < units ? group + a.chunk_rows : units;
-    first = group * a.rows_per_gate;
-    last = u1 * a.rows_per_gate;
-  } else {
-    group = blockIdx.x / a.cpg;
-    const int64_t c = blockIdx.x - group * a.cpg;
-    const int64_t end = (group + 1) * a.rows_per_gate;
-    first = group * a.rows_per_gate + c * a.chunk_rows;
-    last = first + a.chunk_rows < end ? first + a.chunk_rows : end;
-    first += tm;
-    step = TEAMS;
-  }
-  const u32x4 zero = {0, 0, 0, 0};
-  u32x4 post_wr[P], pre_wr[P], gr[P];
-  auto load_pre_pars = [&]() {
-    const int d = anew(a.d);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int at = (p * TEAM + lane) * N;
-      pre_wr[p] = par_piece<T, R>(a.pre_w, 0, at, d, 1.0f);
-    }
-  };
-  auto load_post_pars = [&]() {
-    const int d = anew(a.d);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int at = (p * TEAM + lane) * N;
-      post_wr[p] = par_piece<T, R>(a.post_w, 0, at, d, 1.0f);
-      if constexpr (GATE == CHUNK) {
-        gr[p] = par_piece<T, R>(a.gate, group * d, at, d, 1.0f);
-      }
-    }
-  };
-  if constexpr (!REREAD) {
-    load_pre_pars();
-    load_post_pars();
-  }
-  Sums<WG, P, N, IN_LDS> s_post, s_pre;
-  Sums<WG, BIAS ? P : 1, N, false> s_postb, s_preb;
-  Sums<WG, GATE == RUN ? P : 1, N, false> s_gate;
-  s_post.clear(shared);
-  s_pre.clear(shared + (IN_LDS ? WG * P * N / 4 : 0));
-  s_postb.clear(nullptr);
-  s_preb.clear(nullptr);
-  s_gate.clear(nullptr);
-  int64_t left = a.rows_per_gate;   // RUN: rows of the gate run still to come
-
-  u32x4 dnr[P], hr[P];
-  auto load_pre = [&](int64_t row) {
-    const int d = anew(a.d);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int at = (p * TEAM + lane) * N;
-      dnr[p] = hr[p] = zero;
-      if (a.pre != MONARCH_NORM_NONE) {
-        dnr[p] = load_piece<T, R>(static_cast<const T*>(a.dn) + row * d, at, d);
-        hr[p] = load_piece<T, R>(static_cast<const T*>(a.h_out) + row * d, at, d);
-      }
-    }
-  };
-  if (AHEAD && first < last) load_pre(first);
-  for (int64_t row = first; row < last; row += step) {
-    const int d = anew(a.d);
-    const int64_t off = row * d;
-    const f32x4 st = *reinterpret_cast<const f32x4*>(a.stats + row * 4);
-    if constexpr (!AHEAD) load_pre(row);
-    u32x4 yr[P];
-    auto load_y = [&]() {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int at = (p * TEAM + lane) * N;
-        yr[p] = zero;
-        if (a.y) yr[p] = load_piece<T, R>(static_cast<const T*>(a.y) + off, at, d);
-        if constexpr (GATE != CHUNK)
-          gr[p] = load_piece<T, R>(static_cast<const T*>(a.gate) + group * d, at, d);
-      }
-    };
-    float D[P][N];
-    {
-      u32x4 dhr[P];
-      auto load_rest = [&]() {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          dhr[p] = zero;
-          if (a.dh_out)
-            dhr[p] = load_piece<T, R>(static_cast<const T*>(a.dh_out) + off,
-                                        (p * TEAM + lane) * N, d);
-        }
-        if constexpr (!LATE) load_y();
-      };
-      if constexpr (REREAD)
-        load_pre_pars();
-      else
-        load_rest();
-      float c1 = 0.0f, c2 = 0.0f;
-      if (a.pre != MONARCH_NORM_NONE) {
-        const float mean = st[2] * st[3];
-        float s[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          float dn[N], h[N], w[N];
-          PieceOf<T>::unpack(dnr[p], dn);
-          if constexpr (R != WHOLE) mask<R, N>(dn, (p * TEAM + lane) * N, d);
-          PieceOf<T>::unpack(hr[p], h);
-          if constexpr (BIAS) s_preb.add(p, dn);
-          forget(pre_wr[p]);
-          PieceOf<T>::unpack(pre_wr[p], w);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            h[i] = fmaf(h[i], st[3], -mean) * dn[i];   // dn hhat
-            s[0] = fmaf(h[i], w[i], s[0]);
-            s[1] = fmaf(dn[i], w[i], s[1]);
-          }
-          s_pre.add(p, h);
-        }
-        if constexpr (REREAD) load_rest();
-        team.template reduce<SumOp, 2>(s);
-        // D = dh' + rho (q - hhat c1 - c2) with hhat = h rho - mean
-        c1 = s[0] * inv_d;
-        c2 = a.pre == MONARCH_NORM_LAYER ? s[1] * inv_d : 0.0f;
-        const float k1 = c1 * st[3] * st[3], k0 = st[3] * (c2 - c1 * mean);
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const int at = (p * TEAM + lane) * N;
-          float dn[N], h[N], w[N];
-          forget(dnr[p]);
-          forget(hr[p]);
-          forget(pre_wr[p]);
-          PieceOf<T>::unpack(dnr[p], dn);
-          PieceOf<T>::unpack(hr[p], h);
-          PieceOf<T>::unpack(dhr[p], D[p]);
-          PieceOf<T>::unpack(pre_wr[p], w);
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            D[p][i] += fmaf(st[3] * dn[i], w[i], -fmaf(h[i], k1, k0));
-          mask<R, N>(D[p], at, d);
-        }
-      } else {
-        if constexpr (REREAD) load_rest();
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          PieceOf<T>::unpack(dhr[p], D[p]);
-          if constexpr (R != WHOLE) mask<R, N>(D[p], (p * TEAM + lane) * N, d);
-        }
-      }
-    }
-    if constexpr (LATE) load_y();
-    if constexpr (REREAD) load_post_pars();
-    if (AHEAD && row + step < last) load_pre(row + step);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int at = (p * TEAM + lane) * N;
-      if (at < d) {
-        float o[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = a.skip * D[p][i];
-        store_piece<T, R>(static_cast<T*>(a.dh) + off, at, d, PieceOf<T>::pack(o));
-      }
-    }
-    if (a.y) {
-      const float mean = st[0] * st[1];
-      float s[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int at = (p * TEAM + lane) * N;
-        float y[N], w[N], g[N], o[N];
-        PieceOf<T>::unpack(yr[p], y);
-        forget(post_wr[p]);
-        forget(gr[p]);
-        PieceOf<T>::unpack(post_wr[p], w);
-        PieceOf<T>::unpack(gr[p], g);
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = fmaf(y[i], st[1], -mean);   // yhat
-        if constexpr (GATE != CHUNK) {
-          // dgate = branch D u
-          float b[N];
-          if constexpr (BIAS)
-            PieceOf<T>::unpack(par_piece<T, R>(a.post_b, 0, at, d, 0.0f), b);
-#pragma unroll
-          for (int i = 0; i < N; ++i) o[i] = D[p][i] * (BIAS ? fmaf(y[i], w[i], b[i]) : y[i] * w[i]);
-          if constexpr (GATE == RUN) {
-            s_gate.add(p, o);
-          } else if (a.dgate) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) o[i] *= a.branch;
-            store_piece<T, R>(static_cast<T*>(a.dgate) + group * d, at, d, PieceOf<T>::pack(o));
-          }
-          // e / branch = g D, which D becomes
-#pragma unroll
-          for (int i = 0; i < N; ++i) D[p][i] *= g[i];
-        }
-        if constexpr (BIAS) s_postb.add(p, D[p]);
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = D[p][i] * y[i];
-        s_post.add(p, o);
-        // D becomes q2 = branch g D w
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if constexpr (GATE == CHUNK) D[p][i] *= g[i];
-          D[p][i] *= a.branch * w[i];
-          s[0] = fmaf(D[p][i], y[i], s[0]);
-          s[1] += D[p][i];
-        }
-      }
-      float k1 = 0.0f, k0 = 0.0f;
-      if (a.post != MONARCH_NORM_NONE) {
-        team.template reduce<SumOp, 2>(s);
-        // dy = rho (q2 - yhat c1 - c2) with yhat = y rho - mean
-        const float c1 = s[0] * inv_d, c2 = a.post == MONARCH_NORM_LAYER ? s[1] * inv_d : 0.0f;
-        k1 = c1 * st[1] * st[1];
-        k0 = st[1] * (c2 - c1 * mean);
-      }
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int at = (p * TEAM + lane) * N;
-        float y[N];
-        forget(yr[p]);
-        PieceOf<T>::unpack(yr[p], y);
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = fmaf(st[1], D[p][i], -fmaf(y[i], k1, k0));
-        store_piece<T, R>(static_cast<T*>(a.dy) + off, at, d, PieceOf<T>::pack(y));
-      }
-    }
-    if constexpr (GATE == TOKEN) ++group;
-    if constexpr (GATE == RUN) {
-      if (--left == 0) {
-        left = a.rows_per_gate;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const int at = (p * TEAM + lane) * N;
-          float o[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i) o[i] = a.branch * s_gate.v[p][i];
-          if (a.dgate)
-            store_piece<T, R>(static_cast<T*>(a.dgate) + group * d, at, d, PieceOf<T>::pack(o));
-        }
-        s_gate.clear(nullptr);
-        ++group;
-      }
-    }
-  }
-  // this chunk's sums: the teams' are added in team order. `shift` is how far a
-  // piece is moved back to end with its row (load_piece).
-  float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.sums * a.d;
-  auto shift = [&](int at) { return R == WHOLE ? 0 : max(at + N - a.d, 0); };
-  auto put = [&](int which, const auto& s) {
-    if (which < 0) return;
-    float* out = part + static_cast<int64_t>(which) * a.d;
-    if constexpr (std::is_same<decltype(s), const Sums<WG, P, N, true>&>::value) {
-      __syncthreads();
-      for (int at = threadIdx.x; at < a.d; at += WG) {
-        const int p = at / (TEAM * N), l = at / N % TEAM, i = at % N + shift(at / N * N);
-        float t = s.at(p, i, l);
-#pragma unroll
-        for (int k = 1; k < TEAMS; ++k) t += s.at(p, i, k * TEAM + l);
-        out[at] = t;
-      }
-    } else {
-      float* to = TEAMS == 1 ? out : reinterpret_cast<float*>(shared) + tm * COLS;
-      if constexpr (TEAMS > 1) __syncthreads();
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int at = (p * TEAM + lane) * N, back = shift(at);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (at < a.d && i >= back) to[at - back + i] = s.v[p][i];
-      }
-      if constexpr (TEAMS > 1) {
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.d; c += WG) {
-          const float* from = reinterpret_cast<const float*>(shared) + c;
-          float t = from[0];
-#pragma unroll
-          for (int k = 1; k < TEAMS; ++k) t += from[k * COLS];
-          out[c] = t;
-        }
-      }
-    }
-  };
-  put(a.s_post, s_post);
-  put(a.s_pre, s_pre);
-  if constexpr (BIAS) {
-    put(a.s_postb, s_postb);
-    put(a.s_preb, s_preb);
-  }
-}
-
-// Joins the chunks' sums. A job is one output row: the weight gradients (sums
-// over every chunk, weighted by the chunk's gate row) and, when chunks hold
-// sums of D alone, one dgate row each. A workgroup takes 32 columns; 32 slices
-// of 32 threads sum contiguous chunk ranges, and the slices are added in order.
-// Bound by latency: 16 loads of a slice, eight at a time; 4.2 us for 512 chunks of
-// 768 columns and 16 gates (15 us with 64 columns x 16 slices).
-struct SandwichJoin {
-  const float* part;
-  const void *gate, *post_w, *post_b;   // gate: null where the sums hold it already
-  void *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
-  int chunks, cpg, d, sums, s_post, s_postb, s_pre, s_preb;
-  float branch;
-};
-
-constexpr int JC = 32, JS = 32;
-constexpr int kWeightJobs = 4;   // post_w, post_b, pre_w, pre_b; then one job a gate row
-
-template <typename T>
-__global__ __launch_bounds__(JC* JS) void sandwich_join_kernel(SandwichJoin a) {
-  __shared__ float buf[2][JS][JC];
-  const int col = threadIdx.x % JC, slice = threadIdx.x / JC;
-  const int at = blockIdx.y * JC + col;
-  const int64_t job = blockIdx.x;
-  int which, which2 = -1;
-  int c0 = 0, c1 = a.chunks;
-  bool gated = false;
-  void* out;
-  if (job < kWeightJobs) {
-    which = job == 0 ? a.s_post : job == 1 ? a.s_postb : job == 2 ? a.s_pre : a.s_preb;
-    out = job == 0 ? a.dpost_w : job == 1 ? a.dpost_b : job == 2 ? a.dpre_w : a.dpre_b;
-    gated = job < 2 && a.gate;
-  } else {
-    which = a.s_post;
-    which2 = a.post_b ? a.s_postb : -1;
-    c0 = static_cast<int>(job - kWeightJobs) * a.cpg;
-    c1 = c0 + a.cpg;
-    out = static_cast<T*>(a.dgate) + (job - kWeightJobs) * a.d;
-  }
-  if (!out || which < 0) return;   // the whole workgroup
-  const int per = (c1 - c0 + JS - 1) / JS;
-  const int b = c0 + slice * per, e = min(b + per, c1);
-  float s = 0.0f, s2 = 0.0f;
-  if (at < a.d) {
-    const int64_t stride = static_cast<int64_t>(a.sums) * a.d;
-    const float* p = a.part + static_cast<int64_t>(which) * a.d + at;
-    const float* p2 = a.part + static_cast<int64_t>(which2 < 0 ? which : which2) * a.d + at;
-    if (which2 >= 0) {
-#pragma unroll 8
-      for (int c = b; c < e; ++c) {
-        s += p[c * stride];
-        s2 += p2[c * stride];
-      }
-    } else if (!gated) {
-#pragma unroll 8
-      for (int c = b; c < e; ++c) s += p[c * stride];
-    } else {
-      int c = b;
-      while (c < e) {   // the chunks of one gate row at a time
-        const int g = c / a.cpg, end = min(e, (g + 1) * a.cpg);
-        float t = 0.0f;
-#pragma unroll 8
-        for (; c < end; ++c) t += p[c * stride];
-        s = fmaf(t, Io<T>::load(a.gate, static_cast<int64_t>(g) * a.d + at), s);
-      }
-    }
-  }
-  buf[0][slice][col] = s;
-  buf[1][slice][col] = s2;
-  __syncthreads();
-  if (slice || at >= a.d) return;
-#pragma unroll
-  for (int k = 1; k < JS; ++k) {
-    s += buf[0][k][col];
-    s2 += buf[1][k][col];
-  }
-  if (job >= kWeightJobs) {
-    s *= a.post_w ? Io<T>::load(a.post_w, at) : 1.0f;
-    if (which2 >= 0) s = fmaf(s2, Io<T>::load(a.post_b, at), s);
-  }
-  if (job < 2 || job >= kWeightJobs) s *= a.branch;
-  Io<T>::store(out, at, s);
-}
-
-// ---------------------------------------------------------------- host side
-
-struct Shape {
-  int team, pieces;
-};
 
 // The smallest team whose threads hold at most `few` (up to a wave) or `many`
 // pieces of a row; `last` for any row that is wider.
@@ -660,36 +24,23 @@ Shape shape_of(int64_t d, bool bf16, int first, int last, int few, int many) {
   return {t, static_cast<int>((pieces + t - 1) / t)};
 }
 
-Shape fwd_shape(int64_t d, bool bf16) {
-  return shape_of(d, bf16, 16, 1024, bf16 ? 3 : 4, bf16 ? 2 : 4);
-}
 Shape bwd_shape(int64_t d, bool bf16) {
   return shape_of(d, bf16, 32, bf16 ? 512 : 1024, bf16 ? 3 : 4, bf16 ? 2 : 4);
 }
 
-struct BwdPlan {
-  Shape shape;
-  int gate;      // CHUNK, RUN or TOKEN
-  bool bias;
-  int64_t chunks, chunk_rows, cpg, rows_per_gate;
-  int sums, s_post, s_postb, s_pre, s_preb;
-  size_t ws;
-};
-
-constexpr int64_t kCus = 256;
 constexpr int64_t kRunRows = 32;     // gate runs up to this long are a team's own
 
 // Everything about a backward call that depends on sizes alone (`with`: which
 // of post_w, post_b, gate, pre_w, pre_b there are, as the sums they need).
-BwdPlan bwd_plan(int64_t rows, int64_t d, int64_t gates, bool has_y, bool post_bias, bool has_pre,
+SandwichBwdPlan bwd_plan(int64_t rows, int64_t d, int64_t gates, bool has_y, bool post_bias, bool has_pre,
                  bool pre_bias, bool bf16) {
-  BwdPlan p = {};
+  SandwichBwdPlan p = {};
   p.shape = bwd_shape(d, bf16);
   p.bias = post_bias || pre_bias;
   p.rows_per_gate = gates > 0 ? rows / gates : rows;
   const int teams = p.shape.team > 64 ? 1 : 256 / p.shape.team;
   // workgroups aimed at: two a CU, one where the sums of a wide row take its LDS
-  const int64_t aim = kCus * (p.shape.team * p.shape.pieces * (bf16 ? 8 : 4) > 8192 ? 1 : 2);
+  const int64_t aim = kSandwichCus * (p.shape.team * p.shape.pieces * (bf16 ? 8 : 4) > 8192 ? 1 : 2);
   // a gate run is a team's own where it is short, or where there are enough of them
   // for every team; one run cut into chunks is joined by as many workgroups
   p.gate = rows == 0 || gates <= 1 || (p.rows_per_gate > kRunRows && gates < aim * teams) ? CHUNK
@@ -726,165 +77,9 @@ int check_sizes(int64_t rows, int64_t d, int64_t gates, int post, int pre, int d
   if (post < MONARCH_NORM_NONE || post > MONARCH_NORM_LAYER || pre < MONARCH_NORM_NONE ||
       pre > MONARCH_NORM_LAYER)
     return MONARCH_ERR_DTYPE;
-  if (rows < 0 || rows >= kLimit || d <= 0 || d > kMaxFeatures || gates < 0) return MONARCH_ERR_SHAPE;
+  if (rows < 0 || rows >= kLimit || d <= 0 || d > kSandwichMaxFeatures || gates < 0) return MONARCH_ERR_SHAPE;
   if (gates > 0 && (rows % gates != 0 || (rows > 0 && gates > rows))) return MONARCH_ERR_SHAPE;
   return MONARCH_OK;
-}
-
-Rows rows_of(int64_t d, bool bf16) {
-  const int n = bf16 ? 8 : 4;
-  return d % n == 0 ? WHOLE : d > n ? CUT : SHORT;
-}
-
-template <typename T, int TEAM, int P>
-void fwd_launch(const SandwichFwd& a, Rows lie, hipStream_t s) {
-  constexpr int WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
-  // one row a team, or the workgroups that fit the chip at once where they load
-  // ahead; 2^20 workgroups are fewer than 2^32 threads
-  const int64_t most = TEAM == 1024 ? kCus : 1 << 20;
-  int64_t grid = (a.rows + TEAMS - 1) / TEAMS;
-  if (grid > most) grid = most;
-  const dim3 g(static_cast<unsigned>(grid)), block(WG);
-  if (lie == CUT) {
-    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true, CUT>), g, block, 0, s, a);
-  } else if (lie == SHORT) {
-    if constexpr (TEAM == 16 && P == 1)
-      hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true, SHORT>), g, block, 0, s, a);
-  } else if (a.post_b || a.pre_b) {
-    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, true, WHOLE>), g, block, 0, s, a);
-  } else {
-    hipLaunchKernelGGL((sandwich_fwd_kernel<T, TEAM, P, false, WHOLE>), g, block, 0, s, a);
-  }
-}
-
-template <typename T, int TEAM, int P>
-void bwd_launch(const SandwichBwd& a, const BwdPlan& p, Rows lie, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.chunks)), block(TEAM > 64 ? TEAM : 256);
-#define BWD_GO(GATE, BIAS, ROWS) \
-  hipLaunchKernelGGL((sandwich_bwd_kernel<T, TEAM, P, GATE, BIAS, ROWS>), grid, block, 0, s, a)
-  // odd widths take the kernels that hold for any gate run and any bias
-  if (lie == CUT) {
-    if (p.gate == CHUNK)
-      BWD_GO(CHUNK, true, CUT);
-    else
-      BWD_GO(RUN, true, CUT);
-  } else if (lie == SHORT) {
-    if constexpr (TEAM == 32 && P == 1) {
-      if (p.gate == CHUNK)
-        BWD_GO(CHUNK, true, SHORT);
-      else
-        BWD_GO(RUN, true, SHORT);
-    }
-  } else {
-    switch (p.gate * 2 + (p.bias ? 1 : 0)) {
-      case CHUNK * 2: BWD_GO(CHUNK, false, WHOLE); break;
-      case CHUNK * 2 + 1: BWD_GO(CHUNK, true, WHOLE); break;
-      case RUN * 2: BWD_GO(RUN, false, WHOLE); break;
-      case RUN * 2 + 1: BWD_GO(RUN, true, WHOLE); break;
-      case TOKEN * 2: BWD_GO(TOKEN, false, WHOLE); break;
-      default: BWD_GO(TOKEN, true, WHOLE); break;
-    }
-  }
-#undef BWD_GO
-}
-
-#define TEAM_CASE(CALL, T, TEAM, P)                \
-  case (TEAM) * 8 + (P): CALL(T, TEAM, P); break;
-
-// The pairs (team, pieces) that fwd_shape and bwd_shape give.
-hipError_t launch_fwd(const SandwichFwd& a, bool bf16, hipStream_t s) {
-  const Shape sh = fwd_shape(a.d, bf16);
-  const Rows lie = rows_of(a.d, bf16);
-#define FWD(T, TEAM, P) fwd_launch<T, TEAM, P>(a, lie, s)
-  if (bf16) {
-    switch (sh.team * 8 + sh.pieces) {
-      TEAM_CASE(FWD, uint16_t, 16, 1)
-      TEAM_CASE(FWD, uint16_t, 16, 2)
-      TEAM_CASE(FWD, uint16_t, 16, 3)
-      TEAM_CASE(FWD, uint16_t, 32, 2)
-      TEAM_CASE(FWD, uint16_t, 32, 3)
-      TEAM_CASE(FWD, uint16_t, 64, 2)
-      TEAM_CASE(FWD, uint16_t, 64, 3)
-      TEAM_CASE(FWD, uint16_t, 128, 2)
-      TEAM_CASE(FWD, uint16_t, 256, 2)
-      TEAM_CASE(FWD, uint16_t, 512, 2)
-      TEAM_CASE(FWD, uint16_t, 1024, 2)
-      default: return hipErrorInvalidConfiguration;
-    }
-  } else {
-    switch (sh.team * 8 + sh.pieces) {
-      TEAM_CASE(FWD, float, 16, 1)
-      TEAM_CASE(FWD, float, 16, 2)
-      TEAM_CASE(FWD, float, 16, 3)
-      TEAM_CASE(FWD, float, 16, 4)
-      TEAM_CASE(FWD, float, 32, 3)
-      TEAM_CASE(FWD, float, 32, 4)
-      TEAM_CASE(FWD, float, 64, 3)
-      TEAM_CASE(FWD, float, 64, 4)
-      TEAM_CASE(FWD, float, 128, 3)
-      TEAM_CASE(FWD, float, 128, 4)
-      TEAM_CASE(FWD, float, 256, 3)
-      TEAM_CASE(FWD, float, 256, 4)
-      TEAM_CASE(FWD, float, 512, 3)
-      TEAM_CASE(FWD, float, 512, 4)
-      TEAM_CASE(FWD, float, 1024, 3)
-      TEAM_CASE(FWD, float, 1024, 4)
-      default: return hipErrorInvalidConfiguration;
-    }
-  }
-#undef FWD
-  return hipGetLastError();
-}
-
-hipError_t launch_bwd(const SandwichBwd& a, const BwdPlan& p, bool bf16, hipStream_t s) {
-  const Rows lie = rows_of(a.d, bf16);
-#define BWD(T, TEAM, P) bwd_launch<T, TEAM, P>(a, p, lie, s)
-  if (bf16) {
-    switch (p.shape.team * 8 + p.shape.pieces) {
-      TEAM_CASE(BWD, uint16_t, 32, 1)
-      TEAM_CASE(BWD, uint16_t, 32, 2)
-      TEAM_CASE(BWD, uint16_t, 32, 3)
-      TEAM_CASE(BWD, uint16_t, 64, 2)
-      TEAM_CASE(BWD, uint16_t, 64, 3)
-      TEAM_CASE(BWD, uint16_t, 128, 2)
-      TEAM_CASE(BWD, uint16_t, 256, 2)
-      TEAM_CASE(BWD, uint16_t, 512, 2)
-      TEAM_CASE(BWD, uint16_t, 512, 3)
-      TEAM_CASE(BWD, uint16_t, 512, 4)
-      default: return hipErrorInvalidConfiguration;
-    }
-  } else {
-    switch (p.shape.team * 8 + p.shape.pieces) {
-      TEAM_CASE(BWD, float, 32, 1)
-      TEAM_CASE(BWD, float, 32, 2)
-      TEAM_CASE(BWD, float, 32, 3)
-      TEAM_CASE(BWD, float, 32, 4)
-      TEAM_CASE(BWD, float, 64, 3)
-      TEAM_CASE(BWD, float, 64, 4)
-      TEAM_CASE(BWD, float, 128, 3)
-      TEAM_CASE(BWD, float, 128, 4)
-      TEAM_CASE(BWD, float, 256, 3)
-      TEAM_CASE(BWD, float, 256, 4)
-      TEAM_CASE(BWD, float, 512, 3)
-      TEAM_CASE(BWD, float, 512, 4)
-      TEAM_CASE(BWD, float, 1024, 3)
-      TEAM_CASE(BWD, float, 1024, 4)
-      default: return hipErrorInvalidConfiguration;
-    }
-  }
-#undef BWD
-  return hipGetLastError();
-}
-#undef TEAM_CASE
-
-hipError_t launch_join(const SandwichJoin& a, int64_t jobs, bool bf16, hipStream_t s) {
-  // gate rows that are joined here are fewer than the teams of a launch (bwd_plan)
-  const dim3 grid(static_cast<unsigned>(jobs), static_cast<unsigned>((a.d + JC - 1) / JC));
-  if (bf16)
-    hipLaunchKernelGGL((sandwich_join_kernel<uint16_t>), grid, dim3(JC * JS), 0, s, a);
-  else
-    hipLaunchKernelGGL((sandwich_join_kernel<float>), grid, dim3(JC * JS), 0, s, a);
-  return hipGetLastError();
 }
 
 bool any_misaligned(std::initializer_list<const void*> ps) {
@@ -894,6 +89,11 @@ bool any_misaligned(std::initializer_list<const void*> ps) {
 }
 
 }  // namespace
+
+Shape sandwich_fwd_shape(int64_t d, bool bf16) {
+  return shape_of(d, bf16, 16, 1024, bf16 ? 3 : 4, bf16 ? 2 : 4);
+}
+
 }  // namespace monarch
 
 using namespace monarch;
@@ -928,7 +128,8 @@ int monarch_sandwich_fwd(const void* h, const void* y, const void* post_w, const
   Tracer tr{events, n_events, 0, s};
   st = record_hip(tr.mark());
   if (st) return st;
-  st = record_hip(launch_fwd(a, dtype == MONARCH_BF16, s));
+  st = record_hip(dtype == MONARCH_BF16 ? sandwich_launch_fwd<uint16_t>(a, s)
+                                         : sandwich_launch_fwd<float>(a, s));
   if (st) return st;
   return record_hip(tr.mark());
 }
@@ -965,7 +166,7 @@ int monarch_sandwich_bwd(const void* dh_out, const void* dn, const void* h_out, 
   if ((dpost_w && !post_w) || (dpost_b && !post_b) || (dgate && gates == 0) ||
       (dpre_w && !pre_w) || (dpre_b && !pre_b))
     return MONARCH_ERR_NULL;
-  const BwdPlan p = bwd_plan(rows, features, gates, y || rows == 0, post_b != nullptr, has_pre,
+  const SandwichBwdPlan p = bwd_plan(rows, features, gates, y || rows == 0, post_b != nullptr, has_pre,
                              pre_b != nullptr, bf16);
   if (rows > 0 && p.ws > 0 && !workspace) return MONARCH_ERR_NULL;
   if (rows > 0 && workspace_bytes < p.ws) return MONARCH_ERR_WORKSPACE;
@@ -984,7 +185,7 @@ int monarch_sandwich_bwd(const void* dh_out, const void* dn, const void* h_out, 
     a.skip = skip_scale, a.branch = branch_scale;
     st = record_hip(tr.mark());
     if (st) return st;
-    st = record_hip(launch_bwd(a, p, bf16, s));
+    st = record_hip(bf16 ? sandwich_launch_bwd<uint16_t>(a, p, s) : sandwich_launch_bwd<float>(a, p, s));
     if (st) return st;
   }
   if (dpost_w || dpost_b || dgate || dpre_w || dpre_b) {
@@ -1000,7 +201,8 @@ int monarch_sandwich_bwd(const void* dh_out, const void* dn, const void* h_out, 
     const int64_t jobs = kWeightJobs + (dgate && p.gate == CHUNK ? gates : 0);
     st = record_hip(tr.mark());
     if (st) return st;
-    st = record_hip(launch_join(j, jobs, bf16, s));
+    st = record_hip(bf16 ? sandwich_launch_join<uint16_t>(j, jobs, s)
+                         : sandwich_launch_join<float>(j, jobs, s));
     if (st) return st;
   }
   return record_hip(tr.mark());

@@ -175,6 +175,15 @@ def test_gate_runs_longer_and_shorter_than_a_chunk(api):
         compare(api, rows, 72, gates, True, "f32", "rms", "rms")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("d", [135, 767, 1023, 4095, 12001])
+def test_odd_widths_by_gate_run(api, d, bias, dtype):
+    """One gate, long runs, short runs and a gate a row: each has its own kernel, with and without biases."""
+    for gates in (0, 2, 35, 70):
+        compare(api, 70, d, gates, bias, dtype, "layer", "rms")
+
+
 @pytest.mark.parametrize("bias", [False, True])
 def test_many_long_gate_runs(api, bias):
     """More runs than a launch has teams are taken whole, whatever their length; fewer are cut."""
