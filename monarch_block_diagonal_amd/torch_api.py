@@ -399,8 +399,10 @@ def _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias, p
 def _on_stream(stream, call, *args, **kw):
     """call(*args, **kw) on a stream of the caller's: results and workspaces come
     from that stream's memory, so that none is handed out again before its work is done."""
-    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                           else torch.cuda.ExternalStream(stream)):
+    if not isinstance(stream, torch.cuda.Stream):
+        # 0 is the default stream's handle; ExternalStream(0) would be a stream of torch's own pool
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
         return call(*args, **kw)
 
 

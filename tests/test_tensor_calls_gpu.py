@@ -1,0 +1,42 @@
+"""The tensor helpers and autograd functions of the sandwich norm and the
+distillation loss as programs call them: streams, memory, views, gradients of
+gradients."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def api():
+    if not torch.cuda.is_available():
+        pytest.fail("a GPU is required for the gpu-marked tests")
+    from monarch_block_diagonal_amd import torch_api
+    return torch_api
+
+
+def test_raw_streams_are_the_ones_named(api):
+    """Handle 0 is the default stream, also where the current one is another."""
+    side = torch.cuda.Stream()
+    now = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    with torch.cuda.stream(torch.cuda.Stream()):
+        assert api._on_stream(0, now) == 0
+        assert api._on_stream(side.cuda_stream, now) == side.cuda_stream
+        assert api._on_stream(side, now) == side.cuda_stream
+
+
+def test_default_stream_by_its_handle(api):
+    """stream=0 follows the work queued on the default stream and comes before what is queued next."""
+    h, y = torch.randn(4096, 768, device="cuda"), torch.randn(4096, 768, device="cuda")
+    z, t = torch.randn(4096, 2000, device="cuda"), torch.randn(4096, 8, device="cuda")
+    ids = torch.randint(0, 2000, (4096, 8), device="cuda")
+    want = [*api.sandwich_forward(h * 2.0, y), *api.distill_step(z * 2.0, t, ids)]
+    torch.cuda.synchronize()
+    a = torch.randn(2048, 2048, device="cuda")
+    for _ in range(8):
+        a = a @ a * 1e-3
+    h2, z2 = h * 2.0, z * 2.0   # queued behind the products
+    got = [x.clone() for x in (*api.sandwich_forward(h2, y, stream=0), *api.distill_step(z2, t, ids, stream=0))]
+    torch.cuda.synchronize()
+    for i, (x, w) in enumerate(zip(got, want)):
+        assert torch.equal(x, w), i
