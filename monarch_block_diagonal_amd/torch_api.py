@@ -74,6 +74,40 @@ def _check(*ts):
             raise ValueError("tensors must live on the GPU")
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    """Hands gradients on, and raises where they are differentiated."""
+
+    @staticmethod
+    def forward(ctx, *grads):
+        return tuple(g.detach() for g in grads)   # no views: optimizers write to gradients in place
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the library's operators have no second derivatives")
+
+
+def _first_derivative_only(backward):
+    """For a Function's backward that calls the library. With create_graph=True its results would be
+    constants to autograd, and a second derivative would lose their part without a word: they get a
+    graph that refuses it instead. (once_differentiable does that only where an incoming gradient
+    requires a gradient itself, which the ones of a plain sum do not.)"""
+
+    @functools.wraps(backward)
+    def wrapped(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        at = [i for i, g in enumerate(out) if g is not None]
+        guarded = _NoSecondDerivative.apply(*[out[i].detach().requires_grad_() for i in at])
+        out = list(out)
+        for i, g in zip(at, guarded):
+            out[i] = g
+        return tuple(out)
+
+    return wrapped
+
+
 def monarch_forward(x, w1, w2, act: int = B.ACT_NONE, stream=None):
     fi, fo, nb1, nb2, b = problem_of(x, w1, w2)
     _check(x, w1, w2)
@@ -486,6 +520,7 @@ class SandwichFunction(torch.autograd.Function):
         return n if ctx.alone else (h_out, n)
 
     @staticmethod
+    @_first_derivative_only
     def backward(ctx, *grads):
         h_out, y, stats, *affine = ctx.saved_tensors
         dh_out, dn = (None, grads[0]) if ctx.alone else grads
@@ -629,6 +664,7 @@ class DistillLossFunction(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @_first_derivative_only
     def backward(ctx, dloss):
         dz = distill_backward(dloss.contiguous(), *ctx.saved_tensors, **ctx.how)
         return dz, None, None, None, None, None

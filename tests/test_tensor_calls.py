@@ -29,3 +29,57 @@ def test_a_raw_stream_is_the_one_named(monkeypatch, handle):
     streams = Streams(monkeypatch)
     streams.current = [0x1234]   # the caller's current stream is another one
     assert T._on_stream(handle, lambda: streams.current[-1]) == handle
+
+
+def _without_kernels(monkeypatch):
+    """Stand-ins for the library's calls: the right shapes, any values."""
+    def forward(h, y=None, *par, **how):
+        return (h if y is None else h.detach() + y.detach()), h.detach().clone(), torch.zeros(len(h), 4)
+
+    def backward(dh_out, dn, h_out, y, stats, *par, **how):
+        like = lambda t: None if t is None else torch.ones_like(t)  # noqa: E731
+        return T.SandwichGrads(like(h_out), like(y), *map(like, par))
+
+    monkeypatch.setattr(T, "sandwich_forward", forward)
+    monkeypatch.setattr(T, "sandwich_backward", backward)
+    monkeypatch.setattr(T, "distill_forward", lambda z, *a, **how: (z.detach().sum(1), torch.zeros(len(z), 4)))
+    monkeypatch.setattr(T, "distill_backward", lambda dloss, z, *a, **how: torch.ones_like(z))
+
+
+def _sandwich(x):
+    w = torch.nn.Parameter(torch.ones(x.shape[1]))
+    return T.SandwichFunction.apply(x, x * x, w, None, None, w, None,
+                                    dict(post_norm=1, pre_norm=1, skip_scale=1.0, branch_scale=1.0, eps=1e-5))[1]
+
+
+def _distill(x):
+    return T.DistillLossFunction.apply(x, torch.zeros(len(x), 2), torch.zeros(len(x), 2, dtype=torch.int64), None)
+
+
+@pytest.mark.parametrize("call", [_sandwich, _distill])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_second_derivatives_are_refused(monkeypatch, call, weighted):
+    """A penalty on a gradient must not lose the part that goes through a kernel, whatever else is in it."""
+    _without_kernels(monkeypatch)
+    x = torch.randn(3, 4, requires_grad=True)
+    out = call(x)
+    s = (out * x.sum()).sum() if weighted else out.sum() + (x ** 3).sum()
+    g, = torch.autograd.grad(s, x, create_graph=True)
+    with pytest.raises(RuntimeError, match="second"):
+        (g * g).sum().backward()
+    # the first derivative is there, with and without a graph of its own
+    assert torch.equal(g.detach(), torch.autograd.grad((call(x) * x.sum()).sum() if weighted else call(x).sum() + (x ** 3).sum(), x)[0])
+
+
+def test_gradients_with_a_graph_can_be_scaled_and_cleared(monkeypatch):
+    """backward(create_graph=True) leaves gradients that clipping and zero_grad may write to."""
+    _without_kernels(monkeypatch)
+    x = torch.randn(3, 4, requires_grad=True)
+    for _ in range(2):
+        out = _sandwich(x)
+        out.sum().backward(create_graph=True)
+        torch.nn.utils.clip_grad_norm_([x], 0.5)
+        with torch.no_grad():
+            x.grad.mul_(2.0)
+        x.grad.detach_().zero_()
+        assert x.grad is not None and not x.grad.any()

@@ -40,3 +40,17 @@ def test_default_stream_by_its_handle(api):
     torch.cuda.synchronize()
     for i, (x, w) in enumerate(zip(got, want)):
         assert torch.equal(x, w), i
+
+
+def test_second_derivatives_are_refused(api):
+    """The first derivative with create_graph=True is the one without; its own derivative raises."""
+    torch.manual_seed(1)
+    x = torch.randn(6, 40, device="cuda", requires_grad=True)
+    m = api.SandwichNorm(40, device="cuda")
+    t, ids = torch.randn(6, 3, device="cuda"), torch.randint(0, 40, (6, 3), device="cuda")
+    for call in (lambda: m(x, x * 2.0)[1].square().sum() + (x ** 3).sum(),
+                 lambda: api.DistillLossFunction.apply(x, t, ids, None).sum() + (x ** 3).sum()):
+        g, = torch.autograd.grad(call(), x, create_graph=True)
+        assert torch.equal(g.detach(), torch.autograd.grad(call(), x)[0])
+        with pytest.raises(RuntimeError, match="second"):
+            g.square().sum().backward()
