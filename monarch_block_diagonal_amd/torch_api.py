@@ -169,6 +169,7 @@ class MonarchLinearFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_derivative_only
     def backward(ctx, dy):
         x, w1, w2, z, y = ctx.saved_tensors
         dx, dw1, dw2 = monarch_backward(dy.contiguous(), x, w1, w2, z, y, ctx.act)
@@ -243,6 +244,7 @@ class MonarchLinearExFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_derivative_only
     def backward(ctx, dy):
         x, w1, w2, z, y = ctx.saved_tensors
         dx, dw1, dw2, db = monarch_backward_ex(dy.contiguous(), x, w1, w2, z, y, ctx.with_bias,

@@ -83,3 +83,19 @@ def test_gradients_with_a_graph_can_be_scaled_and_cleared(monkeypatch):
             x.grad.mul_(2.0)
         x.grad.detach_().zero_()
         assert x.grad is not None and not x.grad.any()
+
+
+def test_second_derivatives_of_the_layers_are_refused(monkeypatch):
+    zeros = lambda *a, **k: (torch.zeros(3, 4), torch.zeros(3, 4))  # noqa: E731
+    ones = lambda *ts: tuple(torch.ones_like(t) for t in ts)  # noqa: E731
+    monkeypatch.setattr(T, "monarch_forward", zeros)
+    monkeypatch.setattr(T, "monarch_forward_ex", zeros)
+    monkeypatch.setattr(T, "monarch_backward", lambda dy, x, w1, w2, z, *a: ones(x, w1, w2))
+    monkeypatch.setattr(T, "monarch_backward_ex", lambda dy, x, w1, w2, z, *a: (*ones(x, w1, w2), None))
+    w = torch.nn.Parameter(torch.ones(2, 2, 2))
+    for call in (lambda x: T.MonarchLinearFunction.apply(x, w, w),
+                 lambda x: T.MonarchLinearExFunction.apply(x, w, w, None, 4)):
+        x = torch.randn(3, 4, requires_grad=True)
+        g, = torch.autograd.grad(call(x).sum() + (x ** 3).sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError, match="second"):
+            (g * g).sum().backward()
