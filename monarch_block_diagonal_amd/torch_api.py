@@ -600,7 +600,10 @@ def _distill_out(logits, rows, vocab, ld, device, out):
     _expect(out, (rows, vocab), "out")
     if out.dtype != logits.dtype or out.get_device() != device:
         raise ValueError("out must have the logits' dtype and device")
-    return out, _rows_apart(out, rows, vocab, "out")
+    dld = _rows_apart(out, rows, vocab, "out")
+    # the library writes behind autograd's back: a backward pass that saved out's present values has to raise
+    torch.autograd.graph.increment_version(out)
+    return out, dld
 
 
 def distill_forward(logits, teacher, ids, labels=None, *, temperature: float = 1.0,

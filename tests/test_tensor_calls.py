@@ -99,3 +99,34 @@ def test_second_derivatives_of_the_layers_are_refused(monkeypatch):
         g, = torch.autograd.grad(call(x).sum() + (x ** 3).sum(), x, create_graph=True)
         with pytest.raises(RuntimeError, match="second"):
             (g * g).sum().backward()
+
+
+@pytest.mark.parametrize("kind", ["step", "backward"])
+def test_overwritten_logits_are_seen_by_autograd(monkeypatch, kind):
+    """out=logits replaces values that a backward pass may have saved: that pass raises, as after any write in place."""
+    monkeypatch.setattr(T, "_distill_shapes", lambda z, *a: (*z.shape, 2, z.shape[1], -1))
+    monkeypatch.setattr(T, "_saved", lambda *a: None)
+    monkeypatch.setattr(T.B, "monarch_distill_step", lambda *a: None)
+    monkeypatch.setattr(T.B, "monarch_distill_bwd", lambda *a: None)
+    t, ids, stats = torch.zeros(3, 2), torch.zeros(3, 2, dtype=torch.int64), torch.zeros(3, 4)
+
+    def write(z, out):
+        if kind == "step":
+            return T.distill_step(z, t, ids, out=out)[1]
+        return T.distill_backward(torch.ones(3), z, t, ids, None, stats, out=out)
+
+    x = torch.randn(3, 5, requires_grad=True)
+    z = torch.tanh(x)   # tanh saves its result for its backward pass
+    dz = write(z.detach(), z.detach())
+    assert dz.data_ptr() == z.data_ptr()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward(dz)
+    z = x * 2.0         # a product by a number saves nothing of its result
+    z.backward(write(z.detach(), z.detach()))
+    z = torch.tanh(x)   # memory of its own, or the library's: nothing to see
+    z.backward(write(z.detach(), torch.empty(3, 5)))
+    z = torch.tanh(x)
+    z.backward(write(z.detach(), None))
+    with torch.inference_mode():   # tensors without a version
+        a = torch.ones(3, 5)
+        write(a, a)

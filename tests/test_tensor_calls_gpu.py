@@ -54,3 +54,18 @@ def test_second_derivatives_are_refused(api):
         assert torch.equal(g.detach(), torch.autograd.grad(call(), x)[0])
         with pytest.raises(RuntimeError, match="second"):
             g.square().sum().backward()
+
+
+def test_overwritten_logits_are_seen_by_autograd(api):
+    torch.manual_seed(2)
+    x = torch.randn(5, 64, device="cuda", requires_grad=True)
+    t, ids = torch.randn(5, 3, device="cuda"), torch.randint(0, 64, (5, 3), device="cuda")
+    z = 8.0 * x
+    _, want = api.distill_step(z.detach().clone(), t, ids)
+    _, dz = api.distill_step(z.detach(), t, ids, out=z.detach())
+    z.backward(dz)
+    assert torch.equal(x.grad, 8.0 * want)
+    z = torch.tanh(x)
+    _, dz = api.distill_step(z.detach(), t, ids, out=z.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward(dz)
