@@ -593,8 +593,13 @@ def _rows_apart(t, rows, cols, name):
 
 
 def _distill_out(logits, rows, vocab, ld, device, out):
-    """(dlogits, its ld): in the logits' own layout, or `out` after checking it."""
+    """(dlogits, its ld): `out` after checking it, or new memory. That has the logits' own
+    layout where their rows have little padding (up to an eighth); rows that lie further
+    apart (a position of a sequence, every k-th row) are stored side by side, each at the
+    offset from a 16-byte boundary that it has in the logits."""
     if out is None:
+        if ld - vocab > vocab // 8:
+            ld = vocab + (ld - vocab) % (16 // logits.element_size())
         out = torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)
         return (out if ld == vocab else out[:, :vocab]), ld
     _expect(out, (rows, vocab), "out")

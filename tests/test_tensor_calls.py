@@ -130,3 +130,21 @@ def test_overwritten_logits_are_seen_by_autograd(monkeypatch, kind):
     with torch.inference_mode():   # tensors without a version
         a = torch.ones(3, 5)
         write(a, a)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_of_rows_far_apart_are_stored_close(dtype):
+    """dlogits takes the memory of the gradient, not that of the tensor whose rows the logits are."""
+    per = 16 // dtype.itemsize
+    for logits in (torch.zeros(16, 20, 501, dtype=dtype)[:, -1], torch.zeros(40, 1001, dtype=dtype)[::3], torch.zeros(9, 700, dtype=dtype)[:, :300],
+                   torch.zeros(9, 304, dtype=dtype)[:, :300], torch.zeros(9, 301, dtype=dtype), torch.zeros(5, 7, dtype=dtype)[:, :2]):
+        rows, vocab = logits.shape
+        ld = T._rows_apart(logits, rows, vocab, "logits")
+        dz, dld = T._distill_out(logits, rows, vocab, ld, -1, None)
+        assert dz.shape == logits.shape and dz.dtype == dtype and dz.stride() == (dld, 1)
+        room = dz.untyped_storage().nbytes() // dtype.itemsize
+        assert room <= rows * (vocab + max(vocab // 8, per))
+        # rows of the gradient start where rows of the logits do between two 16-byte boundaries
+        assert (dld - ld) % per == 0
+    padded = torch.zeros(4, 50304, dtype=dtype)[:, :50257]   # a little padding stays: rows start at cache lines
+    assert T._distill_out(padded, 4, 50257, 50304, -1, None)[1] == 50304

@@ -69,3 +69,19 @@ def test_overwritten_logits_are_seen_by_autograd(api):
     _, dz = api.distill_step(z.detach(), t, ids, out=z.detach())
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         z.backward(dz)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_of_a_sequence_s_last_position(api, dtype):
+    """Rows far apart: the gradient of the same rows side by side, in memory of its own size."""
+    torch.manual_seed(3)
+    full = torch.randn(16, 30, 501, device="cuda").to(dtype)
+    t, ids = torch.randn(16, 4, device="cuda"), torch.randint(0, 501, (16, 4), device="cuda")
+    loss, dz = api.distill_step(full[:, -1], t, ids, temperature=2.0)
+    want = api.distill_step(full[:, -1].contiguous(), t, ids, temperature=2.0)
+    for got, w in ((loss, want[0]), (dz, want[1])):
+        torch.testing.assert_close(got, w, rtol=2.0 ** -7 if dtype == torch.bfloat16 else 1e-5, atol=1e-6)
+    assert dz.untyped_storage().nbytes() < 16 * 520 * dtype.itemsize
+    x = full.clone().requires_grad_()
+    api.DistillLossFunction.apply(x[:, -1], t, ids, None, 2.0).sum().backward()
+    assert torch.equal(x.grad[:, -1], dz) and not x.grad[:, :-1].any()
