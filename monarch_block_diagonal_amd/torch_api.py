@@ -506,15 +506,22 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
     return g
 
 
+def _whole(t):
+    """t as the library takes it: contiguous, and at a 16-byte boundary (a slice of odd rows is not)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class SandwichFunction(torch.autograd.Function):
     """sandwich_forward's (h_out, n) with gradients; n alone without y, None for
     the n of NORM_NONE."""
 
     @staticmethod
     def forward(ctx, h, y, post_weight, post_bias, gate, pre_weight, pre_bias, how):
-        affine = [None if t is None else t.contiguous()
-                  for t in (post_weight, post_bias, gate, pre_weight, pre_bias)]
-        h, y = h.contiguous(), None if y is None else y.contiguous()
+        affine = [_whole(t) for t in (post_weight, post_bias, gate, pre_weight, pre_bias)]
+        h, y = _whole(h), _whole(y)
         h_out, n, stats = sandwich_forward(h, y, *affine, **how)
         ctx.how, ctx.alone = how, y is None
         ctx.set_materialize_grads(False)
@@ -530,8 +537,7 @@ class SandwichFunction(torch.autograd.Function):
             dn = torch.zeros_like(h_out)
         if dh_out is None and ctx.how["pre_norm"] == B.NORM_NONE:
             dh_out = torch.zeros_like(h_out)
-        cont = lambda t: None if t is None else t.contiguous()  # noqa: E731
-        return (*sandwich_backward(cont(dh_out), cont(dn), h_out, y, stats, *affine, **ctx.how), None)
+        return (*sandwich_backward(_whole(dh_out), _whole(dn), h_out, y, stats, *affine, **ctx.how), None)
 
 
 class SandwichNorm(torch.nn.Module):

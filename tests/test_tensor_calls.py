@@ -148,3 +148,31 @@ def test_gradients_of_rows_far_apart_are_stored_close(dtype):
         assert (dld - ld) % per == 0
     padded = torch.zeros(4, 50304, dtype=dtype)[:, :50257]   # a little padding stays: rows start at cache lines
     assert T._distill_out(padded, 4, 50257, 50304, -1, None)[1] == 50304
+
+
+def _off(*shape):
+    """A contiguous tensor that starts between two 16-byte boundaries, as a slice of odd rows does."""
+    n = 1
+    for s in shape:
+        n *= s
+    t = torch.randn(n + 1)[1:].view(shape)
+    assert t.is_contiguous() and t.data_ptr() % 16
+    return t
+
+
+def test_sandwich_function_takes_slices(monkeypatch):
+    """x[1:] of odd rows, and the gradients that cat hands back, start anywhere; the library's tensors may not."""
+    def aligned(*ts):
+        assert all(t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0) for t in ts)
+
+    _without_kernels(monkeypatch)
+    forward, backward = T.sandwich_forward, T.sandwich_backward
+    monkeypatch.setattr(T, "sandwich_forward", lambda h, y, *par, **how: (aligned(h, y, *par), forward(h, y, *par, **how))[1])
+    monkeypatch.setattr(T, "sandwich_backward", lambda *a, **how: (aligned(*a), backward(*a, **how))[1])
+    how = dict(post_norm=1, pre_norm=1, skip_scale=1.0, branch_scale=1.0, eps=1e-5)
+    h, y, gate = (t.requires_grad_() for t in (_off(3, 5), _off(3, 5), _off(3, 5)))
+    w, b = _off(5), _off(5)
+    h_out, n = T.SandwichFunction.apply(h, y, w, b, gate, w, b, how)
+    torch.cat([torch.ones(1, 5), h_out, n]).square().sum().backward()
+    assert h.grad is not None and gate.grad.shape == gate.shape
+    T.SandwichFunction.apply(h, None, None, None, None, w, b, how).sum().backward()

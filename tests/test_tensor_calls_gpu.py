@@ -85,3 +85,21 @@ def test_gradient_of_a_sequence_s_last_position(api, dtype):
     x = full.clone().requires_grad_()
     api.DistillLossFunction.apply(x[:, -1], t, ids, None, 2.0).sum().backward()
     assert torch.equal(x.grad[:, -1], dz) and not x.grad[:, :-1].any()
+
+
+@pytest.mark.parametrize("d", [625, 33])
+def test_sandwich_norm_between_slices_of_odd_rows(api, d):
+    """h[1:] and what cat hands back lie off every 16-byte boundary: results and gradients of the aligned copies."""
+    torch.manual_seed(4)
+    m = api.SandwichNorm(d, bias=True, device="cuda")
+    h, y = torch.randn(8, d, device="cuda", requires_grad=True), torch.randn(8, d, device="cuda", requires_grad=True)
+    head = torch.randn(1, d, device="cuda")
+    h_out, n = m(h[1:], y[1:])
+    torch.cat([head, h_out, n]).square().sum().backward()
+    got = [h_out, n, h.grad, y.grad]
+    h2, y2 = (t.detach()[1:].clone().requires_grad_() for t in (h, y))
+    h_out, n = m(h2, y2)
+    (h_out.square().sum() + n.square().sum()).backward()
+    assert torch.equal(got[0], h_out) and torch.equal(got[1], n)
+    assert torch.equal(got[2][1:], h2.grad) and torch.equal(got[3][1:], y2.grad)
+    assert not got[2][0].any() and not got[3][0].any()
