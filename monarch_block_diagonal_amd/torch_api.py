@@ -74,6 +74,14 @@ def _check(*ts):
             raise ValueError("tensors must live on the GPU")
 
 
+def _whole(t):
+    """t as the library takes it: contiguous, and at a 16-byte boundary (a slice of odd rows is not)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class _NoSecondDerivative(torch.autograd.Function):
     """Hands gradients on, and raises where they are differentiated."""
 
@@ -162,7 +170,7 @@ class MonarchLinearFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w1, w2, act: int = B.ACT_NONE):
-        x, w1, w2 = x.contiguous(), w1.contiguous(), w2.contiguous()
+        x, w1, w2 = _whole(x), _whole(w1), _whole(w2)
         y, z = monarch_forward(x, w1, w2, act)
         ctx.act = act
         ctx.save_for_backward(x, w1, w2, z, y if act == B.ACT_RELU else None)
@@ -172,7 +180,7 @@ class MonarchLinearFunction(torch.autograd.Function):
     @_first_derivative_only
     def backward(ctx, dy):
         x, w1, w2, z, y = ctx.saved_tensors
-        dx, dw1, dw2 = monarch_backward(dy.contiguous(), x, w1, w2, z, y, ctx.act)
+        dx, dw1, dw2 = monarch_backward(_whole(dy), x, w1, w2, z, y, ctx.act)
         return dx, dw1, dw2, None
 
 
@@ -235,8 +243,8 @@ class MonarchLinearExFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w1, w2, bias, out_features: int, act: int = B.ACT_NONE):
-        x, w1, w2 = x.contiguous(), w1.contiguous(), w2.contiguous()
-        bias = bias.contiguous() if bias is not None else None
+        x, w1, w2 = _whole(x), _whole(w1), _whole(w2)
+        bias = _whole(bias)
         y, z = monarch_forward_ex(x, w1, w2, out_features, bias, act)
         ctx.act = act
         ctx.with_bias = bias is not None
@@ -247,8 +255,7 @@ class MonarchLinearExFunction(torch.autograd.Function):
     @_first_derivative_only
     def backward(ctx, dy):
         x, w1, w2, z, y = ctx.saved_tensors
-        dx, dw1, dw2, db = monarch_backward_ex(dy.contiguous(), x, w1, w2, z, y, ctx.with_bias,
-                                               ctx.act)
+        dx, dw1, dw2, db = monarch_backward_ex(_whole(dy), x, w1, w2, z, y, ctx.with_bias, ctx.act)
         return dx, dw1, dw2, db, None, None
 
 
@@ -504,14 +511,6 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
                            g.dpre_weight, g.dpre_bias, ws, need, rows, d, gates, post_norm,
                            pre_norm, skip_scale, branch_scale, code)
     return g
-
-
-def _whole(t):
-    """t as the library takes it: contiguous, and at a 16-byte boundary (a slice of odd rows is not)."""
-    if t is None:
-        return None
-    t = t.contiguous()
-    return t.clone() if t.data_ptr() % 16 else t
 
 
 class SandwichFunction(torch.autograd.Function):

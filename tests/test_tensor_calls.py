@@ -176,3 +176,24 @@ def test_sandwich_function_takes_slices(monkeypatch):
     torch.cat([torch.ones(1, 5), h_out, n]).square().sum().backward()
     assert h.grad is not None and gate.grad.shape == gate.shape
     T.SandwichFunction.apply(h, None, None, None, None, w, b, how).sum().backward()
+
+
+def test_layer_functions_take_slices(monkeypatch):
+    def aligned(*ts):
+        assert all(t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0) for t in ts if t is None or torch.is_tensor(t))
+
+    def fwd(x, w1, w2, *a):
+        aligned(x, w1, w2, *a)
+        return torch.zeros(3, 5), torch.zeros(3, 6)
+
+    def bwd(dy, x, w1, w2, *a):
+        aligned(dy, x, w1, w2, *a)
+        return tuple(torch.ones_like(t) for t in (x, w1, w2))
+
+    monkeypatch.setattr(T, "monarch_forward", fwd)
+    monkeypatch.setattr(T, "monarch_forward_ex", lambda x, w1, w2, out, bias, act: fwd(x, w1, w2, bias))
+    monkeypatch.setattr(T, "monarch_backward", bwd)
+    monkeypatch.setattr(T, "monarch_backward_ex", lambda *a: (*bwd(*a), torch.ones(5)))
+    x, w, b = (t.requires_grad_() for t in (_off(3, 5), _off(2, 3, 3), _off(5)))
+    for out in (T.MonarchLinearFunction.apply(x, w, w), T.MonarchLinearExFunction.apply(x, w, w, b, 5)):
+        torch.cat([torch.ones(1, 5), out]).square().sum().backward()

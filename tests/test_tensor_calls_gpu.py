@@ -103,3 +103,15 @@ def test_sandwich_norm_between_slices_of_odd_rows(api, d):
     assert torch.equal(got[0], h_out) and torch.equal(got[1], n)
     assert torch.equal(got[2][1:], h2.grad) and torch.equal(got[3][1:], y2.grad)
     assert not got[2][0].any() and not got[3][0].any()
+
+
+def test_layer_between_slices_of_odd_rows(api):
+    torch.manual_seed(5)
+    m = api.MonarchLinear(33, 65, 4, device="cuda")
+    x = torch.randn(9, 33, device="cuda", requires_grad=True)
+    y = m(x[1:])
+    torch.cat([torch.ones(1, 65, device="cuda"), y]).square().sum().backward()
+    x2 = x.detach()[1:].clone().requires_grad_()
+    y2 = m(x2)
+    y2.square().sum().backward()
+    assert torch.equal(y, y2) and torch.equal(x.grad[1:], x2.grad) and not x.grad[0].any()
