@@ -426,8 +426,9 @@ def _sandwich_shapes(h, y, post_weight, post_bias, gate, pre_weight, pre_bias, p
             pre_weight, pre_bias)
     gates = 0
     if gate is not None:
-        gates = gate.shape[0] if gate.dim() == 2 else 0
-        if gates == 0 or rows % gates or (rows and gates > rows):
+        gates = gate.shape[0] if gate.dim() == 2 else -1
+        # no rows: any number of gate rows, none too
+        if gates < 0 or (rows and (gates == 0 or rows % gates)):
             raise ValueError(f"gate has shape {tuple(gate.shape)}, expected (gates, {d}) with gates "
                              f"dividing {rows} rows")
         _beside(device, dtype, (gates, d), "gate", gate)

@@ -197,3 +197,15 @@ def test_layer_functions_take_slices(monkeypatch):
     x, w, b = (t.requires_grad_() for t in (_off(3, 5), _off(2, 3, 3), _off(5)))
     for out in (T.MonarchLinearFunction.apply(x, w, w), T.MonarchLinearExFunction.apply(x, w, w, b, 5)):
         torch.cat([torch.ones(1, 5), out]).square().sum().backward()
+
+
+def test_a_gate_a_row_of_no_rows(monkeypatch):
+    """An empty batch has no gate rows either; a batch with rows needs some."""
+    monkeypatch.setattr(T.B, "current_device", lambda: -1)   # a CPU tensor's device
+    shapes = lambda h, y, gate: T._sandwich_shapes(h, y, None, None, gate, None, None, 1, 1.0)[:3]  # noqa: E731
+    none = torch.empty(0, 64)
+    assert shapes(none, none, torch.empty(0, 64)) == (0, 64, 0)
+    assert shapes(none, none, torch.ones(3, 64)) == (0, 64, 3)
+    for h, gate in ((torch.ones(2, 64), torch.empty(0, 64)), (none, torch.empty(0, 63)), (none, torch.empty(0)), (none, torch.empty(64))):
+        with pytest.raises(ValueError):
+            shapes(h, h.clone(), gate)

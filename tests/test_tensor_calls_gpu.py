@@ -115,3 +115,18 @@ def test_layer_between_slices_of_odd_rows(api):
     y2 = m(x2)
     y2.square().sum().backward()
     assert torch.equal(y, y2) and torch.equal(x.grad[1:], x2.grad) and not x.grad[0].any()
+
+
+def test_no_rows_with_a_gate(api):
+    """An empty batch: with a gate a row, with one that every row shares, through the module."""
+    none, w = torch.empty(0, 64, device="cuda"), torch.ones(64, device="cuda")
+    for gate in (torch.empty(0, 64, device="cuda"), torch.ones(1, 64, device="cuda"), torch.ones(3, 64, device="cuda")):
+        h_out, n, stats = api.sandwich_forward(none, none.clone(), w, None, gate, w, None)
+        g = api.sandwich_backward(none, none, h_out, none, stats, w, None, gate, w, None)
+        assert h_out.shape == n.shape == (0, 64) and g.dgate.shape == gate.shape and not g.dgate.any()
+        assert not g.dpost_weight.any() and not g.dpre_weight.any()
+    m = api.SandwichNorm(64, device="cuda")
+    h = torch.empty(2, 0, 64, device="cuda", requires_grad=True)
+    h_out, n = m(h, h * 1.0, gate=torch.empty(0, 64, device="cuda"))
+    (h_out.sum() + n.sum()).backward()
+    assert h.grad.shape == h.shape and not m.pre_weight.grad.any()
