@@ -669,18 +669,30 @@ def distill_step(logits, teacher, ids, labels=None, row_weight=None, *, temperat
 
 
 class DistillLossFunction(torch.autograd.Function):
-    """distill_forward's loss [rows] with its gradient by the logits. Where the
-    rows' weights are known before the loss, distill_step is one pass instead of two."""
+    """distill_forward's loss with its gradient by the logits, for logits [..., vocab], teacher
+    and ids [..., top] and labels [...]: one loss a row, [...]. What does not lie as the
+    library takes it is copied. Where the rows' weights are known before the loss,
+    distill_step is one pass instead of two."""
 
     @staticmethod
     def forward(ctx, logits, teacher, ids, labels, temperature: float = 1.0, mix: float = 1.0):
+        lead = logits.shape[:-1]
+        for t, shape, name in ((teacher, (*lead, teacher.shape[-1]), "teacher"), (ids, teacher.shape, "ids"),
+                               (labels, lead, "labels")):
+            _expect(t, shape, name)
+        flat = lambda t: t.reshape(lead.numel(), t.shape[-1])  # noqa: E731
+        z = flat(logits)
+        if z.numel() and (z.stride(1) != 1 or z.stride(0) < z.shape[1]):
+            z = z.contiguous()
+        saved = (z, flat(teacher).contiguous(), flat(ids).contiguous(),
+                 None if labels is None else labels.reshape(lead.numel()).contiguous())
         ctx.how = dict(temperature=temperature, mix=mix)
-        loss, stats = distill_forward(logits, teacher, ids, labels, **ctx.how)
-        ctx.save_for_backward(logits, teacher, ids, labels, stats)
-        return loss
+        loss, stats = distill_forward(*saved, **ctx.how)
+        ctx.save_for_backward(*saved, stats)
+        return loss.view(lead)
 
     @staticmethod
     @_first_derivative_only
     def backward(ctx, dloss):
-        dz = distill_backward(dloss.contiguous(), *ctx.saved_tensors, **ctx.how)
-        return dz, None, None, None, None, None
+        dz = distill_backward(dloss.reshape(-1).contiguous(), *ctx.saved_tensors, **ctx.how)
+        return dz.view(*dloss.shape, dz.shape[1]), None, None, None, None, None

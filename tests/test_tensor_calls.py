@@ -209,3 +209,40 @@ def test_a_gate_a_row_of_no_rows(monkeypatch):
     for h, gate in ((torch.ones(2, 64), torch.empty(0, 64)), (none, torch.empty(0, 63)), (none, torch.empty(0)), (none, torch.empty(64))):
         with pytest.raises(ValueError):
             shapes(h, h.clone(), gate)
+
+
+def test_distill_function_takes_batches_of_sequences_and_slices(monkeypatch):
+    """[batch, tokens, vocab] logits, a slice of a stored teacher, a transposed label: rows reach the library as it takes them."""
+    def rows(z, t, ids, labels):
+        assert z.dim() == t.dim() == ids.dim() == 2 and len(z) == len(t) == len(ids) and z.stride(1) == 1 and z.stride(0) >= z.shape[1]
+        assert t.is_contiguous() and ids.is_contiguous() and (labels is None or (labels.dim() == 1 and labels.is_contiguous()))
+
+    def forward(z, t, ids, labels, **how):
+        rows(z, t, ids, labels)
+        return z.sum(1) + t.sum(1) + (0 if labels is None else labels), torch.zeros(len(z), 4)
+
+    def backward(dloss, z, t, ids, labels, stats, **how):
+        rows(z, t, ids, labels)
+        assert dloss.dim() == 1 and dloss.is_contiguous() and len(dloss) == len(z)
+        return dloss[:, None] * z
+
+    monkeypatch.setattr(T, "distill_forward", forward)
+    monkeypatch.setattr(T, "distill_backward", backward)
+    for lead in ((6,), (2, 3), (2, 1, 3), (), (0, 3)):
+        z = torch.randn(*lead, 5).requires_grad_()
+        t, ids = torch.randn(*lead, 4)[..., :2], torch.zeros(*lead, 4, dtype=torch.int64)[..., :2]
+        labels = torch.zeros(lead[::-1], dtype=torch.int64)
+        labels = labels.permute(tuple(range(len(lead)))[::-1])
+        w = torch.rand(lead)
+        for given in (z, torch.cat([z, z], -1)[..., 5:], z.detach().transpose(0, -1).contiguous().transpose(0, -1).requires_grad_()):
+            loss = T.DistillLossFunction.apply(given, t, ids, labels)
+            assert loss.shape == torch.Size(lead)
+            g, = torch.autograd.grad((loss * w).sum(), given)
+            assert torch.equal(g, w[..., None] * given)
+        loss = T.DistillLossFunction.apply(z, t[..., :0], ids[..., :0], None, 2.0, 0.5)
+        assert loss.shape == torch.Size(lead)
+    z, t, ids = torch.randn(2, 3, 5), torch.randn(3, 2, 4), torch.zeros(2, 3, 4, dtype=torch.int64)
+    for args in ((z, t, ids, None), (z, t.view(2, 3, 4), ids.view(3, 2, 4), None), (z, t.view(2, 3, 4), ids, torch.zeros(3, 2, dtype=torch.int64)),
+                 (z, t.view(2, 3, 4), ids, torch.zeros(6, dtype=torch.int64)), (z, t.view(6, 4), ids.view(6, 4), None)):
+        with pytest.raises(ValueError):
+            T.DistillLossFunction.apply(*args)

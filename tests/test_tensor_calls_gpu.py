@@ -130,3 +130,19 @@ def test_no_rows_with_a_gate(api):
     h_out, n = m(h, h * 1.0, gate=torch.empty(0, 64, device="cuda"))
     (h_out.sum() + n.sum()).backward()
     assert h.grad.shape == h.shape and not m.pre_weight.grad.any()
+
+
+def test_distill_function_of_sequences(api):
+    """[batch, tokens, vocab] logits without their last position, the first entries of a stored teacher."""
+    torch.manual_seed(6)
+    z = torch.randn(3, 8, 333, device="cuda", requires_grad=True)
+    t, ids = torch.randn(3, 7, 20, device="cuda"), torch.randint(0, 333, (3, 7, 20), device="cuda")
+    labels, w = torch.randint(0, 333, (3, 8), device="cuda"), torch.rand(3, 7, device="cuda")
+    loss = api.DistillLossFunction.apply(z[:, :-1], t[..., :5], ids[..., :5], labels[:, 1:], 2.0, 0.5)
+    (loss * w).sum().backward()
+    rows = lambda x: x.reshape(21, *x.shape[2:]).contiguous()  # noqa: E731
+    zr = rows(z.detach()[:, :-1])
+    want, stats = api.distill_forward(zr, rows(t[..., :5]), rows(ids[..., :5]), rows(labels[:, 1:]), temperature=2.0, mix=0.5)
+    dz = api.distill_backward(rows(w), zr, rows(t[..., :5]), rows(ids[..., :5]), rows(labels[:, 1:]), stats, temperature=2.0, mix=0.5)
+    assert torch.equal(loss, want.view(3, 7))
+    assert torch.equal(z.grad[:, :-1], dz.view(3, 7, 333)) and not z.grad[:, -1].any()
