@@ -347,8 +347,8 @@ size_t monarch_sandwich_bwd_workspace_bytes(int64_t rows, int64_t features, int6
 /* Backward pass from dh_out (NULL: zero) and dn (with a norm_pre): dh and dy
  * [rows, features], and the gradients of the parameters, each of which may be
  * NULL when it is not wanted. h_out, y, stats and the parameters are those of the
- * forward call. Without norm_pre, dn and h_out are not used and dh_out is
- * needed. With y NULL only dh, dpre_w and dpre_b are computed (dh with
+ * forward call. Without norm_pre, dn and h_out are not used, dh_out is
+ * needed, and dpre_w and dpre_b have to be NULL. With y NULL only dh, dpre_w and dpre_b are computed (dh with
  * skip_scale). Everything is overwritten; sums over rows run in a fixed order.
  * dh may be dh_out or dn. rows == 0 zeroes the parameters' gradients. */
 int monarch_sandwich_bwd(const void* dh_out, const void* dn, const void* h_out, const void* y,

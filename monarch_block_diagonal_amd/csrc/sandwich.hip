@@ -164,7 +164,7 @@ int monarch_sandwich_bwd(const void* dh_out, const void* dn, const void* h_out, 
     return MONARCH_ERR_ALIGN;
   if (rows > 0 && !y && (dy || dpost_w || dpost_b || dgate)) return MONARCH_ERR_NULL;
   if ((dpost_w && !post_w) || (dpost_b && !post_b) || (dgate && gates == 0) ||
-      (dpre_w && !pre_w) || (dpre_b && !pre_b))
+      (dpre_w && !(has_pre && pre_w)) || (dpre_b && !(has_pre && pre_b)))
     return MONARCH_ERR_NULL;
   const SandwichBwdPlan p = bwd_plan(rows, features, gates, y || rows == 0, post_b != nullptr, has_pre,
                              pre_b != nullptr, bf16);

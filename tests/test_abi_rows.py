@@ -131,3 +131,11 @@ def test_distill_null_and_align():
         assert distill("fwd", **{name: A + by}) == B.MONARCH_ERR_ALIGN, name
     assert distill("step", dz=A + 2) == B.MONARCH_ERR_ALIGN
     assert distill("step", per=A + 2) == B.MONARCH_ERR_ALIGN
+
+
+def test_sandwich_bwd_gradients_of_an_absent_norm():
+    """Without norm_pre its parameters are not used: asking for their gradients is an error, not memory left as it was."""
+    gone = dict(pre=0, dn=None, ho=None)
+    for rows, gates in ((6, 2), (0, 0)):
+        for kw in (dict(dw=A2, db=None), dict(dw=None, db=A2)):
+            assert sandwich_bwd(**gone, rows=rows, gates=gates, dg=A2 if gates else None, **kw) == B.MONARCH_ERR_NULL
