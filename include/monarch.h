@@ -327,8 +327,8 @@ int monarch_dyad_describe(int direction, int64_t in_features, int64_t out_featur
  *   written and may be NULL; skip_scale, the gate and post_* are not used).
  *   stats: fp32 [rows, 4], written by the forward pass for the backward pass
  *   (mean and reciprocal root of y's row, then of h_out's).
- * features <= 16384, gates divides rows. All sums are fp32; each result is
- * rounded once. Outputs must not alias inputs, except that h_out may be h and
+ * features <= 16384, gates divides rows (at most 2^21 where rows is 0). All
+ * sums are fp32; each result is rounded once. Outputs must not alias inputs, except that h_out may be h and
  * n may be y. eps < 0 or a scale that is not finite gives MONARCH_ERR_VALUE,
  * a norm out of range MONARCH_ERR_DTYPE; otherwise errors as for monarch_fwd.
  * rows == 0 returns MONARCH_OK. */

@@ -13,6 +13,8 @@ namespace monarch {
 namespace {
 
 constexpr int64_t kLimit = int64_t(1) << 31;
+// gate rows where there are no rows: each is a workgroup of the join
+constexpr int64_t kEmptyGates = int64_t(1) << 21;
 
 // The smallest team whose threads hold at most `few` (up to a wave) or `many`
 // pieces of a row; `last` for any row that is wider.
@@ -78,7 +80,7 @@ int check_sizes(int64_t rows, int64_t d, int64_t gates, int post, int pre, int d
       pre > MONARCH_NORM_LAYER)
     return MONARCH_ERR_DTYPE;
   if (rows < 0 || rows >= kLimit || d <= 0 || d > kSandwichMaxFeatures || gates < 0) return MONARCH_ERR_SHAPE;
-  if (gates > 0 && (rows % gates != 0 || (rows > 0 && gates > rows))) return MONARCH_ERR_SHAPE;
+  if (gates > (rows > 0 ? rows : kEmptyGates) || (gates > 0 && rows % gates != 0)) return MONARCH_ERR_SHAPE;
   return MONARCH_OK;
 }
 

@@ -139,3 +139,12 @@ def test_sandwich_bwd_gradients_of_an_absent_norm():
     for rows, gates in ((6, 2), (0, 0)):
         for kw in (dict(dw=A2, db=None), dict(dw=None, db=A2)):
             assert sandwich_bwd(**gone, rows=rows, gates=gates, dg=A2 if gates else None, **kw) == B.MONARCH_ERR_NULL
+
+
+def test_sandwich_gate_rows_of_no_rows():
+    """rows == 0 zeroes dgate, whose rows are counted in workgroups: a count past a launch is refused, not cut."""
+    none = dict(rows=0, h=None, y=None, ho=None, n=None, st=None)
+    assert sandwich_fwd(**none, gates=1 << 21) == B.MONARCH_OK
+    for gates in ((1 << 21) + 1, 1 << 31, 1 << 33):
+        assert sandwich_fwd(**none, gates=gates) == B.MONARCH_ERR_SHAPE
+        assert sandwich_bwd(rows=0, gates=gates) == B.MONARCH_ERR_SHAPE
