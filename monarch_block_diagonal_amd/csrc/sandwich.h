@@ -27,9 +27,9 @@ struct SandwichFwd {
 
 // How the rows of a backward call are cut (GATE). CHUNK: chunk c holds rows of one
 // gate row only (chunk / cpg), and its sums are of D alone; the gate and the
-// branch scale are applied when the chunks are joined. RUN: short gate runs, or
-// many; each is summed by one team, which stores its dgate row itself, and the
-// chunk's sums are of g * D. TOKEN: RUN with one row a run.
+// branch scale are applied when the chunks are joined. RUN: many gate runs, or
+// short ones where cutting them does not pay; each is summed by one team, which
+// stores its dgate row itself, and the chunk's sums are of g * D. TOKEN: RUN with one row a run.
 enum { CHUNK = 0, RUN = 1, TOKEN = 2 };
 
 struct SandwichBwd {

@@ -30,7 +30,20 @@ Shape bwd_shape(int64_t d, bool bf16) {
   return shape_of(d, bf16, 32, bf16 ? 512 : 1024, bf16 ? 3 : 4, bf16 ? 2 : 4);
 }
 
-constexpr int64_t kRunRows = 32;     // gate runs up to this long are a team's own
+constexpr int64_t kRunRows = 32;   // gate runs up to this long may be a team's own however few there are
+
+// Whether short gate runs are cut into chunks: where the rows that one team would take
+// in turn cost more than joining the gate rows' sums does. Both are fitted to
+// measured crossovers (runs of 2 to 32 rows, 64 to 16384 features, both types): a row 0.75
+// us and 45 ns an element of a thread, three times that for rows whose sums take their
+// CU's LDS; joining 30 ns a gate row and 3 ns a workgroup of 32 columns. Of 458 drawn
+// sizes 9 came out more than 15% slower than the other way would have (70% at most).
+// Backward and join, cut against whole: 64 x 768 bf16 with 2 gates 9 / 76 us, 16384 x
+// 768 with 512 gates 73 / 91, with 2048 gates 204 / 40; 256 x 16384 with 8 gates 46 / 326.
+bool cut_short_runs(int64_t rows_per_gate, int64_t d, int64_t gates, const Shape& s, bool wide, bool bf16) {
+  const int64_t row = (750 + 45 * s.pieces * (bf16 ? 8 : 4)) * (wide ? 3 : 1);
+  return gates * (30 + 3 * ((d + 31) / 32)) < rows_per_gate * row;
+}
 
 // Everything about a backward call that depends on sizes alone (`with`: which
 // of post_w, post_b, gate, pre_w, pre_b there are, as the sums they need).
@@ -42,12 +55,13 @@ SandwichBwdPlan bwd_plan(int64_t rows, int64_t d, int64_t gates, bool has_y, boo
   p.rows_per_gate = gates > 0 ? rows / gates : rows;
   const int teams = p.shape.team > 64 ? 1 : 256 / p.shape.team;
   // workgroups aimed at: two a CU, one where the sums of a wide row take its LDS
-  const int64_t aim = kSandwichCus * (p.shape.team * p.shape.pieces * (bf16 ? 8 : 4) > 8192 ? 1 : 2);
-  // a gate run is a team's own where it is short, or where there are enough of them
-  // for every team; one run cut into chunks is joined by as many workgroups
-  p.gate = rows == 0 || gates <= 1 || (p.rows_per_gate > kRunRows && gates < aim * teams) ? CHUNK
-           : p.rows_per_gate > 1 ? RUN
-                                 : TOKEN;
+  const bool wide = p.shape.team * p.shape.pieces * (bf16 ? 8 : 4) > 8192;
+  const int64_t aim = kSandwichCus * (wide ? 1 : 2);
+  // a gate run is a team's own where there are enough of them for every team, or where
+  // it is short and cutting it does not pay
+  const bool own = gates >= aim * teams ||
+                   (p.rows_per_gate <= kRunRows && !cut_short_runs(p.rows_per_gate, d, gates, p.shape, wide, bf16));
+  p.gate = rows == 0 || gates <= 1 ? CHUNK : p.rows_per_gate == 1 ? TOKEN : own ? RUN : CHUNK;
   if (rows == 0) {
     p.cpg = 0;   // no chunk: every sum is empty
   } else if (p.gate != CHUNK) {

@@ -148,3 +148,19 @@ def test_sandwich_gate_rows_of_no_rows():
     for gates in ((1 << 21) + 1, 1 << 31, 1 << 33):
         assert sandwich_fwd(**none, gates=gates) == B.MONARCH_ERR_SHAPE
         assert sandwich_bwd(rows=0, gates=gates) == B.MONARCH_ERR_SHAPE
+
+
+def chunks(rows, d, gates, dtype=B.BF16):
+    """Workgroups of the backward kernel: each leaves two partial rows of d."""
+    return M.monarch_sandwich_bwd_workspace_bytes(rows, d, gates, False, dtype) // (2 * d * 4)
+
+
+def test_few_gate_runs_are_cut():
+    """Short gate runs are a team's own where there are enough of them; a few are cut over the chip as long ones are."""
+    for dtype in (B.F32, B.BF16):
+        for rows, d, gates in ((512, 768, 16), (64, 768, 2), (256, 16384, 8), (32 * 256, 768, 256), (128, 64, 4), (2048, 2048, 64), (16 * 16, 8192, 16)):
+            # a row a team (at most 8 a workgroup), or a workgroup a CU
+            assert chunks(rows, d, gates, dtype) >= min(rows // 8, 256), (rows, d, gates, dtype)
+        # many: no partial rows of their own, at most as many chunks as a launch has workgroups
+        for rows, d, gates in ((16384, 768, 2048), (32 * 4096, 768, 4096), (4096, 64, 2048), (4096, 16384, 512)):
+            assert chunks(rows, d, gates, dtype) <= 512, (rows, d, gates, dtype)

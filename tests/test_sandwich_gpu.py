@@ -327,3 +327,22 @@ def test_refusals(api):
                  (h, h, h_out, h, stats.double())):
         with pytest.raises(ValueError):
             api.sandwich_backward(*args)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("rows,d,gates", [(512, 768, 16), (64, 768, 2), (256, 16384, 8), (90, 767, 6), (28, 7, 4), (30, 4095, 3)])
+def test_few_short_gate_runs(api, rows, d, gates, bias, dtype):
+    """Cut into chunks over the whole chip."""
+    compare(api, rows, d, gates, bias, dtype, "rms", "layer", branch=-0.5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("d,gates,run", [
+    (7, 4096, 3), (72, 3000, 5), (135, 700, 2), (136, 700, 32), (767, 700, 2), (768, 1100, 9), (1023, 700, 3), (4095, 512, 2), (4096, 512, 3),
+    (12001, 256, 2), (16384, 256, 2),
+])
+def test_many_short_gate_runs(api, d, gates, run, bias, dtype):
+    """Each a team's own."""
+    compare(api, gates * run, d, gates, bias, dtype, "layer", "rms", branch=-0.5)
