@@ -347,7 +347,9 @@ size_t monarch_sandwich_bwd_workspace_bytes(int64_t rows, int64_t features, int6
 /* Backward pass from dh_out (NULL: zero) and dn (with a norm_pre): dh and dy
  * [rows, features], and the gradients of the parameters, each of which may be
  * NULL when it is not wanted. h_out, y, stats and the parameters are those of the
- * forward call. Without norm_pre, dn and h_out are not used, dh_out is
+ * forward call; h_out is read as it was stored, so in bf16 the gradients carry its
+ * rounding besides their own (dpre_w most, more so where norm_pre is LAYER and a
+ * row's mean is much larger than its spread). Without norm_pre, dn and h_out are not used, dh_out is
  * needed, and dpre_w and dpre_b have to be NULL. With y NULL only dh, dpre_w and dpre_b are computed (dh with
  * skip_scale). Everything is overwritten; sums over rows run in a fixed order.
  * dh may be dh_out or dn. rows == 0 zeroes the parameters' gradients. */
@@ -375,7 +377,8 @@ int monarch_sandwich_describe(int direction, int64_t rows, int64_t features, int
  *   loss[i] = mix * temperature^2 * sum_k p_k (log p_k - log q[id_k])
  *             - (1 - mix) * log s[c]
  * An entry is valid when 0 <= id_k < vocab and t_k > -inf (pad shorter lists with
- * id -1), a label when 0 <= c < vocab (mark ignored rows with any other value, as
+ * id -1; a teacher's NaN is not > -inf, so it is taken for padding, where a NaN among
+ * the student's logits comes out), a label when 0 <= c < vocab (mark ignored rows with any other value, as
  * -100). Entries that name the same id add up. Without a valid entry the first
  * term is 0, without a label the second. A row with neither has loss 0 and
  * gradient 0 whatever its logits hold; so has a row whose logits are -inf

@@ -487,7 +487,8 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
                       branch_scale: float = 1.0, stream=None, eps: float | None = None):
     """SandwichGrads from the gradients dh_out (None: zero) and dn of the
     forward's results. h_out and stats are the forward's (eps is in stats; it is
-    accepted so that both calls take the same keywords)."""
+    accepted so that both calls take the same keywords); in bf16 the gradients
+    carry h_out's rounding besides their own."""
     if stream is not None:
         return _on_stream(stream, sandwich_backward, dh_out, dn, h_out, y, stats, post_weight,
                           post_bias, gate, pre_weight, pre_bias, post_norm=post_norm,
@@ -624,7 +625,7 @@ def distill_forward(logits, teacher, ids, labels=None, *, temperature: float = 1
         loss = mix * temperature^2 * KL(p || softmax(logits / temperature)) + (1 - mix) * CE(labels)
 
     p = softmax(teacher / temperature) over the row's entries, which sit at the
-    columns `ids` (int64; -1 pads). labels (int64) outside the vocabulary are ignored.
+    columns `ids` (int64; -1 pads, and so do teacher logits that are -inf or NaN). labels (int64) outside the vocabulary are ignored.
     stats goes to distill_backward."""
     if stream is not None:
         return _on_stream(stream, distill_forward, logits, teacher, ids, labels,
