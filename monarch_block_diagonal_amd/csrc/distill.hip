@@ -19,12 +19,14 @@
 //
 // Loss and gradient together read and write each logit once: bound by HBM while
 // every CU has many rows to take, by the phases of a row (load, about 20 operations a
-// logit, store) where it has few. Measured: loss of 4096 x 50257 bf16 at T = 2 with
-// labels 77 us, 5.3 TB/s (its arithmetic busy 86% of the time, but no slower than T =
-// 1, which has a tenth less); both of 16384 x 50257
-// bf16 586 us a call, 5.6 TB/s, as a copy; of 1024 x 50257 bf16 (4 rows a CU) 49 us,
-// 4.2 TB/s; of 1000 x 10000 fp32 26.7 us; of 2048 x 131072 fp32, which no CU holds, 480
-// us, 4.5 TB/s. Read twice instead of held, the second took 784 us and the last 718.
+// logit, store) where it has few. Measured (a call among others): loss of 4096 x 50257
+// bf16 at T = 2 with labels 77 us, 5.4 TB/s (its arithmetic busy 86% of the time, but no
+// slower than T = 1, which has a tenth less); both of 16384 x 50257 bf16 588 us, 5.6
+// TB/s, which a copy of that size reaches (40 calls timed one by one: median 594, 583 to
+// 624; in a kernel trace, which runs them apart, median 621, 593 to 648); of 1024 x 50257 bf16 (4
+// rows a CU) 48 us, 4.3 TB/s; of 1000 x 10000 fp32 26.6 us; of 2048 x 131072 fp32, which no
+// CU holds, 486 us, 4.4 TB/s. Read twice instead of held, the second took 784 us and the
+// last 718.
 // Kept out by measurement: workgroups that load their next row into the registers
 // that a gradient frees (621 -> 672 us: the waits at a row's start then cover its
 // stores), and 2^(z c - M) as one fused operation with a second path for rows far

@@ -75,10 +75,10 @@ __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][
 
 // One row a team. A team of 1024 threads leaves room for one workgroup a CU: it
 // takes rows in turn and loads the next one while the present one is normed a
-// second time. Measured (every tensor once): 16384 x 768 bf16 18.7 us, 5.4 TB/s;
-// 10000 x 625 fp32 20.2 us, 5.0 TB/s; 8192 x 16384 bf16 with a gate a row 240 us,
-// 5.6 TB/s, which is what a copy of that size reaches; one row of 768 4.2 us, the
-// launch. Small teams of 32 lanes x 3 pieces beat 64 x 2 for 768 features (20.3
+// second time. Measured (every tensor once; medians of kernel traces): 16384 x 768 bf16
+// 18.9 us, 5.3 TB/s; 10000 x 625 fp32 19.9 us, 5.0 TB/s; 8192 x 16384 bf16 with a gate a
+// row 242 us, 5.5 TB/s, where a copy of that size reaches 5.6; one row of 768 4.0 us,
+// the launch. Small teams of 32 lanes x 3 pieces beat 64 x 2 for 768 features (20.3
 // against 21.1 us): every lane holds whole pieces.
 template <typename T, int TEAM, int P, bool BIAS, Rows R>
 __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 4 : 3) void sandwich_fwd_kernel(SandwichFwd a) {
@@ -215,9 +215,9 @@ struct Sums {
 // x 768 bf16). Wide rows leave no registers for the sums: they lie in LDS (131 KB
 // for 16384 columns; in registers the kernel spilled, 1208 -> 488 us), parameters
 // are read again from the caches, and the next row's dn and h' are under way during
-// the second half of a row. Measured: 16384 x 768 bf16 with 16 gates 29.4 us, 5.1
-// TB/s; 10000 x 625 fp32 with biases 30.4 us, 4.9 TB/s; 8192 x 16384 bf16 with a gate
-// a row 417 us, 5.1 TB/s.
+// the second half of a row. Measured (medians of kernel traces): 16384 x 768 bf16
+// with 16 gates 29.5 us, 5.1 TB/s; 10000 x 625 fp32 with biases 30.4 us, 4.9 TB/s; 8192 x
+// 16384 bf16 with a gate a row 421 us, 5.1 TB/s.
 template <typename T, int TEAM, int P, int GATE, bool BIAS, Rows R>
 __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(SandwichBwd a) {
   constexpr int N = PieceOf<T>::N, WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
@@ -643,9 +643,10 @@ void bwd_launch(const SandwichBwd& a, const SandwichBwdPlan& p, Rows lie, hipStr
     case TOKEN * 2: BWD_GO(TOKEN, false, ROWS); break;       \
     default: BWD_GO(TOKEN, true, ROWS); break;               \
   }
-  // Odd widths have all six kernels too: with one for biases and any gate run, 16384
-  // x 767 bf16 with a gate a row took 66 us (now 52), 2048 x 16383 385 (145) and 310
-  // with a gate for 8 rows (129).
+  // Odd widths have all six kernels too, against one for biases and any gate run. A
+  // gate a row, before and after: 16384 x 767 bf16 66 and 52 us (with biases 71 and 58),
+  // 2048 x 16383 bf16 385 and 145, 2048 x 12001 fp32 191 and 172. It costs rows of about 1000
+  // features with biases a little: 16384 x 1023 bf16 73 and 77, 625 fp32 46.4 and 48.2.
   if (lie == WHOLE) {
     BWD_ANY(WHOLE)
   } else if (lie == CUT) {
