@@ -56,7 +56,7 @@
 extern "C" {
 #endif
 
-#define MONARCH_ABI_VERSION 5
+#define MONARCH_ABI_VERSION 6
 
 typedef enum {
   MONARCH_OK = 0,
@@ -325,11 +325,13 @@ int monarch_dyad_describe(int direction, int64_t in_features, int64_t out_featur
  *   Any of post_w, post_b, pre_w, pre_b may be NULL (1, or 0 for a bias).
  *   y NULL: the norm before the first block. h_out is h (h_out is not
  *   written and may be NULL; skip_scale, the gate and post_* are not used).
- *   stats: fp32 [rows, 4], written by the forward pass for the backward pass
- *   (mean and reciprocal root of y's row, then of h_out's).
+ *   stats: monarch_sandwich_stats_bytes, written by the forward pass for the
+ *   backward pass: fp32 [rows, 4] (mean and reciprocal root of y's row, then of
+ *   h_out's), and in bf16 with y and a norm_pre behind them four more bits of every
+ *   value of h_out than its rounding holds, [rows, ceil(features / 8)] words.
  * features <= 16384, gates divides rows (at most 2^21 where rows is 0). All
- * sums are fp32; each result is rounded once. Outputs must not alias inputs, except that h_out may be h and
- * n may be y. eps < 0 or a scale that is not finite gives MONARCH_ERR_VALUE,
+ * sums are fp32; each result is rounded once. Outputs must not alias inputs,
+ * except that h_out may be h and n may be y. eps < 0 or a scale that is not finite gives MONARCH_ERR_VALUE,
  * a norm out of range MONARCH_ERR_DTYPE; otherwise errors as for monarch_fwd.
  * rows == 0 returns MONARCH_OK. */
 typedef enum { MONARCH_NORM_NONE = 0, MONARCH_NORM_RMS = 1, MONARCH_NORM_LAYER = 2 } monarch_norm;
@@ -340,6 +342,10 @@ int monarch_sandwich_fwd(const void* h, const void* y, const void* post_w, const
                          int post_norm, int pre_norm, float skip_scale, float branch_scale,
                          float eps, int dtype, void* stream, void* const* events, int n_events);
 
+/* Bytes of stats (with_y: y is given). */
+size_t monarch_sandwich_stats_bytes(int64_t rows, int64_t features, int with_y, int pre_norm,
+                                    int dtype);
+
 /* Workspace bytes of monarch_sandwich_bwd (with_bias: post_b or pre_b is given). */
 size_t monarch_sandwich_bwd_workspace_bytes(int64_t rows, int64_t features, int64_t gates,
                                             int with_bias, int dtype);
@@ -347,10 +353,9 @@ size_t monarch_sandwich_bwd_workspace_bytes(int64_t rows, int64_t features, int6
 /* Backward pass from dh_out (NULL: zero) and dn (with a norm_pre): dh and dy
  * [rows, features], and the gradients of the parameters, each of which may be
  * NULL when it is not wanted. h_out, y, stats and the parameters are those of the
- * forward call; h_out is read as it was stored, so in bf16 the gradients carry its
- * rounding besides their own (dpre_w most, more so where norm_pre is LAYER and a
- * row's mean is much larger than its spread). Without norm_pre, dn and h_out are not used, dh_out is
- * needed, and dpre_w and dpre_b have to be NULL. With y NULL only dh, dpre_w and dpre_b are computed (dh with
+ * forward call (h_out is taken with the bits that stats keeps of it). Without
+ * norm_pre, dn and h_out are not used, dh_out is needed, and dpre_w and dpre_b
+ * have to be NULL. With y NULL only dh, dpre_w and dpre_b are computed (dh with
  * skip_scale). Everything is overwritten; sums over rows run in a fixed order.
  * dh may be dh_out or dn. rows == 0 zeroes the parameters' gradients. */
 int monarch_sandwich_bwd(const void* dh_out, const void* dn, const void* h_out, const void* y,

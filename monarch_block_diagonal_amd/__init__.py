@@ -16,7 +16,7 @@ from .binding import (  # noqa: F401
     monarch_hyper_describe, monarch_dyad_fwd_workspace_bytes, monarch_dyad_fwd,
     monarch_dyad_bwd_workspace_bytes, monarch_dyad_bwd, monarch_dyad_describe,
     monarch_bwd_noalloc, monarch_stream_copy, NORM_NONE, NORM_RMS, NORM_LAYER,
-    monarch_sandwich_fwd, monarch_sandwich_bwd_workspace_bytes, monarch_sandwich_bwd,
-    monarch_sandwich_describe, monarch_distill_fwd, monarch_distill_bwd, monarch_distill_step,
+    monarch_sandwich_fwd, monarch_sandwich_stats_bytes, monarch_sandwich_bwd_workspace_bytes,
+    monarch_sandwich_bwd, monarch_sandwich_describe, monarch_distill_fwd, monarch_distill_bwd, monarch_distill_step,
     DISTILL_MAX_TOP,
 )

@@ -47,8 +47,8 @@ EXPORTED = (
     "monarch_hyper_describe", "monarch_dyad_fwd_workspace_bytes", "monarch_dyad_fwd",
     "monarch_dyad_bwd_workspace_bytes",
     "monarch_dyad_bwd", "monarch_dyad_describe", "monarch_bwd_noalloc", "monarch_stream_copy",
-    "monarch_sandwich_fwd", "monarch_sandwich_bwd_workspace_bytes", "monarch_sandwich_bwd",
-    "monarch_sandwich_describe", "monarch_distill_fwd", "monarch_distill_bwd",
+    "monarch_sandwich_fwd", "monarch_sandwich_stats_bytes", "monarch_sandwich_bwd_workspace_bytes",
+    "monarch_sandwich_bwd", "monarch_sandwich_describe", "monarch_distill_fwd", "monarch_distill_bwd",
     "monarch_distill_step",
 )
 
@@ -134,6 +134,8 @@ def load_library():
     lib.monarch_sandwich_fwd.argtypes = ([vp] * 10 + [i64] * 3 + [c_int] * 2 + [c_float] * 3 +
                                          [c_int, vp] + ev)
     lib.monarch_sandwich_fwd.restype = c_int
+    lib.monarch_sandwich_stats_bytes.argtypes = [i64] * 2 + [c_int] * 3
+    lib.monarch_sandwich_stats_bytes.restype = sz
     lib.monarch_sandwich_bwd_workspace_bytes.argtypes = [i64] * 3 + [c_int] * 2
     lib.monarch_sandwich_bwd_workspace_bytes.restype = sz
     lib.monarch_sandwich_bwd.argtypes = ([vp] * 18 + [sz] + [i64] * 3 + [c_int] * 2 +
@@ -430,6 +432,10 @@ def monarch_sandwich_fwd(h, y, post_w, post_b, gate, pre_w, pre_b, h_out, n, sta
     _check(load_library().monarch_sandwich_fwd(
         *_addresses(h, y, post_w, post_b, gate, pre_w, pre_b, h_out, n, stats), rows, features,
         gates, post_norm, pre_norm, skip_scale, branch_scale, eps, dtype, _stream(stream), arr, ne))
+
+
+def monarch_sandwich_stats_bytes(rows, features, with_y, pre_norm, dtype) -> int:
+    return load_library().monarch_sandwich_stats_bytes(rows, features, 1 if with_y else 0, pre_norm, dtype)
 
 
 def monarch_sandwich_bwd_workspace_bytes(rows, features, gates, with_bias, dtype) -> int:

@@ -20,6 +20,7 @@ struct SandwichFwd {
   const void *h, *y, *post_w, *post_b, *gate, *pre_w, *pre_b;
   void *h_out, *n_out;
   float* stats;
+  uint32_t* low;   // bits that h_out's rounding to bf16 left, a word a piece (low_bits); null: not kept
   int64_t rows, rows_per_gate;
   int d, post, pre;
   float skip, branch, eps;
@@ -35,6 +36,8 @@ enum { CHUNK = 0, RUN = 1, TOKEN = 2 };
 struct SandwichBwd {
   const void *dh_out, *dn, *h_out, *y;
   const float* stats;
+  const uint32_t* low;   // as for the forward pass; where nothing is kept, any address
+  int low_row;           // words a row; 0: h_out is taken as it is
   const void *post_w, *post_b, *gate, *pre_w, *pre_b;
   void *dh, *dy, *dgate;
   float* part;          // [chunks][sums][d]

@@ -98,6 +98,10 @@ int check_sizes(int64_t rows, int64_t d, int64_t gates, int post, int pre, int d
   return MONARCH_OK;
 }
 
+// Whether the forward pass keeps what h_out's rounding left, for the backward pass:
+// behind the statistics, a word for 8 elements.
+bool keeps_low(const void* y, int pre, bool bf16) { return y && pre != MONARCH_NORM_NONE && bf16; }
+
 bool any_misaligned(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (misaligned(p)) return true;
@@ -137,6 +141,7 @@ int monarch_sandwich_fwd(const void* h, const void* y, const void* post_w, const
   a.h = h, a.y = y, a.post_w = post_w, a.post_b = post_b, a.gate = gates > 0 ? gate : nullptr;
   a.pre_w = pre_w, a.pre_b = pre_b, a.h_out = h_out, a.n_out = n_out;
   a.stats = static_cast<float*>(stats);
+  a.low = keeps_low(y, pre_norm, dtype == MONARCH_BF16) ? static_cast<uint32_t*>(stats) + rows * 4 : nullptr;
   a.rows = rows, a.rows_per_gate = gates > 0 ? rows / gates : rows;
   a.d = static_cast<int>(features), a.post = post_norm, a.pre = pre_norm;
   a.skip = skip_scale, a.branch = branch_scale, a.eps = eps;
@@ -148,6 +153,12 @@ int monarch_sandwich_fwd(const void* h, const void* y, const void* post_w, const
                                          : sandwich_launch_fwd<float>(a, s));
   if (st) return st;
   return record_hip(tr.mark());
+}
+
+size_t monarch_sandwich_stats_bytes(int64_t rows, int64_t features, int with_y, int pre_norm, int dtype) {
+  if (check_sizes(rows, features, 0, 0, pre_norm, dtype)) return 0;
+  const bool low = keeps_low(with_y ? &with_y : nullptr, pre_norm, dtype == MONARCH_BF16);
+  return static_cast<size_t>(rows) * (4 + (low ? (features + 7) / 8 : 0)) * sizeof(float);
 }
 
 size_t monarch_sandwich_bwd_workspace_bytes(int64_t rows, int64_t features, int64_t gates,
@@ -192,6 +203,8 @@ int monarch_sandwich_bwd(const void* dh_out, const void* dn, const void* h_out, 
     SandwichBwd a;
     a.dh_out = dh_out, a.dn = dn, a.h_out = h_out, a.y = y;
     a.stats = static_cast<const float*>(stats);
+    a.low_row = keeps_low(y, pre_norm, bf16) ? static_cast<int>((features + 7) / 8) : 0;
+    a.low = static_cast<const uint32_t*>(stats) + (a.low_row ? rows * 4 : 0);
     a.post_w = post_w, a.post_b = post_b, a.gate = gates > 0 ? gate : nullptr;
     a.pre_w = has_pre ? pre_w : nullptr, a.pre_b = has_pre ? pre_b : nullptr;
     a.dh = dh, a.dy = dy, a.dgate = dgate, a.part = static_cast<float*>(workspace);

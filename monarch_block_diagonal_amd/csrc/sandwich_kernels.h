@@ -19,9 +19,12 @@
 // read once and written once, which is what bounds both passes (about 10
 // operations a value forward, 35 backward). All arithmetic and all sums are
 // fp32; results are rounded once, at their store. n is computed from h' before
-// its rounding. The backward pass reads h' as it was stored: in bf16 its results
-// carry that rounding besides their own (2.4e-3 off the formula's where one
-// rounding is 1.7e-3), for a pass that needs neither h nor the gated branch again.
+// its rounding, and the backward pass needs that h' too: in bf16 the forward pass keeps 4
+// more bits a value beside the statistics (low_bits). From h_out alone dw_pre was 2.6e-3
+// off the formula's where one rounding is 1.7e-3, and more where a LAYER row's mean is
+// larger than its spread. The half byte a value is 6% of the forward pass's bytes and 4%
+// of the backward pass's (forward and backward with join, 16384 x 768 18.2 / 31.7 us
+// without it, 19.7 / 35.0 with; 8192 x 16384 with a gate a row 248 / 428 and 264 / 440).
 #pragma once
 
 #include <type_traits>
@@ -40,6 +43,44 @@ __device__ __forceinline__ u32x4 par_piece(const void* p, int64_t off, int at, i
   if (p) return load_piece<T, R>(static_cast<const T*>(p) + off, at, d);
   const uint32_t w = sizeof(T) == 2 ? (__float_as_uint(fill) >> 16) * 0x10001u : __float_as_uint(fill);
   return u32x4{w, w, w, w};
+}
+
+// Four more bits of each of a piece's values than their roundings to bf16 hold: the
+// difference from the rounding in sixteenths of its last place, -8 .. 7. A value that
+// bf16 holds gives 0; what is left is at most a sixteenth, mostly a 32nd, of a last place.
+// The difference is that of the bit patterns, which also runs over exponents: the
+// pattern's low half as a signed number, one less where the upper half is even, so that
+// a tie (to even) falls on its side. Two values at a time in 16-bit halves; element 2 k
+// in bits 4 k, element 2 k + 1 in bits 16 + 4 k.
+__device__ __forceinline__ uint32_t low_bits(const float (&v)[8]) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  uint32_t word = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = __float_as_uint(v[2 * k]), b = __float_as_uint(v[2 * k + 1]);
+    const uint32_t low = __builtin_amdgcn_perm(b, a, 0x05040100u);
+    const uint32_t even = ~__builtin_amdgcn_perm(b, a, 0x07060302u) & 0x00010001u;
+    s16x2 x, one, t = {0x800, 0x800};
+    __builtin_memcpy(&x, &low, 4);
+    __builtin_memcpy(&one, &even, 4);
+    t = __builtin_elementwise_add_sat(static_cast<s16x2>(x - one), t);
+    uint32_t top;   // four bits at the top of each half
+    __builtin_memcpy(&top, &t, 4);
+    word = (word >> 4 & 0x0fff0fffu) | (top & 0xf000f000u);
+  }
+  return word;
+}
+
+// A piece of h' for the backward pass: h_out with the bits that were kept.
+template <typename T, int N>
+__device__ __forceinline__ void unpack_low(const u32x4& r, uint32_t word, float (&v)[N]) {
+  PieceOf<T>::unpack(r, v);
+  if constexpr (N == 8)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int q = static_cast<int>(word << (28 - 4 * (i / 2) - 16 * (i % 2))) >> 28;
+      v[i] = __uint_as_float(__float_as_uint(v[i]) + (static_cast<uint32_t>(q) << 12));
+    }
 }
 
 // mean and 1/sqrt(mean square about it + eps) of the team's row (zero past d)
@@ -73,6 +114,18 @@ __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][
   rho = 1.0f / sqrtf(team.sum(q) / static_cast<float>(d) + eps);
 }
 
+// The start of a row. Where a row is the workgroup's it is held in scalar registers
+// and taken as it is: the compiler would keep the sum of the tensor's address and each
+// piece's place over the loop instead, two registers a piece and tensor (2048 x 16384
+// fp32 backward 206 -> 176 us).
+template <int TEAM, typename T, typename V>
+__device__ __forceinline__ auto row_start(V* p, int64_t off) {
+  typedef typename std::conditional<std::is_const<V>::value, const T, T>::type E;
+  E* r = static_cast<E*>(p) + off;
+  if constexpr (TEAM > 64) asm volatile("" : "+s"(r));
+  return r;
+}
+
 // One row a team. A team of 1024 threads leaves room for one workgroup a CU: it
 // takes rows in turn and loads the next one while the present one is normed a
 // second time. Measured (every tensor once; medians of kernel traces): 16384 x 768 bf16
@@ -86,19 +139,20 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 
   constexpr bool AHEAD = TEAM == 1024 && P <= 3;
   __shared__ typename Team<TEAM>::Lds lds;
   Team<TEAM> team(&lds);
-  const int lane = threadIdx.x % TEAM;
+  const int lane = TEAMS == 1 ? threadIdx.x : threadIdx.x % TEAM, tm = TEAMS == 1 ? 0 : threadIdx.x / TEAM;
   const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
   u32x4 hr[P], yr[P];
   auto load = [&](int64_t row) {
     const int d = anew(a.d);
+    const T *h = row_start<TEAM, T>(a.h, row * d), *y = row_start<TEAM, T>(a.y, row * d);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
-      hr[p] = load_piece<T, R>(static_cast<const T*>(a.h) + row * d, at, d);
-      if (a.y) yr[p] = load_piece<T, R>(static_cast<const T*>(a.y) + row * d, at, d);
+      hr[p] = load_piece<T, R>(h, at, d);
+      if (a.y) yr[p] = load_piece<T, R>(y, at, d);
     }
   };
-  int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + tm;
   if (AHEAD && row < a.rows) load(row);
   for (; row < a.rows; row += step) {
     const int d = anew(a.d);
@@ -118,6 +172,8 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 
       const int64_t goff = a.gate ? row / a.rows_per_gate * d : 0;
       // branch * yhat, so that the scale costs nothing a value
       const float scale = a.branch * rho_y, mean = mu_y * scale;
+      T* h_out = row_start<TEAM, T>(a.h_out, off);
+      uint32_t* low = row_start<TEAM, uint32_t>(a.low, row * ((d + N - 1) / N));
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
@@ -135,7 +191,10 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 
           if constexpr (BIAS) u = fmaf(a.branch, b[i], u);
           v[p][i] = fmaf(a.skip, t[i], g[i] * u);
         }
-        store_piece<T, R>(static_cast<T*>(a.h_out) + off, at, d, PieceOf<T>::pack(v[p]));
+        store_piece<T, R>(h_out, at, d, PieceOf<T>::pack(v[p]));
+        if constexpr (N == 8)
+          if (a.low && at < d)
+            __builtin_nontemporal_store(low_bits(v[p]), low + static_cast<unsigned>(at) / 8);
         mask<R, N>(v[p], at, d);
       }
     } else {
@@ -149,6 +208,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 
     if (a.pre != MONARCH_NORM_NONE) {
       row_stats<R, TEAM, P, N>(team, v, lane, d, a.pre, a.eps, mu_h, rho_h);
       const float mean_h = mu_h * rho_h;
+      T* n_out = row_start<TEAM, T>(a.n_out, off);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
@@ -161,7 +221,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 
           v[p][i] = fmaf(v[p][i], rho_h, -mean_h) * w[i];
           if constexpr (BIAS) v[p][i] += b[i];
         }
-        store_piece<T, R>(static_cast<T*>(a.n_out) + off, at, d, PieceOf<T>::pack(v[p]));
+        store_piece<T, R>(n_out, at, d, PieceOf<T>::pack(v[p]));
       }
     }
     if (lane == 0) *reinterpret_cast<f32x4*>(a.stats + row * 4) = f32x4{mu_y, rho_y, mu_h, rho_h};
@@ -233,7 +293,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
   __shared__ typename Team<TEAM>::Lds lds;
   __shared__ f32x4 shared[IN_LDS ? 2 * WG * P * N / 4 : TEAMS > 1 ? TEAMS * COLS / 4 : 1];
   Team<TEAM> team(&lds);
-  const int lane = threadIdx.x % TEAM, tm = threadIdx.x / TEAM;
+  const int lane = TEAMS == 1 ? threadIdx.x : threadIdx.x % TEAM, tm = TEAMS == 1 ? 0 : threadIdx.x / TEAM;
   const float inv_d = 1.0f / static_cast<float>(a.d);
   // rows [first, last) of this team, taken every `step`
   int64_t first, last, group = 0;
@@ -290,17 +350,27 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
   int64_t left = a.rows_per_gate;   // RUN: rows of the gate run still to come
 
   u32x4 dnr[P], hr[P];
+  uint32_t lowr[P];
   auto load_pre = [&](int64_t row) {
     const int d = anew(a.d);
+    const T *dn = row_start<TEAM, T>(a.dn, row * d), *h = row_start<TEAM, T>(a.h_out, row * d);
+    const uint32_t* low = row_start<TEAM, uint32_t>(a.low, row * a.low_row);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
       dnr[p] = hr[p] = zero;
+      // a word of another piece past the row, any where none are kept: both do not count
+      // (low_word)
+      lowr[p] = 0;
+      if constexpr (N == 8) lowr[p] = low[at < d && a.low_row ? static_cast<unsigned>(at) / 8 : 0u];
       if (a.pre != MONARCH_NORM_NONE) {
-        dnr[p] = load_piece<T, R>(static_cast<const T*>(a.dn) + row * d, at, d);
-        hr[p] = load_piece<T, R>(static_cast<const T*>(a.h_out) + row * d, at, d);
+        dnr[p] = load_piece<T, R>(dn, at, d);
+        hr[p] = load_piece<T, R>(h, at, d);
       }
     }
+  };
+  auto low_word = [&](int p) {
+    return (p * TEAM + lane) * N < a.d && a.low_row ? lowr[p] : 0u;
   };
   if (AHEAD && first < last) load_pre(first);
   for (int64_t row = first; row < last; row += step) {
@@ -310,25 +380,26 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
     if constexpr (!AHEAD) load_pre(row);
     u32x4 yr[P];
     auto load_y = [&]() {
+      const T *y = row_start<TEAM, T>(a.y, off), *g = row_start<TEAM, T>(a.gate, group * d);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
         yr[p] = zero;
-        if (a.y) yr[p] = load_piece<T, R>(static_cast<const T*>(a.y) + off, at, d);
+        if (a.y) yr[p] = load_piece<T, R>(y, at, d);
         if constexpr (GATE != CHUNK)
-          gr[p] = load_piece<T, R>(static_cast<const T*>(a.gate) + group * d, at, d);
+          gr[p] = load_piece<T, R>(g, at, d);
       }
     };
     float D[P][N];
     {
       u32x4 dhr[P];
       auto load_rest = [&]() {
+        const T* dh_out = row_start<TEAM, T>(a.dh_out, off);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           dhr[p] = zero;
           if (a.dh_out)
-            dhr[p] = load_piece<T, R>(static_cast<const T*>(a.dh_out) + off,
-                                        (p * TEAM + lane) * N, d);
+            dhr[p] = load_piece<T, R>(dh_out, (p * TEAM + lane) * N, d);
         }
         if constexpr (!LATE) load_y();
       };
@@ -345,7 +416,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           float dn[N], h[N], w[N];
           PieceOf<T>::unpack(dnr[p], dn);
           if constexpr (R != WHOLE) mask<R, N>(dn, (p * TEAM + lane) * N, d);
-          PieceOf<T>::unpack(hr[p], h);
+          unpack_low<T>(hr[p], low_word(p), h);
           if constexpr (BIAS) s_preb.add(p, dn);
           forget(pre_wr[p]);
           PieceOf<T>::unpack(pre_wr[p], w);
@@ -369,9 +440,10 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           float dn[N], h[N], w[N];
           forget(dnr[p]);
           forget(hr[p]);
+          if constexpr (N == 8) forget(lowr[p]);
           forget(pre_wr[p]);
           PieceOf<T>::unpack(dnr[p], dn);
-          PieceOf<T>::unpack(hr[p], h);
+          unpack_low<T>(hr[p], low_word(p), h);
           PieceOf<T>::unpack(dhr[p], D[p]);
           PieceOf<T>::unpack(pre_wr[p], w);
 #pragma unroll
@@ -391,6 +463,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
     if constexpr (LATE) load_y();
     if constexpr (REREAD) load_post_pars();
     if (AHEAD && row + step < last) load_pre(row + step);
+    T* dh = row_start<TEAM, T>(a.dh, off);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int at = (p * TEAM + lane) * N;
@@ -398,12 +471,13 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
         float o[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = a.skip * D[p][i];
-        store_piece<T, R>(static_cast<T*>(a.dh) + off, at, d, PieceOf<T>::pack(o));
+        store_piece<T, R>(dh, at, d, PieceOf<T>::pack(o));
       }
     }
     if (a.y) {
       const float mean = st[0] * st[1];
       float s[2] = {0.0f, 0.0f};
+      T *dgate = row_start<TEAM, T>(a.dgate, group * d), *dy = row_start<TEAM, T>(a.dy, off);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = (p * TEAM + lane) * N;
@@ -427,7 +501,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
           } else if (a.dgate) {
 #pragma unroll
             for (int i = 0; i < N; ++i) o[i] *= a.branch;
-            store_piece<T, R>(static_cast<T*>(a.dgate) + group * d, at, d, PieceOf<T>::pack(o));
+            store_piece<T, R>(dgate, at, d, PieceOf<T>::pack(o));
           }
           // e / branch = g D, which D becomes
 #pragma unroll
@@ -462,7 +536,7 @@ __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(Sa
         PieceOf<T>::unpack(yr[p], y);
 #pragma unroll
         for (int i = 0; i < N; ++i) y[i] = fmaf(st[1], D[p][i], -fmaf(y[i], k1, k0));
-        store_piece<T, R>(static_cast<T*>(a.dy) + off, at, d, PieceOf<T>::pack(y));
+        store_piece<T, R>(dy, at, d, PieceOf<T>::pack(y));
       }
     }
     if constexpr (GATE == TOKEN) ++group;

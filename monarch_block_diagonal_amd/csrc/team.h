@@ -73,10 +73,10 @@ __device__ __forceinline__ u32x4 load_piece(const T* row, int at, int d) {
   constexpr int N = PieceOf<T>::N;
   if constexpr (R == WHOLE) {
     u32x4 r = {0, 0, 0, 0};
-    if (at < d) r = *reinterpret_cast<const u32x4*>(row + at);
+    if (at < d) r = *reinterpret_cast<const u32x4*>(row + static_cast<unsigned>(at));
     return r;
   } else if constexpr (R == CUT) {
-    return *reinterpret_cast<const typename PieceOf<T>::Raw*>(row + min(at, d - N));
+    return *reinterpret_cast<const typename PieceOf<T>::Raw*>(row + static_cast<unsigned>(min(at, d - N)));
   } else {
     u32x4 r = {0, 0, 0, 0};
 #pragma unroll 1
@@ -113,11 +113,11 @@ template <typename T, Rows R>
 __device__ __forceinline__ void store_piece(T* row, int at, int d, u32x4 r) {
   constexpr int N = PieceOf<T>::N;
   if constexpr (R == WHOLE) {
-    if (at < d) __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(row + at));
+    if (at < d) __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(row + static_cast<unsigned>(at)));
     return;
   }
   if (at + N <= d) {
-    __builtin_nontemporal_store(r, reinterpret_cast<typename PieceOf<T>::Raw*>(row + at));
+    __builtin_nontemporal_store(r, reinterpret_cast<typename PieceOf<T>::Raw*>(row + static_cast<unsigned>(at)));
     return;
   }
   if (at >= d) return;
@@ -138,6 +138,7 @@ __device__ __forceinline__ void store_piece(T* row, int at, int d, u32x4 r) {
 // Keeps the compiler from carrying what it computed from r to the next use of
 // r: unpacking again is cheaper than the registers.
 __device__ __forceinline__ void forget(u32x4& r) { asm volatile("" : "+v"(r)); }
+__device__ __forceinline__ void forget(uint32_t& r) { asm volatile("" : "+v"(r)); }
 
 // A loop-invariant value that is to be computed with anew in every iteration:
 // offsets and conditions derived from it would otherwise be kept in registers.

@@ -398,11 +398,11 @@ def _refuse(t, name, shape, dtype):
     raise ValueError(f"{name} must live on the current GPU, where the call's stream is")
 
 
-def _saved(stats, rows, device):
+def _saved(stats, shape, dtype, device):
     """Checks what a forward call saved for its backward call."""
-    if stats.dtype is not torch.float32:
-        raise ValueError("stats must be the fp32 tensor the forward returned")
-    _beside(device, torch.float32, (rows, 4), "stats", stats)
+    if stats.dtype is not dtype:
+        raise ValueError(f"stats must be the {dtype} tensor the forward returned")
+    _beside(device, dtype, shape, "stats", stats)
 
 
 def _beside(device, dtype, shape, names, *tensors):
@@ -454,6 +454,13 @@ def _on_stream(stream, call, *args, **kw):
 _sandwich_workspace = functools.lru_cache(maxsize=256)(B.monarch_sandwich_bwd_workspace_bytes)
 
 
+def _sandwich_stats(rows, d, y, pre_norm, dtype):
+    """(shape, dtype) of stats, monarch_sandwich_stats_bytes long."""
+    if y is None or pre_norm == B.NORM_NONE or dtype != torch.bfloat16:
+        return (rows, 4), torch.float32
+    return (rows, 4 + _cdiv(d, 8)), torch.int32
+
+
 def sandwich_forward(h, y=None, post_weight=None, post_bias=None, gate=None, pre_weight=None,
                      pre_bias=None, *, post_norm: int = B.NORM_RMS, pre_norm: int = B.NORM_RMS,
                      skip_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-5,
@@ -465,7 +472,9 @@ def sandwich_forward(h, y=None, post_weight=None, post_bias=None, gate=None, pre
 
     gate [gates, features] holds one row for rows/gates consecutive rows. Without
     y, h_out is h itself (the norm before the first block); with pre_norm
-    NORM_NONE, n is None. stats [rows, 4] goes to sandwich_backward."""
+    NORM_NONE, n is None. stats goes to sandwich_backward: fp32 [rows, 4], and in bf16
+    with y and a pre_norm int32 [rows, 4 + ceil(features / 8)], which also holds four more
+    bits of every value of h_out than its rounding does."""
     if stream is not None:
         return _on_stream(stream, sandwich_forward, h, y, post_weight, post_bias, gate,
                           pre_weight, pre_bias, post_norm=post_norm, pre_norm=pre_norm,
@@ -474,7 +483,8 @@ def sandwich_forward(h, y=None, post_weight=None, post_bias=None, gate=None, pre
                                          pre_norm, skip_scale)
     h_out = torch.empty_like(h) if y is not None else h
     n = torch.empty_like(h) if pre_norm != B.NORM_NONE else None
-    stats = torch.empty((rows, 4), dtype=torch.float32, device=h.device)
+    shape, kind = _sandwich_stats(rows, d, y, pre_norm, h.dtype)
+    stats = torch.empty(shape, dtype=kind, device=h.device)
     B.monarch_sandwich_fwd(h, y, post_weight, post_bias, gate, pre_weight, pre_bias,
                            h_out if y is not None else None, n, stats, rows, d, gates, post_norm,
                            pre_norm, skip_scale, branch_scale, eps, dtype_code(h))
@@ -487,8 +497,7 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
                       branch_scale: float = 1.0, stream=None, eps: float | None = None):
     """SandwichGrads from the gradients dh_out (None: zero) and dn of the
     forward's results. h_out and stats are the forward's (eps is in stats; it is
-    accepted so that both calls take the same keywords); in bf16 the gradients
-    carry h_out's rounding besides their own."""
+    accepted so that both calls take the same keywords)."""
     if stream is not None:
         return _on_stream(stream, sandwich_backward, dh_out, dn, h_out, y, stats, post_weight,
                           post_bias, gate, pre_weight, pre_bias, post_norm=post_norm,
@@ -501,7 +510,7 @@ def sandwich_backward(dh_out, dn, h_out, y, stats, post_weight=None, post_bias=N
     rows, d, gates, device = _sandwich_shapes(ref, y, post_weight, post_bias, gate, pre_weight,
                                               pre_bias, pre_norm, skip_scale)
     _beside(device, ref.dtype, (rows, d), "dh_out dn", dh_out, dn)
-    _saved(stats, rows, device)
+    _saved(stats, *_sandwich_stats(rows, d, y, pre_norm, ref.dtype), device)
     like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
     g = SandwichGrads(like(ref), like(y), like(post_weight), like(post_bias), like(gate),
                       like(pre_weight), like(pre_bias))
@@ -645,7 +654,7 @@ def distill_backward(dloss, logits, teacher, ids, labels, stats, *, temperature:
         return _on_stream(stream, distill_backward, dloss, logits, teacher, ids, labels, stats,
                           temperature=temperature, mix=mix, out=out)
     rows, vocab, top, ld, device = _distill_shapes(logits, teacher, ids, labels, dloss, "dloss")
-    _saved(stats, rows, device)
+    _saved(stats, (rows, 4), torch.float32, device)
     dz, dld = _distill_out(logits, rows, vocab, ld, device, out)
     B.monarch_distill_bwd(dloss, logits, ld, teacher, ids, labels, stats, dz, dld, rows, vocab, top,
                           temperature, mix, dtype_code(logits))

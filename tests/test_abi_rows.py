@@ -164,3 +164,20 @@ def test_few_gate_runs_are_cut():
         # many: no partial rows of their own, at most as many chunks as a launch has workgroups
         for rows, d, gates in ((16384, 768, 2048), (32 * 4096, 768, 4096), (4096, 64, 2048), (4096, 16384, 512)):
             assert chunks(rows, d, gates, dtype) <= 512, (rows, d, gates, dtype)
+
+
+def test_sandwich_stats():
+    """Statistics of a row, and in bf16 behind them half a byte for each value of a joined and normed h_out."""
+    from monarch_block_diagonal_amd import torch_api as T
+    torch = pytest.importorskip("torch")
+    for rows, d in ((1, 1), (6, 64), (1000, 767), (3, 16384), (1 << 20, 9), (0, 64)):
+        for dtype, code in ((torch.float32, B.F32), (torch.bfloat16, B.BF16)):
+            for y in (None, True):
+                for pre in (0, 1, 2):
+                    kept = (d + 7) // 8 if y and pre and code == B.BF16 else 0
+                    need = M.monarch_sandwich_stats_bytes(rows, d, y is not None, pre, code)
+                    assert need == rows * (16 + 4 * kept)
+                    shape, kind = T._sandwich_stats(rows, d, y, pre, dtype)
+                    assert shape[0] * shape[1] * kind.itemsize == need
+    for bad in ((-1, 64, 1, 1, B.F32), (6, 0, 1, 1, B.F32), (6, 16385, 1, 1, B.F32), (6, 64, 1, 3, B.F32), (6, 64, 1, 1, 2)):
+        assert M.monarch_sandwich_stats_bytes(*bad) == 0

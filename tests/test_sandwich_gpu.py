@@ -346,3 +346,36 @@ def test_few_short_gate_runs(api, rows, d, gates, bias, dtype):
 def test_many_short_gate_runs(api, d, gates, run, bias, dtype):
     """Each a team's own."""
     compare(api, gates * run, d, gates, bias, dtype, "layer", "rms", branch=-0.5)
+
+
+@pytest.mark.parametrize("rows,d,gates,pre,mean", [
+    (2048, 768, 16, "rms", 0.0), (2048, 768, 0, "layer", 24.0), (300, 767, 300, "layer", 24.0), (900, 2048, 300, "rms", 24.0),
+    (700, 7, 1, "layer", 0.0), (257, 6151, 257, "rms", 0.0), (200, 16384, 4, "layer", 24.0),
+])
+def test_bf16_gradients_carry_one_rounding(api, rows, d, gates, pre, mean):
+    """The gradients of h' itself: their own rounding, and no more of h_out's than the kept bits leave.
+
+    In 2-norms, in units of a gradient's own rounding to bf16: a value of h' is off by at most 1/16 of what h_out's is (1/32
+    but for ties), so with r the size of h' over that of the centred row a gradient that takes hhat value by value is off
+    by r/16 besides; twice that for the spread of the mantissas, and a tenth of a rounding for everything in fp32.
+    From h_out alone dpre_weight would be sqrt(1 + r^2) off."""
+    a, dh, dn = draw(rows, d, gates, True, "bf16", pre=pre)
+    a["h"] = S.round_to_bf16(a["h"] * np.float32(0.5) + np.float32(mean))
+    how = dict(post_norm=KINDS["rms"], pre_norm=KINDS[pre], skip_scale=1.0, branch_scale=0.5)
+    D = {k: dev(v, "bf16") for k, v in a.items()}
+    par = (D["post_w"], D["post_b"], D["gate"], D["pre_w"], D["pre_b"])
+    h_out, n, stats = api.sandwich_forward(D["h"], D["y"], *par, **how)
+    g = api.sandwich_backward(dev(dh, "bf16"), dev(dn, "bf16"), h_out, D["y"], stats, *par, **how)
+    par = (a["post_w"], a["post_b"], a["gate"], a["pre_w"], a["pre_b"])
+    rh, _ = O.forward(a["h"], a["y"], *par, "rms", pre, 1.0, 0.5)
+    rg = O.backward(dh, dn, a["h"], a["y"], *par, "rms", pre, 1.0, 0.5)
+    _, c, _ = O.norm(rh, pre, 1e-5)
+    r = float(np.linalg.norm(rh) / np.linalg.norm(c))
+    for mine, theirs in (("dh", "dh"), ("dy", "dy"), ("dpre_weight", "dpre_w"), ("dgate", "dgate"), ("dpost_weight", "dpost_w")):
+        if mine == "dgate" and not gates:
+            continue
+        want = rg[theirs]
+        own = np.linalg.norm(host(torch.from_numpy(want).to(torch.bfloat16)) - want)
+        off = np.linalg.norm(host(getattr(g, mine)) - want)
+        print(f"[rounding] {rows}x{d} {pre} mean={mean} r={r:.1f} {mine}: {off / own:.2f} roundings", flush=True)
+        assert off <= np.hypot(1.1, r / 8) * own, (mine, off / own, r)
