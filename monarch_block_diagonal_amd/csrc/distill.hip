@@ -22,8 +22,8 @@
 // logit, store) where it has few. Measured (a call among others): loss of 4096 x 50257
 // bf16 at T = 2 with labels 77 us, 5.4 TB/s (its arithmetic busy 86% of the time, but no
 // slower than T = 1, which has a tenth less); both of 16384 x 50257 bf16 588 us, 5.6
-// TB/s, which a copy of that size reaches (40 calls timed one by one: median 594, 583 to
-// 624; in a kernel trace, which runs them apart, median 621, 593 to 648); of 1024 x 50257 bf16 (4
+// TB/s, which a copy of that size reaches (40 calls timed one by one: median 595, 583 to
+// 625; in kernel traces, which run them apart, medians 621 to 642, 593 at least); of 1024 x 50257 bf16 (4
 // rows a CU) 48 us, 4.3 TB/s; of 1000 x 10000 fp32 26.6 us; of 2048 x 131072 fp32, which no
 // CU holds, 486 us, 4.4 TB/s. Read twice instead of held, the second took 784 us and the
 // last 718.

@@ -23,7 +23,7 @@
 // more bits a value beside the statistics (low_bits). From h_out alone dw_pre was 2.6e-3
 // off the formula's where one rounding is 1.7e-3, and more where a LAYER row's mean is
 // larger than its spread. The half byte a value is 6% of the forward pass's bytes and 4%
-// of the backward pass's (forward and backward with join, 16384 x 768 18.2 / 31.7 us
+// of the backward pass's (forward / backward and join, 16384 x 768 18.2 / 31.7 us
 // without it, 19.7 / 35.0 with; 8192 x 16384 with a gate a row 248 / 428 and 264 / 440).
 #pragma once
 
@@ -117,7 +117,7 @@ __device__ __forceinline__ void row_stats(Team<TEAM>& team, const float (&v)[P][
 // The start of a row. Where a row is the workgroup's it is held in scalar registers
 // and taken as it is: the compiler would keep the sum of the tensor's address and each
 // piece's place over the loop instead, two registers a piece and tensor (2048 x 16384
-// fp32 backward 206 -> 176 us).
+// fp32 backward and join 206 -> 176 us).
 template <int TEAM, typename T, typename V>
 __device__ __forceinline__ auto row_start(V* p, int64_t off) {
   typedef typename std::conditional<std::is_const<V>::value, const T, T>::type E;
@@ -128,10 +128,9 @@ __device__ __forceinline__ auto row_start(V* p, int64_t off) {
 
 // One row a team. A team of 1024 threads leaves room for one workgroup a CU: it
 // takes rows in turn and loads the next one while the present one is normed a
-// second time. Measured (every tensor once; medians of kernel traces): 16384 x 768 bf16
-// 18.9 us, 5.3 TB/s; 10000 x 625 fp32 19.9 us, 5.0 TB/s; 8192 x 16384 bf16 with a gate a
-// row 242 us, 5.5 TB/s, where a copy of that size reaches 5.6; one row of 768 4.0 us,
-// the launch. Small teams of 32 lanes x 3 pieces beat 64 x 2 for 768 features (20.3
+// second time. Measured (every tensor once): 16384 x 768 bf16 19.7 us, 5.4 TB/s; 10000 x
+// 625 fp32 20.3 us, 4.9 TB/s; 8192 x 16384 bf16 with a gate a row 264 us, 5.3 TB/s, where a
+// copy of that size reaches 5.6; one row of 768 4.1 us, the launch. Small teams of 32 lanes x 3 pieces beat 64 x 2 for 768 features (20.3
 // against 21.1 us): every lane holds whole pieces.
 template <typename T, int TEAM, int P, bool BIAS, Rows R>
 __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256, TEAM > 512 || R == WHOLE ? 4 : 3) void sandwich_fwd_kernel(SandwichFwd a) {
@@ -275,9 +274,9 @@ struct Sums {
 // x 768 bf16). Wide rows leave no registers for the sums: they lie in LDS (131 KB
 // for 16384 columns; in registers the kernel spilled, 1208 -> 488 us), parameters
 // are read again from the caches, and the next row's dn and h' are under way during
-// the second half of a row. Measured (medians of kernel traces): 16384 x 768 bf16
-// with 16 gates 29.5 us, 5.1 TB/s; 10000 x 625 fp32 with biases 30.4 us, 4.9 TB/s; 8192 x
-// 16384 bf16 with a gate a row 421 us, 5.1 TB/s.
+// the second half of a row. Measured: 16384 x 768 bf16 with 16 gates 31 us, 5.1
+// TB/s; 10000 x 625 fp32 with biases 30.6 us, 4.9 TB/s; 8192 x 16384 bf16 with a gate a row 429
+// us, 5.1 TB/s (calls among others; run apart, in a kernel trace, up to a tenth longer).
 template <typename T, int TEAM, int P, int GATE, bool BIAS, Rows R>
 __global__ __launch_bounds__(TEAM > 64 ? TEAM : 256) void sandwich_bwd_kernel(SandwichBwd a) {
   constexpr int N = PieceOf<T>::N, WG = TEAM > 64 ? TEAM : 256, TEAMS = WG / TEAM;
