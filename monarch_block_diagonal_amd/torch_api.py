@@ -665,7 +665,8 @@ def distill_step(logits, teacher, ids, labels=None, row_weight=None, *, temperat
                  mix: float = 1.0, out=None, stream=None):
     """(loss [rows], dlogits) in one pass: dlogits is the gradient of
     sum(row_weight * loss) (row_weight None: 1 for every row). out may be
-    logits itself, which saves a tensor of their size."""
+    logits itself, which saves a tensor of their size (autograd sees that they
+    changed: what saved their values for its backward pass raises there)."""
     if stream is not None:
         return _on_stream(stream, distill_step, logits, teacher, ids, labels, row_weight,
                           temperature=temperature, mix=mix, out=out)
