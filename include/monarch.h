@@ -56,7 +56,7 @@
 extern "C" {
 #endif
 
-#define MONARCH_ABI_VERSION 6
+#define MONARCH_ABI_VERSION 7
 
 typedef enum {
   MONARCH_OK = 0,
@@ -417,6 +417,69 @@ int monarch_distill_step(const void* logits, int64_t ld, const void* teacher, co
                          const void* labels, const void* row_weight, void* loss, void* dlogits,
                          int64_t dld, int64_t rows, int64_t vocab, int64_t top, float temperature,
                          float mix, int dtype, void* stream, void* const* events, int n_events);
+
+/* ---------------------------------------------------------------------------
+ * Head loss: monarch_distill_*'s loss of a student whose logits are not kept, and the
+ * softmax cross entropy without a teacher. The logits of row i are z = w x_i for a dense
+ * head w [vocab, features]; with T = temperature, q = softmax(z / T), s = softmax(z), and p, entries
+ * and labels as for monarch_distill_*:
+ *   loss[i] = mix * T^2 * sum_k p_k (log p_k - log q[id_k]) - (1 - mix) * log s[label]
+ * top 0 or mix 0 leaves the cross entropy alone (temperature is then not used), labels
+ * NULL or mix 1 the teacher's term alone. A row without a label and a valid entry (of a
+ * term that counts) has loss 0 and gradient 0 and adds nothing to dw, whatever it
+ * holds, and costs no product: padded tokens, prompts.
+ *   x [rows, ldx]: row i's features start at i*ldx (ldx >= features, in elements), aligned
+ *   to their element size only; w and dw [vocab, features], dx [rows, features] contiguous.
+ *   features <= 2^20, vocab <= 2^30, top <= MONARCH_DISTILL_MAX_TOP.
+ *   loss fp32 [rows]; labels int64 [rows]; teacher fp32, ids int64 [rows, top];
+ *   stats: monarch_head_stats_bytes, written by the forward pass for the backward pass.
+ *   workspace: monarch_head_workspace_bytes of the call (0 forward, 1 backward, 2 step): a copy
+ *   of x, in fp32 or with features % 8 != 0 one of w, a piece of the vocabulary's gradient
+ *   of the logits (at most 1 GiB, or 256 words of it) and partial sums. The calls keep nothing else of size rows * vocab.
+ * Logits and all sums are fp32 (fp32 operands are multiplied as three bf16 parts each,
+ * exact to 2^-23 of a product). In bf16 the gradient of the logits is rounded to bf16 between its
+ * products; dx and dw are rounded once. Sums run in a fixed order.
+ *
+ * monarch_head_bwd: dx and dw from dloss (fp32 [rows]) and the forward's inputs and
+ * stats. monarch_head_step: loss, dx and dw for row_weight (fp32 [rows], NULL: 1) in dloss's
+ * place. dx and dw are overwritten; rows == 0 zeroes dw. Errors as for monarch_distill_*;
+ * w, dx, dw, stats and workspace are aligned to 16 bytes. */
+size_t monarch_head_workspace_bytes(int call, int64_t rows, int64_t features, int64_t vocab,
+                                    int64_t top, int dtype);
+size_t monarch_head_stats_bytes(int64_t rows, int64_t top);
+
+int monarch_head_fwd(const void* x, int64_t ldx, const void* w, const void* labels,
+                     const void* teacher, const void* ids, void* loss, void* stats, void* workspace,
+                     size_t workspace_bytes, int64_t rows, int64_t features, int64_t vocab,
+                     int64_t top, float temperature, float mix, int dtype, void* stream,
+                     void* const* events, int n_events);
+int monarch_head_bwd(const void* dloss, const void* x, int64_t ldx, const void* w,
+                     const void* labels, const void* teacher, const void* ids, const void* stats,
+                     void* dx, void* dw, void* workspace, size_t workspace_bytes, int64_t rows,
+                     int64_t features, int64_t vocab, int64_t top, float temperature, float mix,
+                     int dtype, void* stream, void* const* events, int n_events);
+int monarch_head_step(const void* x, int64_t ldx, const void* w, const void* labels,
+                      const void* teacher, const void* ids, const void* row_weight, void* loss,
+                      void* dx, void* dw, void* workspace, size_t workspace_bytes, int64_t rows,
+                      int64_t features, int64_t vocab, int64_t top, float temperature, float mix,
+                      int dtype, void* stream, void* const* events, int n_events);
+
+/* ---------------------------------------------------------------------------
+ * Dropout joined to a residual:
+ *   y[i] = residual[i] + (r_i >= t ? x[i] * 65536 / (65536 - t) : 0),  t = round(65536 p)
+ * for the n elements of x, residual (NULL: 0) and y, rounded once. r_i are 16 bits of
+ * Philox4x32-10 with key seed and counter (i / 8 in its low, offset in its high 64 bits):
+ * the four words' lower and upper halves in turn are elements 0 to 7. No mask is
+ * stored: the gradient by x is the same call of dy without a residual, with the same p, seed and
+ * offset. A call with an offset of its own draws its own numbers.
+ * state (NULL, or two uint64 in device memory, 8-byte aligned): seed and offset are read there when the
+ * kernel runs instead of taken from the arguments, so that replays of a captured
+ * graph can draw anew.
+ * 0 <= p <= 1 or MONARCH_ERR_VALUE, n <= 2^41; y may be x or residual. What is dropped
+ * may hold anything (NaN too). n == 0 returns MONARCH_OK; otherwise errors as for monarch_fwd. */
+int monarch_dropout(const void* x, const void* residual, void* y, int64_t n, double p,
+                    uint64_t seed, uint64_t offset, const void* state, int dtype, void* stream,
+                    void* const* events, int n_events);
 
 /* ---------------------------------------------------------------------------
  * Stream copy: copies `bytes` bytes from src to dst (device buffers, 16-byte

@@ -49,7 +49,8 @@ EXPORTED = (
     "monarch_dyad_bwd", "monarch_dyad_describe", "monarch_bwd_noalloc", "monarch_stream_copy",
     "monarch_sandwich_fwd", "monarch_sandwich_stats_bytes", "monarch_sandwich_bwd_workspace_bytes",
     "monarch_sandwich_bwd", "monarch_sandwich_describe", "monarch_distill_fwd", "monarch_distill_bwd",
-    "monarch_distill_step",
+    "monarch_distill_step", "monarch_head_workspace_bytes", "monarch_head_stats_bytes",
+    "monarch_head_fwd", "monarch_head_bwd", "monarch_head_step", "monarch_dropout",
 )
 
 _lib = None
@@ -131,6 +132,20 @@ def load_library():
     lib.monarch_dyad_describe.argtypes = [c_int] + [i64] * 4 + [c_int, ctypes.c_char_p, sz]
     lib.monarch_dyad_describe.restype = c_int
     c_float = ctypes.c_float
+    lib.monarch_head_workspace_bytes.argtypes = [c_int] + [i64] * 4 + [c_int]
+    lib.monarch_head_workspace_bytes.restype = sz
+    lib.monarch_head_stats_bytes.argtypes = [i64] * 2
+    lib.monarch_head_stats_bytes.restype = sz
+    head = [sz] + [i64] * 4 + [c_float] * 2 + [c_int, vp] + ev
+    lib.monarch_head_fwd.argtypes = [vp, i64] + [vp] * 7 + head
+    lib.monarch_head_fwd.restype = c_int
+    lib.monarch_head_bwd.argtypes = [vp, vp, i64] + [vp] * 8 + head
+    lib.monarch_head_bwd.restype = c_int
+    lib.monarch_head_step.argtypes = [vp, i64] + [vp] * 9 + head
+    lib.monarch_head_step.restype = c_int
+    u64 = ctypes.c_uint64
+    lib.monarch_dropout.argtypes = [vp] * 3 + [i64, ctypes.c_double, u64, u64, vp, c_int, vp] + ev
+    lib.monarch_dropout.restype = c_int
     lib.monarch_sandwich_fwd.argtypes = ([vp] * 10 + [i64] * 3 + [c_int] * 2 + [c_float] * 3 +
                                          [c_int, vp] + ev)
     lib.monarch_sandwich_fwd.restype = c_int
@@ -486,3 +501,47 @@ def monarch_distill_step(logits, ld, teacher, ids, labels, row_weight, loss, dlo
     z, *rest = _addresses(logits, teacher, ids, labels, row_weight, loss, dlogits)
     _check(load_library().monarch_distill_step(z, ld, *rest, dld, rows, vocab, top, temperature, mix,
                                                dtype, _stream(stream), arr, n))
+
+
+HEAD_FWD, HEAD_BWD, HEAD_STEP = 0, 1, 2
+
+
+def monarch_head_workspace_bytes(call, rows, features, vocab, top, dtype) -> int:
+    return load_library().monarch_head_workspace_bytes(call, rows, features, vocab, top, dtype)
+
+
+def monarch_head_stats_bytes(rows, top) -> int:
+    return load_library().monarch_head_stats_bytes(rows, top)
+
+
+def monarch_head_fwd(x, ldx, w, labels, teacher, ids, loss, stats, workspace, workspace_bytes, rows,
+                     features, vocab, top, temperature, mix, dtype, stream=None, events=None) -> None:
+    arr, n = _events(events)
+    a, *rest = _addresses(x, w, labels, teacher, ids, loss, stats, workspace)
+    _check(load_library().monarch_head_fwd(a, ldx, *rest, workspace_bytes, rows, features, vocab, top,
+                                           temperature, mix, dtype, _stream(stream), arr, n))
+
+
+def monarch_head_bwd(dloss, x, ldx, w, labels, teacher, ids, stats, dx, dw, workspace, workspace_bytes,
+                     rows, features, vocab, top, temperature, mix, dtype, stream=None,
+                     events=None) -> None:
+    arr, n = _events(events)
+    g, a, *rest = _addresses(dloss, x, w, labels, teacher, ids, stats, dx, dw, workspace)
+    _check(load_library().monarch_head_bwd(g, a, ldx, *rest, workspace_bytes, rows, features, vocab,
+                                           top, temperature, mix, dtype, _stream(stream), arr, n))
+
+
+def monarch_head_step(x, ldx, w, labels, teacher, ids, row_weight, loss, dx, dw, workspace,
+                      workspace_bytes, rows, features, vocab, top, temperature, mix, dtype,
+                      stream=None, events=None) -> None:
+    arr, n = _events(events)
+    a, *rest = _addresses(x, w, labels, teacher, ids, row_weight, loss, dx, dw, workspace)
+    _check(load_library().monarch_head_step(a, ldx, *rest, workspace_bytes, rows, features, vocab, top,
+                                            temperature, mix, dtype, _stream(stream), arr, n))
+
+
+def monarch_dropout(x, residual, y, n, p, seed, offset, state, dtype, stream=None, events=None) -> None:
+    arr, ne = _events(events)
+    a, r, o, st = _addresses(x, residual, y, state)
+    _check(load_library().monarch_dropout(a, r, o, n, p, seed, offset, st, dtype, _stream(stream), arr,
+                                          ne))

@@ -1,0 +1,67 @@
+// The head loss's launches (internal): planning and C entries in head.hip, the
+// products in head_gemm.hip.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_pipe.h"
+
+namespace monarch {
+
+constexpr int64_t kHeadRows = 256;   // rows of the workspace's copies are a multiple of this, and so are a piece's columns
+
+// What the products' epilogues take of a row: its largest logit and the factors of
+// its exponentials; the label's share is taken off at the label.
+struct HeadRow {
+  float m, a, b, off;   // g = a 2^((z - m) ct) + b 2^((z - m) log2 e) - off [v = label]
+};
+
+enum HeadShape { HEAD_256 = 0, HEAD_128 = 1, HEAD_32 = 2 };
+
+struct HeadLogits {
+  PipeProduct pr;             // A: the head's words, B: the rows
+  const int* count;           // rows in use
+  int64_t vocab, v0, v1;      // words of this launch: [v0, v1)
+  int64_t d;                  // k
+  int64_t np;                 // rows of the workspace's copies
+  float ct;                   // log2(e) / temperature
+  const int* label;           // a row: its label, -1 without one
+  // sums: part [tiles of words][np][3] (largest logit, sum at T, sum at 1), z of the label
+  float* part;
+  float* z_label;
+  // gradient: g [planes][np][vp]
+  const HeadRow* row;
+  uint16_t* g;
+  int64_t vp, g_plane;
+};
+
+struct HeadDx {
+  PipeProduct pr;             // A: the head's words [v][d], B: g [n][v]
+  const int* count;
+  int64_t d, dp, np;
+  int64_t k, chunk;           // words of this piece, words a split
+  int splits;
+  float* part;                // [splits][np][dp]
+  int add;                    // whether a piece before has written part
+};
+
+struct HeadDw {
+  PipeProduct pr;             // A: the rows [n][d], B: g [n][v]
+  const int* count;
+  int64_t d, dp, cols;        // cols: words of this piece
+  int splits;
+  float* part;                // [splits][cols][dp], or null:
+  void* dw;                   // the piece's first word of dw [vocab][d]
+  int bf16;
+};
+
+int64_t head_tile_words(HeadShape s);    // words of a logits tile
+int64_t head_tile_rows(HeadShape s);     // rows of a logits and a dx tile
+// second: the labels' softmax has exponentials of its own
+hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, bool second, hipStream_t st);
+hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, bool second, hipStream_t st);
+hipError_t head_launch_dx(const HeadDx& a, HeadShape s, hipStream_t st);
+hipError_t head_launch_dw(const HeadDw& a, HeadShape s, hipStream_t st);
+
+}  // namespace monarch

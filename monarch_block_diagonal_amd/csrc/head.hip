@@ -1,0 +1,760 @@
+// Head loss: the loss of rows x [n][d] under a dense head w [vocab][d] and its
+// gradients by both, in pieces of the vocabulary; the logits z = x w^T are never kept.
+//
+// With q = softmax(z / T), s = softmax(z), p = softmax(t / T) over a row's valid teacher
+// entries (id_k, t_k), label c and row weight r:
+//   loss = mix T^2 sum_k p_k (log p_k - log q[id_k]) - (1 - mix) log s[c]
+//   g_v  = r (mix T (q_v - sum_{k: id_k = v} p_k) + (1 - mix) (s_v - [v = c]))
+//   dx = g w, dw = g^T x
+//
+// A forward pass takes every tile of logits from its product to (maximum, sum at T,
+// sum at 1) of its rows, and joins these over the tiles. A backward pass knows the sums,
+// so it computes the logits again, a piece of the vocabulary at a time, turns them into
+// g in the product's epilogue, writes that piece of g to the workspace and multiplies
+// it twice. Rows that count nothing (no label, no entry) are left out of all products:
+// the rows that do are first copied side by side, with their columns padded to whole K
+// tiles; what a row left out holds (NaN too) reaches nothing.
+//
+// The teacher's columns of g are few: their logits are taken from products of their
+// own in the forward pass (a wave an entry), and each is written again behind the piece's
+// epilogue with its share of p, once, in fp32 up to its one rounding.
+#include <math.h>
+
+#include "api_internal.h"
+#include "head.h"
+#include "kernels.h"
+#include "monarch.h"
+#include "team.h"
+
+namespace monarch {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int64_t kLimit = int64_t(1) << 31;
+constexpr int64_t kMaxFeatures = int64_t(1) << 20;
+constexpr int64_t kPieceBytes = int64_t(1) << 30;   // of g
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The rows in use.
+struct Rows {
+  int* count;
+  int* idx;      // [np] row of x
+  int* pos;      // [rows] place among them, -1
+  int* label;    // [np] label, -1 without one
+  int* has;      // [np] whether the row has a valid entry
+  int* flag;     // [rows] whether it has (before the rows are counted)
+};
+
+struct Call {
+  const void* x;
+  const void* w;
+  const float* teacher;
+  const int64_t* ids;
+  const int64_t* labels;
+  const float* weight;        // null: 1
+  float *loss, *stats;
+  void *dx, *dw;
+  int64_t rows, ldx, d, vocab;
+  int top;
+  float temperature, mix;     // temperature 1 where there is no first term
+  bool bf16, told, taught, second;
+};
+
+__device__ __forceinline__ bool entry_ok(int64_t id, float t, int64_t vocab) {
+  return id >= 0 && id < vocab && t > -INFINITY;
+}
+
+// A wave a row: does it have an entry?
+__global__ __launch_bounds__(256) void head_flag_kernel(Call c, Rows r) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (i >= c.rows) return;
+  bool any = false;
+  for (int k = threadIdx.x & 63; k < c.top; k += 64)
+    any |= entry_ok(c.ids[i * c.top + k], c.teacher[i * c.top + k], c.vocab);
+  const bool all = __any(any);
+  if ((threadIdx.x & 63) == 0) r.flag[i] = all;
+}
+
+// One workgroup: the rows in use, in their order; loss and statistics of the others are 0.
+__global__ __launch_bounds__(1024) void head_rows_kernel(Call c, Rows r, uint32_t* zeros) {
+  constexpr int PER = 4;
+  __shared__ int s_wave[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (threadIdx.x < 4) zeros[threadIdx.x] = 0;
+  int base = 0;
+  for (int64_t first = 0; first < c.rows; first += 1024 * PER) {
+    int label[PER], has[PER], mine = 0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int64_t i = first + threadIdx.x * PER + e;
+      label[e] = -1, has[e] = 0;
+      if (i < c.rows) {
+        if (c.told) {
+          const int64_t l = c.labels[i];
+          if (l >= 0 && l < c.vocab) label[e] = static_cast<int>(l);
+        }
+        if (c.taught) has[e] = r.flag[i];
+      }
+      mine += label[e] >= 0 || has[e];
+    }
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 63) s_wave[wave] = upto;
+    __syncthreads();
+    int at = base + upto - mine, all = base;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) at += s_wave[w];
+      all += s_wave[w];
+    }
+    base = all;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int64_t i = first + threadIdx.x * PER + e;
+      if (i >= c.rows) continue;
+      const bool used = label[e] >= 0 || has[e];
+      r.pos[i] = used ? at : -1;
+      if (used) {
+        r.idx[at] = static_cast<int>(i), r.label[at] = label[e], r.has[at] = has[e];
+        ++at;
+      } else if (c.loss) {
+        c.loss[i] = 0.f;
+        *reinterpret_cast<f32x4*>(c.stats + i * 4) = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+    __syncthreads();
+  }
+  // the last tile's other rows
+  const int end = (base + static_cast<int>(kHeadRows) - 1) / static_cast<int>(kHeadRows) * static_cast<int>(kHeadRows);
+  for (int k = base + threadIdx.x; k < end; k += 1024) r.idx[k] = 0, r.label[k] = -1, r.has[k] = 0;
+  if (threadIdx.x == 0) *r.count = base;
+}
+
+// One value as bf16, and what is left of it.
+__device__ __forceinline__ uint16_t next_part(float& v) {
+  const uint16_t h = f32_to_bf16(v);
+  v = isfinite(v) ? v - bf16_to_f32(h) : 0.f;
+  return h;
+}
+
+// Rows of d elements (with idx: rows idx[k] for k < *count, zeros up to the next whole
+// tile) copied to rows of dp, zeros behind them; fp32 as three bf16 planes. A workgroup a row.
+template <typename T>
+__global__ __launch_bounds__(256) void head_copy_kernel(const T* __restrict__ src, int64_t ld, const int* idx,
+                                                        const int* count, int64_t d, int64_t dp,
+                                                        uint16_t* __restrict__ dst, int64_t plane) {
+  constexpr bool F32 = sizeof(T) == 4;
+  const int64_t k = blockIdx.x;
+  bool zero = false;
+  int64_t row = k;
+  if (idx) {
+    const int n = *count;
+    if (k >= (n + kHeadRows - 1) / kHeadRows * kHeadRows) return;
+    zero = k >= n;
+    row = zero ? 0 : idx[k];
+  }
+  const T* s = src + row * ld;
+  uint16_t* o = dst + k * dp;
+  const bool whole = ((reinterpret_cast<uintptr_t>(s) & 15) == 0) && d % (F32 ? 4 : 8) == 0;
+  if constexpr (F32) {
+    for (int64_t e = threadIdx.x * 4; e < dp; e += 1024) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (!zero && e < d) {
+        if (whole) {
+          const f32x4 q = *reinterpret_cast<const f32x4*>(s + e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = q[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (e + i < d) v[i] = s[e + i];
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        uint16_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = next_part(v[i]);
+        __builtin_memcpy(o + p * plane + e, h, 8);
+      }
+    }
+  } else {
+    for (int64_t e = threadIdx.x * 8; e < dp; e += 2048) {
+      u32x4 v = {0, 0, 0, 0};
+      if (!zero && e < d) {
+        if (whole) {
+          v = *reinterpret_cast<const u32x4*>(s + e);
+        } else {
+          uint16_t h[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[i] = e + i < d ? s[e + i] : uint16_t(0);
+          __builtin_memcpy(&v, h, 16);
+        }
+      }
+      *reinterpret_cast<u32x4*>(o + e) = v;
+    }
+  }
+}
+
+// Logits of the teacher's entries: a wave takes four of a row at a time. Stored by row
+// of x behind the statistics; 0 for an entry that is not valid.
+template <typename T>
+__global__ __launch_bounds__(256) void head_entries_kernel(Call c, Rows r, const T* __restrict__ xs, int64_t ldx,
+                                                           bool by_row, const T* __restrict__ ws, int64_t ldw) {
+  const int k = blockIdx.x;
+  if (k >= *r.count || !r.has[k]) return;
+  const int64_t i = r.idx[k];
+  const T* x = xs + (by_row ? i : static_cast<int64_t>(k)) * ldx;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float* out = c.stats + c.rows * 4 + i * c.top;
+  for (int j0 = wave * 4; j0 < c.top; j0 += 16) {
+    const T* w[4];
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    bool ok[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + e < c.top ? j0 + e : c.top - 1;
+      const int64_t id = c.ids[i * c.top + j];
+      ok[e] = entry_ok(id, c.teacher[i * c.top + j], c.vocab);
+      w[e] = ws + (ok[e] ? id : 0) * ldw;
+    }
+    if constexpr (sizeof(T) == 2) {
+      for (int64_t at = lane * 8; at < c.d; at += 512) {
+        // rows of the head in place are whole pieces; padded copies end in zeros
+        float a[8];
+        PieceOf<uint16_t>::unpack(*reinterpret_cast<const u32x4*>(x + at), a);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float b[8];
+          PieceOf<uint16_t>::unpack(*reinterpret_cast<const u32x4*>(w[e] + at), b);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) sum[e] = fmaf(a[q], b[q], sum[e]);
+        }
+      }
+    } else {
+      for (int64_t at = lane; at < c.d; at += 64) {
+        const float a = x[at];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = fmaf(a, w[e][at], sum[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float s = lanes_reduce<SumOp, 64>(sum[e]);
+      if (lane == 0 && j0 + e < c.top) out[j0 + e] = ok[e] ? s : 0.f;
+    }
+  }
+}
+
+// Maximum and logarithm of the sum of exp(t / T) over a row's valid entries, by one wave.
+__device__ __forceinline__ void teacher_sums(const Call& c, int64_t i, int lane, float* top, float* sum) {
+  const float ct = kLog2e / c.temperature;
+  float m = -3.402823466e38f;
+  for (int j = lane; j < c.top; j += 64)
+    if (entry_ok(c.ids[i * c.top + j], c.teacher[i * c.top + j], c.vocab)) m = fmaxf(m, c.teacher[i * c.top + j]);
+  m = lanes_reduce<MaxOp, 64>(m);
+  float s = 0.f;
+  for (int j = lane; j < c.top; j += 64)
+    if (entry_ok(c.ids[i * c.top + j], c.teacher[i * c.top + j], c.vocab)) s += exp2_of((c.teacher[i * c.top + j] - m) * ct);
+  *top = m;
+  *sum = lanes_reduce<SumOp, 64>(s);
+}
+
+// Joins the tiles' sums of RW rows a workgroup, and gives the rows' losses.
+template <int RW>
+__global__ __launch_bounds__(256) void head_loss_kernel(Call c, Rows r, const float* __restrict__ part, int64_t np,
+                                                        int tiles, const float* __restrict__ z_label) {
+  constexpr int SL = 256 / RW;
+  __shared__ float s[3][256];
+  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * RW;
+  const int count = *r.count;
+  if (k0 >= count) return;
+  const float ct = kLog2e / c.temperature;
+  const int col = threadIdx.x % RW, slice = threadIdx.x / RW;
+  const float* at = part + k0 + col;
+  float m = -3.402823466e38f, st = 0.f, s1 = 0.f;
+  // in fixed order: tiles slice, slice + SL, ...
+  for (int t = slice; t < tiles; t += SL) {
+    const float* o = at + static_cast<int64_t>(t) * 3 * np;
+    const float tm = o[0], ts = o[np], t1 = o[2 * np];
+    const float to = fmaxf(m, tm), f = m - to, g = tm - to;
+    st = st * exp2_of(f * ct) + ts * exp2_of(g * ct);
+    s1 = s1 * exp2_of(f * kLog2e) + t1 * exp2_of(g * kLog2e);
+    m = to;
+  }
+  s[0][threadIdx.x] = m, s[1][threadIdx.x] = st, s[2][threadIdx.x] = s1;
+  for (int half = SL / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (slice < half) {
+      const int u = threadIdx.x + half * RW;
+      const float tm = s[0][u], to = fmaxf(m, tm), f = m - to, g = tm - to;
+      st = st * exp2_of(f * ct) + s[1][u] * exp2_of(g * ct);
+      s1 = s1 * exp2_of(f * kLog2e) + s[2][u] * exp2_of(g * kLog2e);
+      m = to;
+      s[0][threadIdx.x] = m, s[1][threadIdx.x] = st, s[2][threadIdx.x] = s1;
+    }
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  for (int w = threadIdx.x >> 6; w < RW; w += 4) {
+    const int64_t k = k0 + w;
+    if (k >= count) break;
+    const int64_t i = r.idx[k];
+    const float rm = s[0][w], rt = s[1][w], r1 = s[2][w];
+    float loss = 0.f;
+    if (r.has[k]) {
+      float tm, ts;
+      teacher_sums(c, i, lane, &tm, &ts);
+      const float log_ts = logf(ts), log_q = logf(rt), by = 1.0f / c.temperature;
+      float kl = 0.f;
+      for (int j = lane; j < c.top; j += 64) {
+        const float t = c.teacher[i * c.top + j];
+        if (!entry_ok(c.ids[i * c.top + j], t, c.vocab)) continue;
+        const float e = exp2_of((t - tm) * (kLog2e * by)), p = e / ts;
+        const float z = c.stats[c.rows * 4 + i * c.top + j];
+        if (p > 0.f) kl += p * (((t - tm) * by - log_ts) - ((z - rm) * by - log_q));
+      }
+      loss = c.mix * c.temperature * c.temperature * lanes_reduce<SumOp, 64>(kl);
+    }
+    if (r.label[k] >= 0) loss += (1.0f - c.mix) * (logf(r1) - (z_label[k] - rm));
+    if (lane == 0) {
+      c.loss[i] = loss;
+      *reinterpret_cast<f32x4*>(c.stats + i * 4) = f32x4{rm, rt, r1, 0.f};
+    }
+  }
+}
+
+// The rows' factors for g (0 for the last tile's other rows).
+__global__ __launch_bounds__(256) void head_factors_kernel(Call c, Rows r, HeadRow* out, float* taught) {
+  const int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int count = *r.count;
+  if (k >= (count + kHeadRows - 1) / kHeadRows * kHeadRows) return;
+  HeadRow o = {0.f, 0.f, 0.f, 0.f};
+  float a = 0.f;
+  if (k < count) {
+    const int64_t i = r.idx[k];
+    const f32x4 st = *reinterpret_cast<const f32x4*>(c.stats + i * 4);
+    const float w = c.weight ? c.weight[i] : 1.0f;
+    a = r.has[k] ? c.mix * c.temperature * w : 0.f;
+    o.m = st[0];
+    o.off = r.label[k] >= 0 ? (1.0f - c.mix) * w : 0.f;
+    if (c.second) {
+      o.a = a / st[1], o.b = o.off / st[2];
+    } else {
+      // one softmax: at T = 1, or with one of the two terms alone
+      o.a = (a + o.off) / st[1];
+    }
+  }
+  out[k] = o;
+  taught[k] = a;
+}
+
+// The teacher's columns of a piece of g: a wave a row.
+__global__ __launch_bounds__(64) void head_taught_kernel(Call c, Rows r, const HeadRow* __restrict__ rows,
+                                                         const float* __restrict__ taught, uint16_t* __restrict__ g,
+                                                         int64_t vp, int64_t plane, int planes, int64_t v0, int64_t v1) {
+  extern __shared__ __align__(16) int s_id[];
+  float* s_p = reinterpret_cast<float*>(s_id + c.top);
+  const int64_t k = blockIdx.x;
+  if (k >= *r.count || !r.has[k]) return;
+  const int64_t i = r.idx[k];
+  const int lane = threadIdx.x;
+  float tm, ts;
+  teacher_sums(c, i, lane, &tm, &ts);
+  const float ct = kLog2e / c.temperature;
+  for (int j = lane; j < c.top; j += 64) {
+    const int64_t id = c.ids[i * c.top + j];
+    const float t = c.teacher[i * c.top + j];
+    const bool ok = entry_ok(id, t, c.vocab);
+    s_id[j] = ok ? static_cast<int>(id) : -1;
+    s_p[j] = ok ? exp2_of((t - tm) * ct) / ts : 0.f;
+  }
+  __syncthreads();
+  const HeadRow h = rows[k];
+  const int label = r.label[k];
+  for (int j = lane; j < c.top; j += 64) {
+    const int id = s_id[j];
+    if (id < v0 || id >= v1) continue;
+    // entries that name one word: the first writes their sum
+    float p = 0.f;
+    bool first = true;
+    for (int u = 0; u < c.top; ++u)
+      if (s_id[u] == id) {
+        first &= u >= j;
+        p += s_p[u];
+      }
+    if (!first) continue;
+    const float z = c.stats[c.rows * 4 + i * c.top + j] - h.m;
+    float v = h.a * exp2_of(z * ct) + (c.second ? h.b * exp2_of(z * kLog2e) : 0.f) - taught[k] * p;
+    if (id == label) v -= h.off;
+    uint16_t* o = g + k * vp + (id - v0);
+    for (int q = 0; q < planes; ++q) o[q * plane] = next_part(v);
+  }
+}
+
+// dx of every row from the splits' sums; rows left out get 0. Four columns a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void head_dx_out_kernel(const float* __restrict__ part, const int* __restrict__ pos,
+                                                          int64_t rows, int64_t np, int64_t d, int64_t dp, int splits,
+                                                          T* __restrict__ dx) {
+  const int64_t per = (d + 3) / 4, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= rows * per) return;
+  const int64_t i = at / per, e = (at - i * per) * 4;
+  const int64_t k = pos[i];
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (k >= 0)
+    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(part + (s * np + k) * dp + e);
+  T* o = dx + i * d + e;
+  if (d % 4 == 0) {
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<u32x2*>(o) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    else
+      *reinterpret_cast<f32x4*>(o) = v;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (e + q < d) Io<T>::store(o, q, v[q]);
+  }
+}
+
+// A piece's dw from the splits' sums.
+template <typename T>
+__global__ __launch_bounds__(256) void head_dw_out_kernel(const float* __restrict__ part, int64_t cols, int64_t d,
+                                                          int64_t dp, int splits, T* __restrict__ dw) {
+  const int64_t per = (d + 3) / 4, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= cols * per) return;
+  const int64_t v = at / per, e = (at - v * per) * 4;
+  f32x4 a = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s) a += *reinterpret_cast<const f32x4*>(part + (s * cols + v) * dp + e);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (e + q < d) Io<T>::store(dw, v * d + e + q, a[q]);
+}
+
+// ------------------------------------------------------------------ planning
+
+enum What { FWD = 0, BWD = 1, STEP = 2 };
+
+int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+
+struct HeadPlan {
+  int64_t d, dp, np, planes;
+  bool copy_w;                 // the head is copied (fp32, or rows that are no whole pieces)
+  HeadShape shape;             // logits
+  HeadShape dx_shape, dw_shape;
+  int64_t tiles;               // of words, forward
+  int64_t vp, pieces;          // words of a piece
+  int dx_splits, dw_splits;
+  int64_t dx_chunk;
+  // byte offsets in the workspace
+  size_t rows, x, w, part, z_label, stats, factors, taught, g, dx, dw, total;
+};
+
+// Splits of a sum of `steps` K tiles over `base` tiles of output, so that the
+// workgroups fill whole rounds of `slots`.
+int pick_splits(int64_t base, int64_t steps, int64_t slots, int64_t most) {
+  int64_t top = steps / 8 < most ? steps / 8 : most;
+  if (top < 1) top = 1;
+  int best = 1;
+  double best_eff = 0.0;
+  for (int64_t s = 1; s <= top; ++s) {
+    const int64_t n = base * s;
+    const double eff = static_cast<double>(n) / static_cast<double>(up(n, slots));
+    if (eff > best_eff + 0.04) best = static_cast<int>(s), best_eff = eff;
+    if (best_eff >= 0.94 || n >= 8 * slots) break;
+  }
+  return best;
+}
+
+HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top, bool bf16) {
+  HeadPlan p = {};
+  p.d = d, p.dp = up(d, kPipeK), p.np = up(rows, kHeadRows), p.planes = bf16 ? 1 : 3;
+  p.copy_w = !bf16 || d % 8 != 0;
+  // the widest tile that leaves work for every CU
+  const int64_t t256 = (up(vocab, 256) / 256) * (up(rows, 256) / 256);
+  p.shape = rows <= 32 ? HEAD_32 : (rows <= 128 || t256 < 384) ? HEAD_128 : HEAD_256;
+  const int64_t tv = head_tile_words(p.shape);
+  p.tiles = (vocab + tv - 1) / tv;
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t here = at;
+    at = static_cast<size_t>(up(static_cast<int64_t>(at) + bytes, 256));
+    return here;
+  };
+  p.rows = take(256 + (p.np * 3 + rows * 2) * 4);
+  p.x = take(p.planes * p.np * p.dp * 2);
+  p.w = p.copy_w ? take(p.planes * vocab * p.dp * 2) : 0;
+  if (what != BWD) {
+    p.part = take(p.tiles * 3 * p.np * 4);
+    p.z_label = take(p.np * 4);
+  }
+  if (what == STEP) p.stats = take(rows * (4 + top) * 4);
+  if (what != FWD) {
+    int64_t vp = up(kPieceBytes / (p.planes * p.np * 2), kHeadRows) - kHeadRows;
+    if (vp < kHeadRows) vp = kHeadRows;
+    p.pieces = (vocab + vp - 1) / vp;
+    p.vp = up((vocab + p.pieces - 1) / p.pieces, kHeadRows);
+    p.pieces = (vocab + p.vp - 1) / p.vp;
+    const bool wide = rows > 128 && d > 128;
+    p.dx_shape = rows <= 32 ? HEAD_32 : wide ? HEAD_256 : HEAD_128;
+    const int64_t tm = head_tile_words(p.dx_shape), tn = head_tile_rows(p.dx_shape);
+    const int64_t base = (up(d, tm) / tm) * (up(rows, tn) / tn), steps = p.vp / kPipeK;
+    int64_t most = (int64_t(1) << 30) / (p.np * p.dp * 4);
+    if (most > 256) most = 256;
+    p.dx_splits = pick_splits(base, steps, wide ? 256 : 512, most);
+    p.dx_chunk = up((p.vp + p.dx_splits - 1) / p.dx_splits, kPipeK);
+    p.dx_splits = static_cast<int>((p.vp + p.dx_chunk - 1) / p.dx_chunk);
+    const int64_t w256 = (up(d, 256) / 256) * (up(p.vp, 256) / 256);
+    p.dw_shape = d > 128 && w256 >= 192 ? HEAD_256 : HEAD_128;
+    const int64_t tw = head_tile_words(p.dw_shape);
+    const int64_t wbase = (up(d, tw) / tw) * (up(p.vp, tw) / tw);
+    const int64_t slots = p.dw_shape == HEAD_256 ? 256 : 512;
+    most = (int64_t(1) << 30) / (p.vp * p.dp * 4);
+    p.dw_splits = wbase >= slots / 2 ? 1 : pick_splits(wbase, up(rows, kPipeK) / kPipeK, slots, most < 64 ? most : 64);
+    p.factors = take(p.np * static_cast<int64_t>(sizeof(HeadRow)));
+    p.taught = take(p.np * 4);
+    p.g = take(p.planes * p.np * p.vp * 2);
+    p.dx = take(p.dx_splits * p.np * p.dp * 4);
+    p.dw = p.dw_splits > 1 ? take(p.dw_splits * p.vp * p.dp * 4) : 0;
+  }
+  p.total = at;
+  return p;
+}
+
+int check_sizes(int64_t rows, int64_t d, int64_t vocab, int64_t ldx, int64_t top, int dtype) {
+  if (dtype != MONARCH_F32 && dtype != MONARCH_BF16) return MONARCH_ERR_DTYPE;
+  if (rows < 0 || rows >= kLimit - kHeadRows || d <= 0 || d > kMaxFeatures || vocab <= 0 || vocab > (int64_t(1) << 30) ||
+      ldx < d || top < 0 || top > MONARCH_DISTILL_MAX_TOP)
+    return MONARCH_ERR_SHAPE;
+  return MONARCH_OK;
+}
+
+bool off_elements(const void* p, int size) { return reinterpret_cast<uintptr_t>(p) % size != 0; }
+
+#define HEAD_TRY(e)                        \
+  do {                                     \
+    const int head_st = record_hip(e);     \
+    if (head_st) return head_st;           \
+  } while (0)
+
+template <typename T>
+hipError_t copy_rows(const void* src, int64_t ld, const int* idx, const int* count, int64_t rows, int64_t d, int64_t dp,
+                     void* dst, int64_t plane, hipStream_t s) {
+  hipLaunchKernelGGL(head_copy_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, static_cast<const T*>(src), ld,
+                     idx, count, d, dp, static_cast<uint16_t*>(dst), plane);
+  return hipGetLastError();
+}
+
+// One call of the three: checks are done.
+int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
+  Rows r;
+  uint32_t* head = reinterpret_cast<uint32_t*>(ws + p.rows);   // 16 bytes of zeros, the count
+  r.count = reinterpret_cast<int*>(head + 4);
+  r.idx = reinterpret_cast<int*>(head + 64);
+  r.label = r.idx + p.np;
+  r.has = r.label + p.np;
+  r.pos = r.has + p.np;
+  r.flag = r.pos + c.rows;
+  uint16_t* xc = reinterpret_cast<uint16_t*>(ws + p.x);
+  if (c.taught) {
+    hipLaunchKernelGGL(head_flag_kernel, dim3(static_cast<unsigned>((c.rows + 3) / 4)), dim3(256), 0, s, c, r);
+    HEAD_TRY(hipGetLastError());
+  }
+  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, s, c, r, head);
+  HEAD_TRY(hipGetLastError());
+  const int64_t xplane = p.np * p.dp, wplane = c.vocab * p.dp;
+  HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.x, c.ldx, r.idx, r.count, p.np, p.d, p.dp, xc, xplane, s)
+                  : copy_rows<float>(c.x, c.ldx, r.idx, r.count, p.np, p.d, p.dp, xc, xplane, s));
+  const uint16_t* w = static_cast<const uint16_t*>(c.w);
+  int64_t ldw = p.d;
+  if (p.copy_w) {
+    HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.w, p.d, nullptr, nullptr, c.vocab, p.d, p.dp, ws + p.w, wplane, s)
+                    : copy_rows<float>(c.w, p.d, nullptr, nullptr, c.vocab, p.d, p.dp, ws + p.w, wplane, s));
+    w = reinterpret_cast<const uint16_t*>(ws + p.w);
+    ldw = p.dp;
+  }
+  HeadLogits l = {};
+  l.pr.zeros = reinterpret_cast<const uint16_t*>(head);
+  l.pr.planes = static_cast<int>(p.planes);
+  l.pr.a.p = w, l.pr.a.ld = ldw, l.pr.a.plane = wplane, l.pr.a.rows = c.vocab, l.pr.a.kvalid = ldw;
+  l.pr.b.p = xc, l.pr.b.ld = p.dp, l.pr.b.plane = xplane, l.pr.b.rows = p.np, l.pr.b.kvalid = p.dp;
+  l.count = r.count, l.vocab = c.vocab, l.d = p.d, l.np = p.np, l.ct = kLog2e / c.temperature, l.label = r.label;
+  if (what != BWD) {
+    if (c.taught) {
+      const dim3 g(static_cast<unsigned>(c.rows));
+      if (c.bf16)
+        hipLaunchKernelGGL(head_entries_kernel<uint16_t>, g, dim3(256), 0, s, c, r, static_cast<const uint16_t*>(xc), p.dp, false, w, ldw);
+      else
+        hipLaunchKernelGGL(head_entries_kernel<float>, g, dim3(256), 0, s, c, r, static_cast<const float*>(c.x), c.ldx, true,
+                           static_cast<const float*>(c.w), p.d);
+      HEAD_TRY(hipGetLastError());
+    }
+    l.v0 = 0, l.v1 = c.vocab;
+    l.part = reinterpret_cast<float*>(ws + p.part), l.z_label = reinterpret_cast<float*>(ws + p.z_label);
+    HEAD_TRY(head_launch_sums(l, p.shape, c.second, s));
+    if (c.rows <= 256)
+      hipLaunchKernelGGL(head_loss_kernel<1>, dim3(static_cast<unsigned>(c.rows)), dim3(256), 0, s, c, r, l.part, p.np,
+                         static_cast<int>(p.tiles), l.z_label);
+    else
+      hipLaunchKernelGGL(head_loss_kernel<16>, dim3(static_cast<unsigned>((c.rows + 15) / 16)), dim3(256), 0, s, c, r, l.part,
+                         p.np, static_cast<int>(p.tiles), l.z_label);
+    HEAD_TRY(hipGetLastError());
+  }
+  if (what == FWD) return MONARCH_OK;
+  HeadRow* factors = reinterpret_cast<HeadRow*>(ws + p.factors);
+  float* taught = reinterpret_cast<float*>(ws + p.taught);
+  hipLaunchKernelGGL(head_factors_kernel, dim3(static_cast<unsigned>(p.np / 256)), dim3(256), 0, s, c, r, factors, taught);
+  HEAD_TRY(hipGetLastError());
+  uint16_t* g = reinterpret_cast<uint16_t*>(ws + p.g);
+  l.row = factors, l.g = g, l.vp = p.vp, l.g_plane = p.np * p.vp;
+  HeadDx x = {};
+  x.pr.zeros = l.pr.zeros, x.pr.planes = l.pr.planes;
+  x.pr.b.p = g, x.pr.b.ld = p.vp, x.pr.b.plane = l.g_plane, x.pr.b.rows = p.np;
+  x.count = r.count, x.d = p.d, x.dp = p.dp, x.np = p.np, x.chunk = p.dx_chunk, x.splits = p.dx_splits;
+  x.part = reinterpret_cast<float*>(ws + p.dx);
+  HeadDw y = {};
+  y.pr.zeros = l.pr.zeros, y.pr.planes = l.pr.planes;
+  y.pr.a.p = xc, y.pr.a.ld = p.dp, y.pr.a.plane = xplane, y.pr.a.rows = p.dp, y.pr.a.kvalid = p.np;
+  y.pr.b.p = g, y.pr.b.ld = p.vp, y.pr.b.plane = l.g_plane, y.pr.b.rows = p.vp, y.pr.b.kvalid = p.np;
+  y.count = r.count, y.d = p.d, y.dp = p.dp, y.splits = p.dw_splits, y.bf16 = c.bf16;
+  y.part = p.dw_splits > 1 ? reinterpret_cast<float*>(ws + p.dw) : nullptr;
+  const int64_t es = c.bf16 ? 2 : 4;
+  for (int64_t v0 = 0; v0 < c.vocab; v0 += p.vp) {
+    const int64_t v1 = v0 + p.vp < c.vocab ? v0 + p.vp : c.vocab;
+    l.v0 = v0, l.v1 = v1;
+    HEAD_TRY(head_launch_grad(l, p.shape, c.second, s));
+    if (c.taught) {
+      hipLaunchKernelGGL(head_taught_kernel, dim3(static_cast<unsigned>(c.rows)), dim3(64), static_cast<size_t>(c.top) * 8, s, c,
+                         r, factors, taught, g, p.vp, l.g_plane, static_cast<int>(p.planes), v0, v1);
+      HEAD_TRY(hipGetLastError());
+    }
+    x.pr.a.p = w + v0 * ldw, x.pr.a.ld = ldw, x.pr.a.plane = wplane, x.pr.a.rows = ldw, x.pr.a.kvalid = v1 - v0;
+    x.k = up(v1 - v0, kPipeK), x.pr.b.kvalid = x.k;
+    x.add = v0 > 0;
+    HEAD_TRY(head_launch_dx(x, p.dx_shape, s));
+    y.cols = v1 - v0;
+    y.dw = static_cast<char*>(c.dw) + v0 * p.d * es;
+    HEAD_TRY(head_launch_dw(y, p.dw_shape, s));
+    if (y.part) {
+      const unsigned n = static_cast<unsigned>((y.cols * ((p.d + 3) / 4) + 255) / 256);
+      if (c.bf16)
+        hipLaunchKernelGGL(head_dw_out_kernel<uint16_t>, dim3(n), dim3(256), 0, s, y.part, y.cols, p.d, p.dp, p.dw_splits,
+                           static_cast<uint16_t*>(y.dw));
+      else
+        hipLaunchKernelGGL(head_dw_out_kernel<float>, dim3(n), dim3(256), 0, s, y.part, y.cols, p.d, p.dp, p.dw_splits,
+                           static_cast<float*>(y.dw));
+      HEAD_TRY(hipGetLastError());
+    }
+  }
+  const int64_t n = (c.rows * ((p.d + 3) / 4) + 255) / 256;
+  if (n > 0x7fffffffLL) return record_hip(hipErrorInvalidConfiguration);
+  if (c.bf16)
+    hipLaunchKernelGGL(head_dx_out_kernel<uint16_t>, dim3(static_cast<unsigned>(n)), dim3(256), 0, s, x.part, r.pos, c.rows,
+                       p.np, p.d, p.dp, p.dx_splits, static_cast<uint16_t*>(c.dx));
+  else
+    hipLaunchKernelGGL(head_dx_out_kernel<float>, dim3(static_cast<unsigned>(n)), dim3(256), 0, s, x.part, r.pos, c.rows, p.np,
+                       p.d, p.dp, p.dx_splits, static_cast<float*>(c.dx));
+  return record_hip(hipGetLastError());
+}
+
+int call(Call c, int what, const void* stats_in, int64_t top, float temperature, float mix, int dtype, void* workspace,
+         size_t workspace_bytes, void* stream, void* const* events, int n_events) {
+  int st = check_sizes(c.rows, c.d, c.vocab, c.ldx, top, dtype);
+  if (st) return st;
+  if (!(temperature >= 1e-6f) || !(temperature <= 1e6f) || !(mix >= 0.0f) || !(mix <= 1.0f)) return MONARCH_ERR_VALUE;
+  c.bf16 = dtype == MONARCH_BF16;
+  c.top = static_cast<int>(top), c.mix = mix;
+  c.told = c.labels && mix < 1.0f;
+  c.taught = top > 0 && mix > 0.0f;
+  c.temperature = c.taught ? temperature : 1.0f;
+  c.second = c.told && c.taught && temperature != 1.0f;
+  if (c.rows > 0) {
+    if (!c.x || !c.w || (top > 0 && (!c.teacher || !c.ids))) return MONARCH_ERR_NULL;
+    if (what != BWD && !c.loss) return MONARCH_ERR_NULL;
+    if (what == FWD && !c.stats) return MONARCH_ERR_NULL;
+    if (what == BWD && (!stats_in || !c.weight)) return MONARCH_ERR_NULL;
+    if (what != FWD && !c.dx) return MONARCH_ERR_NULL;
+    if (!workspace) return MONARCH_ERR_NULL;
+  }
+  if (what != FWD && !c.dw) return MONARCH_ERR_NULL;
+  if (off_elements(c.x, c.bf16 ? 2 : 4) || misaligned(c.w) || off_elements(c.teacher, 4) || off_elements(c.ids, 8) ||
+      off_elements(c.labels, 8) || off_elements(c.weight, 4) || off_elements(c.loss, 4) || misaligned(c.stats) ||
+      misaligned(stats_in) || misaligned(c.dx) || misaligned(c.dw) || misaligned(workspace))
+    return MONARCH_ERR_ALIGN;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (c.rows == 0) {
+    if (what == FWD) return MONARCH_OK;
+    return record_hip(launch_zero(c.dw, static_cast<size_t>(c.vocab * c.d) * (c.bf16 ? 2 : 4), s));
+  }
+  const HeadPlan p = head_plan(what, c.rows, c.d, c.vocab, top, c.bf16);
+  if (workspace_bytes < p.total) return MONARCH_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  if (what == STEP) c.stats = reinterpret_cast<float*>(ws + p.stats);
+  if (what == BWD) c.stats = const_cast<float*>(static_cast<const float*>(stats_in)), c.loss = nullptr;
+  Tracer tr{events, n_events, 0, s};
+  st = record_hip(tr.mark());
+  if (st) return st;
+  st = run(c, p, what, ws, s);
+  if (st) return st;
+  return record_hip(tr.mark());
+}
+
+}  // namespace
+}  // namespace monarch
+
+using namespace monarch;
+
+extern "C" {
+
+size_t monarch_head_workspace_bytes(int call, int64_t rows, int64_t features, int64_t vocab, int64_t top, int dtype) {
+  if (call < 0 || call > 2 || check_sizes(rows, features, vocab, features, top, dtype) || rows == 0) return 0;
+  return head_plan(call, rows, features, vocab, top, dtype == MONARCH_BF16).total;
+}
+
+size_t monarch_head_stats_bytes(int64_t rows, int64_t top) {
+  if (rows < 0 || rows >= kLimit - kHeadRows || top < 0 || top > MONARCH_DISTILL_MAX_TOP) return 0;
+  return static_cast<size_t>(rows) * (4 + top) * sizeof(float);
+}
+
+int monarch_head_fwd(const void* x, int64_t ldx, const void* w, const void* labels, const void* teacher, const void* ids,
+                     void* loss, void* stats, void* workspace, size_t workspace_bytes, int64_t rows, int64_t features,
+                     int64_t vocab, int64_t top, float temperature, float mix, int dtype, void* stream, void* const* events,
+                     int n_events) {
+  Call c = {};
+  c.x = x, c.ldx = ldx, c.w = w, c.labels = static_cast<const int64_t*>(labels);
+  c.teacher = static_cast<const float*>(teacher), c.ids = static_cast<const int64_t*>(ids);
+  c.loss = static_cast<float*>(loss), c.stats = static_cast<float*>(stats);
+  c.rows = rows, c.d = features, c.vocab = vocab;
+  return call(c, FWD, nullptr, top, temperature, mix, dtype, workspace, workspace_bytes, stream, events, n_events);
+}
+
+int monarch_head_bwd(const void* dloss, const void* x, int64_t ldx, const void* w, const void* labels, const void* teacher,
+                     const void* ids, const void* stats, void* dx, void* dw, void* workspace, size_t workspace_bytes,
+                     int64_t rows, int64_t features, int64_t vocab, int64_t top, float temperature, float mix, int dtype,
+                     void* stream, void* const* events, int n_events) {
+  Call c = {};
+  c.x = x, c.ldx = ldx, c.w = w, c.labels = static_cast<const int64_t*>(labels);
+  c.teacher = static_cast<const float*>(teacher), c.ids = static_cast<const int64_t*>(ids);
+  c.weight = static_cast<const float*>(dloss), c.dx = dx, c.dw = dw;
+  c.rows = rows, c.d = features, c.vocab = vocab;
+  return call(c, BWD, stats, top, temperature, mix, dtype, workspace, workspace_bytes, stream, events, n_events);
+}
+
+int monarch_head_step(const void* x, int64_t ldx, const void* w, const void* labels, const void* teacher, const void* ids,
+                      const void* row_weight, void* loss, void* dx, void* dw, void* workspace, size_t workspace_bytes,
+                      int64_t rows, int64_t features, int64_t vocab, int64_t top, float temperature, float mix, int dtype,
+                      void* stream, void* const* events, int n_events) {
+  Call c = {};
+  c.x = x, c.ldx = ldx, c.w = w, c.labels = static_cast<const int64_t*>(labels);
+  c.teacher = static_cast<const float*>(teacher), c.ids = static_cast<const int64_t*>(ids);
+  c.weight = static_cast<const float*>(row_weight), c.loss = static_cast<float*>(loss), c.dx = dx, c.dw = dw;
+  c.rows = rows, c.d = features, c.vocab = vocab;
+  return call(c, STEP, nullptr, top, temperature, mix, dtype, workspace, workspace_bytes, stream, events, n_events);
+}
+
+}  // extern "C"

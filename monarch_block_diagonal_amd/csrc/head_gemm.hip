@@ -1,0 +1,373 @@
+// The three products of the head loss, each with its epilogue (gfx950).
+//
+//   logits   z[v, n] = sum_d w[v, d] x[n, d]     words down, rows across: a lane holds
+//            4 consecutive words of one row in each MFMA tile, so that a row's
+//            maximum and sum of exponentials are taken in registers, four lanes
+//            meet by two swaps, and only (maximum, sums) of a tile leave the chip;
+//            or, for the gradient, g = a q + b s - off [v = label], rounded to
+//            bf16 (fp32: three bf16 planes, exact), [n][v] through LDS.
+//   dx       [d, n] = sum_v w[v, d] g[n, v]       split over the words
+//   dw       [d, v] = sum_n x[n, d] g[n, v]
+//
+// g is one piece of the vocabulary: it stays in a workspace that does not grow with
+// the vocabulary.
+#include "head.h"
+#include "kernels.h"
+
+namespace monarch {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLowest = -3.402823466e38f;
+
+using Shape256 = PipeShape<2, 4, 8, 4, 4>;
+using Shape128 = PipeShape<2, 2, 4, 4, 4>;
+using Shape32 = PipeShape<4, 1, 2, 2, 8>;
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Workgroup b of a grid: consecutive tiles share an XCD (workgroups are dealt round
+// to the 8 of them), and with it an L2.
+__device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t n) {
+  const int64_t x = b & 7, i = b >> 3, per = n >> 3, more = n & 7;
+  return x * per + (x < more ? x : more) + i;
+}
+
+// max / sum over the four lanes that hold one column of MFMA tiles (lane % 16 alike)
+template <bool MAX>
+__device__ __forceinline__ float over_groups(float v) {
+  auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
+  v = MAX ? fmaxf(a, b) : a + b;
+  s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
+  return MAX ? fmaxf(a, b) : a + b;
+}
+
+// (words, rows) of tile t: rows in panels of 8 tiles, a panel's words after each other,
+// so that the workgroups that run together share words and rows in their L2.
+__device__ __forceinline__ void logits_tile(int64_t t, int64_t vt, int64_t nt, int64_t* v, int64_t* n) {
+  const int64_t panel = t / (8 * vt), wide = nt - panel * 8 < 8 ? nt - panel * 8 : 8;
+  const int64_t r = t - panel * 8 * vt;
+  *v = r / wide;
+  *n = panel * 8 + r % wide;
+}
+
+template <class S, bool SECOND>
+__global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t vt, int64_t nt) {
+  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+  int64_t tv, tn;
+  logits_tile(xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
+  const int64_t v0 = p.v0 + tv * S::BM, n0 = tn * S::BN;
+  if (n0 >= *p.count) return;
+  f32x4 acc[S::FM][S::FN];
+  pipe_product<S, false, false>(p.pr, v0, n0, 0, p.d, lds, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / S::WN, wn = wave % S::WN, l15 = lane & 15, lh = lane >> 4;
+  const int64_t vw = v0 + wm * S::FM * 16 + 4 * lh;   // this lane's first word
+  const bool cut = v0 + S::BM > p.v1;
+  float* part = reinterpret_cast<float*>(lds);        // [WM][3][BN]
+#pragma unroll
+  for (int ni = 0; ni < S::FN; ++ni) {
+    const int col = (wn * S::FN + ni) * 16 + l15;
+    if (cut) {
+#pragma unroll
+      for (int mi = 0; mi < S::FM; ++mi)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (vw + mi * 16 + v >= p.v1) acc[mi][ni][v] = -INFINITY;
+    }
+    float m = kLowest;
+#pragma unroll
+    for (int mi = 0; mi < S::FM; ++mi)
+      m = fmaxf(fmaxf(fmaxf(m, acc[mi][ni][0]), fmaxf(acc[mi][ni][1], acc[mi][ni][2])), acc[mi][ni][3]);
+    m = over_groups<true>(m);
+    float st = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int mi = 0; mi < S::FM; ++mi)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float z = acc[mi][ni][v] - m;
+        st += exp2_of(z * p.ct);
+        if constexpr (SECOND) s1 += exp2_of(z * kLog2e);
+      }
+    st = over_groups<false>(st);
+    if constexpr (SECOND) s1 = over_groups<false>(s1);
+    if (lh == 0) {
+      part[(wm * 3 + 0) * S::BN + col] = m;
+      part[(wm * 3 + 1) * S::BN + col] = st;
+      part[(wm * 3 + 2) * S::BN + col] = SECOND ? s1 : 0.f;
+    }
+    // the lane that holds the label's logit hands it out
+    const int64_t at = static_cast<int64_t>(p.label[n0 + col]) - vw;
+    const bool mine = at >= 0 && at < S::FM * 16 && (at & 15) < 4;
+    if (__any(mine)) {
+#pragma unroll
+      for (int mi = 0; mi < S::FM; ++mi)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (at == mi * 16 + v) p.z_label[n0 + col] = acc[mi][ni][v];
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < S::BN; c += S::NT) {
+    float m = part[c];
+#pragma unroll
+    for (int w = 1; w < S::WM; ++w) m = fmaxf(m, part[w * 3 * S::BN + c]);
+    float st = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < S::WM; ++w) {
+      const float by = part[w * 3 * S::BN + c] - m;
+      st += part[(w * 3 + 1) * S::BN + c] * exp2_of(by * p.ct);
+      if constexpr (SECOND) s1 += part[(w * 3 + 2) * S::BN + c] * exp2_of(by * kLog2e);
+    }
+    float* o = p.part + (tv * 3) * p.np + n0 + c;
+    o[0] = m;
+    o[p.np] = st;
+    o[2 * p.np] = SECOND ? s1 : st;
+  }
+}
+
+// Four fp32 values as bf16, and what is left of them (the next plane's).
+__device__ __forceinline__ u32x2 next_plane(f32x4& v) {
+  const u32x2 r = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  const float hi[4] = {__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u),
+                       __uint_as_float(r[1] << 16), __uint_as_float(r[1] & 0xffff0000u)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = isfinite(v[i]) ? v[i] - hi[i] : 0.f;
+  return r;
+}
+
+// Byte offset in LDS of 8 bytes (4 elements) at element e of row r of a bf16 tile
+// with ROW elements a row: 16-byte pieces swapped within a row by r, so that the 16
+// rows of a store fall on all banks.
+template <int ROW>
+__device__ __forceinline__ int staged(int r, int e) {
+  constexpr int M = ROW / 8 < 32 ? ROW / 8 - 1 : 31;
+  return r * ROW * 2 + ((((e >> 3) ^ (r & M)) << 4) | ((e & 4) << 1));
+}
+
+template <class S, bool SECOND>
+__global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t vt, int64_t nt) {
+  static_assert(S::BM * S::BN * 2 <= S::LDS, "a tile of g is staged in LDS");
+  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+  int64_t tv, tn;
+  logits_tile(xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
+  const int64_t v0 = p.v0 + tv * S::BM, n0 = tn * S::BN;
+  if (n0 >= *p.count) return;
+  f32x4 acc[S::FM][S::FN];
+  pipe_product<S, false, false>(p.pr, v0, n0, 0, p.d, lds, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / S::WN, wn = wave % S::WN, l15 = lane & 15, lh = lane >> 4;
+  const int64_t vw = v0 + wm * S::FM * 16 + 4 * lh;
+  const bool cut = v0 + S::BM > p.v1;
+#pragma unroll
+  for (int ni = 0; ni < S::FN; ++ni) {
+    const int64_t n = n0 + (wn * S::FN + ni) * 16 + l15;
+    const HeadRow r = p.row[n];
+    const int64_t at = static_cast<int64_t>(p.label[n]) - vw;
+    const bool mine = at >= 0 && at < S::FM * 16 && (at & 15) < 4;
+    const bool any = __any(mine);
+#pragma unroll
+    for (int mi = 0; mi < S::FM; ++mi) {
+      f32x4 g;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float z = acc[mi][ni][v] - r.m;
+        g[v] = r.a * exp2_of(z * p.ct);
+        if constexpr (SECOND) g[v] = fmaf(r.b, exp2_of(z * kLog2e), g[v]);
+      }
+      if (any) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (at == mi * 16 + v) g[v] -= r.off;
+      }
+      if (cut) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (vw + mi * 16 + v >= p.v1) g[v] = 0.f;
+      }
+      acc[mi][ni] = g;
+    }
+  }
+  const int planes = p.pr.planes;
+  for (int k = 0; k < planes; ++k) {
+    if (k > 0) __syncthreads();
+#pragma unroll
+    for (int ni = 0; ni < S::FN; ++ni)
+#pragma unroll
+      for (int mi = 0; mi < S::FM; ++mi) {
+        const u32x2 w = next_plane(acc[mi][ni]);
+        *reinterpret_cast<u32x2*>(lds + staged<S::BM>((wn * S::FN + ni) * 16 + l15, (wm * S::FM + mi) * 16 + 4 * lh)) = w;
+      }
+    __syncthreads();
+    constexpr int CH = S::BM / 8;
+    uint16_t* out = p.g + k * p.g_plane + n0 * p.vp + tv * S::BM;
+    for (int c = threadIdx.x; c < S::BN * CH; c += S::NT) {
+      const int row = c / CH, e = (c % CH) * 8;
+      *reinterpret_cast<u32x4*>(out + row * p.vp + e) = *reinterpret_cast<const u32x4*>(lds + staged<S::BM>(row, e));
+    }
+  }
+}
+
+template <class S>
+__global__ __launch_bounds__(S::NT) void head_dx_kernel(HeadDx p, int64_t dt, int64_t nt) {
+  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+  int64_t t = xcd_tile(blockIdx.x, gridDim.x);
+  const int64_t td = t % dt;
+  t /= dt;
+  const int64_t tn = t % nt, split = t / nt;
+  const int64_t d0 = td * S::BM, n0 = tn * S::BN;
+  if (n0 >= *p.count) return;
+  const int64_t kb = split * p.chunk, ke = kb + p.chunk < p.k ? kb + p.chunk : p.k;
+  f32x4 acc[S::FM][S::FN];
+  pipe_product<S, true, false>(p.pr, d0, n0, kb, ke, lds, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / S::WN, wn = wave % S::WN, l15 = lane & 15, lh = lane >> 4;
+#pragma unroll
+  for (int ni = 0; ni < S::FN; ++ni) {
+    const int64_t n = n0 + (wn * S::FN + ni) * 16 + l15;
+    float* o = p.part + (split * p.np + n) * p.dp;
+#pragma unroll
+    for (int mi = 0; mi < S::FM; ++mi) {
+      const int64_t d = d0 + (wm * S::FM + mi) * 16 + 4 * lh;
+      if (d < p.dp) {   // dp is a multiple of 32
+        f32x4* at = reinterpret_cast<f32x4*>(o + d);
+        *at = p.add ? acc[mi][ni] + *at : acc[mi][ni];
+      }
+    }
+  }
+}
+
+template <class S>
+__global__ __launch_bounds__(S::NT) void head_dw_kernel(HeadDw p, int64_t dt, int64_t vt) {
+  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+  int64_t t = xcd_tile(blockIdx.x, gridDim.x);
+  const int64_t td = t % dt;
+  t /= dt;
+  const int64_t tv = t % vt, split = t / vt;
+  const int64_t d0 = td * S::BM, v0 = tv * S::BN;
+  const int64_t count = *p.count;
+  const int64_t steps = (count + kPipeK - 1) / kPipeK, per = (steps + p.splits - 1) / p.splits;
+  const int64_t kb = split * per * kPipeK, end = (split + 1) * per < steps ? (split + 1) * per : steps;
+  f32x4 acc[S::FM][S::FN];
+  pipe_product<S, true, true>(p.pr, d0, v0, kb, end * kPipeK, lds, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / S::WN, wn = wave % S::WN, l15 = lane & 15, lh = lane >> 4;
+  if (p.part || !p.bf16) {
+    // fp32: a split's sums, or the result
+    const int64_t ld = p.part ? p.dp : p.d;
+    float* base = p.part ? p.part + split * p.cols * p.dp : static_cast<float*>(p.dw);
+#pragma unroll
+    for (int ni = 0; ni < S::FN; ++ni) {
+      const int64_t v = v0 + (wn * S::FN + ni) * 16 + l15;
+      if (v >= p.cols) continue;
+      float* o = base + v * ld;
+#pragma unroll
+      for (int mi = 0; mi < S::FM; ++mi) {
+        const int64_t d = d0 + (wm * S::FM + mi) * 16 + 4 * lh;
+        if (ld % 4 == 0) {
+          if (d < ld) *reinterpret_cast<f32x4*>(o + d) = acc[mi][ni];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (d + e < ld) o[d + e] = acc[mi][ni][e];
+        }
+      }
+    }
+    return;
+  }
+  static_assert(S::BM * S::BN * 2 <= S::LDS, "a tile of dw is staged in LDS");
+#pragma unroll
+  for (int ni = 0; ni < S::FN; ++ni)
+#pragma unroll
+    for (int mi = 0; mi < S::FM; ++mi) {
+      const u32x2 w = {pack_bf16x2(acc[mi][ni][0], acc[mi][ni][1]), pack_bf16x2(acc[mi][ni][2], acc[mi][ni][3])};
+      *reinterpret_cast<u32x2*>(lds + staged<S::BM>((wn * S::FN + ni) * 16 + l15, (wm * S::FM + mi) * 16 + 4 * lh)) = w;
+    }
+  __syncthreads();
+  uint16_t* dw = static_cast<uint16_t*>(p.dw);
+  if (p.d % 8 == 0) {
+    constexpr int CH = S::BM / 8;
+    for (int c = threadIdx.x; c < S::BN * CH; c += S::NT) {
+      const int row = c / CH, e = (c % CH) * 8;
+      if (v0 + row < p.cols && d0 + e < p.d)
+        __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(lds + staged<S::BM>(row, e)),
+                                    reinterpret_cast<u32x4*>(dw + (v0 + row) * p.d + d0 + e));
+    }
+  } else {
+    for (int c = threadIdx.x; c < S::BN * S::BM; c += S::NT) {
+      const int row = c / S::BM, e = c % S::BM;
+      if (v0 + row < p.cols && d0 + e < p.d)
+        dw[(v0 + row) * p.d + d0 + e] = *reinterpret_cast<const uint16_t*>(lds + staged<S::BM>(row, e) + (e & 3) * 2);
+    }
+  }
+}
+
+int64_t tiles(int64_t n, int64_t by) { return (n + by - 1) / by; }
+
+hipError_t check_grid(int64_t grid) { return grid > 0x7fffffffLL ? hipErrorInvalidConfiguration : hipSuccess; }
+
+template <class S>
+hipError_t sums(const HeadLogits& a, bool second, hipStream_t st) {
+  const int64_t vt = tiles(a.v1 - a.v0, S::BM), nt = tiles(a.np, S::BN);
+  if (hipError_t e = check_grid(vt * nt)) return e;
+  const dim3 g(static_cast<unsigned>(vt * nt));
+  if (second)
+    hipLaunchKernelGGL((head_sums_kernel<S, true>), g, dim3(S::NT), 0, st, a, vt, nt);
+  else
+    hipLaunchKernelGGL((head_sums_kernel<S, false>), g, dim3(S::NT), 0, st, a, vt, nt);
+  return hipGetLastError();
+}
+
+template <class S>
+hipError_t grad(const HeadLogits& a, bool second, hipStream_t st) {
+  const int64_t vt = tiles(a.v1 - a.v0, S::BM), nt = tiles(a.np, S::BN);
+  if (hipError_t e = check_grid(vt * nt)) return e;
+  const dim3 g(static_cast<unsigned>(vt * nt));
+  if (second)
+    hipLaunchKernelGGL((head_grad_kernel<S, true>), g, dim3(S::NT), 0, st, a, vt, nt);
+  else
+    hipLaunchKernelGGL((head_grad_kernel<S, false>), g, dim3(S::NT), 0, st, a, vt, nt);
+  return hipGetLastError();
+}
+
+template <class S>
+hipError_t dx(const HeadDx& a, hipStream_t st) {
+  const int64_t dt = tiles(a.d, S::BM), nt = tiles(a.np, S::BN), n = dt * nt * a.splits;
+  if (hipError_t e = check_grid(n)) return e;
+  hipLaunchKernelGGL((head_dx_kernel<S>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, nt);
+  return hipGetLastError();
+}
+
+template <class S>
+hipError_t dw(const HeadDw& a, hipStream_t st) {
+  const int64_t dt = tiles(a.d, S::BM), vt = tiles(a.cols, S::BN), n = dt * vt * a.splits;
+  if (hipError_t e = check_grid(n)) return e;
+  hipLaunchKernelGGL((head_dw_kernel<S>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, vt);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t head_tile_words(HeadShape s) { return s == HEAD_256 ? Shape256::BM : s == HEAD_128 ? Shape128::BM : Shape32::BM; }
+int64_t head_tile_rows(HeadShape s) { return s == HEAD_256 ? Shape256::BN : s == HEAD_128 ? Shape128::BN : Shape32::BN; }
+
+hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, bool second, hipStream_t st) {
+  return s == HEAD_256 ? sums<Shape256>(a, second, st) : s == HEAD_128 ? sums<Shape128>(a, second, st) : sums<Shape32>(a, second, st);
+}
+hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, bool second, hipStream_t st) {
+  return s == HEAD_256 ? grad<Shape256>(a, second, st) : s == HEAD_128 ? grad<Shape128>(a, second, st) : grad<Shape32>(a, second, st);
+}
+hipError_t head_launch_dx(const HeadDx& a, HeadShape s, hipStream_t st) {
+  return s == HEAD_256 ? dx<Shape256>(a, st) : s == HEAD_128 ? dx<Shape128>(a, st) : dx<Shape32>(a, st);
+}
+hipError_t head_launch_dw(const HeadDw& a, HeadShape s, hipStream_t st) {
+  return s == HEAD_256 ? dw<Shape256>(a, st) : dw<Shape128>(a, st);
+}
+
+}  // namespace monarch

@@ -12,7 +12,9 @@ explicit intermediate width, optional bias).
 Around and after the layers: sandwich_forward / sandwich_backward (SandwichNorm)
 for the norms, gate and residual join between two blocks, and distill_forward /
 distill_backward / distill_step (DistillLossFunction) for training against a
-teacher's top logits.
+teacher's top logits; head_loss_forward / head_loss_backward / head_loss_step (HeadLossFunction) for
+the same loss, or the cross entropy, from a dense head's input without its logits; dropout_forward /
+dropout_backward (Dropout) for dropout at a residual join, without a stored mask.
 """
 from __future__ import annotations
 
@@ -707,3 +709,201 @@ class DistillLossFunction(torch.autograd.Function):
     def backward(ctx, dloss):
         dz = distill_backward(dloss.reshape(-1).contiguous(), *ctx.saved_tensors, **ctx.how)
         return dz.view(*dloss.shape, dz.shape[1]), None, None, None, None, None
+
+
+def _head_shapes(x, w, labels, teacher, ids, per_row, name):
+    """(rows, features, vocab, top, ldx, device) after checking x [rows, features] (rows may lie
+    apart), w [vocab, features], labels and per_row [rows], teacher and ids [rows, top]."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [rows, features], w [vocab, features]")
+    rows, d = x.shape
+    vocab, device = w.shape[0], B.current_device()
+    _beside(device, x.dtype, (vocab, d), "w", w)
+    if (teacher is None) != (ids is None):
+        raise ValueError("teacher and ids come together")
+    top = 0
+    if teacher is not None:
+        top = teacher.shape[1] if teacher.dim() == 2 else -1
+        if top < 0 or top > B.DISTILL_MAX_TOP:
+            raise ValueError(f"the teacher's logits must be [rows, top], top at most {B.DISTILL_MAX_TOP}")
+        _beside(device, torch.float32, (rows, top), "teacher", teacher)
+        _beside(device, torch.int64, (rows, top), "ids", ids)
+    _beside(device, torch.int64, (rows,), "labels", labels)
+    _beside(device, torch.float32, (rows,), name, per_row)
+    if x.get_device() != device:
+        raise ValueError("x must live on the current GPU, where the call's stream is")
+    return rows, d, vocab, top, _rows_apart(x, rows, d, "x"), device
+
+
+# a function of the sizes alone: asked for once for each of them
+_head_workspace = functools.lru_cache(maxsize=256)(B.monarch_head_workspace_bytes)
+
+
+def head_loss_forward(x, w, labels=None, teacher=None, ids=None, *, temperature: float = 1.0,
+                      mix: float = 0.0, stream=None):
+    """(loss [rows], stats) of rows x [rows, features] under a dense head w [vocab, features], whose
+    logits z = x wᵀ are not kept:
+
+        loss = mix * temperature^2 * KL(p || softmax(z / temperature)) + (1 - mix) * CE(labels)
+
+    with labels, teacher and ids as for distill_forward; without a teacher it is the softmax cross
+    entropy. Rows without a label and a valid entry have loss 0 and cost nothing. stats goes to
+    head_loss_backward."""
+    if stream is not None:
+        return _on_stream(stream, head_loss_forward, x, w, labels, teacher, ids,
+                          temperature=temperature, mix=mix)
+    rows, d, vocab, top, ldx, _ = _head_shapes(x, w, labels, teacher, ids, None, "")
+    code = dtype_code(x)
+    loss = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    stats = torch.empty((rows * (4 + top),), dtype=torch.float32, device=x.device)
+    need = _head_workspace(B.HEAD_FWD, rows, d, vocab, top, code)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    B.monarch_head_fwd(x, ldx, w, labels, teacher, ids, loss, stats, ws, need, rows, d, vocab, top,
+                       temperature, mix, code)
+    return loss, stats
+
+
+def head_loss_backward(dloss, x, w, labels, teacher, ids, stats, *, temperature: float = 1.0,
+                       mix: float = 0.0, stream=None):
+    """(dx, dw) for dloss [rows]; stats is the forward's. The logits are computed again."""
+    if stream is not None:
+        return _on_stream(stream, head_loss_backward, dloss, x, w, labels, teacher, ids, stats,
+                          temperature=temperature, mix=mix)
+    rows, d, vocab, top, ldx, device = _head_shapes(x, w, labels, teacher, ids, dloss, "dloss")
+    _saved(stats, (rows * (4 + top),), torch.float32, device)
+    code = dtype_code(x)
+    dx = torch.empty((rows, d), dtype=x.dtype, device=x.device)
+    dw = torch.empty_like(w)
+    need = _head_workspace(B.HEAD_BWD, rows, d, vocab, top, code)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    B.monarch_head_bwd(dloss, x, ldx, w, labels, teacher, ids, stats, dx, dw, ws, need, rows, d, vocab,
+                       top, temperature, mix, code)
+    return dx, dw
+
+
+def head_loss_step(x, w, labels=None, teacher=None, ids=None, row_weight=None, *,
+                   temperature: float = 1.0, mix: float = 0.0, stream=None):
+    """(loss [rows], dx, dw) in one call: the gradients of sum(row_weight * loss) (row_weight
+    None: 1 for every row)."""
+    if stream is not None:
+        return _on_stream(stream, head_loss_step, x, w, labels, teacher, ids, row_weight,
+                          temperature=temperature, mix=mix)
+    rows, d, vocab, top, ldx, _ = _head_shapes(x, w, labels, teacher, ids, row_weight, "row_weight")
+    code = dtype_code(x)
+    loss = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    dx = torch.empty((rows, d), dtype=x.dtype, device=x.device)
+    dw = torch.empty_like(w)
+    need = _head_workspace(B.HEAD_STEP, rows, d, vocab, top, code)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    B.monarch_head_step(x, ldx, w, labels, teacher, ids, row_weight, loss, dx, dw, ws, need, rows, d,
+                        vocab, top, temperature, mix, code)
+    return loss, dx, dw
+
+
+class HeadLossFunction(torch.autograd.Function):
+    """head_loss_forward's loss with its gradients by x and w, for x [..., features], labels [...],
+    teacher and ids [..., top]: one loss a row, [...]. What does not lie as the library takes it is
+    copied. Where the rows' weights are known before the loss, head_loss_step computes the logits of
+    the backward pass behind those of the forward pass in one call."""
+
+    @staticmethod
+    def forward(ctx, x, w, labels, teacher, ids, temperature: float = 1.0, mix: float = 0.0):
+        lead = x.shape[:-1]
+        _expect(labels, lead, "labels")
+        if teacher is not None and ids is not None:
+            _expect(teacher, (*lead, teacher.shape[-1]), "teacher")
+            _expect(ids, teacher.shape, "ids")
+        flat = lambda t: None if t is None else t.reshape(lead.numel(), t.shape[-1])  # noqa: E731
+        rows = flat(x)
+        if rows.numel() and (rows.stride(1) != 1 or rows.stride(0) < rows.shape[1]):
+            rows = rows.contiguous()
+        whole = lambda t: None if t is None else t.contiguous()  # noqa: E731
+        saved = (rows, _whole(w), whole(None if labels is None else labels.reshape(lead.numel())),
+                 whole(flat(teacher)), whole(flat(ids)))
+        ctx.how, ctx.lead = dict(temperature=temperature, mix=mix), lead
+        loss, stats = head_loss_forward(*saved, **ctx.how)
+        ctx.save_for_backward(*saved, stats)
+        return loss.view(lead)
+
+    @staticmethod
+    @_first_derivative_only
+    def backward(ctx, dloss):
+        dx, dw = head_loss_backward(dloss.reshape(-1).contiguous(), *ctx.saved_tensors, **ctx.how)
+        return dx.view(*ctx.lead, dx.shape[1]), dw, None, None, None, None, None
+
+
+def _dropout_args(p, seed, offset, state, device):
+    """(seed, offset) after checking them; p is checked by the library."""
+    if state is not None:
+        _beside(device, torch.int64, (2,), "state", state)
+        return 0, 0
+    if seed is None:
+        raise ValueError("dropout needs a seed or a state")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset must be in [0, 2^64)")
+    return seed, offset
+
+
+def dropout_forward(x, p: float, seed: Optional[int] = None, offset: int = 0, residual=None, *,
+                    state=None, stream=None):
+    """residual + dropout(x) (residual None: dropout(x)) for x and residual of any one shape:
+
+        y = residual + (r >= t ? x / (1 - t / 65536) : 0),    t = round(65536 p)
+
+    r: 16 bits for each element, drawn from (seed, offset) and its place alone, so no mask is kept and
+    the backward pass draws them again; give every call an offset of its own. state (int64 [2] on the
+    GPU: seed and offset) takes their place where a captured graph draws anew at each replay: the
+    program then changes it between replays, and behind the backward pass that draws from it."""
+    if stream is not None:
+        return _on_stream(stream, dropout_forward, x, p, seed, offset, residual, state=state)
+    device = B.current_device()
+    _beside(device, x.dtype, x.shape, "x residual", x, residual)
+    seed, offset = _dropout_args(p, seed, offset, state, device)
+    y = torch.empty_like(x)
+    B.monarch_dropout(x, residual, y, x.numel(), p, seed, offset, state, dtype_code(x))
+    return y
+
+
+def dropout_backward(dy, p: float, seed: Optional[int] = None, offset: int = 0, *, state=None,
+                     stream=None):
+    """dx of dropout_forward's call with the same p, seed and offset (or state); the residual's
+    gradient is dy itself."""
+    return dropout_forward(dy, p, seed, offset, state=state, stream=stream)
+
+
+class DropoutFunction(torch.autograd.Function):
+    """dropout_forward with gradients by x and the residual. A state's present value is kept for the
+    backward pass."""
+
+    @staticmethod
+    def forward(ctx, x, p, seed, offset, residual, state):
+        ctx.p, ctx.seed, ctx.offset, ctx.joined = p, seed, offset, residual is not None
+        ctx.save_for_backward(None if state is None else state.clone())
+        return dropout_forward(_whole(x), p, seed, offset, _whole(residual), state=state)
+
+    @staticmethod
+    @_first_derivative_only
+    def backward(ctx, dy):
+        state, = ctx.saved_tensors
+        dx = dropout_backward(_whole(dy), ctx.p, ctx.seed, ctx.offset, state=state) if ctx.needs_input_grad[0] else None
+        return dx, None, None, None, dy if ctx.joined else None, None
+
+
+class Dropout(torch.nn.Module):
+    """residual + dropout(x) in training, residual + x otherwise. Every call draws anew: call k of a
+    module has offset k. The seed is drawn from torch's generator unless given. A captured graph would
+    replay one offset: pass a `state` then (dropout_forward)."""
+
+    def __init__(self, p: float = 0.1, seed: Optional[int] = None):
+        super().__init__()
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"p must be in [0, 1], got {p}")
+        self.p = p
+        self.seed = int(torch.randint(0, (1 << 63) - 1, ())) if seed is None else seed
+        self.calls = 0
+
+    def forward(self, x, residual=None, state=None):
+        if not self.training or self.p == 0.0:
+            return x if residual is None else residual + x
+        offset, self.calls = self.calls, self.calls + 1
+        return DropoutFunction.apply(x, self.p, self.seed, offset, residual, state)
