@@ -14,8 +14,10 @@
 //           multiply stage s.
 // One barrier a step, no wait for the loads of later stages.
 //
-// KC stage: rows of 64 bytes, 16-byte piece q of row r at q ^ ((r >> 2) & 3): the 16
-// rows of a fragment read fall on all banks. KM stage: rows of 2*ROWS bytes, one for
+// KC stage: rows of 64 bytes, 16-byte piece q of row r at q ^ (-(r / 4) mod 4). A 16-byte read of 64
+// lanes is served in four groups of 16, lanes 0-3, 12-15, 20-23, 24-27 first, 4-11, 16-19,
+// 28-31 then, and so on: the groups are why it is not q ^ (r / 4) mod 4, which puts two
+// rows of a group on the same banks (half of all LDS cycles were conflicts). KM stage: rows of 2*ROWS bytes, one for
 // each k, read by ds_read_b64_tr_b16 (16 lanes give four rows of 32 bytes, lane i gets
 // column i of the four); the 32-byte slot of column group t in row k is t ^ g(k), g =
 // (k & 3) + 4 ((k >> 3) & 3), so that the 16 rows of such a read fall on all banks.
@@ -29,6 +31,9 @@
 
 #include "common.h"
 
+#ifndef PIPE_SCHED
+#define PIPE_SCHED
+#endif
 namespace monarch {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -39,18 +44,20 @@ struct PipeOperand {
   int64_t ld = 0;
   int64_t plane = 0;      // from one bf16 plane to the next (fp32)
   int64_t rows = 0;       // valid rows (m or n); others are read from a valid place
-  int64_t kvalid = 0;     // valid k; KC: zeros are taken beyond, KM: the last valid k's
+  int64_t kvalid = 0;     // valid k of a; KC: zeros are taken beyond, KM: the last valid k's
 };
 
 struct PipeProduct {
   PipeOperand a, b;
   const uint16_t* zeros = nullptr;   // 16 bytes of zeros
-  int planes = 1;                    // 1: bf16, 3: fp32 as three planes
 };
 
 constexpr int kPipeK = 32;
 
 __device__ __forceinline__ int pipe_swizzle(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
+
+// KC: where a row's 16-byte pieces are turned to.
+__device__ __forceinline__ int pipe_turn(int r) { return (4 - ((r >> 2) & 3)) & 3; }
 
 // The loads and fragment reads of one operand tile of ROWS rows, by NW waves.
 template <bool KM, int ROWS, int NW>
@@ -59,69 +66,77 @@ struct PipeTile {
   static constexpr int TOTAL = BYTES / 1024;                    // wave loads a stage
   static constexpr int PER = TOTAL >= NW ? TOTAL / NW : 1;      // a wave's own (few: shared, the same bytes twice)
   static_assert(TOTAL <= NW || TOTAL % NW == 0, "whole loads a wave");
+  static constexpr int FRAGS = KM ? 2 : 1;                      // LDS reads a fragment
   static constexpr int CHUNKS = ROWS / 8;                       // KM: 16-byte pieces of one k
   static constexpr int MASK = ROWS / 16 < 16 ? ROWS / 16 - 1 : 15;
 
-  const uint16_t* ptr[PER];
-  int kq[PER];   // this lane's k within a tile (KC: of its piece's first element)
-  int lds[PER];  // byte offset of the wave's load
-  int64_t ld;
+  const uint16_t* ptr[PER];   // what this lane loads next
+  int64_t adv;                // from one K tile to the next
 
-  __device__ __forceinline__ void init(const PipeOperand& o, int64_t r0, int wave, int lane) {
-    ld = o.ld;
+  __device__ __forceinline__ static int load_of(int i, int wave) { return TOTAL >= NW ? wave * PER + i : wave % TOTAL; }
+
+  __device__ __forceinline__ void init(const PipeOperand& o, int64_t r0, int64_t k0, int wave, int lane) {
+    adv = KM ? kPipeK * o.ld : kPipeK;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int j = TOTAL >= NW ? wave * PER + i : wave % TOTAL;
-      lds[i] = j * 1024;
+      const int j = load_of(i, wave);
       if constexpr (KM) {
         const int k = j * (1024 / (ROWS * 2)) + lane / CHUNKS, pos = lane % CHUNKS;
         const int c = ((((pos >> 1) ^ (pipe_swizzle(k) & MASK)) << 1) | (pos & 1)) * 8;
-        kq[i] = k;
-        ptr[i] = o.p + k * ld + (r0 + c < o.rows ? r0 + c : 0);
+        ptr[i] = o.p + (k0 + k) * o.ld + (r0 + c < o.rows ? r0 + c : 0);
       } else {
         const int r = j * 16 + (lane >> 2);
-        const int q = (lane & 3) ^ ((r >> 2) & 3);
-        kq[i] = q * 8;
+        const int q = (lane & 3) ^ pipe_turn(r);
         const int64_t row = r0 + r < o.rows ? r0 + r : o.rows - 1;
-        ptr[i] = o.p + row * ld + q * 8;
+        ptr[i] = o.p + row * o.ld + k0 + q * 8;
       }
     }
   }
 
-  // Loads the tile at k0 (`off`: its plane's offset).
-  __device__ __forceinline__ void issue(const PipeOperand& o, const uint16_t* zeros, char* stage, int64_t k0,
-                                        int64_t off) {
-    const bool tail = k0 + kPipeK > o.kvalid;
-    const int64_t step = off + (KM ? k0 * ld : k0);
+  __device__ __forceinline__ static void load(const uint16_t* s, char* at) {
+    __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)(s),
+                                     (__attribute__((address_space(3))) void*)(at), 16, 0, 0);
+  }
+  // Loads the next tile, whose k are all valid.
+  __device__ __forceinline__ void issue(char* stage, int wave) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const uint16_t* s = ptr[i] + step;
-      if (tail) {
-        if constexpr (KM) {
-          const int64_t over = k0 + kq[i] - (o.kvalid - 1);
-          if (over > 0) s -= over * ld;
-        } else {
-          if (k0 + kq[i] >= o.kvalid) s = zeros;
-        }
+      load(ptr[i], stage + load_of(i, wave) * 1024);
+      ptr[i] += adv;
+    }
+  }
+  // Loads the next tile, of which only `valid` > 0 k are.
+  __device__ __forceinline__ void issue_cut(const PipeOperand& o, const uint16_t* zeros, char* stage, int wave, int lane,
+                                            int64_t valid) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint16_t* s = ptr[i];
+      const int j = load_of(i, wave);
+      if constexpr (KM) {
+        const int64_t over = j * (1024 / (ROWS * 2)) + lane / CHUNKS - (valid - 1);
+        if (over > 0) s -= over * o.ld;
+      } else {
+        if (((lane & 3) ^ pipe_turn(j * 16 + (lane >> 2))) * 8 >= valid) s = zeros;
       }
-      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)(s),
-                                       (__attribute__((address_space(3))) void*)(stage + lds[i]), 16, 0, 0);
+      load(s, stage + load_of(i, wave) * 1024);
+      ptr[i] += adv;
     }
   }
 
-  // Byte offset of this lane's fragment reads (tile t of 16 rows adds frag()).
-  __device__ __forceinline__ static int base(int lane) {
+  // Byte offset in a stage of this lane's read of fragment t0 (t0 + t, t below a power of two that divides t0:
+  // read()). KM: the slot bits of an offset are 0 but for the swizzle, so that a tile's number is
+  // one exclusive or away.
+  __device__ __forceinline__ static int base(int lane, int t0) {
     const int l15 = lane & 15, lh = lane >> 4;
     if constexpr (KM)
-      return (8 * lh + (l15 >> 2)) * (ROWS * 2) + (l15 & 3) * 8;
+      return ((8 * lh + (l15 >> 2)) * (ROWS * 2) + (l15 & 3) * 8) ^ ((t0 ^ (((l15 >> 2) | (lh << 2)) & MASK)) << 5);
     else
-      return l15 * 64 + ((lh ^ ((l15 >> 2) & 3)) << 4);
+      return t0 * 1024 + l15 * 64 + ((lh ^ pipe_turn(l15)) << 4);
   }
-  __device__ __forceinline__ static bf16x8 read(const char* stage, int base, int t, int lane) {
+  __device__ __forceinline__ static bf16x8 read(const char* stage, int base, int t) {
     bf16x8 r;
     if constexpr (KM) {
-      const int g = (((lane & 15) >> 2) | ((lane >> 4) << 2)) & MASK;
-      const char* at = stage + base + ((t ^ g) << 5);
+      const char* at = stage + (base ^ (t << 5));
       typedef __attribute__((address_space(3))) s16x4 Lds;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)(at));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)(at + 4 * ROWS * 2));
@@ -151,6 +166,14 @@ __device__ __forceinline__ void pipe_wait_stages(int later) {
   }
 }
 
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void pipe_each(F f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    pipe_each<N, I + 1>(f);
+  }
+}
+
 // WM x WN waves of FM x FN tiles of 16 x 16.
 template <int WM_, int WN_, int FM_, int FN_, int NST_>
 struct PipeShape {
@@ -161,13 +184,15 @@ struct PipeShape {
 };
 
 // acc[mi][ni], lane l: rows m0 + (wm*FM + mi)*16 + 4*(l/16) + v, column n0 + (wn*FN + ni)*16 + l%16.
-// Sums k in [kb, ke) (kb a multiple of 32). Ends with a barrier: `lds` is free.
-template <class S, bool AKM, bool BKM>
+// Sums k in [kb, ke) (kb a multiple of 32); F32: over six products of planes. Only a's k may end
+// inside the last tile, and only without F32. Ends with a barrier: `lds` is free.
+template <class S, bool AKM, bool BKM, bool F32>
 __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, int64_t n0, int64_t kb, int64_t ke,
                                              char* lds, f32x4 (&acc)[S::FM][S::FN]) {
   using TA = PipeTile<AKM, S::BM, S::NW>;
   using TB = PipeTile<BKM, S::BN, S::NW>;
   constexpr int NI = TA::PER + TB::PER, FM = S::FM, FN = S::FN, NST = S::NST;
+  static_assert(NST % 2 == 0, "stage and register slot of a step go together");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
 #pragma unroll
@@ -175,39 +200,63 @@ __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, i
 #pragma unroll
     for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int ksteps = ke > kb ? static_cast<int>((ke - kb + kPipeK - 1) / kPipeK) : 0;
-  const int nsteps = ksteps * (p.planes == 1 ? 1 : 6);
+  const int nsteps = ksteps * (F32 ? 6 : 1);
   if (nsteps == 0) return;
+  PipeOperand oa = p.a, ob = p.b;
+  if constexpr (F32) oa.p += 2 * oa.plane;
   TA a;
-  a.init(p.a, m0, wave, lane);
+  a.init(oa, m0, kb, wave, lane);
   TB b;
-  b.init(p.b, n0, wave, lane);
-  const int ab = TA::base(lane), bb = TB::base(lane);
+  b.init(ob, n0, kb, wave, lane);
+  static_assert((FM & (FM - 1)) == 0 && (FN & (FN - 1)) == 0, "tiles of a wave");
+  const int ab = TA::base(lane, wm * FM), bb = TB::base(lane, wn * FN);
+  // of the last tile's k of a: all, or those before kvalid
+  const int64_t last_valid = oa.kvalid - kb - static_cast<int64_t>(ksteps - 1) * kPipeK;
 
-  // planes of A and B in the order of their products: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
-  int ik = 0, iseg = 0;   // the next tile to load
-  uint32_t seqa = 0x001102, seqb = 0x010120;
-  int64_t offa = p.planes == 1 ? 0 : 2 * p.a.plane, offb = 0;
-  auto issue = [&](int st) {
-    char* at = lds + st * S::STAGE;
-    const int64_t k0 = kb + static_cast<int64_t>(ik) * kPipeK;
-    a.issue(p.a, p.zeros, at, k0, offa);
-    b.issue(p.b, p.zeros, at + TA::BYTES, k0, offb);
-    if (++ik == ksteps) {
-      ik = 0, ++iseg;
-      if (p.planes != 1) {
-        offa = ((seqa >> (4 * iseg)) & 3) * p.a.plane;
-        offb = ((seqb >> (4 * iseg)) & 3) * p.b.plane;
+  // F32: planes of a and b in the order of their products: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
+  int ik = 0, iseg = 0;
+  auto next_tile = [&]() {
+    if constexpr (F32) {
+      if (++ik == ksteps) {
+        ik = 0;
+        constexpr uint32_t seqa = 0x001102, seqb = 0x010120;
+        const int na = (seqa >> (4 * iseg + 4)) & 3, pa = (seqa >> (4 * iseg)) & 3;
+        const int nb = (seqb >> (4 * iseg + 4)) & 3, pb = (seqb >> (4 * iseg)) & 3;
+        ++iseg;
+        const int64_t ja = (na - pa) * oa.plane - ksteps * a.adv, jb = (nb - pb) * ob.plane - ksteps * b.adv;
+#pragma unroll
+        for (int i = 0; i < TA::PER; ++i) a.ptr[i] += ja;
+#pragma unroll
+        for (int i = 0; i < TB::PER; ++i) b.ptr[i] += jb;
       }
     }
+  };
+  auto issue = [&](int st) {
+    char* at = lds + st * S::STAGE;
+    a.issue(at, wave);
+    b.issue(at + TA::BYTES, wave);
+  };
+  auto issue_any = [&](int st, int tile) {
+    char* at = lds + st * S::STAGE;
+    if (!F32 && tile == nsteps - 1 && last_valid < kPipeK)
+      a.issue_cut(oa, p.zeros, at, wave, lane, last_valid);
+    else
+      a.issue(at, wave);
+    b.issue(at + TA::BYTES, wave);
+    next_tile();
   };
   bf16x8 fa[2][FM], fb[2][FN];
   auto read = [&](auto slot, int st) {
     constexpr int X = decltype(slot)::value;
     const char* at = lds + st * S::STAGE;
+    // offsets of single fragments are not kept over steps (they would not fit beside the sums)
+    int ar = ab, br = bb;
+    if constexpr (AKM) asm volatile("" : "+v"(ar));
+    if constexpr (BKM) asm volatile("" : "+v"(br));
 #pragma unroll
-    for (int mi = 0; mi < FM; ++mi) fa[X][mi] = TA::read(at, ab, wm * FM + mi, lane);
+    for (int mi = 0; mi < FM; ++mi) fa[X][mi] = TA::read(at, ar, mi);
 #pragma unroll
-    for (int ni = 0; ni < FN; ++ni) fb[X][ni] = TB::read(at + TA::BYTES, bb, wn * FN + ni, lane);
+    for (int ni = 0; ni < FN; ++ni) fb[X][ni] = TB::read(at + TA::BYTES, br, ni);
   };
   auto multiply = [&](auto slot) {
     constexpr int X = decltype(slot)::value;
@@ -217,37 +266,48 @@ __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, i
       for (int ni = 0; ni < FN; ++ni)
         acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[X][mi], fb[X][ni], acc[mi][ni], 0, 0, 0);
   };
+  auto meet = [&]() {
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
   // waits until at most `later` < NST stages' loads are in flight
   auto landed = [&](int later) {
     asm volatile("" ::: "memory");
     pipe_wait_stages<NI, NST - 1>(later);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    meet();
   };
-  using Zero = std::integral_constant<int, 0>;
-  using One = std::integral_constant<int, 1>;
-  constexpr int AHEAD = NST;   // stages loaded before the first step
 #pragma unroll 1
-  for (int s = 0; s < AHEAD && s < nsteps; ++s) issue(s);
-  landed((nsteps < AHEAD ? nsteps : AHEAD) - 1);
-  read(Zero{}, 0);
-  int st = 0;   // stage of step s
-  auto step = [&](auto now, auto next, int s) {
+  for (int s = 0; s < NST && s < nsteps; ++s) issue_any(s, s);
+  landed((nsteps < NST ? nsteps : NST) - 1);
+  read(std::integral_constant<int, 0>{}, 0);
+  // a step in the middle: a whole tile is loaded, NST - 2 stages stay in flight
+  auto step = [&](auto stage) {
+    constexpr int ST = decltype(stage)::value, X = ST & 1;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(pipe_wait((NST - 2) * NI));
+    meet();
+    issue(ST);
+    read(std::integral_constant<int, 1 - X>{}, ST + 1 == NST ? 0 : ST + 1);
+    multiply(std::integral_constant<int, X>{});
+    PIPE_SCHED
+    next_tile();
+  };
+  auto last_step = [&](auto stage, int s) {
+    constexpr int ST = decltype(stage)::value, X = ST & 1;
+    if (s >= nsteps) return;
     const int left = nsteps - 2 - s;   // stages behind s+1
-    const int st1 = st + 1 == NST ? 0 : st + 1;
     if (s + 1 < nsteps) {
       landed(left < NST - 2 ? left : NST - 2);
-      if (s + NST < nsteps) issue(st);
-      read(next, st1);
+      if (s + NST < nsteps) issue_any(ST, s + NST);
+      read(std::integral_constant<int, 1 - X>{}, ST + 1 == NST ? 0 : ST + 1);
     }
-    multiply(now);
-    st = st1;
+    multiply(std::integral_constant<int, X>{});
   };
+  int s = 0;
 #pragma unroll 1
-  for (int s = 0; s < nsteps; s += 2) {
-    step(Zero{}, One{}, s);
-    if (s + 1 < nsteps) step(One{}, Zero{}, s + 1);
-  }
+  for (; s + NST + NST < nsteps; s += NST) pipe_each<NST>([&](auto i) { step(i); });
+#pragma unroll 1
+  for (; s < nsteps; s += NST) pipe_each<NST>([&](auto i) { last_step(i, s + decltype(i)::value); });
   __syncthreads();
 }
 

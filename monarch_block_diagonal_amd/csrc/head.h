@@ -22,6 +22,7 @@ enum HeadShape { HEAD_256 = 0, HEAD_128 = 1, HEAD_32 = 2 };
 struct HeadLogits {
   PipeProduct pr;             // A: the head's words, B: the rows
   const int* count;           // rows in use
+  int f32;                    // operands are fp32, as three planes
   int64_t vocab, v0, v1;      // words of this launch: [v0, v1)
   int64_t d;                  // k
   int64_t np;                 // rows of the workspace's copies
@@ -39,6 +40,7 @@ struct HeadLogits {
 struct HeadDx {
   PipeProduct pr;             // A: the head's words [v][d], B: g [n][v]
   const int* count;
+  int f32;
   int64_t d, dp, np;
   int64_t k, chunk;           // words of this piece, words a split
   int splits;
@@ -49,11 +51,11 @@ struct HeadDx {
 struct HeadDw {
   PipeProduct pr;             // A: the rows [n][d], B: g [n][v]
   const int* count;
+  int f32;
   int64_t d, dp, cols;        // cols: words of this piece
   int splits;
   float* part;                // [splits][cols][dp], or null:
   void* dw;                   // the piece's first word of dw [vocab][d]
-  int bf16;
 };
 
 int64_t head_tile_words(HeadShape s);    // words of a logits tile

@@ -142,16 +142,17 @@ __device__ __forceinline__ uint16_t next_part(float& v) {
   return h;
 }
 
-// Rows of d elements (with idx: rows idx[k] for k < *count, zeros up to the next whole
-// tile) copied to rows of dp, zeros behind them; fp32 as three bf16 planes. A workgroup a row.
+// Rows of d elements copied to rows of dp, zeros behind them; fp32 as three bf16 planes.
+// With idx the rows are idx[k] for k < *count, then zeros up to the next whole tile;
+// without, k for k < rows, zeros behind. A workgroup a row.
 template <typename T>
 __global__ __launch_bounds__(256) void head_copy_kernel(const T* __restrict__ src, int64_t ld, const int* idx,
-                                                        const int* count, int64_t d, int64_t dp,
+                                                        const int* count, int64_t rows, int64_t d, int64_t dp,
                                                         uint16_t* __restrict__ dst, int64_t plane) {
   constexpr bool F32 = sizeof(T) == 4;
   const int64_t k = blockIdx.x;
-  bool zero = false;
-  int64_t row = k;
+  bool zero = k >= rows;
+  int64_t row = zero ? 0 : k;
   if (idx) {
     const int n = *count;
     if (k >= (n + kHeadRows - 1) / kHeadRows * kHeadRows) return;
@@ -488,7 +489,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
   };
   p.rows = take(256 + (p.np * 3 + rows * 2) * 4);
   p.x = take(p.planes * p.np * p.dp * 2);
-  p.w = p.copy_w ? take(p.planes * vocab * p.dp * 2) : 0;
+  p.w = p.copy_w ? take(p.planes * (vocab + kPipeK) * p.dp * 2) : 0;   // 32 rows of zeros behind: whole K tiles of words
   if (what != BWD) {
     p.part = take(p.tiles * 3 * p.np * 4);
     p.z_label = take(p.np * 4);
@@ -543,10 +544,10 @@ bool off_elements(const void* p, int size) { return reinterpret_cast<uintptr_t>(
   } while (0)
 
 template <typename T>
-hipError_t copy_rows(const void* src, int64_t ld, const int* idx, const int* count, int64_t rows, int64_t d, int64_t dp,
-                     void* dst, int64_t plane, hipStream_t s) {
-  hipLaunchKernelGGL(head_copy_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, static_cast<const T*>(src), ld,
-                     idx, count, d, dp, static_cast<uint16_t*>(dst), plane);
+hipError_t copy_rows(const void* src, int64_t ld, const int* idx, const int* count, int64_t rows, int64_t grid, int64_t d,
+                     int64_t dp, void* dst, int64_t plane, hipStream_t s) {
+  hipLaunchKernelGGL(head_copy_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, static_cast<const T*>(src), ld,
+                     idx, count, rows, d, dp, static_cast<uint16_t*>(dst), plane);
   return hipGetLastError();
 }
 
@@ -567,21 +568,21 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
   }
   hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, s, c, r, head);
   HEAD_TRY(hipGetLastError());
-  const int64_t xplane = p.np * p.dp, wplane = c.vocab * p.dp;
-  HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.x, c.ldx, r.idx, r.count, p.np, p.d, p.dp, xc, xplane, s)
-                  : copy_rows<float>(c.x, c.ldx, r.idx, r.count, p.np, p.d, p.dp, xc, xplane, s));
+  const int64_t xplane = p.np * p.dp, wplane = (c.vocab + kPipeK) * p.dp;
+  HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.x, c.ldx, r.idx, r.count, c.rows, p.np, p.d, p.dp, xc, xplane, s)
+                  : copy_rows<float>(c.x, c.ldx, r.idx, r.count, c.rows, p.np, p.d, p.dp, xc, xplane, s));
   const uint16_t* w = static_cast<const uint16_t*>(c.w);
   int64_t ldw = p.d;
   if (p.copy_w) {
-    HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.w, p.d, nullptr, nullptr, c.vocab, p.d, p.dp, ws + p.w, wplane, s)
-                    : copy_rows<float>(c.w, p.d, nullptr, nullptr, c.vocab, p.d, p.dp, ws + p.w, wplane, s));
+    HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.w, p.d, nullptr, nullptr, c.vocab, c.vocab + kPipeK, p.d, p.dp, ws + p.w, wplane, s)
+                    : copy_rows<float>(c.w, p.d, nullptr, nullptr, c.vocab, c.vocab + kPipeK, p.d, p.dp, ws + p.w, wplane, s));
     w = reinterpret_cast<const uint16_t*>(ws + p.w);
     ldw = p.dp;
   }
   HeadLogits l = {};
   l.pr.zeros = reinterpret_cast<const uint16_t*>(head);
-  l.pr.planes = static_cast<int>(p.planes);
-  l.pr.a.p = w, l.pr.a.ld = ldw, l.pr.a.plane = wplane, l.pr.a.rows = c.vocab, l.pr.a.kvalid = ldw;
+  l.f32 = !c.bf16;
+  l.pr.a.p = w, l.pr.a.ld = ldw, l.pr.a.plane = wplane, l.pr.a.rows = c.vocab, l.pr.a.kvalid = ldw;   // in place the last K tile may be cut
   l.pr.b.p = xc, l.pr.b.ld = p.dp, l.pr.b.plane = xplane, l.pr.b.rows = p.np, l.pr.b.kvalid = p.dp;
   l.count = r.count, l.vocab = c.vocab, l.d = p.d, l.np = p.np, l.ct = kLog2e / c.temperature, l.label = r.label;
   if (what != BWD) {
@@ -613,15 +614,15 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
   uint16_t* g = reinterpret_cast<uint16_t*>(ws + p.g);
   l.row = factors, l.g = g, l.vp = p.vp, l.g_plane = p.np * p.vp;
   HeadDx x = {};
-  x.pr.zeros = l.pr.zeros, x.pr.planes = l.pr.planes;
+  x.pr.zeros = l.pr.zeros, x.f32 = l.f32;
   x.pr.b.p = g, x.pr.b.ld = p.vp, x.pr.b.plane = l.g_plane, x.pr.b.rows = p.np;
   x.count = r.count, x.d = p.d, x.dp = p.dp, x.np = p.np, x.chunk = p.dx_chunk, x.splits = p.dx_splits;
   x.part = reinterpret_cast<float*>(ws + p.dx);
   HeadDw y = {};
-  y.pr.zeros = l.pr.zeros, y.pr.planes = l.pr.planes;
+  y.pr.zeros = l.pr.zeros, y.f32 = l.f32;
   y.pr.a.p = xc, y.pr.a.ld = p.dp, y.pr.a.plane = xplane, y.pr.a.rows = p.dp, y.pr.a.kvalid = p.np;
   y.pr.b.p = g, y.pr.b.ld = p.vp, y.pr.b.plane = l.g_plane, y.pr.b.rows = p.vp, y.pr.b.kvalid = p.np;
-  y.count = r.count, y.d = p.d, y.dp = p.dp, y.splits = p.dw_splits, y.bf16 = c.bf16;
+  y.count = r.count, y.d = p.d, y.dp = p.dp, y.splits = p.dw_splits;
   y.part = p.dw_splits > 1 ? reinterpret_cast<float*>(ws + p.dw) : nullptr;
   const int64_t es = c.bf16 ? 2 : 4;
   for (int64_t v0 = 0; v0 < c.vocab; v0 += p.vp) {
@@ -633,8 +634,8 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
                          r, factors, taught, g, p.vp, l.g_plane, static_cast<int>(p.planes), v0, v1);
       HEAD_TRY(hipGetLastError());
     }
-    x.pr.a.p = w + v0 * ldw, x.pr.a.ld = ldw, x.pr.a.plane = wplane, x.pr.a.rows = ldw, x.pr.a.kvalid = v1 - v0;
-    x.k = up(v1 - v0, kPipeK), x.pr.b.kvalid = x.k;
+    x.k = up(v1 - v0, kPipeK);
+    x.pr.a.p = w + v0 * ldw, x.pr.a.ld = ldw, x.pr.a.plane = wplane, x.pr.a.rows = ldw, x.pr.a.kvalid = p.copy_w ? x.k : v1 - v0;
     x.add = v0 > 0;
     HEAD_TRY(head_launch_dx(x, p.dx_shape, s));
     y.cols = v1 - v0;

@@ -20,7 +20,10 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLowest = -3.402823466e38f;
 
-using Shape256 = PipeShape<2, 4, 8, 4, 4>;
+#ifndef S256
+#define S256 2, 4, 8, 4, 4
+#endif
+using Shape256 = PipeShape<S256>;
 using Shape128 = PipeShape<2, 2, 4, 4, 4>;
 using Shape32 = PipeShape<4, 1, 2, 2, 8>;
 
@@ -53,7 +56,7 @@ __device__ __forceinline__ void logits_tile(int64_t t, int64_t vt, int64_t nt, i
   *n = panel * 8 + r % wide;
 }
 
-template <class S, bool SECOND>
+template <class S, bool SECOND, bool F32>
 __global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t vt, int64_t nt) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
   int64_t tv, tn;
@@ -61,7 +64,7 @@ __global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t 
   const int64_t v0 = p.v0 + tv * S::BM, n0 = tn * S::BN;
   if (n0 >= *p.count) return;
   f32x4 acc[S::FM][S::FN];
-  pipe_product<S, false, false>(p.pr, v0, n0, 0, p.d, lds, acc);
+  pipe_product<S, false, false, F32>(p.pr, v0, n0, 0, p.d, lds, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / S::WN, wn = wave % S::WN, l15 = lane & 15, lh = lane >> 4;
@@ -148,7 +151,7 @@ __device__ __forceinline__ int staged(int r, int e) {
   return r * ROW * 2 + ((((e >> 3) ^ (r & M)) << 4) | ((e & 4) << 1));
 }
 
-template <class S, bool SECOND>
+template <class S, bool SECOND, bool F32>
 __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t vt, int64_t nt) {
   static_assert(S::BM * S::BN * 2 <= S::LDS, "a tile of g is staged in LDS");
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
@@ -157,7 +160,7 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
   const int64_t v0 = p.v0 + tv * S::BM, n0 = tn * S::BN;
   if (n0 >= *p.count) return;
   f32x4 acc[S::FM][S::FN];
-  pipe_product<S, false, false>(p.pr, v0, n0, 0, p.d, lds, acc);
+  pipe_product<S, false, false, F32>(p.pr, v0, n0, 0, p.d, lds, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / S::WN, wn = wave % S::WN, l15 = lane & 15, lh = lane >> 4;
@@ -192,7 +195,7 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
       acc[mi][ni] = g;
     }
   }
-  const int planes = p.pr.planes;
+  constexpr int planes = F32 ? 3 : 1;
   for (int k = 0; k < planes; ++k) {
     if (k > 0) __syncthreads();
 #pragma unroll
@@ -212,7 +215,7 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
   }
 }
 
-template <class S>
+template <class S, bool F32>
 __global__ __launch_bounds__(S::NT) void head_dx_kernel(HeadDx p, int64_t dt, int64_t nt) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
   int64_t t = xcd_tile(blockIdx.x, gridDim.x);
@@ -223,7 +226,7 @@ __global__ __launch_bounds__(S::NT) void head_dx_kernel(HeadDx p, int64_t dt, in
   if (n0 >= *p.count) return;
   const int64_t kb = split * p.chunk, ke = kb + p.chunk < p.k ? kb + p.chunk : p.k;
   f32x4 acc[S::FM][S::FN];
-  pipe_product<S, true, false>(p.pr, d0, n0, kb, ke, lds, acc);
+  pipe_product<S, true, false, F32>(p.pr, d0, n0, kb, ke, lds, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / S::WN, wn = wave % S::WN, l15 = lane & 15, lh = lane >> 4;
@@ -242,7 +245,7 @@ __global__ __launch_bounds__(S::NT) void head_dx_kernel(HeadDx p, int64_t dt, in
   }
 }
 
-template <class S>
+template <class S, bool F32>
 __global__ __launch_bounds__(S::NT) void head_dw_kernel(HeadDw p, int64_t dt, int64_t vt) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
   int64_t t = xcd_tile(blockIdx.x, gridDim.x);
@@ -254,11 +257,11 @@ __global__ __launch_bounds__(S::NT) void head_dw_kernel(HeadDw p, int64_t dt, in
   const int64_t steps = (count + kPipeK - 1) / kPipeK, per = (steps + p.splits - 1) / p.splits;
   const int64_t kb = split * per * kPipeK, end = (split + 1) * per < steps ? (split + 1) * per : steps;
   f32x4 acc[S::FM][S::FN];
-  pipe_product<S, true, true>(p.pr, d0, v0, kb, end * kPipeK, lds, acc);
+  pipe_product<S, true, true, F32>(p.pr, d0, v0, kb, end * kPipeK, lds, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / S::WN, wn = wave % S::WN, l15 = lane & 15, lh = lane >> 4;
-  if (p.part || !p.bf16) {
+  if (F32 || p.part) {
     // fp32: a split's sums, or the result
     const int64_t ld = p.part ? p.dp : p.d;
     float* base = p.part ? p.part + split * p.cols * p.dp : static_cast<float*>(p.dw);
@@ -317,10 +320,17 @@ hipError_t sums(const HeadLogits& a, bool second, hipStream_t st) {
   const int64_t vt = tiles(a.v1 - a.v0, S::BM), nt = tiles(a.np, S::BN);
   if (hipError_t e = check_grid(vt * nt)) return e;
   const dim3 g(static_cast<unsigned>(vt * nt));
-  if (second)
-    hipLaunchKernelGGL((head_sums_kernel<S, true>), g, dim3(S::NT), 0, st, a, vt, nt);
-  else
-    hipLaunchKernelGGL((head_sums_kernel<S, false>), g, dim3(S::NT), 0, st, a, vt, nt);
+  if (a.f32) {
+    if (second)
+      hipLaunchKernelGGL((head_sums_kernel<S, true, true>), g, dim3(S::NT), 0, st, a, vt, nt);
+    else
+      hipLaunchKernelGGL((head_sums_kernel<S, false, true>), g, dim3(S::NT), 0, st, a, vt, nt);
+  } else {
+    if (second)
+      hipLaunchKernelGGL((head_sums_kernel<S, true, false>), g, dim3(S::NT), 0, st, a, vt, nt);
+    else
+      hipLaunchKernelGGL((head_sums_kernel<S, false, false>), g, dim3(S::NT), 0, st, a, vt, nt);
+  }
   return hipGetLastError();
 }
 
@@ -329,10 +339,17 @@ hipError_t grad(const HeadLogits& a, bool second, hipStream_t st) {
   const int64_t vt = tiles(a.v1 - a.v0, S::BM), nt = tiles(a.np, S::BN);
   if (hipError_t e = check_grid(vt * nt)) return e;
   const dim3 g(static_cast<unsigned>(vt * nt));
-  if (second)
-    hipLaunchKernelGGL((head_grad_kernel<S, true>), g, dim3(S::NT), 0, st, a, vt, nt);
-  else
-    hipLaunchKernelGGL((head_grad_kernel<S, false>), g, dim3(S::NT), 0, st, a, vt, nt);
+  if (a.f32) {
+    if (second)
+      hipLaunchKernelGGL((head_grad_kernel<S, true, true>), g, dim3(S::NT), 0, st, a, vt, nt);
+    else
+      hipLaunchKernelGGL((head_grad_kernel<S, false, true>), g, dim3(S::NT), 0, st, a, vt, nt);
+  } else {
+    if (second)
+      hipLaunchKernelGGL((head_grad_kernel<S, true, false>), g, dim3(S::NT), 0, st, a, vt, nt);
+    else
+      hipLaunchKernelGGL((head_grad_kernel<S, false, false>), g, dim3(S::NT), 0, st, a, vt, nt);
+  }
   return hipGetLastError();
 }
 
@@ -340,7 +357,10 @@ template <class S>
 hipError_t dx(const HeadDx& a, hipStream_t st) {
   const int64_t dt = tiles(a.d, S::BM), nt = tiles(a.np, S::BN), n = dt * nt * a.splits;
   if (hipError_t e = check_grid(n)) return e;
-  hipLaunchKernelGGL((head_dx_kernel<S>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, nt);
+  if (a.f32)
+    hipLaunchKernelGGL((head_dx_kernel<S, true>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, nt);
+  else
+    hipLaunchKernelGGL((head_dx_kernel<S, false>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, nt);
   return hipGetLastError();
 }
 
@@ -348,7 +368,10 @@ template <class S>
 hipError_t dw(const HeadDw& a, hipStream_t st) {
   const int64_t dt = tiles(a.d, S::BM), vt = tiles(a.cols, S::BN), n = dt * vt * a.splits;
   if (hipError_t e = check_grid(n)) return e;
-  hipLaunchKernelGGL((head_dw_kernel<S>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, vt);
+  if (a.f32)
+    hipLaunchKernelGGL((head_dw_kernel<S, true>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, vt);
+  else
+    hipLaunchKernelGGL((head_dw_kernel<S, false>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, vt);
   return hipGetLastError();
 }
 
