@@ -5,22 +5,26 @@
 //
 // An operand lies in memory either with k side by side (KC: element (r, k) at
 // p + r*ld + k) or with its rows side by side (KM: at p + k*ld + r), so that none of
-// x w^T, g w and g^T x needs a transposed copy. K tiles of 32 go from memory straight
+// x w^T, g w and g^T x needs a transposed copy. K tiles of 64 go from memory straight
 // into LDS (global_load_lds_dwordx4: a wave's 64 pieces of 16 bytes land in 1 KB in
-// lane order), NST stages deep, and from there into MFMA operands a step ahead of
-// their use, so that a wave's matrix instructions never wait for its own LDS reads:
-//   step s: wait for the loads of stage s+1 and this wave's reads of stage s; barrier;
-//           load stage s+NST into the place of stage s; read stage s+1 into registers;
-//           multiply stage s.
-// One barrier a step, no wait for the loads of later stages.
+// lane order), NST of them, and from there half by half (32 k, one MFMA's) into
+// operand registers ahead of their use:
+//   tile t: read its second half; multiply its first;
+//           wait for tile t+1 and for this wave's reads of tile t; barrier;
+//           load tile t+NST into the place of tile t;
+//           read the first half of tile t+1; multiply the second half of tile t.
+// One barrier a tile, and a wave's matrix instructions never wait for its own LDS reads.
 //
-// KC stage: rows of 64 bytes, 16-byte piece q of row r at q ^ (-(r / 4) mod 4). A 16-byte read of 64
-// lanes is served in four groups of 16, lanes 0-3, 12-15, 20-23, 24-27 first, 4-11, 16-19,
-// 28-31 then, and so on: the groups are why it is not q ^ (r / 4) mod 4, which puts two
-// rows of a group on the same banks (half of all LDS cycles were conflicts). KM stage: rows of 2*ROWS bytes, one for
-// each k, read by ds_read_b64_tr_b16 (16 lanes give four rows of 32 bytes, lane i gets
-// column i of the four); the 32-byte slot of column group t in row k is t ^ g(k), g =
-// (k & 3) + 4 ((k >> 3) & 3), so that the 16 rows of such a read fall on all banks.
+// What bounds the 256 x 256 tile is the way from L2 into the CU: measured apart, 4096 x 4096 x
+// 131072 takes 1.5 ms a product when every load hits L1. Lines of 128 bytes have to be
+// taken whole (K tiles of 32 took 64-byte halves of KC rows, and a KC tile as long as two KM ones).
+//
+// KC tile: rows of 128 bytes, 16-byte piece q of row r at q ^ ((r / 2) mod 8). A 16-byte read of
+// 64 lanes is served in four groups of 16: lanes 0-3, 12-15, 20-23, 24-27, then 4-11, 16-19,
+// 28-31, and so on; the 16 rows and pieces of each group fall on all banks. KM tile: rows of
+// 2*ROWS bytes, one for each k, read by ds_read_b64_tr_b16 (16 lanes give four rows of 32
+// bytes, lane i gets column i of the four); the 32-byte slot of column group t in row k is
+// t ^ g(k), g = (k & 3) + 4 ((k >> 3) & 3), so that the 16 rows of such a read fall on all banks.
 //
 // fp32 operands come as three bf16 planes (a = a0 + a1 + a2, exact: 8 bits of the
 // mantissa each) and their product as six products of planes, least first; what is
@@ -31,9 +35,6 @@
 
 #include "common.h"
 
-#ifndef PIPE_SCHED
-#define PIPE_SCHED
-#endif
 namespace monarch {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -52,12 +53,12 @@ struct PipeProduct {
   const uint16_t* zeros = nullptr;   // 16 bytes of zeros
 };
 
-constexpr int kPipeK = 32;
+constexpr int kPipeK = 64;   // k of a tile, two halves
 
 __device__ __forceinline__ int pipe_swizzle(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
 
 // KC: where a row's 16-byte pieces are turned to.
-__device__ __forceinline__ int pipe_turn(int r) { return (4 - ((r >> 2) & 3)) & 3; }
+__device__ __forceinline__ int pipe_turn(int r) { return (r >> 1) & 7; }
 
 // The loads and fragment reads of one operand tile of ROWS rows, by NW waves.
 template <bool KM, int ROWS, int NW>
@@ -85,8 +86,8 @@ struct PipeTile {
         const int c = ((((pos >> 1) ^ (pipe_swizzle(k) & MASK)) << 1) | (pos & 1)) * 8;
         ptr[i] = o.p + (k0 + k) * o.ld + (r0 + c < o.rows ? r0 + c : 0);
       } else {
-        const int r = j * 16 + (lane >> 2);
-        const int q = (lane & 3) ^ pipe_turn(r);
+        const int r = j * 8 + (lane >> 3);
+        const int q = (lane & 7) ^ pipe_turn(r);
         const int64_t row = r0 + r < o.rows ? r0 + r : o.rows - 1;
         ptr[i] = o.p + row * o.ld + k0 + q * 8;
       }
@@ -116,34 +117,34 @@ struct PipeTile {
         const int64_t over = j * (1024 / (ROWS * 2)) + lane / CHUNKS - (valid - 1);
         if (over > 0) s -= over * o.ld;
       } else {
-        if (((lane & 3) ^ pipe_turn(j * 16 + (lane >> 2))) * 8 >= valid) s = zeros;
+        if (((lane & 7) ^ pipe_turn(j * 8 + (lane >> 3))) * 8 >= valid) s = zeros;
       }
       load(s, stage + load_of(i, wave) * 1024);
       ptr[i] += adv;
     }
   }
 
-  // Byte offset in a stage of this lane's read of fragment t0 (t0 + t, t below a power of two that divides t0:
-  // read()). KM: the slot bits of an offset are 0 but for the swizzle, so that a tile's number is
-  // one exclusive or away.
+  // Byte offset in a tile of this lane's reads of fragments t0 + t (t below a power of two that divides t0).
+  // KM: the slot bits of an offset are 0 but for the swizzle, so that a fragment's number
+  // is one exclusive or away; KC: so is the half of the tile.
   __device__ __forceinline__ static int base(int lane, int t0) {
     const int l15 = lane & 15, lh = lane >> 4;
     if constexpr (KM)
       return ((8 * lh + (l15 >> 2)) * (ROWS * 2) + (l15 & 3) * 8) ^ ((t0 ^ (((l15 >> 2) | (lh << 2)) & MASK)) << 5);
     else
-      return t0 * 1024 + l15 * 64 + ((lh ^ pipe_turn(l15)) << 4);
+      return t0 * 2048 + l15 * 128 + ((lh ^ pipe_turn(l15)) << 4);
   }
-  __device__ __forceinline__ static bf16x8 read(const char* stage, int base, int t) {
+  __device__ __forceinline__ static bf16x8 read(const char* stage, int base, int t, int half) {
     bf16x8 r;
     if constexpr (KM) {
-      const char* at = stage + (base ^ (t << 5));
+      const char* at = stage + (base ^ (t << 5)) + half * 32 * ROWS * 2;
       typedef __attribute__((address_space(3))) s16x4 Lds;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)(at));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)(at + 4 * ROWS * 2));
       __builtin_memcpy(&r, &lo, 8);
       __builtin_memcpy(reinterpret_cast<char*>(&r) + 8, &hi, 8);
     } else {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(stage + base + t * 1024);
+      const u32x4 v = *reinterpret_cast<const u32x4*>(stage + (base ^ (half << 6)) + t * 2048);
       __builtin_memcpy(&r, &v, 16);
     }
     return r;
@@ -184,7 +185,7 @@ struct PipeShape {
 };
 
 // acc[mi][ni], lane l: rows m0 + (wm*FM + mi)*16 + 4*(l/16) + v, column n0 + (wn*FN + ni)*16 + l%16.
-// Sums k in [kb, ke) (kb a multiple of 32); F32: over six products of planes. Only a's k may end
+// Sums k in [kb, ke) (kb a multiple of 64); F32: over six products of planes. Only a's k may end
 // inside the last tile, and only without F32. Ends with a barrier: `lds` is free.
 template <class S, bool AKM, bool BKM, bool F32>
 __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, int64_t n0, int64_t kb, int64_t ke,
@@ -192,38 +193,37 @@ __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, i
   using TA = PipeTile<AKM, S::BM, S::NW>;
   using TB = PipeTile<BKM, S::BN, S::NW>;
   constexpr int NI = TA::PER + TB::PER, FM = S::FM, FN = S::FN, NST = S::NST;
-  static_assert(NST % 2 == 0, "stage and register slot of a step go together");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
 #pragma unroll
   for (int mi = 0; mi < FM; ++mi)
 #pragma unroll
     for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int ksteps = ke > kb ? static_cast<int>((ke - kb + kPipeK - 1) / kPipeK) : 0;
-  const int nsteps = ksteps * (F32 ? 6 : 1);
-  if (nsteps == 0) return;
+  const int ktiles = ke > kb ? static_cast<int>((ke - kb + kPipeK - 1) / kPipeK) : 0;
+  const int ntiles = ktiles * (F32 ? 6 : 1);
+  if (ntiles == 0) return;
   PipeOperand oa = p.a, ob = p.b;
   if constexpr (F32) oa.p += 2 * oa.plane;
   TA a;
   a.init(oa, m0, kb, wave, lane);
   TB b;
   b.init(ob, n0, kb, wave, lane);
-  static_assert((FM & (FM - 1)) == 0 && (FN & (FN - 1)) == 0, "tiles of a wave");
+  static_assert((FM & (FM - 1)) == 0 && (FN & (FN - 1)) == 0, "fragments of a wave");
   const int ab = TA::base(lane, wm * FM), bb = TB::base(lane, wn * FN);
   // of the last tile's k of a: all, or those before kvalid
-  const int64_t last_valid = oa.kvalid - kb - static_cast<int64_t>(ksteps - 1) * kPipeK;
+  const int64_t last_valid = oa.kvalid - kb - static_cast<int64_t>(ktiles - 1) * kPipeK;
 
   // F32: planes of a and b in the order of their products: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
   int ik = 0, iseg = 0;
   auto next_tile = [&]() {
     if constexpr (F32) {
-      if (++ik == ksteps) {
+      if (++ik == ktiles) {
         ik = 0;
         constexpr uint32_t seqa = 0x001102, seqb = 0x010120;
         const int na = (seqa >> (4 * iseg + 4)) & 3, pa = (seqa >> (4 * iseg)) & 3;
         const int nb = (seqb >> (4 * iseg + 4)) & 3, pb = (seqb >> (4 * iseg)) & 3;
         ++iseg;
-        const int64_t ja = (na - pa) * oa.plane - ksteps * a.adv, jb = (nb - pb) * ob.plane - ksteps * b.adv;
+        const int64_t ja = (na - pa) * oa.plane - ktiles * a.adv, jb = (nb - pb) * ob.plane - ktiles * b.adv;
 #pragma unroll
         for (int i = 0; i < TA::PER; ++i) a.ptr[i] += ja;
 #pragma unroll
@@ -235,10 +235,11 @@ __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, i
     char* at = lds + st * S::STAGE;
     a.issue(at, wave);
     b.issue(at + TA::BYTES, wave);
+    next_tile();
   };
   auto issue_any = [&](int st, int tile) {
     char* at = lds + st * S::STAGE;
-    if (!F32 && tile == nsteps - 1 && last_valid < kPipeK)
+    if (!F32 && tile == ntiles - 1 && last_valid < kPipeK)
       a.issue_cut(oa, p.zeros, at, wave, lane, last_valid);
     else
       a.issue(at, wave);
@@ -246,68 +247,72 @@ __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, i
     next_tile();
   };
   bf16x8 fa[2][FM], fb[2][FN];
-  auto read = [&](auto slot, int st) {
-    constexpr int X = decltype(slot)::value;
+  auto read = [&](auto half, int st) {
+    constexpr int X = decltype(half)::value;
     const char* at = lds + st * S::STAGE;
-    // offsets of single fragments are not kept over steps (they would not fit beside the sums)
+    // offsets of single fragments are not kept from tile to tile (they would not fit beside the sums)
     int ar = ab, br = bb;
     if constexpr (AKM) asm volatile("" : "+v"(ar));
     if constexpr (BKM) asm volatile("" : "+v"(br));
 #pragma unroll
-    for (int mi = 0; mi < FM; ++mi) fa[X][mi] = TA::read(at, ar, mi);
+    for (int mi = 0; mi < FM; ++mi) fa[X][mi] = TA::read(at, ar, mi, X);
 #pragma unroll
-    for (int ni = 0; ni < FN; ++ni) fb[X][ni] = TB::read(at + TA::BYTES, br, ni);
+    for (int ni = 0; ni < FN; ++ni) fb[X][ni] = TB::read(at + TA::BYTES, br, ni, X);
   };
-  auto multiply = [&](auto slot) {
-    constexpr int X = decltype(slot)::value;
+  auto multiply = [&](auto half) {
+    constexpr int X = decltype(half)::value;
 #pragma unroll
     for (int mi = 0; mi < FM; ++mi)
 #pragma unroll
       for (int ni = 0; ni < FN; ++ni)
         acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[X][mi], fb[X][ni], acc[mi][ni], 0, 0, 0);
   };
+  using First = std::integral_constant<int, 0>;
+  using Second = std::integral_constant<int, 1>;
   auto meet = [&]() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  // waits until at most `later` < NST stages' loads are in flight
+  // waits until at most `later` < NST tiles' loads are in flight
   auto landed = [&](int later) {
     asm volatile("" ::: "memory");
     pipe_wait_stages<NI, NST - 1>(later);
     meet();
   };
 #pragma unroll 1
-  for (int s = 0; s < NST && s < nsteps; ++s) issue_any(s, s);
-  landed((nsteps < NST ? nsteps : NST) - 1);
-  read(std::integral_constant<int, 0>{}, 0);
-  // a step in the middle: a whole tile is loaded, NST - 2 stages stay in flight
-  auto step = [&](auto stage) {
-    constexpr int ST = decltype(stage)::value, X = ST & 1;
+  for (int t = 0; t < NST && t < ntiles; ++t) issue_any(t, t);
+  landed((ntiles < NST ? ntiles : NST) - 1);
+  read(First{}, 0);
+  // a tile in the middle: a whole tile is loaded, NST - 2 stay in flight
+  auto tile = [&](auto stage) {
+    constexpr int ST = decltype(stage)::value;
+    read(Second{}, ST);
+    multiply(First{});
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(pipe_wait((NST - 2) * NI));
     meet();
     issue(ST);
-    read(std::integral_constant<int, 1 - X>{}, ST + 1 == NST ? 0 : ST + 1);
-    multiply(std::integral_constant<int, X>{});
-    PIPE_SCHED
-    next_tile();
+    read(First{}, ST + 1 == NST ? 0 : ST + 1);
+    multiply(Second{});
   };
-  auto last_step = [&](auto stage, int s) {
-    constexpr int ST = decltype(stage)::value, X = ST & 1;
-    if (s >= nsteps) return;
-    const int left = nsteps - 2 - s;   // stages behind s+1
-    if (s + 1 < nsteps) {
+  auto last_tile = [&](auto stage, int t) {
+    constexpr int ST = decltype(stage)::value;
+    if (t >= ntiles) return;
+    read(Second{}, ST);
+    multiply(First{});
+    const int left = ntiles - 2 - t;   // tiles behind t+1
+    if (t + 1 < ntiles) {
       landed(left < NST - 2 ? left : NST - 2);
-      if (s + NST < nsteps) issue_any(ST, s + NST);
-      read(std::integral_constant<int, 1 - X>{}, ST + 1 == NST ? 0 : ST + 1);
+      if (t + NST < ntiles) issue_any(ST, t + NST);
+      read(First{}, ST + 1 == NST ? 0 : ST + 1);
     }
-    multiply(std::integral_constant<int, X>{});
+    multiply(Second{});
   };
-  int s = 0;
+  int t = 0;
 #pragma unroll 1
-  for (; s + NST + NST < nsteps; s += NST) pipe_each<NST>([&](auto i) { step(i); });
+  for (; t + NST + NST < ntiles; t += NST) pipe_each<NST>([&](auto i) { tile(i); });
 #pragma unroll 1
-  for (; s < nsteps; s += NST) pipe_each<NST>([&](auto i) { last_step(i, s + decltype(i)::value); });
+  for (; t < ntiles; t += NST) pipe_each<NST>([&](auto i) { last_tile(i, t + decltype(i)::value); });
   __syncthreads();
 }
 

@@ -489,7 +489,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
   };
   p.rows = take(256 + (p.np * 3 + rows * 2) * 4);
   p.x = take(p.planes * p.np * p.dp * 2);
-  p.w = p.copy_w ? take(p.planes * (vocab + kPipeK) * p.dp * 2) : 0;   // 32 rows of zeros behind: whole K tiles of words
+  p.w = p.copy_w ? take(p.planes * (vocab + kPipeK) * p.dp * 2) : 0;   // zeros behind: whole K tiles of words
   if (what != BWD) {
     p.part = take(p.tiles * 3 * p.np * 4);
     p.z_label = take(p.np * 4);

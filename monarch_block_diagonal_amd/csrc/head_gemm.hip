@@ -21,11 +21,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLowest = -3.402823466e38f;
 
 #ifndef S256
-#define S256 2, 4, 8, 4, 4
+#define S256 2, 4, 8, 4, 2
 #endif
 using Shape256 = PipeShape<S256>;
-using Shape128 = PipeShape<2, 2, 4, 4, 4>;
-using Shape32 = PipeShape<4, 1, 2, 2, 8>;
+using Shape128 = PipeShape<2, 2, 4, 4, 2>;
+using Shape32 = PipeShape<4, 1, 2, 2, 4>;
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -47,20 +47,22 @@ __device__ __forceinline__ float over_groups(float v) {
   return MAX ? fmaxf(a, b) : a + b;
 }
 
-// (words, rows) of tile t: rows in panels of 8 tiles, a panel's words after each other,
-// so that the workgroups that run together share words and rows in their L2.
-__device__ __forceinline__ void logits_tile(int64_t t, int64_t vt, int64_t nt, int64_t* v, int64_t* n) {
-  const int64_t panel = t / (8 * vt), wide = nt - panel * 8 < 8 ? nt - panel * 8 : 8;
-  const int64_t r = t - panel * 8 * vt;
-  *v = r / wide;
-  *n = panel * 8 + r % wide;
+// Tile t of an outer x inner grid of tiles: the inner ones in panels of 8, a panel's outer ones
+// after each other, so that the 32 workgroups that an XCD runs together take about 4 x 8 tiles
+// and share their operands' tiles in its L2 (12 of 64 K tiles come from outside it; 18 where 16 x 2
+// run together).
+__device__ __forceinline__ void panel_tile(int64_t t, int64_t outer, int64_t inner, int64_t* o, int64_t* i) {
+  const int64_t panel = t / (8 * outer), wide = inner - panel * 8 < 8 ? inner - panel * 8 : 8;
+  const int64_t r = t - panel * 8 * outer;
+  *o = r / wide;
+  *i = panel * 8 + r % wide;
 }
 
 template <class S, bool SECOND, bool F32>
 __global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t vt, int64_t nt) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
   int64_t tv, tn;
-  logits_tile(xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
+  panel_tile(xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
   const int64_t v0 = p.v0 + tv * S::BM, n0 = tn * S::BN;
   if (n0 >= *p.count) return;
   f32x4 acc[S::FM][S::FN];
@@ -154,9 +156,10 @@ __device__ __forceinline__ int staged(int r, int e) {
 template <class S, bool SECOND, bool F32>
 __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t vt, int64_t nt) {
   static_assert(S::BM * S::BN * 2 <= S::LDS, "a tile of g is staged in LDS");
+  static_assert(S::BN % kPipeK == 0 || 2 * S::BN == kPipeK, "with the 0s, whole K tiles of rows");
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
   int64_t tv, tn;
-  logits_tile(xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
+  panel_tile(xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
   const int64_t v0 = p.v0 + tv * S::BM, n0 = tn * S::BN;
   if (n0 >= *p.count) return;
   f32x4 acc[S::FM][S::FN];
@@ -211,6 +214,8 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
     for (int c = threadIdx.x; c < S::BN * CH; c += S::NT) {
       const int row = c / CH, e = (c % CH) * 8;
       *reinterpret_cast<u32x4*>(out + row * p.vp + e) = *reinterpret_cast<const u32x4*>(lds + staged<S::BM>(row, e));
+      // a K tile of dw's is 64 rows: the other ones are 0
+      if constexpr (S::BN < kPipeK) *reinterpret_cast<u32x4*>(out + (S::BN + row) * p.vp + e) = u32x4{0, 0, 0, 0};
     }
   }
 }
@@ -218,10 +223,9 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
 template <class S, bool F32>
 __global__ __launch_bounds__(S::NT) void head_dx_kernel(HeadDx p, int64_t dt, int64_t nt) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
-  int64_t t = xcd_tile(blockIdx.x, gridDim.x);
-  const int64_t td = t % dt;
-  t /= dt;
-  const int64_t tn = t % nt, split = t / nt;
+  const int64_t t = xcd_tile(blockIdx.x, gridDim.x), split = t / (dt * nt);
+  int64_t td, tn;
+  panel_tile(t - split * dt * nt, nt, dt, &tn, &td);
   const int64_t d0 = td * S::BM, n0 = tn * S::BN;
   if (n0 >= *p.count) return;
   const int64_t kb = split * p.chunk, ke = kb + p.chunk < p.k ? kb + p.chunk : p.k;
@@ -237,7 +241,7 @@ __global__ __launch_bounds__(S::NT) void head_dx_kernel(HeadDx p, int64_t dt, in
 #pragma unroll
     for (int mi = 0; mi < S::FM; ++mi) {
       const int64_t d = d0 + (wm * S::FM + mi) * 16 + 4 * lh;
-      if (d < p.dp) {   // dp is a multiple of 32
+      if (d < p.dp) {   // dp is a multiple of 64
         f32x4* at = reinterpret_cast<f32x4*>(o + d);
         *at = p.add ? acc[mi][ni] + *at : acc[mi][ni];
       }
@@ -248,10 +252,9 @@ __global__ __launch_bounds__(S::NT) void head_dx_kernel(HeadDx p, int64_t dt, in
 template <class S, bool F32>
 __global__ __launch_bounds__(S::NT) void head_dw_kernel(HeadDw p, int64_t dt, int64_t vt) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
-  int64_t t = xcd_tile(blockIdx.x, gridDim.x);
-  const int64_t td = t % dt;
-  t /= dt;
-  const int64_t tv = t % vt, split = t / vt;
+  const int64_t t = xcd_tile(blockIdx.x, gridDim.x), split = t / (dt * vt);
+  int64_t td, tv;
+  panel_tile(t - split * dt * vt, vt, dt, &tv, &td);
   const int64_t d0 = td * S::BM, v0 = tv * S::BN;
   const int64_t count = *p.count;
   const int64_t steps = (count + kPipeK - 1) / kPipeK, per = (steps + p.splits - 1) / p.splits;
