@@ -435,7 +435,7 @@ int monarch_distill_step(const void* logits, int64_t ld, const void* teacher, co
  *   stats: monarch_head_stats_bytes, written by the forward pass for the backward pass.
  *   workspace: monarch_head_workspace_bytes of the call (0 forward, 1 backward, 2 step): a copy
  *   of x, in fp32 or with features % 8 != 0 one of w, a piece of the vocabulary's gradient
- *   of the logits (at most 1 GiB, or 256 words of it) and partial sums. The calls keep nothing else of size rows * vocab.
+ *   of the logits (at most 2 GiB, or 256 words of it) and partial sums (at most 1 GiB each, or one sum). The calls keep nothing else of size rows * vocab.
  * Logits and all sums are fp32 (fp32 operands are multiplied as three bf16 parts each,
  * exact to 2^-23 of a product). In bf16 the gradient of the logits is rounded to bf16 between its
  * products; dx and dw are rounded once. Sums run in a fixed order.

@@ -46,6 +46,7 @@ struct HeadDx {
   int splits;
   float* part;                // [splits][np][dp]
   int add;                    // whether a piece before has written part
+  int64_t dt, nt;             // tiles (set by the launch)
 };
 
 struct HeadDw {
@@ -56,6 +57,7 @@ struct HeadDw {
   int splits;
   float* part;                // [splits][cols][dp], or null:
   void* dw;                   // the piece's first word of dw [vocab][d]
+  int64_t dt, vt;             // tiles (set by the launch)
 };
 
 int64_t head_tile_words(HeadShape s);    // words of a logits tile
@@ -63,7 +65,7 @@ int64_t head_tile_rows(HeadShape s);     // rows of a logits and a dx tile
 // second: the labels' softmax has exponentials of its own
 hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, bool second, hipStream_t st);
 hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, bool second, hipStream_t st);
-hipError_t head_launch_dx(const HeadDx& a, HeadShape s, hipStream_t st);
-hipError_t head_launch_dw(const HeadDw& a, HeadShape s, hipStream_t st);
+// dx and dw of a piece (HEAD_32: dx's tiles, dw's are HEAD_128's)
+hipError_t head_launch_products(const HeadDx& x, const HeadDw& w, HeadShape s, hipStream_t st);
 
 }  // namespace monarch

@@ -32,7 +32,7 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int64_t kLimit = int64_t(1) << 31;
 constexpr int64_t kMaxFeatures = int64_t(1) << 20;
-constexpr int64_t kPieceBytes = int64_t(1) << 30;   // of g
+constexpr int64_t kPieceBytes = int64_t(1) << 31;   // of g
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -446,8 +446,7 @@ int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 struct HeadPlan {
   int64_t d, dp, np, planes;
   bool copy_w;                 // the head is copied (fp32, or rows that are no whole pieces)
-  HeadShape shape;             // logits
-  HeadShape dx_shape, dw_shape;
+  HeadShape shape, products;   // of the logits, and of dx and dw
   int64_t tiles;               // of words, forward
   int64_t vp, pieces;          // words of a piece
   int dx_splits, dw_splits;
@@ -456,20 +455,19 @@ struct HeadPlan {
   size_t rows, x, w, part, z_label, stats, factors, taught, g, dx, dw, total;
 };
 
-// Splits of a sum of `steps` K tiles over `base` tiles of output, so that the
-// workgroups fill whole rounds of `slots`.
-int pick_splits(int64_t base, int64_t steps, int64_t slots, int64_t most) {
-  int64_t top = steps / 8 < most ? steps / 8 : most;
-  if (top < 1) top = 1;
-  int best = 1;
-  double best_eff = 0.0;
-  for (int64_t s = 1; s <= top; ++s) {
-    const int64_t n = base * s;
-    const double eff = static_cast<double>(n) / static_cast<double>(up(n, slots));
-    if (eff > best_eff + 0.04) best = static_cast<int>(s), best_eff = eff;
-    if (best_eff >= 0.94 || n >= 8 * slots) break;
+// When `slots` places that take `first` tiles of length a, then `more` of length b, are done.
+double done_at(int64_t slots, int64_t first, double a, int64_t more, double b) {
+  const int64_t rounds = first / slots, late = first % slots;
+  // `late` places are free at (rounds + 1) a, the others at rounds a: count what fits until t, and raise t
+  const double early_at = rounds * a, late_at = early_at + a;
+  double t = early_at;
+  for (;;) {
+    const double e = floor((t - early_at) / b + 1e-9), l = t >= late_at ? floor((t - late_at) / b + 1e-9) : 0.0;
+    if ((slots - late) * e + late * l >= static_cast<double>(more)) break;
+    const double next_e = early_at + (e + 1) * b, next_l = t >= late_at ? late_at + (l + 1) * b : late_at + b;
+    t = late > 0 && next_l < next_e ? next_l : next_e;
   }
-  return best;
+  return late > 0 && t < late_at ? late_at : t;
 }
 
 HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top, bool bf16) {
@@ -501,22 +499,31 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
     p.pieces = (vocab + vp - 1) / vp;
     p.vp = up((vocab + p.pieces - 1) / p.pieces, kHeadRows);
     p.pieces = (vocab + p.vp - 1) / p.vp;
-    const bool wide = rows > 128 && d > 128;
-    p.dx_shape = rows <= 32 ? HEAD_32 : wide ? HEAD_256 : HEAD_128;
-    const int64_t tm = head_tile_words(p.dx_shape), tn = head_tile_rows(p.dx_shape);
-    const int64_t base = (up(d, tm) / tm) * (up(rows, tn) / tn), steps = p.vp / kPipeK;
-    int64_t most = (int64_t(1) << 30) / (p.np * p.dp * 4);
-    if (most > 256) most = 256;
-    p.dx_splits = pick_splits(base, steps, wide ? 256 : 512, most);
-    p.dx_chunk = up((p.vp + p.dx_splits - 1) / p.dx_splits, kPipeK);
+    // dx: rows x features, summed over the piece's words; dw: words x features, summed over rows
+    const bool wide = rows > 128 && d > 128 && (up(d, 256) / 256) * (up(p.vp, 256) / 256) >= 96;
+    p.products = rows <= 32 ? HEAD_32 : wide ? HEAD_256 : HEAD_128;
+    const int64_t xm = head_tile_words(p.products), xn = head_tile_rows(p.products);
+    const int64_t wm = wide ? 256 : 128;
+    const int64_t slots = wide ? 256 : 512;
+    const int64_t dx_tiles = (up(d, xm) / xm) * (up(rows, xn) / xn), dw_tiles = (up(d, wm) / wm) * (up(p.vp, wm) / wm);
+    // dw is split only where its tiles do not fill half the chip
+    int64_t ws = dw_tiles >= slots / 2 ? 1 : slots / dw_tiles;
+    if (ws > (rows + 511) / 512) ws = (rows + 511) / 512;
+    while (ws > 1 && ws * p.vp * p.dp * 4 > (int64_t(1) << 30)) --ws;
+    p.dw_splits = static_cast<int>(ws);
+    // dx's splits fill the places that dw leaves free: the split whose tiles are done first, by what was
+    // measured of a tile (13 ns a k of a 256 x 256 tile, 7 of a 128 x 128 one, where two share a CU;
+    // 300 k for a tile's start and end) and of the splits' sums (written and read at 2.5 TB/s)
+    const double ns = (wide ? 13.0 : 7.0) * (bf16 ? 1 : 6), ends = 300.0 / (bf16 ? 1 : 6);
+    double best = 0.0;
+    int64_t xs = 0;
+    for (int64_t n = 1; n <= 64 && (n == 1 || (p.vp / n >= 512 && n * p.np * p.dp * 4 <= (int64_t(1) << 30))); ++n) {
+      const double t = ns * done_at(slots, dw_tiles * ws, static_cast<double>(rows) / ws + ends, dx_tiles * n,
+                                    static_cast<double>(p.vp) / n + ends) + n * static_cast<double>(p.np * p.dp) * 4 / 2500.0;
+      if (xs == 0 || t < best) best = t, xs = n;
+    }
+    p.dx_chunk = up((p.vp + xs - 1) / xs, kPipeK);
     p.dx_splits = static_cast<int>((p.vp + p.dx_chunk - 1) / p.dx_chunk);
-    const int64_t w256 = (up(d, 256) / 256) * (up(p.vp, 256) / 256);
-    p.dw_shape = d > 128 && w256 >= 192 ? HEAD_256 : HEAD_128;
-    const int64_t tw = head_tile_words(p.dw_shape);
-    const int64_t wbase = (up(d, tw) / tw) * (up(p.vp, tw) / tw);
-    const int64_t slots = p.dw_shape == HEAD_256 ? 256 : 512;
-    most = (int64_t(1) << 30) / (p.vp * p.dp * 4);
-    p.dw_splits = wbase >= slots / 2 ? 1 : pick_splits(wbase, up(rows, kPipeK) / kPipeK, slots, most < 64 ? most : 64);
     p.factors = take(p.np * static_cast<int64_t>(sizeof(HeadRow)));
     p.taught = take(p.np * 4);
     p.g = take(p.planes * p.np * p.vp * 2);
@@ -637,10 +644,9 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
     x.k = up(v1 - v0, kPipeK);
     x.pr.a.p = w + v0 * ldw, x.pr.a.ld = ldw, x.pr.a.plane = wplane, x.pr.a.rows = ldw, x.pr.a.kvalid = p.copy_w ? x.k : v1 - v0;
     x.add = v0 > 0;
-    HEAD_TRY(head_launch_dx(x, p.dx_shape, s));
     y.cols = v1 - v0;
     y.dw = static_cast<char*>(c.dw) + v0 * p.d * es;
-    HEAD_TRY(head_launch_dw(y, p.dw_shape, s));
+    HEAD_TRY(head_launch_products(x, y, p.products, s));
     if (y.part) {
       const unsigned n = static_cast<unsigned>((y.cols * ((p.d + 3) / 4) + 255) / 256);
       if (c.bf16)

@@ -221,9 +221,9 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
 }
 
 template <class S, bool F32>
-__global__ __launch_bounds__(S::NT) void head_dx_kernel(HeadDx p, int64_t dt, int64_t nt) {
-  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
-  const int64_t t = xcd_tile(blockIdx.x, gridDim.x), split = t / (dt * nt);
+__device__ __forceinline__ void dx_tile(const HeadDx& p, int64_t at, char* lds) {
+  const int64_t dt = p.dt, nt = p.nt;
+  const int64_t t = xcd_tile(at, dt * nt * p.splits), split = t / (dt * nt);
   int64_t td, tn;
   panel_tile(t - split * dt * nt, nt, dt, &tn, &td);
   const int64_t d0 = td * S::BM, n0 = tn * S::BN;
@@ -250,9 +250,9 @@ __global__ __launch_bounds__(S::NT) void head_dx_kernel(HeadDx p, int64_t dt, in
 }
 
 template <class S, bool F32>
-__global__ __launch_bounds__(S::NT) void head_dw_kernel(HeadDw p, int64_t dt, int64_t vt) {
-  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
-  const int64_t t = xcd_tile(blockIdx.x, gridDim.x), split = t / (dt * vt);
+__device__ __forceinline__ void dw_tile(const HeadDw& p, int64_t at, char* lds) {
+  const int64_t dt = p.dt, vt = p.vt;
+  const int64_t t = xcd_tile(at, dt * vt * p.splits), split = t / (dt * vt);
   int64_t td, tv;
   panel_tile(t - split * dt * vt, vt, dt, &tv, &td);
   const int64_t d0 = td * S::BM, v0 = tv * S::BN;
@@ -314,6 +314,20 @@ __global__ __launch_bounds__(S::NT) void head_dw_kernel(HeadDw p, int64_t dt, in
   }
 }
 
+// Both products of a piece of g in one launch: neither fills the chip in whole rounds by
+// itself, and dx's shorter tiles take the places that dw's leave free (16384 x 768 x
+// 25128 words: dw alone is 1.16 rounds).
+template <class SX, class SW, bool F32>
+__global__ __launch_bounds__(SX::NT) void head_products_kernel(HeadDx x, HeadDw w, int64_t dw_tiles) {
+  static_assert(SX::NT == SW::NT, "one workgroup size");
+  __shared__ __attribute__((aligned(16))) char lds[SX::LDS > SW::LDS ? SX::LDS : SW::LDS];
+  const int64_t at = blockIdx.x;
+  if (at < dw_tiles)
+    dw_tile<SW, F32>(w, at, lds);
+  else
+    dx_tile<SX, F32>(x, at - dw_tiles, lds);
+}
+
 int64_t tiles(int64_t n, int64_t by) { return (n + by - 1) / by; }
 
 hipError_t check_grid(int64_t grid) { return grid > 0x7fffffffLL ? hipErrorInvalidConfiguration : hipSuccess; }
@@ -356,25 +370,16 @@ hipError_t grad(const HeadLogits& a, bool second, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <class S>
-hipError_t dx(const HeadDx& a, hipStream_t st) {
-  const int64_t dt = tiles(a.d, S::BM), nt = tiles(a.np, S::BN), n = dt * nt * a.splits;
+template <class SX, class SW>
+hipError_t products(HeadDx x, HeadDw w, hipStream_t st) {
+  x.dt = tiles(x.d, SX::BM), x.nt = tiles(x.np, SX::BN);
+  w.dt = tiles(w.d, SW::BM), w.vt = tiles(w.cols, SW::BN);
+  const int64_t dw_tiles = w.dt * w.vt * w.splits, n = dw_tiles + x.dt * x.nt * x.splits;
   if (hipError_t e = check_grid(n)) return e;
-  if (a.f32)
-    hipLaunchKernelGGL((head_dx_kernel<S, true>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, nt);
+  if (x.f32)
+    hipLaunchKernelGGL((head_products_kernel<SX, SW, true>), dim3(static_cast<unsigned>(n)), dim3(SX::NT), 0, st, x, w, dw_tiles);
   else
-    hipLaunchKernelGGL((head_dx_kernel<S, false>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, nt);
-  return hipGetLastError();
-}
-
-template <class S>
-hipError_t dw(const HeadDw& a, hipStream_t st) {
-  const int64_t dt = tiles(a.d, S::BM), vt = tiles(a.cols, S::BN), n = dt * vt * a.splits;
-  if (hipError_t e = check_grid(n)) return e;
-  if (a.f32)
-    hipLaunchKernelGGL((head_dw_kernel<S, true>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, vt);
-  else
-    hipLaunchKernelGGL((head_dw_kernel<S, false>), dim3(static_cast<unsigned>(n)), dim3(S::NT), 0, st, a, dt, vt);
+    hipLaunchKernelGGL((head_products_kernel<SX, SW, false>), dim3(static_cast<unsigned>(n)), dim3(SX::NT), 0, st, x, w, dw_tiles);
   return hipGetLastError();
 }
 
@@ -389,11 +394,10 @@ hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, bool second, hipSt
 hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, bool second, hipStream_t st) {
   return s == HEAD_256 ? grad<Shape256>(a, second, st) : s == HEAD_128 ? grad<Shape128>(a, second, st) : grad<Shape32>(a, second, st);
 }
-hipError_t head_launch_dx(const HeadDx& a, HeadShape s, hipStream_t st) {
-  return s == HEAD_256 ? dx<Shape256>(a, st) : s == HEAD_128 ? dx<Shape128>(a, st) : dx<Shape32>(a, st);
-}
-hipError_t head_launch_dw(const HeadDw& a, HeadShape s, hipStream_t st) {
-  return s == HEAD_256 ? dw<Shape256>(a, st) : dw<Shape128>(a, st);
+hipError_t head_launch_products(const HeadDx& x, const HeadDw& w, HeadShape s, hipStream_t st) {
+  return s == HEAD_256   ? products<Shape256, Shape256>(x, w, st)
+         : s == HEAD_128 ? products<Shape128, Shape128>(x, w, st)
+                         : products<Shape32, Shape128>(x, w, st);
 }
 
 }  // namespace monarch

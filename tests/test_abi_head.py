@@ -55,15 +55,15 @@ def test_head_workspace():
             assert M.monarch_head_workspace_bytes(k, *bad) == 0
     assert M.monarch_head_workspace_bytes(3, 4, 64, 100, 8, B.F32) == 0
     assert M.monarch_head_stats_bytes(5, 8) == 5 * 12 * 4 and M.monarch_head_stats_bytes(-1, 8) == 0
-    # the gradient of the logits is held a piece at a time: at most 1 GiB of it and as much of each split sum, copies of
+    # the gradient of the logits is held a piece at a time: at most 2 GiB of it and 1 GiB of each split sum, copies of
     # x, and a tile's sums of every 128 words at least
     for dt, es in ((B.BF16, 2), (B.F32, 4)):
         for rows, d, vocab in ((16384, 768, 50257), (4096, 4096, 131072), (65536, 1024, 131072), (8, 768, 50257), (1000, 625, 10000)):
             parts = 3 if es == 4 else 1
-            np_, dp = (rows + 255) // 256 * 256, (d + 31) // 32 * 32
-            copies = parts * (np_ + (vocab if es == 4 or d % 8 else 0)) * dp * 2
+            np_, dp = (rows + 255) // 256 * 256, (d + 63) // 64 * 64
+            copies = parts * (np_ + (vocab + 64 if es == 4 or d % 8 else 0)) * dp * 2
             sums = 3 * 4 * np_ * ((vocab + 127) // 128)
-            assert M.monarch_head_workspace_bytes(B.HEAD_STEP, rows, d, vocab, 0, dt) <= copies + sums + (3 << 30) + np_ * dp * 4 + (np_ + rows) * 64
+            assert M.monarch_head_workspace_bytes(B.HEAD_STEP, rows, d, vocab, 0, dt) <= copies + sums + (4 << 30) + np_ * dp * 4 + (np_ + rows) * 64
 
 
 def test_head_no_rows():
