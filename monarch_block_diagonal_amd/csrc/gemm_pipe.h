@@ -27,8 +27,8 @@
 // t ^ g(k), g = (k & 3) + 4 ((k >> 3) & 3), so that the 16 rows of such a read fall on all banks.
 //
 // fp32 operands come as three bf16 planes (a = a0 + a1 + a2, exact: 8 bits of the
-// mantissa each) and their product as six products of planes, least first; what is
-// left out is at most 2^-23 of |a||b|. Six bf16 products take 6/16 of one fp32 MFMA product's time.
+// mantissa each) and their product as six products of planes; what is left out is at
+// most 2^-23 of |a||b|. Six bf16 products take 6/16 of one fp32 MFMA product's time.
 #pragma once
 
 #include <type_traits>
@@ -71,56 +71,61 @@ struct PipeTile {
   static constexpr int CHUNKS = ROWS / 8;                       // KM: 16-byte pieces of one k
   static constexpr int MASK = ROWS / 16 < 16 ? ROWS / 16 - 1 : 15;
 
-  const uint16_t* ptr[PER];   // what this lane loads next
-  int64_t adv;                // from one K tile to the next
+  const uint16_t* at;         // the tile, the same for the wave's lanes
+  uint32_t off[PER];          // this lane's pieces in it, in bytes
+  int64_t adv;                // elements from one K tile to the next
 
   __device__ __forceinline__ static int load_of(int i, int wave) { return TOTAL >= NW ? wave * PER + i : wave % TOTAL; }
 
   __device__ __forceinline__ void init(const PipeOperand& o, int64_t r0, int64_t k0, int wave, int lane) {
     adv = KM ? kPipeK * o.ld : kPipeK;
+    at = KM ? o.p + k0 * o.ld + r0 : o.p + r0 * o.ld + k0;
+    // rows beyond the valid ones are taken from a valid place; r0 is valid
+    const int64_t room = o.rows - r0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int j = load_of(i, wave);
       if constexpr (KM) {
         const int k = j * (1024 / (ROWS * 2)) + lane / CHUNKS, pos = lane % CHUNKS;
         const int c = ((((pos >> 1) ^ (pipe_swizzle(k) & MASK)) << 1) | (pos & 1)) * 8;
-        ptr[i] = o.p + (k0 + k) * o.ld + (r0 + c < o.rows ? r0 + c : 0);
+        off[i] = static_cast<uint32_t>(k * o.ld + (c < room ? c : room - 8)) * 2;
       } else {
         const int r = j * 8 + (lane >> 3);
         const int q = (lane & 7) ^ pipe_turn(r);
-        const int64_t row = r0 + r < o.rows ? r0 + r : o.rows - 1;
-        ptr[i] = o.p + row * o.ld + k0 + q * 8;
+        off[i] = static_cast<uint32_t>((r < room ? r : room - 1) * o.ld + q * 8) * 2;
       }
     }
   }
 
-  __device__ __forceinline__ static void load(const uint16_t* s, char* at) {
+  __device__ __forceinline__ static void load(const void* s, char* to) {
     __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)(s),
-                                     (__attribute__((address_space(3))) void*)(at), 16, 0, 0);
+                                     (__attribute__((address_space(3))) void*)(to), 16, 0, 0);
   }
-  // Loads the next tile, whose k are all valid.
-  __device__ __forceinline__ void issue(char* stage, int wave) {
+  // Loads the tile `by` elements behind this one, whose k are all valid.
+  __device__ __forceinline__ void issue(char* to, int wave, int64_t by) const {
+    const char* from = reinterpret_cast<const char*>(at + by);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      load(ptr[i], stage + load_of(i, wave) * 1024);
-      ptr[i] += adv;
+      // an address is a scalar base and 32 bits of a lane's own: sums of both are not kept in registers
+      uint32_t o = off[i];
+      asm volatile("" : "+v"(o));
+      load(from + o, to + load_of(i, wave) * 1024);
     }
   }
-  // Loads the next tile, of which only `valid` > 0 k are.
-  __device__ __forceinline__ void issue_cut(const PipeOperand& o, const uint16_t* zeros, char* stage, int wave, int lane,
-                                            int64_t valid) {
+  // Loads this tile, of which only `valid` > 0 k are.
+  __device__ __forceinline__ void issue_cut(const PipeOperand& o, const uint16_t* zeros, char* to, int wave, int lane,
+                                            int64_t valid) const {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const uint16_t* s = ptr[i];
+      const char* s = reinterpret_cast<const char*>(at) + off[i];
       const int j = load_of(i, wave);
       if constexpr (KM) {
         const int64_t over = j * (1024 / (ROWS * 2)) + lane / CHUNKS - (valid - 1);
-        if (over > 0) s -= over * o.ld;
+        if (over > 0) s -= over * o.ld * 2;
       } else {
-        if (((lane & 7) ^ pipe_turn(j * 8 + (lane >> 3))) * 8 >= valid) s = zeros;
+        if (((lane & 7) ^ pipe_turn(j * 8 + (lane >> 3))) * 8 >= valid) s = reinterpret_cast<const char*>(zeros);
       }
-      load(s, stage + load_of(i, wave) * 1024);
-      ptr[i] += adv;
+      load(s, to + load_of(i, wave) * 1024);
     }
   }
 
@@ -185,10 +190,10 @@ struct PipeShape {
 };
 
 // acc[mi][ni], lane l: rows m0 + (wm*FM + mi)*16 + 4*(l/16) + v, column n0 + (wn*FN + ni)*16 + l%16.
-// Sums k in [kb, ke) (kb a multiple of 64); F32: over six products of planes. Only a's k may end
-// inside the last tile, and only without F32. Ends with a barrier: `lds` is free.
-template <class S, bool AKM, bool BKM, bool F32>
-__device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, int64_t n0, int64_t kb, int64_t ke,
+// Sums k in [kb, ke) (kb a multiple of 64). Only a's k may end inside the last tile. Ends with a
+// barrier: `lds` is free.
+template <class S, bool AKM, bool BKM>
+__device__ __forceinline__ void pipe_product_bf16(const PipeProduct& p, int64_t m0, int64_t n0, int64_t kb, int64_t ke,
                                              char* lds, f32x4 (&acc)[S::FM][S::FN]) {
   using TA = PipeTile<AKM, S::BM, S::NW>;
   using TB = PipeTile<BKM, S::BN, S::NW>;
@@ -199,52 +204,31 @@ __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, i
   for (int mi = 0; mi < FM; ++mi)
 #pragma unroll
     for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int ktiles = ke > kb ? static_cast<int>((ke - kb + kPipeK - 1) / kPipeK) : 0;
-  const int ntiles = ktiles * (F32 ? 6 : 1);
+  const int ntiles = ke > kb ? static_cast<int>((ke - kb + kPipeK - 1) / kPipeK) : 0;
   if (ntiles == 0) return;
-  PipeOperand oa = p.a, ob = p.b;
-  if constexpr (F32) oa.p += 2 * oa.plane;
   TA a;
-  a.init(oa, m0, kb, wave, lane);
+  a.init(p.a, m0, kb, wave, lane);
   TB b;
-  b.init(ob, n0, kb, wave, lane);
+  b.init(p.b, n0, kb, wave, lane);
   static_assert((FM & (FM - 1)) == 0 && (FN & (FN - 1)) == 0, "fragments of a wave");
   const int ab = TA::base(lane, wm * FM), bb = TB::base(lane, wn * FN);
   // of the last tile's k of a: all, or those before kvalid
-  const int64_t last_valid = oa.kvalid - kb - static_cast<int64_t>(ktiles - 1) * kPipeK;
+  const int64_t last_valid = p.a.kvalid - kb - static_cast<int64_t>(ntiles - 1) * kPipeK;
 
-  // F32: planes of a and b in the order of their products: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
-  int ik = 0, iseg = 0;
-  auto next_tile = [&]() {
-    if constexpr (F32) {
-      if (++ik == ktiles) {
-        ik = 0;
-        constexpr uint32_t seqa = 0x001102, seqb = 0x010120;
-        const int na = (seqa >> (4 * iseg + 4)) & 3, pa = (seqa >> (4 * iseg)) & 3;
-        const int nb = (seqb >> (4 * iseg + 4)) & 3, pb = (seqb >> (4 * iseg)) & 3;
-        ++iseg;
-        const int64_t ja = (na - pa) * oa.plane - ktiles * a.adv, jb = (nb - pb) * ob.plane - ktiles * b.adv;
-#pragma unroll
-        for (int i = 0; i < TA::PER; ++i) a.ptr[i] += ja;
-#pragma unroll
-        for (int i = 0; i < TB::PER; ++i) b.ptr[i] += jb;
-      }
-    }
-  };
   auto issue = [&](int st) {
     char* at = lds + st * S::STAGE;
-    a.issue(at, wave);
-    b.issue(at + TA::BYTES, wave);
-    next_tile();
+    a.issue(at, wave, 0);
+    b.issue(at + TA::BYTES, wave, 0);
+    a.at += a.adv, b.at += b.adv;
   };
   auto issue_any = [&](int st, int tile) {
     char* at = lds + st * S::STAGE;
-    if (!F32 && tile == ntiles - 1 && last_valid < kPipeK)
-      a.issue_cut(oa, p.zeros, at, wave, lane, last_valid);
+    if (tile == ntiles - 1 && last_valid < kPipeK)
+      a.issue_cut(p.a, p.zeros, at, wave, lane, last_valid);
     else
-      a.issue(at, wave);
-    b.issue(at + TA::BYTES, wave);
-    next_tile();
+      a.issue(at, wave, 0);
+    b.issue(at + TA::BYTES, wave, 0);
+    a.at += a.adv, b.at += b.adv;
   };
   bf16x8 fa[2][FM], fb[2][FN];
   auto read = [&](auto half, int st) {
@@ -269,6 +253,12 @@ __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, i
   };
   using First = std::integral_constant<int, 0>;
   using Second = std::integral_constant<int, 1>;
+  // Reads and matrix instructions mix freely within a tile (apart, they take twice the time), but the next
+  // tile's reads stay behind: mixed in, they cost 4 to 6% (4096 x 4096 x 131072: 15.7 -> 15.3 ms).
+  auto multiply_second = [&]() {
+    multiply(Second{});
+    __builtin_amdgcn_sched_barrier(0);
+  };
   auto meet = [&]() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -293,7 +283,7 @@ __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, i
     meet();
     issue(ST);
     read(First{}, ST + 1 == NST ? 0 : ST + 1);
-    multiply(Second{});
+    multiply_second();
   };
   auto last_tile = [&](auto stage, int t) {
     constexpr int ST = decltype(stage)::value;
@@ -306,7 +296,7 @@ __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, i
       if (t + NST < ntiles) issue_any(ST, t + NST);
       read(First{}, ST + 1 == NST ? 0 : ST + 1);
     }
-    multiply(Second{});
+    multiply_second();
   };
   int t = 0;
 #pragma unroll 1
@@ -314,6 +304,153 @@ __device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, i
 #pragma unroll 1
   for (; t < ntiles; t += NST) pipe_each<NST>([&](auto i) { last_tile(i, t + decltype(i)::value); });
   __syncthreads();
+}
+
+// The same for fp32 operands in three bf16 planes. A k tile's six products follow each other so that
+// each has one operand of the one before:
+//   (a2, b0) (a1, b0) (a1, b1) (a0, b1) (a0, b2) (a0, b0)
+// and 7 tiles come through LDS for them instead of 12, the operand that stays in registers.
+// LDS holds two tiles of either operand. A tile is read into registers by the product
+// that takes it up, and the place is given to the operand's tile after next at once:
+//   product           0        1      2       3      4      5
+//   takes up        a2 b0     a1     b1      a0     b2     b0
+//   then loads      a0 b2     a2'    b0      a1'    b0'    b1'     (': of the next k tile)
+// No k is cut: the planes are copies that end in zeros.
+template <class S, bool AKM, bool BKM>
+__device__ __forceinline__ void pipe_product_f32(const PipeProduct& p, int64_t m0, int64_t n0, int64_t kb, int64_t ke,
+                                                 char* lds, f32x4 (&acc)[S::FM][S::FN]) {
+  using TA = PipeTile<AKM, S::BM, S::NW>;
+  using TB = PipeTile<BKM, S::BN, S::NW>;
+  constexpr int FM = S::FM, FN = S::FN, LA = TA::PER, LB = TB::PER;
+  static_assert(2 * (TA::BYTES + TB::BYTES) <= S::LDS, "two tiles of each operand");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+#pragma unroll
+  for (int mi = 0; mi < FM; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int ktiles = ke > kb ? static_cast<int>((ke - kb + kPipeK - 1) / kPipeK) : 0;
+  if (ktiles == 0) return;
+  TA a;
+  a.init(p.a, m0, kb, wave, lane);
+  TB b;
+  b.init(p.b, n0, kb, wave, lane);
+  const int ab = TA::base(lane, wm * FM), bb = TB::base(lane, wn * FN);
+  char* const lds_b = lds + 2 * TA::BYTES;
+  bf16x8 fa[2][FM], fb[2][FN];
+  auto read_a = [&](auto half, int place) {
+    constexpr int X = decltype(half)::value;
+    int r = ab;
+    asm volatile("" : "+v"(r));
+#pragma unroll
+    for (int mi = 0; mi < FM; ++mi) fa[X][mi] = TA::read(lds + place * TA::BYTES, r, mi, X);
+  };
+  auto read_b = [&](auto half, int place) {
+    constexpr int X = decltype(half)::value;
+    int r = bb;
+    asm volatile("" : "+v"(r));
+#pragma unroll
+    for (int ni = 0; ni < FN; ++ni) fb[X][ni] = TB::read(lds_b + place * TB::BYTES, r, ni, X);
+  };
+  auto multiply = [&](auto half) {
+    constexpr int X = decltype(half)::value;
+#pragma unroll
+    for (int mi = 0; mi < FM; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < FN; ++ni)
+        acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[X][mi], fb[X][ni], acc[mi][ni], 0, 0, 0);
+  };
+  using First = std::integral_constant<int, 0>;
+  using Second = std::integral_constant<int, 1>;
+  auto multiply_second = [&]() {
+    multiply(Second{});
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // places: of a's tiles in the order a2 a1 a0 every second, of b's in the order b0 b1 b2 b0
+  int64_t ka = 0, kbo = 0;   // offsets of this k tile in a plane
+  int pa = 0;                // place of this k tile's a2 (three tiles a k tile: it alternates)
+  auto load_a = [&](int plane, int64_t k, int place) { a.issue(lds + place * TA::BYTES, wave, plane * p.a.plane + k); };
+  auto load_b = [&](int plane, int64_t k, int place) { b.issue(lds_b + place * TB::BYTES, wave, plane * p.b.plane + k); };
+  // waits until at most the last N loads of this wave are in flight, and for the other waves
+  auto landed = [&](auto n) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(pipe_wait(decltype(n)::value));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  using A = std::integral_constant<int, LA>;
+  using B = std::integral_constant<int, LB>;
+  using AB = std::integral_constant<int, LA + LB>;
+  using None = std::integral_constant<int, 0>;
+  load_a(2, 0, 0);
+  load_b(0, 0, 0);
+  load_a(1, 0, 1);
+  load_b(1, 0, 1);
+  landed(AB{});
+  read_a(First{}, 0);
+  read_b(First{}, 0);
+#pragma unroll 1
+  for (int k = 0; k < ktiles; ++k) {
+    // behind the last k tile it is loaded again and not read
+    const bool more = k + 1 < ktiles;
+    const int64_t ka1 = more ? ka + a.adv : ka, kb1 = more ? kbo + b.adv : kbo;
+    // 0: a2 b0
+    read_a(Second{}, pa);
+    read_b(Second{}, 0);
+    multiply(First{});
+    landed(B{});           // in flight: b1
+    load_a(0, ka, pa);
+    load_b(2, kbo, 0);
+    read_a(First{}, pa ^ 1);
+    multiply_second();
+    // 1: a1 b0
+    read_a(Second{}, pa ^ 1);
+    multiply(First{});
+    landed(AB{});          // a0, b2
+    load_a(2, ka1, pa ^ 1);
+    read_b(First{}, 1);
+    multiply_second();
+    // 2: a1 b1
+    read_b(Second{}, 1);
+    multiply(First{});
+    landed(AB{});          // b2, a2'
+    load_b(0, kbo, 1);
+    read_a(First{}, pa);
+    multiply_second();
+    // 3: a0 b1
+    read_a(Second{}, pa);
+    multiply(First{});
+    landed(AB{});          // a2', b0
+    load_a(1, ka1, pa);
+    read_b(First{}, 0);
+    multiply_second();
+    // 4: a0 b2
+    read_b(Second{}, 0);
+    multiply(First{});
+    landed(A{});           // a1'
+    load_b(0, kb1, 0);
+    read_b(First{}, 1);
+    multiply_second();
+    // 5: a0 b0
+    read_b(Second{}, 1);
+    multiply(First{});
+    landed(None{});
+    load_b(1, kb1, 1);
+    read_a(First{}, pa ^ 1);
+    read_b(First{}, 0);
+    multiply_second();
+    ka = ka1, kbo = kb1, pa ^= 1;
+  }
+  landed(None{});   // what was loaded last has to be in LDS before that is used otherwise
+}
+
+template <class S, bool AKM, bool BKM, bool F32>
+__device__ __forceinline__ void pipe_product(const PipeProduct& p, int64_t m0, int64_t n0, int64_t kb, int64_t ke,
+                                             char* lds, f32x4 (&acc)[S::FM][S::FN]) {
+  if constexpr (F32)
+    pipe_product_f32<S, AKM, BKM>(p, m0, n0, kb, ke, lds, acc);
+  else
+    pipe_product_bf16<S, AKM, BKM>(p, m0, n0, kb, ke, lds, acc);
 }
 
 }  // namespace monarch

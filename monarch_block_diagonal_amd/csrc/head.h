@@ -17,6 +17,13 @@ struct HeadRow {
   float m, a, b, off;   // g = a 2^((z - m) ct) + b 2^((z - m) log2 e) - off [v = label]
 };
 
+// The labels' softmax beside the teacher's at T.
+enum HeadSecond {
+  HEAD_ONE = 0,     // none, or T = 1: one softmax
+  HEAD_OWN = 1,     // exponentials of its own
+  HEAD_SQUARE = 2   // T = 2: e^z is the square of e^(z/2)
+};
+
 enum HeadShape { HEAD_256 = 0, HEAD_128 = 1, HEAD_32 = 2 };
 
 struct HeadLogits {
@@ -62,9 +69,8 @@ struct HeadDw {
 
 int64_t head_tile_words(HeadShape s);    // words of a logits tile
 int64_t head_tile_rows(HeadShape s);     // rows of a logits and a dx tile
-// second: the labels' softmax has exponentials of its own
-hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, bool second, hipStream_t st);
-hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, bool second, hipStream_t st);
+hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st);
+hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st);
 // dx and dw of a piece (HEAD_32: dx's tiles, dw's are HEAD_128's)
 hipError_t head_launch_products(const HeadDx& x, const HeadDw& w, HeadShape s, hipStream_t st);
 

@@ -58,7 +58,8 @@ struct Call {
   int64_t rows, ldx, d, vocab;
   int top;
   float temperature, mix;     // temperature 1 where there is no first term
-  bool bf16, told, taught, second;
+  bool bf16, told, taught;
+  HeadSecond second;
 };
 
 __device__ __forceinline__ bool entry_ok(int64_t id, float t, int64_t vocab) {
@@ -344,7 +345,7 @@ __global__ __launch_bounds__(256) void head_factors_kernel(Call c, Rows r, HeadR
     a = r.has[k] ? c.mix * c.temperature * w : 0.f;
     o.m = st[0];
     o.off = r.label[k] >= 0 ? (1.0f - c.mix) * w : 0.f;
-    if (c.second) {
+    if (c.second != HEAD_ONE) {
       o.a = a / st[1], o.b = o.off / st[2];
     } else {
       // one softmax: at T = 1, or with one of the two terms alone
@@ -391,7 +392,7 @@ __global__ __launch_bounds__(64) void head_taught_kernel(Call c, Rows r, const H
       }
     if (!first) continue;
     const float z = c.stats[c.rows * 4 + i * c.top + j] - h.m;
-    float v = h.a * exp2_of(z * ct) + (c.second ? h.b * exp2_of(z * kLog2e) : 0.f) - taught[k] * p;
+    float v = h.a * exp2_of(z * ct) + (c.second != HEAD_ONE ? h.b * exp2_of(z * kLog2e) : 0.f) - taught[k] * p;
     if (id == label) v -= h.off;
     uint16_t* o = g + k * vp + (id - v0);
     for (int q = 0; q < planes; ++q) o[q * plane] = next_part(v);
@@ -442,6 +443,7 @@ __global__ __launch_bounds__(256) void head_dw_out_kernel(const float* __restric
 enum What { FWD = 0, BWD = 1, STEP = 2 };
 
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+int64_t tiles_of(int64_t v, int64_t tile) { return (v + tile - 1) / tile; }
 
 struct HeadPlan {
   int64_t d, dp, np, planes;
@@ -474,9 +476,11 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
   HeadPlan p = {};
   p.d = d, p.dp = up(d, kPipeK), p.np = up(rows, kHeadRows), p.planes = bf16 ? 1 : 3;
   p.copy_w = !bf16 || d % 8 != 0;
-  // the widest tile that leaves work for every CU
-  const int64_t t256 = (up(vocab, 256) / 256) * (up(rows, 256) / 256);
-  p.shape = rows <= 32 ? HEAD_32 : (rows <= 128 || t256 < 384) ? HEAD_128 : HEAD_256;
+  // Rounds of 256 x 256 tiles (one a CU) against rounds of 128 x 128 tiles (two a CU), which take 0.6 of the
+  // time: measured, 4096 x 768 x 50257 bf16 1368 us with the first and 1456 with the second (13 and 25
+  // rounds), 600 x 2000 x 10000 204 and 170 (1 and 1).
+  auto rounds = [&](int64_t tile, int64_t places) { return up(tiles_of(vocab, tile) * tiles_of(rows, tile), places) / places; };
+  p.shape = rows <= 32 ? HEAD_32 : rounds(256, 256) <= 0.6 * rounds(128, 512) ? HEAD_256 : HEAD_128;
   const int64_t tv = head_tile_words(p.shape);
   p.tiles = (vocab + tv - 1) / tv;
   size_t at = 0;
@@ -500,20 +504,24 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
     p.vp = up((vocab + p.pieces - 1) / p.pieces, kHeadRows);
     p.pieces = (vocab + p.vp - 1) / p.vp;
     // dx: rows x features, summed over the piece's words; dw: words x features, summed over rows
-    const bool wide = rows > 128 && d > 128 && (up(d, 256) / 256) * (up(p.vp, 256) / 256) >= 96;
+    // 256 x 256 tiles where there is enough to do: 4096 x 768 x 50257 bf16 1368 us, 1494 with 128 x 128
+    // (fp32 5370, 5999); 1000 x 625 x 10000 fp32 365 us, with 128 x 128 330
+    const bool wide = rows > 128 && d > 128 && static_cast<double>(rows) * vocab * d >= 2e10;
     p.products = rows <= 32 ? HEAD_32 : wide ? HEAD_256 : HEAD_128;
     const int64_t xm = head_tile_words(p.products), xn = head_tile_rows(p.products);
     const int64_t wm = wide ? 256 : 128;
     const int64_t slots = wide ? 256 : 512;
-    const int64_t dx_tiles = (up(d, xm) / xm) * (up(rows, xn) / xn), dw_tiles = (up(d, wm) / wm) * (up(p.vp, wm) / wm);
+    const int64_t dx_tiles = tiles_of(d, xm) * tiles_of(rows, xn), dw_tiles = tiles_of(d, wm) * tiles_of(p.vp, wm);
     // dw is split only where its tiles do not fill half the chip
     int64_t ws = dw_tiles >= slots / 2 ? 1 : slots / dw_tiles;
     if (ws > (rows + 511) / 512) ws = (rows + 511) / 512;
     while (ws > 1 && ws * p.vp * p.dp * 4 > (int64_t(1) << 30)) --ws;
     p.dw_splits = static_cast<int>(ws);
-    // dx's splits fill the places that dw leaves free: the split whose tiles are done first, by what was
-    // measured of a tile (13 ns a k of a 256 x 256 tile, 7 of a 128 x 128 one, where two share a CU;
-    // 300 k for a tile's start and end) and of the splits' sums (written and read at 2.5 TB/s)
+    // dx's splits fill the places that dw leaves free: the split whose tiles are done first, by a tile's
+    // time at the matrix instructions' rate (13 ns a k of a 256 x 256 tile, 7 of a 128 x 128 one, where two
+    // share a CU; fp32 six times that) with 300 k for its start and end, and the splits' sums, written and
+    // read at 2.5 TB/s (with the times that tiles take in practice, up to twice as long, splits
+    // come out finer and the step slower: 1024 x 768 x 50257 bf16 400 -> 440 us)
     const double ns = (wide ? 13.0 : 7.0) * (bf16 ? 1 : 6), ends = 300.0 / (bf16 ? 1 : 6);
     double best = 0.0;
     int64_t xs = 0;
@@ -679,7 +687,7 @@ int call(Call c, int what, const void* stats_in, int64_t top, float temperature,
   c.told = c.labels && mix < 1.0f;
   c.taught = top > 0 && mix > 0.0f;
   c.temperature = c.taught ? temperature : 1.0f;
-  c.second = c.told && c.taught && temperature != 1.0f;
+  c.second = !c.told || !c.taught || temperature == 1.0f ? HEAD_ONE : temperature == 2.0f ? HEAD_SQUARE : HEAD_OWN;
   if (c.rows > 0) {
     if (!c.x || !c.w || (top > 0 && (!c.teacher || !c.ids))) return MONARCH_ERR_NULL;
     if (what != BWD && !c.loss) return MONARCH_ERR_NULL;

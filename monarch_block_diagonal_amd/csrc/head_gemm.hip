@@ -20,10 +20,7 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLowest = -3.402823466e38f;
 
-#ifndef S256
-#define S256 2, 4, 8, 4, 2
-#endif
-using Shape256 = PipeShape<S256>;
+using Shape256 = PipeShape<2, 4, 8, 4, 2>;
 using Shape128 = PipeShape<2, 2, 4, 4, 2>;
 using Shape32 = PipeShape<4, 1, 2, 2, 4>;
 
@@ -58,7 +55,7 @@ __device__ __forceinline__ void panel_tile(int64_t t, int64_t outer, int64_t inn
   *i = panel * 8 + r % wide;
 }
 
-template <class S, bool SECOND, bool F32>
+template <class S, HeadSecond SECOND, bool F32>
 __global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t vt, int64_t nt) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
   int64_t tv, tn;
@@ -94,15 +91,17 @@ __global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t 
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const float z = acc[mi][ni][v] - m;
-        st += exp2_of(z * p.ct);
-        if constexpr (SECOND) s1 += exp2_of(z * kLog2e);
+        const float e = exp2_of(z * p.ct);
+        st += e;
+        if constexpr (SECOND == HEAD_OWN) s1 += exp2_of(z * kLog2e);
+        if constexpr (SECOND == HEAD_SQUARE) s1 = fmaf(e, e, s1);
       }
     st = over_groups<false>(st);
-    if constexpr (SECOND) s1 = over_groups<false>(s1);
+    if constexpr (SECOND != HEAD_ONE) s1 = over_groups<false>(s1);
     if (lh == 0) {
       part[(wm * 3 + 0) * S::BN + col] = m;
       part[(wm * 3 + 1) * S::BN + col] = st;
-      part[(wm * 3 + 2) * S::BN + col] = SECOND ? s1 : 0.f;
+      part[(wm * 3 + 2) * S::BN + col] = SECOND != HEAD_ONE ? s1 : 0.f;
     }
     // the lane that holds the label's logit hands it out
     const int64_t at = static_cast<int64_t>(p.label[n0 + col]) - vw;
@@ -125,12 +124,12 @@ __global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t 
     for (int w = 0; w < S::WM; ++w) {
       const float by = part[w * 3 * S::BN + c] - m;
       st += part[(w * 3 + 1) * S::BN + c] * exp2_of(by * p.ct);
-      if constexpr (SECOND) s1 += part[(w * 3 + 2) * S::BN + c] * exp2_of(by * kLog2e);
+      if constexpr (SECOND != HEAD_ONE) s1 += part[(w * 3 + 2) * S::BN + c] * exp2_of(by * kLog2e);
     }
     float* o = p.part + (tv * 3) * p.np + n0 + c;
     o[0] = m;
     o[p.np] = st;
-    o[2 * p.np] = SECOND ? s1 : st;
+    o[2 * p.np] = SECOND != HEAD_ONE ? s1 : st;
   }
 }
 
@@ -153,7 +152,7 @@ __device__ __forceinline__ int staged(int r, int e) {
   return r * ROW * 2 + ((((e >> 3) ^ (r & M)) << 4) | ((e & 4) << 1));
 }
 
-template <class S, bool SECOND, bool F32>
+template <class S, HeadSecond SECOND, bool F32>
 __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t vt, int64_t nt) {
   static_assert(S::BM * S::BN * 2 <= S::LDS, "a tile of g is staged in LDS");
   static_assert(S::BN % kPipeK == 0 || 2 * S::BN == kPipeK, "with the 0s, whole K tiles of rows");
@@ -182,8 +181,10 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const float z = acc[mi][ni][v] - r.m;
-        g[v] = r.a * exp2_of(z * p.ct);
-        if constexpr (SECOND) g[v] = fmaf(r.b, exp2_of(z * kLog2e), g[v]);
+        const float e = exp2_of(z * p.ct);
+        g[v] = r.a * e;
+        if constexpr (SECOND == HEAD_OWN) g[v] = fmaf(r.b, exp2_of(z * kLog2e), g[v]);
+        if constexpr (SECOND == HEAD_SQUARE) g[v] = fmaf(r.b * e, e, g[v]);
       }
       if (any) {
 #pragma unroll
@@ -332,42 +333,30 @@ int64_t tiles(int64_t n, int64_t by) { return (n + by - 1) / by; }
 
 hipError_t check_grid(int64_t grid) { return grid > 0x7fffffffLL ? hipErrorInvalidConfiguration : hipSuccess; }
 
-template <class S>
-hipError_t sums(const HeadLogits& a, bool second, hipStream_t st) {
+template <class S, bool GRAD, HeadSecond SECOND, bool F32>
+hipError_t logits(const HeadLogits& a, hipStream_t st) {
   const int64_t vt = tiles(a.v1 - a.v0, S::BM), nt = tiles(a.np, S::BN);
   if (hipError_t e = check_grid(vt * nt)) return e;
   const dim3 g(static_cast<unsigned>(vt * nt));
-  if (a.f32) {
-    if (second)
-      hipLaunchKernelGGL((head_sums_kernel<S, true, true>), g, dim3(S::NT), 0, st, a, vt, nt);
-    else
-      hipLaunchKernelGGL((head_sums_kernel<S, false, true>), g, dim3(S::NT), 0, st, a, vt, nt);
-  } else {
-    if (second)
-      hipLaunchKernelGGL((head_sums_kernel<S, true, false>), g, dim3(S::NT), 0, st, a, vt, nt);
-    else
-      hipLaunchKernelGGL((head_sums_kernel<S, false, false>), g, dim3(S::NT), 0, st, a, vt, nt);
-  }
+  if constexpr (GRAD)
+    hipLaunchKernelGGL((head_grad_kernel<S, SECOND, F32>), g, dim3(S::NT), 0, st, a, vt, nt);
+  else
+    hipLaunchKernelGGL((head_sums_kernel<S, SECOND, F32>), g, dim3(S::NT), 0, st, a, vt, nt);
   return hipGetLastError();
 }
 
-template <class S>
-hipError_t grad(const HeadLogits& a, bool second, hipStream_t st) {
-  const int64_t vt = tiles(a.v1 - a.v0, S::BM), nt = tiles(a.np, S::BN);
-  if (hipError_t e = check_grid(vt * nt)) return e;
-  const dim3 g(static_cast<unsigned>(vt * nt));
-  if (a.f32) {
-    if (second)
-      hipLaunchKernelGGL((head_grad_kernel<S, true, true>), g, dim3(S::NT), 0, st, a, vt, nt);
-    else
-      hipLaunchKernelGGL((head_grad_kernel<S, false, true>), g, dim3(S::NT), 0, st, a, vt, nt);
-  } else {
-    if (second)
-      hipLaunchKernelGGL((head_grad_kernel<S, true, false>), g, dim3(S::NT), 0, st, a, vt, nt);
-    else
-      hipLaunchKernelGGL((head_grad_kernel<S, false, false>), g, dim3(S::NT), 0, st, a, vt, nt);
-  }
-  return hipGetLastError();
+template <class S, bool GRAD>
+hipError_t logits(const HeadLogits& a, HeadSecond second, hipStream_t st) {
+  if (second == HEAD_ONE) return a.f32 ? logits<S, GRAD, HEAD_ONE, true>(a, st) : logits<S, GRAD, HEAD_ONE, false>(a, st);
+  if (second == HEAD_OWN) return a.f32 ? logits<S, GRAD, HEAD_OWN, true>(a, st) : logits<S, GRAD, HEAD_OWN, false>(a, st);
+  return a.f32 ? logits<S, GRAD, HEAD_SQUARE, true>(a, st) : logits<S, GRAD, HEAD_SQUARE, false>(a, st);
+}
+
+template <bool GRAD>
+hipError_t logits(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st) {
+  return s == HEAD_256   ? logits<Shape256, GRAD>(a, second, st)
+         : s == HEAD_128 ? logits<Shape128, GRAD>(a, second, st)
+                         : logits<Shape32, GRAD>(a, second, st);
 }
 
 template <class SX, class SW>
@@ -388,11 +377,11 @@ hipError_t products(HeadDx x, HeadDw w, hipStream_t st) {
 int64_t head_tile_words(HeadShape s) { return s == HEAD_256 ? Shape256::BM : s == HEAD_128 ? Shape128::BM : Shape32::BM; }
 int64_t head_tile_rows(HeadShape s) { return s == HEAD_256 ? Shape256::BN : s == HEAD_128 ? Shape128::BN : Shape32::BN; }
 
-hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, bool second, hipStream_t st) {
-  return s == HEAD_256 ? sums<Shape256>(a, second, st) : s == HEAD_128 ? sums<Shape128>(a, second, st) : sums<Shape32>(a, second, st);
+hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st) {
+  return logits<false>(a, s, second, st);
 }
-hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, bool second, hipStream_t st) {
-  return s == HEAD_256 ? grad<Shape256>(a, second, st) : s == HEAD_128 ? grad<Shape128>(a, second, st) : grad<Shape32>(a, second, st);
+hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st) {
+  return logits<true>(a, s, second, st);
 }
 hipError_t head_launch_products(const HeadDx& x, const HeadDw& w, HeadShape s, hipStream_t st) {
   return s == HEAD_256   ? products<Shape256, Shape256>(x, w, st)
