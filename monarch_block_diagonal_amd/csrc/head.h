@@ -24,15 +24,16 @@ enum HeadSecond {
   HEAD_SQUARE = 2   // T = 2: e^z is the square of e^(z/2)
 };
 
-enum HeadShape { HEAD_256 = 0, HEAD_128 = 1, HEAD_32 = 2 };
+enum HeadShape { HEAD_256 = 0, HEAD_128 = 1, HEAD_32 = 2, HEAD_THIN = 3 };   // HEAD_THIN: logits of at most 32 rows
 
 struct HeadLogits {
   PipeProduct pr;             // A: the head's words, B: the rows
+  const float* raw;           // fp32, HEAD_THIN: the head itself [vocab][d]
   const int* count;           // rows in use
   int f32;                    // operands are fp32, as three planes
   int64_t vocab, v0, v1;      // words of this launch: [v0, v1)
   int64_t d;                  // k
-  int64_t np;                 // rows of the workspace's copies
+  int64_t rows, np;           // rows of the call, and of the workspace's copies
   float ct;                   // log2(e) / temperature
   const int* label;           // a row: its label, -1 without one
   // sums: part [tiles of words][np][3] (largest logit, sum at T, sum at 1), z of the label
@@ -67,7 +68,7 @@ struct HeadDw {
   int64_t dt, vt;             // tiles (set by the launch)
 };
 
-int64_t head_tile_words(HeadShape s);    // words of a logits tile
+int64_t head_tile_words(HeadShape s, int64_t vocab);    // words behind one of a logits launch's sums
 int64_t head_tile_rows(HeadShape s);     // rows of a logits and a dx tile
 hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st);
 hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st);

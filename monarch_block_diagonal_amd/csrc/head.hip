@@ -66,6 +66,26 @@ __device__ __forceinline__ bool entry_ok(int64_t id, float t, int64_t vocab) {
   return id >= 0 && id < vocab && t > -INFINITY;
 }
 
+// A row of d bf16 elements copied to dp, zeros behind them (or zeros throughout), by N threads.
+template <int N>
+__device__ __forceinline__ void copy_row(const uint16_t* s, bool zero, int64_t d, int64_t dp, uint16_t* o, int t) {
+  const bool whole = ((reinterpret_cast<uintptr_t>(s) & 15) == 0) && d % 8 == 0;
+  for (int64_t e = t * 8; e < dp; e += N * 8) {
+    u32x4 v = {0, 0, 0, 0};
+    if (!zero && e < d) {
+      if (whole) {
+        v = *reinterpret_cast<const u32x4*>(s + e);
+      } else {
+        uint16_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = e + i < d ? s[e + i] : uint16_t(0);
+        __builtin_memcpy(&v, h, 16);
+      }
+    }
+    *reinterpret_cast<u32x4*>(o + e) = v;
+  }
+}
+
 // A wave a row: does it have an entry?
 __global__ __launch_bounds__(256) void head_flag_kernel(Call c, Rows r) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -78,7 +98,8 @@ __global__ __launch_bounds__(256) void head_flag_kernel(Call c, Rows r) {
 }
 
 // One workgroup: the rows in use, in their order; loss and statistics of the others are 0.
-__global__ __launch_bounds__(1024) void head_rows_kernel(Call c, Rows r, uint32_t* zeros) {
+// With xc (few rows in bf16) it copies them too, as head_copy_kernel would.
+__global__ __launch_bounds__(1024) void head_rows_kernel(Call c, Rows r, uint32_t* zeros, uint16_t* xc, int64_t dp) {
   constexpr int PER = 4;
   __shared__ int s_wave[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -134,6 +155,11 @@ __global__ __launch_bounds__(1024) void head_rows_kernel(Call c, Rows r, uint32_
   const int end = (base + static_cast<int>(kHeadRows) - 1) / static_cast<int>(kHeadRows) * static_cast<int>(kHeadRows);
   for (int k = base + threadIdx.x; k < end; k += 1024) r.idx[k] = 0, r.label[k] = -1, r.has[k] = 0;
   if (threadIdx.x == 0) *r.count = base;
+  if (xc) {
+    __syncthreads();
+    // a wave a row at a time; 64 rows are a K tile of dw's
+    for (int k = wave; k < kPipeK; k += 16) copy_row<64>(static_cast<const uint16_t*>(c.x) + (k < base ? r.idx[k] : 0) * c.ldx, k >= base, c.d, dp, xc + k * dp, lane);
+  }
 }
 
 // One value as bf16, and what is left of it.
@@ -162,8 +188,8 @@ __global__ __launch_bounds__(256) void head_copy_kernel(const T* __restrict__ sr
   }
   const T* s = src + row * ld;
   uint16_t* o = dst + k * dp;
-  const bool whole = ((reinterpret_cast<uintptr_t>(s) & 15) == 0) && d % (F32 ? 4 : 8) == 0;
   if constexpr (F32) {
+    const bool whole = ((reinterpret_cast<uintptr_t>(s) & 15) == 0) && d % 4 == 0;
     for (int64_t e = threadIdx.x * 4; e < dp; e += 1024) {
       float v[4] = {0.f, 0.f, 0.f, 0.f};
       if (!zero && e < d) {
@@ -186,20 +212,7 @@ __global__ __launch_bounds__(256) void head_copy_kernel(const T* __restrict__ sr
       }
     }
   } else {
-    for (int64_t e = threadIdx.x * 8; e < dp; e += 2048) {
-      u32x4 v = {0, 0, 0, 0};
-      if (!zero && e < d) {
-        if (whole) {
-          v = *reinterpret_cast<const u32x4*>(s + e);
-        } else {
-          uint16_t h[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[i] = e + i < d ? s[e + i] : uint16_t(0);
-          __builtin_memcpy(&v, h, 16);
-        }
-      }
-      *reinterpret_cast<u32x4*>(o + e) = v;
-    }
+    copy_row<256>(s, zero, d, dp, o, threadIdx.x);
   }
 }
 
@@ -480,8 +493,9 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
   // time: measured, 4096 x 768 x 50257 bf16 1368 us with the first and 1456 with the second (13 and 25
   // rounds), 600 x 2000 x 10000 204 and 170 (1 and 1).
   auto rounds = [&](int64_t tile, int64_t places) { return up(tiles_of(vocab, tile) * tiles_of(rows, tile), places) / places; };
-  p.shape = rows <= 32 ? HEAD_32 : rounds(256, 256) <= 0.6 * rounds(128, 512) ? HEAD_256 : HEAD_128;
-  const int64_t tv = head_tile_words(p.shape);
+  // fp32 rows of the head that start off 16 bytes take HEAD_32's tiles, of a copy
+  p.shape = rows <= 32 ? (bf16 || d % 4 == 0 ? HEAD_THIN : HEAD_32) : rounds(256, 256) <= 0.6 * rounds(128, 512) ? HEAD_256 : HEAD_128;
+  const int64_t tv = head_tile_words(p.shape, vocab);
   p.tiles = (vocab + tv - 1) / tv;
   size_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -491,6 +505,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
   };
   p.rows = take(256 + (p.np * 3 + rows * 2) * 4);
   p.x = take(p.planes * p.np * p.dp * 2);
+  p.copy_w = p.copy_w && !(what == FWD && !bf16 && p.shape == HEAD_THIN);   // which takes the head as it is
   p.w = p.copy_w ? take(p.planes * (vocab + kPipeK) * p.dp * 2) : 0;   // zeros behind: whole K tiles of words
   if (what != BWD) {
     p.part = take(p.tiles * 3 * p.np * 4);
@@ -508,7 +523,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
     // (fp32 5370, 5999); 1000 x 625 x 10000 fp32 365 us, with 128 x 128 330
     const bool wide = rows > 128 && d > 128 && static_cast<double>(rows) * vocab * d >= 2e10;
     p.products = rows <= 32 ? HEAD_32 : wide ? HEAD_256 : HEAD_128;
-    const int64_t xm = head_tile_words(p.products), xn = head_tile_rows(p.products);
+    const int64_t xm = head_tile_words(p.products, vocab), xn = head_tile_rows(p.products);
     const int64_t wm = wide ? 256 : 128;
     const int64_t slots = wide ? 256 : 512;
     const int64_t dx_tiles = tiles_of(d, xm) * tiles_of(rows, xn), dw_tiles = tiles_of(d, wm) * tiles_of(p.vp, wm);
@@ -581,10 +596,12 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
     hipLaunchKernelGGL(head_flag_kernel, dim3(static_cast<unsigned>((c.rows + 3) / 4)), dim3(256), 0, s, c, r);
     HEAD_TRY(hipGetLastError());
   }
-  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, s, c, r, head);
+  const bool few = c.bf16 && c.rows <= 32;
+  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, s, c, r, head, few ? xc : nullptr, p.dp);
   HEAD_TRY(hipGetLastError());
   const int64_t xplane = p.np * p.dp, wplane = (c.vocab + kPipeK) * p.dp;
-  HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.x, c.ldx, r.idx, r.count, c.rows, p.np, p.d, p.dp, xc, xplane, s)
+  if (!few)
+    HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.x, c.ldx, r.idx, r.count, c.rows, p.np, p.d, p.dp, xc, xplane, s)
                   : copy_rows<float>(c.x, c.ldx, r.idx, r.count, c.rows, p.np, p.d, p.dp, xc, xplane, s));
   const uint16_t* w = static_cast<const uint16_t*>(c.w);
   int64_t ldw = p.d;
@@ -596,10 +613,10 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
   }
   HeadLogits l = {};
   l.pr.zeros = reinterpret_cast<const uint16_t*>(head);
-  l.f32 = !c.bf16;
+  l.f32 = !c.bf16, l.raw = static_cast<const float*>(c.w);
   l.pr.a.p = w, l.pr.a.ld = ldw, l.pr.a.plane = wplane, l.pr.a.rows = c.vocab, l.pr.a.kvalid = ldw;   // in place the last K tile may be cut
   l.pr.b.p = xc, l.pr.b.ld = p.dp, l.pr.b.plane = xplane, l.pr.b.rows = p.np, l.pr.b.kvalid = p.dp;
-  l.count = r.count, l.vocab = c.vocab, l.d = p.d, l.np = p.np, l.ct = kLog2e / c.temperature, l.label = r.label;
+  l.count = r.count, l.vocab = c.vocab, l.d = p.d, l.rows = c.rows, l.np = p.np, l.ct = kLog2e / c.temperature, l.label = r.label;
   if (what != BWD) {
     if (c.taught) {
       const dim3 g(static_cast<unsigned>(c.rows));

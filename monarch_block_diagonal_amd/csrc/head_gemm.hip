@@ -221,6 +221,217 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
   }
 }
 
+// Logits of at most 16 * NB rows: bound by reading the head once. A workgroup takes a run of
+// words, 64 at a time, 16 a wave, and a head's row comes in pieces of 512 bytes: K tiles of 256 (fp32:
+// 128) go straight into LDS, three in flight, one after another over the run's words, so that
+// loads never pause. A row's maximum and sums run on in registers over the run; lanes meet at its end.
+// Read in pieces of 128 bytes (HEAD_32's tiles), the forward pass of 32 x 4096 x 131072 bf16 takes
+// 400 us, this way 267 (4.0 TB/s). In fp32 the head is taken as it is and cut into its three bf16 parts
+// in registers, where the wider tiles read a copy of planes.
+//
+// A K tile's row r holds its 16-byte piece q at q ^ (r mod 16): the 16 rows of a read fall on all banks.
+constexpr int kThinWords = 64;
+
+template <int NB, bool F32>
+struct ThinShape {
+  static constexpr int K = F32 ? 128 : 256;
+  // 1 KB loads of a K tile: the words' rows of 512 bytes, then the rows' (fp32: of 256 bytes in each of three planes)
+  static constexpr int W_LOADS = kThinWords / 2, LOADS = W_LOADS + (F32 ? 3 * 16 * NB / 4 : 16 * NB / 2);
+  static constexpr int STAGE = LOADS * 1024, NST = F32 && NB == 2 ? 2 : 3, LDS = STAGE * NST;
+  static constexpr int PER = LOADS / 4;
+};
+
+// 8 fp32 values as three bf16 fragments.
+__device__ __forceinline__ void three_parts(f32x4 lo, f32x4 hi, bf16x8 (&f)[3]) {
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const u32x2 a = next_plane(lo), b = next_plane(hi);
+    const u32x4 v = {a[0], a[1], b[0], b[1]};
+    __builtin_memcpy(&f[q], &v, 16);
+  }
+}
+
+template <int NB, bool GRAD, HeadSecond SECOND, bool F32>
+__global__ __launch_bounds__(256) void head_thin_kernel(HeadLogits p, int64_t run) {
+  using S = ThinShape<NB, F32>;
+  constexpr int NST = S::NST, PER = S::PER, kThinK = S::K;
+  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+  __shared__ float part[4][3][16 * NB];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l15 = lane & 15, lh = lane >> 4;
+  const int64_t first = p.v0 + blockIdx.x * run, end = first + run < p.v1 ? first + run : p.v1;
+  const int64_t kw = F32 ? p.d : p.pr.a.kvalid, kx = p.pr.b.kvalid;
+  const int ktiles = static_cast<int>((kw + kThinK - 1) / kThinK);
+  const int ntiles = static_cast<int>((end - first + kThinWords - 1) / kThinWords) * ktiles;
+  int lk = 0;
+  int64_t lv = first;
+  auto issue = [&](int st) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int j = wave * PER + i;
+      const void* s = p.pr.zeros;
+      if (j < S::W_LOADS) {
+        const int row = j * 2 + (lane >> 5), piece = (lane & 31) ^ (row & 15);
+        const int64_t v = lv + row, k = lk * kThinK + piece * (F32 ? 4 : 8);
+        if (v < end && k < kw) {
+          if constexpr (F32)
+            s = p.raw + v * p.d + k;
+          else
+            s = p.pr.a.p + v * p.pr.a.ld + k;
+        }
+      } else if constexpr (F32) {
+        const int row = (j - S::W_LOADS) * 4 + (lane >> 4), plane = row / (16 * NB), r = row % (16 * NB);
+        const int64_t k = lk * kThinK + (((lane & 15) ^ (r & 15)) << 3);
+        if (k < kx) s = p.pr.b.p + plane * p.pr.b.plane + r * p.pr.b.ld + k;
+      } else {
+        const int row = (j - S::W_LOADS) * 2 + (lane >> 5);
+        const int64_t k = lk * kThinK + (((lane & 31) ^ (row & 15)) << 3);
+        if (k < kx) s = p.pr.b.p + row * p.pr.b.ld + k;
+      }
+      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)(s),
+                                       (__attribute__((address_space(3))) void*)(lds + st * S::STAGE + j * 1024), 16, 0, 0);
+    }
+    if (++lk == ktiles) lk = 0, lv += kThinWords;
+  };
+  f32x4 acc[NB];
+  float m[NB], st[NB], s1[NB];
+  int label[NB];
+  HeadRow r[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    m[b] = kLowest, st[b] = 0.f, s1[b] = 0.f;
+    label[b] = p.label[b * 16 + l15];
+    if constexpr (GRAD) r[b] = p.row[b * 16 + l15];
+  }
+  for (int t = 0; t < NST && t < ntiles; ++t) issue(t);
+  int k = 0, place = 0;
+  int64_t v0 = first;
+#pragma unroll 1
+  for (int t = 0; t < ntiles; ++t) {
+    const int later = ntiles - 1 - t < NST - 1 ? ntiles - 1 - t : NST - 1;
+    asm volatile("" ::: "memory");
+    pipe_wait_stages<PER, NST - 1>(later);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const char* at = lds + place * S::STAGE;
+    const char* words = at + (wave * 16 + l15) * 512;
+    const char* rows = at + S::W_LOADS * 1024;
+#pragma unroll
+    for (int u = 0; u < kThinK / 32; ++u) {
+      if constexpr (F32) {
+        const int piece = 8 * u + 2 * lh;
+        bf16x8 fa[3];
+        three_parts(*reinterpret_cast<const f32x4*>(words + ((piece ^ l15) << 4)),
+                    *reinterpret_cast<const f32x4*>(words + (((piece + 1) ^ l15) << 4)), fa);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          bf16x8 fb[3];
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(rows + ((q * NB + b) * 16 + l15) * 256 + (((4 * u + lh) ^ l15) << 4));
+            __builtin_memcpy(&fb[q], &x, 16);
+          }
+          constexpr int pa[6] = {2, 0, 1, 1, 0, 0}, pb[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+          for (int q = 0; q < 6; ++q) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[pa[q]], fb[pb[q]], acc[b], 0, 0, 0);
+        }
+      } else {
+        const int piece = ((4 * u + lh) ^ l15) << 4;
+        bf16x8 fa, fb;
+        const u32x4 a = *reinterpret_cast<const u32x4*>(words + piece);
+        __builtin_memcpy(&fa, &a, 16);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(rows + (b * 16 + l15) * 512 + piece);
+          __builtin_memcpy(&fb, &x, 16);
+          acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, fb, acc[b], 0, 0, 0);
+        }
+      }
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(pipe_wait(63));   // its reads are done
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (t + NST < ntiles) issue(place);
+    place = place + 1 == NST ? 0 : place + 1;
+    if (++k < ktiles) continue;
+    k = 0;
+    const int64_t vw = v0 + wave * 16 + 4 * lh;
+    v0 += kThinWords;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int n = b * 16 + l15;
+      const int64_t own = label[b] - vw;
+      if constexpr (GRAD) {
+        f32x4 g;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float z = acc[b][v] - r[b].m, e = exp2_of(z * p.ct);
+          g[v] = r[b].a * e;
+          if constexpr (SECOND == HEAD_OWN) g[v] = fmaf(r[b].b, exp2_of(z * kLog2e), g[v]);
+          if constexpr (SECOND == HEAD_SQUARE) g[v] = fmaf(r[b].b * e, e, g[v]);
+          if (own == v) g[v] -= r[b].off;
+          if (vw + v >= end) g[v] = 0.f;
+        }
+        // a gradient's runs are whole tiles, as K tiles of dx's are (behind the last word g has room)
+        uint16_t* o = p.g + n * p.vp + (vw - p.v0);
+#pragma unroll
+        for (int q = 0; q < (F32 ? 3 : 1); ++q) {
+          *reinterpret_cast<u32x2*>(o) = next_plane(g);
+          // a K tile of dw's is 64 rows: the other ones are 0
+#pragma unroll
+          for (int z = 16 * NB; z < kPipeK; z += 16 * NB) *reinterpret_cast<u32x2*>(o + z * p.vp) = u32x2{0, 0};
+          o += p.g_plane;
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if (vw + v >= end) acc[b][v] = -INFINITY;
+          if (own == v && vw + v < end) p.z_label[n] = acc[b][v];
+        }
+        const float to = fmaxf(fmaxf(fmaxf(m[b], acc[b][0]), fmaxf(acc[b][1], acc[b][2])), acc[b][3]);
+        st[b] *= exp2_of((m[b] - to) * p.ct);
+        if constexpr (SECOND != HEAD_ONE) s1[b] *= exp2_of((m[b] - to) * kLog2e);
+        m[b] = to;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float z = acc[b][v] - to, e = exp2_of(z * p.ct);
+          st[b] += e;
+          if constexpr (SECOND == HEAD_OWN) s1[b] += exp2_of(z * kLog2e);
+          if constexpr (SECOND == HEAD_SQUARE) s1[b] = fmaf(e, e, s1[b]);
+        }
+      }
+      acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+  if constexpr (!GRAD) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const float to = over_groups<true>(m[b]);
+      st[b] = over_groups<false>(st[b] * exp2_of((m[b] - to) * p.ct));
+      if constexpr (SECOND != HEAD_ONE) s1[b] = over_groups<false>(s1[b] * exp2_of((m[b] - to) * kLog2e));
+      if (lh == 0) part[wave][0][b * 16 + l15] = to, part[wave][1][b * 16 + l15] = st[b], part[wave][2][b * 16 + l15] = s1[b];
+    }
+    __syncthreads();
+    if (threadIdx.x < 16 * NB) {
+      const int n = threadIdx.x;
+      float to = part[0][0][n], t = 0.f, o1 = 0.f;
+#pragma unroll
+      for (int i = 1; i < 4; ++i) to = fmaxf(to, part[i][0][n]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float by = part[i][0][n] - to;
+        t += part[i][1][n] * exp2_of(by * p.ct);
+        if constexpr (SECOND != HEAD_ONE) o1 += part[i][2][n] * exp2_of(by * kLog2e);
+      }
+      float* o = p.part + static_cast<int64_t>(blockIdx.x) * 3 * p.np + n;
+      o[0] = to;
+      o[p.np] = t;
+      o[2 * p.np] = SECOND != HEAD_ONE ? o1 : t;
+    }
+  }
+}
+
 template <class S, bool F32>
 __device__ __forceinline__ void dx_tile(const HeadDx& p, int64_t at, char* lds) {
   const int64_t dt = p.dt, nt = p.nt;
@@ -352,8 +563,28 @@ hipError_t logits(const HeadLogits& a, HeadSecond second, hipStream_t st) {
   return a.f32 ? logits<S, GRAD, HEAD_SQUARE, true>(a, st) : logits<S, GRAD, HEAD_SQUARE, false>(a, st);
 }
 
+// Words of a workgroup's run, for one workgroup a CU: whole tiles, or whole waves' words.
+int64_t thin_run(int64_t words, int64_t of) { return tiles(words, 256 * of) * of; }
+
+template <bool GRAD, int NB, bool F32>
+hipError_t thin(const HeadLogits& a, HeadSecond second, hipStream_t st) {
+  const int64_t run = thin_run(a.v1 - a.v0, GRAD ? kThinWords : 16);
+  const dim3 g(static_cast<unsigned>(tiles(a.v1 - a.v0, run)));
+  if (second == HEAD_ONE)
+    hipLaunchKernelGGL((head_thin_kernel<NB, GRAD, HEAD_ONE, F32>), g, dim3(256), 0, st, a, run);
+  else if (second == HEAD_OWN)
+    hipLaunchKernelGGL((head_thin_kernel<NB, GRAD, HEAD_OWN, F32>), g, dim3(256), 0, st, a, run);
+  else
+    hipLaunchKernelGGL((head_thin_kernel<NB, GRAD, HEAD_SQUARE, F32>), g, dim3(256), 0, st, a, run);
+  return hipGetLastError();
+}
+
 template <bool GRAD>
 hipError_t logits(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st) {
+  if (s == HEAD_THIN) {
+    if (a.f32) return a.rows <= 16 ? thin<GRAD, 1, true>(a, second, st) : thin<GRAD, 2, true>(a, second, st);
+    return a.rows <= 16 ? thin<GRAD, 1, false>(a, second, st) : thin<GRAD, 2, false>(a, second, st);
+  }
   return s == HEAD_256   ? logits<Shape256, GRAD>(a, second, st)
          : s == HEAD_128 ? logits<Shape128, GRAD>(a, second, st)
                          : logits<Shape32, GRAD>(a, second, st);
@@ -374,7 +605,7 @@ hipError_t products(HeadDx x, HeadDw w, hipStream_t st) {
 
 }  // namespace
 
-int64_t head_tile_words(HeadShape s) { return s == HEAD_256 ? Shape256::BM : s == HEAD_128 ? Shape128::BM : Shape32::BM; }
+int64_t head_tile_words(HeadShape s, int64_t vocab) { return s == HEAD_THIN ? thin_run(vocab, 16) : s == HEAD_256 ? Shape256::BM : s == HEAD_128 ? Shape128::BM : Shape32::BM; }
 int64_t head_tile_rows(HeadShape s) { return s == HEAD_256 ? Shape256::BN : s == HEAD_128 ? Shape128::BN : Shape32::BN; }
 
 hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st) {

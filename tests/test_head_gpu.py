@@ -84,6 +84,15 @@ def test_distillation(api, rows, d, vocab, top, T, mix, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,d,vocab,top", [(1, 320, 70001, 0), (16, 72, 40000, 5), (17, 264, 33000, 0), (32, 600, 20050, 3), (29, 37, 50257, 2), (5, 1028, 66000, 0)])
+def test_few_rows(api, rows, d, vocab, top, dtype):
+    """Runs of words over several tiles, that end inside a tile; K tiles that end inside a row."""
+    x, w, labels, t, ids, r = draw(rows, d, vocab, dtype, top=top, holes=rows > 2, seed=23)
+    for T, mix in (((1.0, 0.0),) if not top else ((2.0, 0.5), (1.3, 0.7), (1.0, 1.0))):
+        check(api, x, w, labels, t, ids, r, T, mix)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_wide_tiles(api, dtype):
     """Enough tiles for the 256 x 256 products; words and rows that end inside a tile, a third of the rows left out."""
     x, w, labels, t, ids, r = draw(1100, 136, 20011, dtype, top=9, holes=True, seed=7)
