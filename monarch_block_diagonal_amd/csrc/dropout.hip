@@ -10,8 +10,10 @@
 // p to 2^-16; with whole words of 32 bits the generator's 20 products of 32 bits for
 // four elements would take longer than the data (a wave's takes 16 cycles each).
 //
-// A thread takes 8 elements at a time: one draw, one or two 16-byte pieces of each
-// tensor. Bound by HBM.
+// A thread takes a 16-byte piece of each tensor at a time and one draw for it: 8 elements
+// in bf16; in fp32 4, of the draw's 8 (the other four are drawn again by the next lane,
+// which costs less than 32 bytes a lane did, whose loads each took half of every line).
+// Bound by HBM.
 #include <math.h>
 
 #include "api_internal.h"
@@ -51,27 +53,24 @@ __device__ __forceinline__ void philox(uint64_t at, uint64_t offset, uint64_t se
   }
 }
 
-// U units of 8 elements a thread, 256 units apart.
+// U pieces a thread, 256 pieces apart.
 template <typename T, bool RES, int U>
 __global__ __launch_bounds__(256) void dropout_kernel(Dropout a) {
-  constexpr int N = PieceOf<T>::N, P = 8 / N;   // elements of a piece, pieces of a unit
+  constexpr int N = PieceOf<T>::N;
   uint64_t seed = a.seed, offset = a.offset;
   if (a.state) seed = a.state[0], offset = a.state[1];
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * U) + threadIdx.x;
-  const int64_t whole = a.n >> 3;
+  const int64_t whole = a.n / N;
   const u32x4* x = static_cast<const u32x4*>(a.x);
   const u32x4* res = static_cast<const u32x4*>(a.residual);
   u32x4* y = static_cast<u32x4*>(a.y);
-  u32x4 v[U][P], r[U][P];
+  u32x4 v[U], r[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t at = first + u * 256;
     if (at < whole) {
-#pragma unroll
-      for (int q = 0; q < P; ++q) {
-        v[u][q] = __builtin_nontemporal_load(x + at * P + q);
-        if constexpr (RES) r[u][q] = __builtin_nontemporal_load(res + at * P + q);
-      }
+      v[u] = __builtin_nontemporal_load(x + at);
+      if constexpr (RES) r[u] = __builtin_nontemporal_load(res + at);
     }
   }
 #pragma unroll
@@ -79,28 +78,26 @@ __global__ __launch_bounds__(256) void dropout_kernel(Dropout a) {
     const int64_t at = first + u * 256;
     if (at > whole) continue;
     uint32_t c[4];
-    philox(static_cast<uint64_t>(at), offset, seed, c);
+    philox(static_cast<uint64_t>(at * N) >> 3, offset, seed, c);
+    if constexpr (N == 4)
+      if (at & 1) c[0] = c[2], c[1] = c[3];
     if (at < whole) {
+      float f[N], g[N];
+      PieceOf<T>::unpack(v[u], f);
+      if constexpr (RES) PieceOf<T>::unpack(r[u], g);
 #pragma unroll
-      for (int q = 0; q < P; ++q) {
-        float f[N], g[N];
-        PieceOf<T>::unpack(v[u][q], f);
-        if constexpr (RES) PieceOf<T>::unpack(r[u][q], g);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const int i = q * N + e;
-          const uint32_t half = (i & 1) ? c[i >> 1] >> 16 : c[i >> 1] & 0xffffu;
-          // chosen, not multiplied: what is dropped may be infinite or NaN
-          const float kept = RES ? fmaf(f[e], a.scale, g[e]) : f[e] * a.scale;
-          f[e] = half >= a.threshold ? kept : RES ? g[e] : 0.0f;
-        }
-        __builtin_nontemporal_store(PieceOf<T>::pack(f), y + at * P + q);
+      for (int i = 0; i < N; ++i) {
+        const uint32_t half = (i & 1) ? c[i >> 1] >> 16 : c[i >> 1] & 0xffffu;
+        // chosen, not multiplied: what is dropped may be infinite or NaN
+        const float kept = RES ? fmaf(f[i], a.scale, g[i]) : f[i] * a.scale;
+        f[i] = half >= a.threshold ? kept : RES ? g[i] : 0.0f;
       }
+      __builtin_nontemporal_store(PieceOf<T>::pack(f), y + at);
     } else {
-      // the last elements, fewer than 8
+      // the last elements, fewer than a piece
 #pragma unroll 1
-      for (int64_t i = at * 8; i < a.n; ++i) {
-        const int e = static_cast<int>(i & 7);
+      for (int64_t i = at * N; i < a.n; ++i) {
+        const int e = static_cast<int>(i - at * N);
         const uint32_t word = e < 4 ? (e < 2 ? c[0] : c[1]) : (e < 6 ? c[2] : c[3]);
         const uint32_t half = (e & 1) ? word >> 16 : word & 0xffffu;
         const float g = RES ? Io<T>::load(a.residual, i) : 0.0f;
@@ -113,15 +110,14 @@ __global__ __launch_bounds__(256) void dropout_kernel(Dropout a) {
 
 template <typename T, bool RES>
 hipError_t launch(const Dropout& a, hipStream_t s) {
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;
-  const int64_t units = (a.n + 7) / 8;
-  // few units: one a thread, so that every CU has some
-  if (units <= 256 * 1024) {
-    hipLaunchKernelGGL((dropout_kernel<T, RES, 1>), dim3(static_cast<unsigned>((units + 255) / 256)), dim3(256), 0, s, a);
-  } else {
-    hipLaunchKernelGGL((dropout_kernel<T, RES, U>), dim3(static_cast<unsigned>((units + 256 * U - 1) / (256 * U))), dim3(256),
+  constexpr int U = 4;
+  const int64_t pieces = (a.n + PieceOf<T>::N - 1) / PieceOf<T>::N;
+  // few pieces: one a thread, so that every CU has some
+  if (pieces <= 256 * 1024)
+    hipLaunchKernelGGL((dropout_kernel<T, RES, 1>), dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((dropout_kernel<T, RES, U>), dim3(static_cast<unsigned>((pieces + 256 * U - 1) / (256 * U))), dim3(256),
                        0, s, a);
-  }
   return hipGetLastError();
 }
 

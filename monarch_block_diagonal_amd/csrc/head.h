@@ -9,6 +9,7 @@
 
 namespace monarch {
 
+constexpr int64_t kThinRows = 32;    // rows that HEAD_THIN takes
 constexpr int64_t kHeadRows = 256;   // rows of the workspace's copies are a multiple of this, and so are a piece's columns
 
 // What the products' epilogues take of a row: its largest logit and the factors of
@@ -23,6 +24,17 @@ enum HeadSecond {
   HEAD_OWN = 1,     // exponentials of its own
   HEAD_SQUARE = 2   // T = 2: e^z is the square of e^(z/2)
 };
+
+// g of one logit; operations and roundings are the same wherever it is computed.
+template <int SECOND>
+__device__ __forceinline__ float head_g(const HeadRow& r, float logit, float ct, bool label) {
+#pragma clang fp contract(off)
+  const float z = logit - r.m, e = __builtin_amdgcn_exp2f(z * ct);
+  float g = r.a * e;
+  if constexpr (SECOND == HEAD_OWN) g = fmaf(r.b, __builtin_amdgcn_exp2f(z * 1.44269504088896340736f), g);
+  if constexpr (SECOND == HEAD_SQUARE) g = fmaf(r.b * e, e, g);
+  return label ? g - r.off : g;
+}
 
 enum HeadShape { HEAD_256 = 0, HEAD_128 = 1, HEAD_32 = 2, HEAD_THIN = 3 };   // HEAD_THIN: logits of at most 32 rows
 
@@ -39,6 +51,7 @@ struct HeadLogits {
   // sums: part [tiles of words][np][3] (largest logit, sum at T, sum at 1), z of the label
   float* part;
   float* z_label;
+  float* z;                   // HEAD_THIN, or null: the logits [rows][vp]
   // gradient: g [planes][np][vp]
   const HeadRow* row;
   uint16_t* g;
@@ -70,6 +83,7 @@ struct HeadDw {
 
 int64_t head_tile_words(HeadShape s, int64_t vocab);    // words behind one of a logits launch's sums
 int64_t head_tile_rows(HeadShape s);     // rows of a logits and a dx tile
+int64_t head_tile_features(HeadShape s); // features of a dx tile
 hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st);
 hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st);
 // dx and dw of a piece (HEAD_32: dx's tiles, dw's are HEAD_128's)

@@ -280,15 +280,37 @@ __device__ __forceinline__ void teacher_sums(const Call& c, int64_t i, int lane,
   *sum = lanes_reduce<SumOp, 64>(s);
 }
 
-// Joins the tiles' sums of RW rows a workgroup, and gives the rows' losses.
+// The factors for g of row k (compact), from its largest logit and sums.
+__device__ __forceinline__ void row_factors(const Call& c, const Rows& r, int64_t k, int64_t i, float m, float st, float s1,
+                                            HeadRow* out, float* taught) {
+  HeadRow o;
+  const float w = c.weight ? c.weight[i] : 1.0f;
+  const float a = r.has[k] ? c.mix * c.temperature * w : 0.f;
+  o.m = m;
+  o.off = r.label[k] >= 0 ? (1.0f - c.mix) * w : 0.f;
+  // one softmax at T = 1, or with one of the two terms alone
+  const bool one = c.second == HEAD_ONE;
+  o.a = one ? (a + o.off) / st : a / st;
+  o.b = one ? 0.f : o.off / s1;
+  out[k] = o;
+  taught[k] = a;
+}
+
+// Joins the tiles' sums of RW rows a workgroup, and gives the rows' losses; in a step their factors for g
+// too, as head_factors_kernel.
 template <int RW>
 __global__ __launch_bounds__(256) void head_loss_kernel(Call c, Rows r, const float* __restrict__ part, int64_t np,
-                                                        int tiles, const float* __restrict__ z_label) {
+                                                        int tiles, const float* __restrict__ z_label, HeadRow* factors,
+                                                        float* taught) {
   constexpr int SL = 256 / RW;
   __shared__ float s[3][256];
   const int64_t k0 = static_cast<int64_t>(blockIdx.x) * RW;
   const int count = *r.count;
-  if (k0 >= count) return;
+  if (k0 >= count) {
+    if (factors && k0 < (count + kHeadRows - 1) / kHeadRows * kHeadRows && threadIdx.x < RW)
+      factors[k0 + threadIdx.x] = HeadRow{0.f, 0.f, 0.f, 0.f}, taught[k0 + threadIdx.x] = 0.f;
+    return;
+  }
   const float ct = kLog2e / c.temperature;
   const int col = threadIdx.x % RW, slice = threadIdx.x / RW;
   const float* at = part + k0 + col;
@@ -318,7 +340,10 @@ __global__ __launch_bounds__(256) void head_loss_kernel(Call c, Rows r, const fl
   const int lane = threadIdx.x & 63;
   for (int w = threadIdx.x >> 6; w < RW; w += 4) {
     const int64_t k = k0 + w;
-    if (k >= count) break;
+    if (k >= count) {
+      if (factors && lane == 0) factors[k] = HeadRow{0.f, 0.f, 0.f, 0.f}, taught[k] = 0.f;
+      continue;
+    }
     const int64_t i = r.idx[k];
     const float rm = s[0][w], rt = s[1][w], r1 = s[2][w];
     float loss = 0.f;
@@ -340,33 +365,55 @@ __global__ __launch_bounds__(256) void head_loss_kernel(Call c, Rows r, const fl
     if (lane == 0) {
       c.loss[i] = loss;
       *reinterpret_cast<f32x4*>(c.stats + i * 4) = f32x4{rm, rt, r1, 0.f};
+      if (factors) row_factors(c, r, k, i, rm, rt, r1, factors, taught);
     }
   }
 }
 
-// The rows' factors for g (0 for the last tile's other rows).
+// The rows' factors for g, from the forward pass's statistics (0 for the last tile's other rows).
 __global__ __launch_bounds__(256) void head_factors_kernel(Call c, Rows r, HeadRow* out, float* taught) {
   const int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int count = *r.count;
   if (k >= (count + kHeadRows - 1) / kHeadRows * kHeadRows) return;
-  HeadRow o = {0.f, 0.f, 0.f, 0.f};
-  float a = 0.f;
   if (k < count) {
     const int64_t i = r.idx[k];
     const f32x4 st = *reinterpret_cast<const f32x4*>(c.stats + i * 4);
-    const float w = c.weight ? c.weight[i] : 1.0f;
-    a = r.has[k] ? c.mix * c.temperature * w : 0.f;
-    o.m = st[0];
-    o.off = r.label[k] >= 0 ? (1.0f - c.mix) * w : 0.f;
-    if (c.second != HEAD_ONE) {
-      o.a = a / st[1], o.b = o.off / st[2];
-    } else {
-      // one softmax: at T = 1, or with one of the two terms alone
-      o.a = (a + o.off) / st[1];
+    row_factors(c, r, k, i, st[0], st[1], st[2], out, taught);
+  } else {
+    out[k] = HeadRow{0.f, 0.f, 0.f, 0.f};
+    taught[k] = 0.f;
+  }
+}
+
+// g of few rows (HEAD_THIN) from their logits, which a step keeps for its length: they are smaller than
+// the head, which would be read again for them. Four words a thread, the 64 rows of a K tile of dw's.
+__global__ __launch_bounds__(256) void head_few_kernel(Call c, Rows r, const HeadRow* __restrict__ rows,
+                                                       const float* __restrict__ z, int64_t zp, uint16_t* __restrict__ g,
+                                                       int64_t vp, int64_t plane) {
+  const int64_t v = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  const int n = blockIdx.y, planes = c.bf16 ? 1 : 3;
+  if (v >= vp) return;
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  if (n < *r.count) {
+    const HeadRow h = rows[n];
+    const f32x4 l = *reinterpret_cast<const f32x4*>(z + n * zp + v);
+    const float ct = kLog2e / c.temperature;
+    const int64_t own = r.label[n] - v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = c.second == HEAD_ONE   ? head_g<HEAD_ONE>(h, l[i], ct, own == i)
+             : c.second == HEAD_OWN ? head_g<HEAD_OWN>(h, l[i], ct, own == i)
+                                    : head_g<HEAD_SQUARE>(h, l[i], ct, own == i);
+      if (v + i >= c.vocab) o[i] = 0.f;
     }
   }
-  out[k] = o;
-  taught[k] = a;
+  uint16_t* to = g + n * vp + v;
+  for (int q = 0; q < planes; ++q, to += plane) {
+    uint16_t part[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[i] = next_part(o[i]);
+    __builtin_memcpy(to, part, 8);
+  }
 }
 
 // The teacher's columns of a piece of g: a wave a row.
@@ -412,18 +459,33 @@ __global__ __launch_bounds__(64) void head_taught_kernel(Call c, Rows r, const H
   }
 }
 
-// dx of every row from the splits' sums; rows left out get 0. Four columns a thread.
-template <typename T>
+// dx of every row from the splits' sums; rows left out get 0. Four columns a thread, SL threads
+// that share the splits (many of them, where rows are few: 64 splits of 8 x 768 11 -> @@ us).
+template <typename T, int SL>
 __global__ __launch_bounds__(256) void head_dx_out_kernel(const float* __restrict__ part, const int* __restrict__ pos,
                                                           int64_t rows, int64_t np, int64_t d, int64_t dp, int splits,
                                                           T* __restrict__ dx) {
-  const int64_t per = (d + 3) / 4, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (at >= rows * per) return;
-  const int64_t i = at / per, e = (at - i * per) * 4;
-  const int64_t k = pos[i];
+  constexpr int OUT = 256 / SL;
+  const int64_t per = (d + 3) / 4, at = static_cast<int64_t>(blockIdx.x) * OUT + threadIdx.x % OUT;
+  const int slice = threadIdx.x / OUT;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (k >= 0)
-    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(part + (s * np + k) * dp + e);
+  int64_t i = 0, e = 0;
+  const bool in = at < rows * per;
+  if (in) {
+    i = at / per, e = (at - i * per) * 4;
+    const int64_t k = pos[i];
+    if (k >= 0)
+      for (int s = slice; s < splits; s += SL) v += *reinterpret_cast<const f32x4*>(part + (s * np + k) * dp + e);
+  }
+  if constexpr (SL > 1) {
+    __shared__ f32x4 sums[256];
+    sums[threadIdx.x] = v;
+    __syncthreads();
+    if (slice > 0) return;
+#pragma unroll
+    for (int s = 1; s < SL; ++s) v += sums[s * OUT + threadIdx.x];
+  }
+  if (!in) return;
   T* o = dx + i * d + e;
   if (d % 4 == 0) {
     if constexpr (sizeof(T) == 2)
@@ -467,7 +529,8 @@ struct HeadPlan {
   int dx_splits, dw_splits;
   int64_t dx_chunk;
   // byte offsets in the workspace
-  size_t rows, x, w, part, z_label, stats, factors, taught, g, dx, dw, total;
+  bool keep;                   // a step of few rows keeps their logits
+  size_t rows, x, w, part, z_label, stats, factors, taught, g, z, dx, dw, total;
 };
 
 // When `slots` places that take `first` tiles of length a, then `more` of length b, are done.
@@ -494,7 +557,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
   // rounds), 600 x 2000 x 10000 204 and 170 (1 and 1).
   auto rounds = [&](int64_t tile, int64_t places) { return up(tiles_of(vocab, tile) * tiles_of(rows, tile), places) / places; };
   // fp32 rows of the head that start off 16 bytes take HEAD_32's tiles, of a copy
-  p.shape = rows <= 32 ? (bf16 || d % 4 == 0 ? HEAD_THIN : HEAD_32) : rounds(256, 256) <= 0.6 * rounds(128, 512) ? HEAD_256 : HEAD_128;
+  p.shape = rows <= kThinRows ? (bf16 || d % 4 == 0 ? HEAD_THIN : HEAD_32) : rounds(256, 256) <= 0.6 * rounds(128, 512) ? HEAD_256 : HEAD_128;
   const int64_t tv = head_tile_words(p.shape, vocab);
   p.tiles = (vocab + tv - 1) / tv;
   size_t at = 0;
@@ -523,7 +586,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
     // (fp32 5370, 5999); 1000 x 625 x 10000 fp32 365 us, with 128 x 128 330
     const bool wide = rows > 128 && d > 128 && static_cast<double>(rows) * vocab * d >= 2e10;
     p.products = rows <= 32 ? HEAD_32 : wide ? HEAD_256 : HEAD_128;
-    const int64_t xm = head_tile_words(p.products, vocab), xn = head_tile_rows(p.products);
+    const int64_t xm = head_tile_features(p.products), xn = head_tile_rows(p.products);
     const int64_t wm = wide ? 256 : 128;
     const int64_t slots = wide ? 256 : 512;
     const int64_t dx_tiles = tiles_of(d, xm) * tiles_of(rows, xn), dw_tiles = tiles_of(d, wm) * tiles_of(p.vp, wm);
@@ -550,6 +613,8 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
     p.factors = take(p.np * static_cast<int64_t>(sizeof(HeadRow)));
     p.taught = take(p.np * 4);
     p.g = take(p.planes * p.np * p.vp * 2);
+    p.keep = what == STEP && p.shape == HEAD_THIN && p.pieces == 1;
+    p.z = p.keep ? take(kThinRows * p.vp * 4) : 0;
     p.dx = take(p.dx_splits * p.np * p.dp * 4);
     p.dw = p.dw_splits > 1 ? take(p.dw_splits * p.vp * p.dp * 4) : 0;
   }
@@ -578,6 +643,21 @@ hipError_t copy_rows(const void* src, int64_t ld, const int* idx, const int* cou
                      int64_t dp, void* dst, int64_t plane, hipStream_t s) {
   hipLaunchKernelGGL(head_copy_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, static_cast<const T*>(src), ld,
                      idx, count, rows, d, dp, static_cast<uint16_t*>(dst), plane);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t dx_out(const Call& c, const HeadPlan& p, const float* part, const int* pos, hipStream_t s) {
+  const int64_t n = c.rows * ((p.d + 3) / 4);
+  const int sl = p.dx_splits >= 16 ? 16 : 1;
+  const int64_t grid = (n + 256 / sl - 1) / (256 / sl);
+  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  if (sl == 16)
+    hipLaunchKernelGGL((head_dx_out_kernel<T, 16>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, pos, c.rows, p.np,
+                       p.d, p.dp, p.dx_splits, static_cast<T*>(c.dx));
+  else
+    hipLaunchKernelGGL((head_dx_out_kernel<T, 1>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, pos, c.rows, p.np,
+                       p.d, p.dp, p.dx_splits, static_cast<T*>(c.dx));
   return hipGetLastError();
 }
 
@@ -617,6 +697,8 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
   l.pr.a.p = w, l.pr.a.ld = ldw, l.pr.a.plane = wplane, l.pr.a.rows = c.vocab, l.pr.a.kvalid = ldw;   // in place the last K tile may be cut
   l.pr.b.p = xc, l.pr.b.ld = p.dp, l.pr.b.plane = xplane, l.pr.b.rows = p.np, l.pr.b.kvalid = p.dp;
   l.count = r.count, l.vocab = c.vocab, l.d = p.d, l.rows = c.rows, l.np = p.np, l.ct = kLog2e / c.temperature, l.label = r.label;
+  HeadRow* factors = what == FWD ? nullptr : reinterpret_cast<HeadRow*>(ws + p.factors);
+  float* taught = what == FWD ? nullptr : reinterpret_cast<float*>(ws + p.taught);
   if (what != BWD) {
     if (c.taught) {
       const dim3 g(static_cast<unsigned>(c.rows));
@@ -628,21 +710,22 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
       HEAD_TRY(hipGetLastError());
     }
     l.v0 = 0, l.v1 = c.vocab;
+    l.z = p.keep ? reinterpret_cast<float*>(ws + p.z) : nullptr, l.vp = p.vp;
     l.part = reinterpret_cast<float*>(ws + p.part), l.z_label = reinterpret_cast<float*>(ws + p.z_label);
     HEAD_TRY(head_launch_sums(l, p.shape, c.second, s));
     if (c.rows <= 256)
-      hipLaunchKernelGGL(head_loss_kernel<1>, dim3(static_cast<unsigned>(c.rows)), dim3(256), 0, s, c, r, l.part, p.np,
-                         static_cast<int>(p.tiles), l.z_label);
+      hipLaunchKernelGGL(head_loss_kernel<1>, dim3(static_cast<unsigned>(p.np)), dim3(256), 0, s, c, r, l.part, p.np,
+                         static_cast<int>(p.tiles), l.z_label, factors, taught);
     else
-      hipLaunchKernelGGL(head_loss_kernel<16>, dim3(static_cast<unsigned>((c.rows + 15) / 16)), dim3(256), 0, s, c, r, l.part,
-                         p.np, static_cast<int>(p.tiles), l.z_label);
+      hipLaunchKernelGGL(head_loss_kernel<16>, dim3(static_cast<unsigned>(p.np / 16)), dim3(256), 0, s, c, r, l.part,
+                         p.np, static_cast<int>(p.tiles), l.z_label, factors, taught);
     HEAD_TRY(hipGetLastError());
   }
   if (what == FWD) return MONARCH_OK;
-  HeadRow* factors = reinterpret_cast<HeadRow*>(ws + p.factors);
-  float* taught = reinterpret_cast<float*>(ws + p.taught);
-  hipLaunchKernelGGL(head_factors_kernel, dim3(static_cast<unsigned>(p.np / 256)), dim3(256), 0, s, c, r, factors, taught);
-  HEAD_TRY(hipGetLastError());
+  if (what == BWD) {
+    hipLaunchKernelGGL(head_factors_kernel, dim3(static_cast<unsigned>(p.np / 256)), dim3(256), 0, s, c, r, factors, taught);
+    HEAD_TRY(hipGetLastError());
+  }
   uint16_t* g = reinterpret_cast<uint16_t*>(ws + p.g);
   l.row = factors, l.g = g, l.vp = p.vp, l.g_plane = p.np * p.vp;
   HeadDx x = {};
@@ -660,7 +743,13 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
   for (int64_t v0 = 0; v0 < c.vocab; v0 += p.vp) {
     const int64_t v1 = v0 + p.vp < c.vocab ? v0 + p.vp : c.vocab;
     l.v0 = v0, l.v1 = v1;
-    HEAD_TRY(head_launch_grad(l, p.shape, c.second, s));
+    if (p.keep) {
+      hipLaunchKernelGGL(head_few_kernel, dim3(static_cast<unsigned>((p.vp / 4 + 255) / 256), kPipeK), dim3(256), 0, s, c, r, factors,
+                         l.z, p.vp, g, p.vp, l.g_plane);
+      HEAD_TRY(hipGetLastError());
+    } else {
+      HEAD_TRY(head_launch_grad(l, p.shape, c.second, s));
+    }
     if (c.taught) {
       hipLaunchKernelGGL(head_taught_kernel, dim3(static_cast<unsigned>(c.rows)), dim3(64), static_cast<size_t>(c.top) * 8, s, c,
                          r, factors, taught, g, p.vp, l.g_plane, static_cast<int>(p.planes), v0, v1);
@@ -683,15 +772,7 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
       HEAD_TRY(hipGetLastError());
     }
   }
-  const int64_t n = (c.rows * ((p.d + 3) / 4) + 255) / 256;
-  if (n > 0x7fffffffLL) return record_hip(hipErrorInvalidConfiguration);
-  if (c.bf16)
-    hipLaunchKernelGGL(head_dx_out_kernel<uint16_t>, dim3(static_cast<unsigned>(n)), dim3(256), 0, s, x.part, r.pos, c.rows,
-                       p.np, p.d, p.dp, p.dx_splits, static_cast<uint16_t*>(c.dx));
-  else
-    hipLaunchKernelGGL(head_dx_out_kernel<float>, dim3(static_cast<unsigned>(n)), dim3(256), 0, s, x.part, r.pos, c.rows, p.np,
-                       p.d, p.dp, p.dx_splits, static_cast<float*>(c.dx));
-  return record_hip(hipGetLastError());
+  return record_hip(c.bf16 ? dx_out<uint16_t>(c, p, x.part, r.pos, s) : dx_out<float>(c, p, x.part, r.pos, s));
 }
 
 int call(Call c, int what, const void* stats_in, int64_t top, float temperature, float mix, int dtype, void* workspace,

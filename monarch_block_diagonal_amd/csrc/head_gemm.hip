@@ -179,13 +179,7 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
     for (int mi = 0; mi < S::FM; ++mi) {
       f32x4 g;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float z = acc[mi][ni][v] - r.m;
-        const float e = exp2_of(z * p.ct);
-        g[v] = r.a * e;
-        if constexpr (SECOND == HEAD_OWN) g[v] = fmaf(r.b, exp2_of(z * kLog2e), g[v]);
-        if constexpr (SECOND == HEAD_SQUARE) g[v] = fmaf(r.b * e, e, g[v]);
-      }
+      for (int v = 0; v < 4; ++v) g[v] = head_g<SECOND>(r, acc[mi][ni][v], p.ct, false);
       if (any) {
 #pragma unroll
         for (int v = 0; v < 4; ++v)
@@ -366,11 +360,7 @@ __global__ __launch_bounds__(256) void head_thin_kernel(HeadLogits p, int64_t ru
         f32x4 g;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const float z = acc[b][v] - r[b].m, e = exp2_of(z * p.ct);
-          g[v] = r[b].a * e;
-          if constexpr (SECOND == HEAD_OWN) g[v] = fmaf(r[b].b, exp2_of(z * kLog2e), g[v]);
-          if constexpr (SECOND == HEAD_SQUARE) g[v] = fmaf(r[b].b * e, e, g[v]);
-          if (own == v) g[v] -= r[b].off;
+          g[v] = head_g<SECOND>(r[b], acc[b][v], p.ct, own == v);
           if (vw + v >= end) g[v] = 0.f;
         }
         // a gradient's runs are whole tiles, as K tiles of dx's are (behind the last word g has room)
@@ -389,6 +379,7 @@ __global__ __launch_bounds__(256) void head_thin_kernel(HeadLogits p, int64_t ru
           if (vw + v >= end) acc[b][v] = -INFINITY;
           if (own == v && vw + v < end) p.z_label[n] = acc[b][v];
         }
+        if (p.z && vw < end) *reinterpret_cast<f32x4*>(p.z + n * p.vp + (vw - p.v0)) = acc[b];
         const float to = fmaxf(fmaxf(fmaxf(m[b], acc[b][0]), fmaxf(acc[b][1], acc[b][2])), acc[b][3]);
         st[b] *= exp2_of((m[b] - to) * p.ct);
         if constexpr (SECOND != HEAD_ONE) s1[b] *= exp2_of((m[b] - to) * kLog2e);
@@ -606,6 +597,7 @@ hipError_t products(HeadDx x, HeadDw w, hipStream_t st) {
 }  // namespace
 
 int64_t head_tile_words(HeadShape s, int64_t vocab) { return s == HEAD_THIN ? thin_run(vocab, 16) : s == HEAD_256 ? Shape256::BM : s == HEAD_128 ? Shape128::BM : Shape32::BM; }
+int64_t head_tile_features(HeadShape s) { return s == HEAD_256 ? Shape256::BM : s == HEAD_128 ? Shape128::BM : Shape32::BM; }
 int64_t head_tile_rows(HeadShape s) { return s == HEAD_256 ? Shape256::BN : s == HEAD_128 ? Shape128::BN : Shape32::BN; }
 
 hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st) {
