@@ -433,12 +433,14 @@ int monarch_distill_step(const void* logits, int64_t ld, const void* teacher, co
  *   features <= 2^20, vocab <= 2^30, top <= MONARCH_DISTILL_MAX_TOP.
  *   loss fp32 [rows]; labels int64 [rows]; teacher fp32, ids int64 [rows, top];
  *   stats: monarch_head_stats_bytes, written by the forward pass for the backward pass.
- *   workspace: monarch_head_workspace_bytes of the call (0 forward, 1 backward, 2 step): a copy
- *   of x, in fp32 or with features % 8 != 0 one of w, a piece of the vocabulary's gradient
- *   of the logits (at most 2 GiB, or 256 words of it) and partial sums (at most 1 GiB each, or one sum). The calls keep nothing else of size rows * vocab.
- * Logits and all sums are fp32 (fp32 operands are multiplied as three bf16 parts each,
- * exact to 2^-23 of a product). In bf16 the gradient of the logits is rounded to bf16 between its
- * products; dx and dw are rounded once. Sums run in a fixed order.
+ *   workspace: monarch_head_workspace_bytes of the call (0 forward, 1 backward, 2 step): a
+ *   copy of x, in fp32 or with features % 8 != 0 one of w, a piece of the vocabulary's gradient of
+ *   the logits (at most 2 GiB, or 256 words of it) and partial sums (at most 1 GiB each, or
+ *   one sum). Nothing else is of size rows * vocab, but that a step of at most 32 rows
+ *   holds their logits until it is done (128 bytes a word, where it would read the head again).
+ * Logits and all sums are fp32 (fp32 operands are multiplied as three bf16 parts each, exact to
+ * 2^-23 of a product; parts under 2^-126 count as 0). In bf16 the gradient of the logits is
+ * rounded to bf16 between its products; dx and dw are rounded once. Sums run in a fixed order.
  *
  * monarch_head_bwd: dx and dw from dloss (fp32 [rows]) and the forward's inputs and
  * stats. monarch_head_step: loss, dx and dw for row_weight (fp32 [rows], NULL: 1) in dloss's

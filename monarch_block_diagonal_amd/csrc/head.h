@@ -25,6 +25,12 @@ enum HeadSecond {
   HEAD_SQUARE = 2   // T = 2: e^z is the square of e^(z/2)
 };
 
+// A finite value's nearest that is finite in bf16 too (the largest ones of fp32 round to infinity).
+__device__ __forceinline__ float finite_bf16(float v) {
+  constexpr float kMost = 3.38953138925153547590e38f;
+  return isfinite(v) ? __builtin_amdgcn_fmed3f(v, -kMost, kMost) : v;
+}
+
 // g of one logit; operations and roundings are the same wherever it is computed.
 template <int SECOND>
 __device__ __forceinline__ float head_g(const HeadRow& r, float logit, float ct, bool label) {

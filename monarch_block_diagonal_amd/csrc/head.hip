@@ -164,7 +164,7 @@ __global__ __launch_bounds__(1024) void head_rows_kernel(Call c, Rows r, uint32_
 
 // One value as bf16, and what is left of it.
 __device__ __forceinline__ uint16_t next_part(float& v) {
-  const uint16_t h = f32_to_bf16(v);
+  const uint16_t h = f32_to_bf16(finite_bf16(v));
   v = isfinite(v) ? v - bf16_to_f32(h) : 0.f;
   return h;
 }
@@ -676,7 +676,7 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
     hipLaunchKernelGGL(head_flag_kernel, dim3(static_cast<unsigned>((c.rows + 3) / 4)), dim3(256), 0, s, c, r);
     HEAD_TRY(hipGetLastError());
   }
-  const bool few = c.bf16 && c.rows <= 32;
+  const bool few = c.bf16 && c.rows <= kThinRows && c.d <= 4096;   // one workgroup's copy
   hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, s, c, r, head, few ? xc : nullptr, p.dp);
   HEAD_TRY(hipGetLastError());
   const int64_t xplane = p.np * p.dp, wplane = (c.vocab + kPipeK) * p.dp;

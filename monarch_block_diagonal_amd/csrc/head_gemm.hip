@@ -133,9 +133,14 @@ __global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t 
   }
 }
 
+// Four fp32 values as bf16.
+__device__ __forceinline__ u32x2 rounded(const f32x4& v) {
+  return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
 // Four fp32 values as bf16, and what is left of them (the next plane's).
 __device__ __forceinline__ u32x2 next_plane(f32x4& v) {
-  const u32x2 r = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  const u32x2 r = {pack_bf16x2(finite_bf16(v[0]), finite_bf16(v[1])), pack_bf16x2(finite_bf16(v[2]), finite_bf16(v[3]))};
   const float hi[4] = {__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u),
                        __uint_as_float(r[1] << 16), __uint_as_float(r[1] & 0xffff0000u)};
 #pragma unroll
@@ -200,7 +205,7 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
     for (int ni = 0; ni < S::FN; ++ni)
 #pragma unroll
       for (int mi = 0; mi < S::FM; ++mi) {
-        const u32x2 w = next_plane(acc[mi][ni]);
+        const u32x2 w = F32 ? next_plane(acc[mi][ni]) : rounded(acc[mi][ni]);
         *reinterpret_cast<u32x2*>(lds + staged<S::BM>((wn * S::FN + ni) * 16 + l15, (wm * S::FM + mi) * 16 + 4 * lh)) = w;
       }
     __syncthreads();
@@ -367,7 +372,7 @@ __global__ __launch_bounds__(256) void head_thin_kernel(HeadLogits p, int64_t ru
         uint16_t* o = p.g + n * p.vp + (vw - p.v0);
 #pragma unroll
         for (int q = 0; q < (F32 ? 3 : 1); ++q) {
-          *reinterpret_cast<u32x2*>(o) = next_plane(g);
+          *reinterpret_cast<u32x2*>(o) = F32 ? next_plane(g) : rounded(g);
           // a K tile of dw's is 64 rows: the other ones are 0
 #pragma unroll
           for (int z = 16 * NB; z < kPipeK; z += 16 * NB) *reinterpret_cast<u32x2*>(o + z * p.vp) = u32x2{0, 0};

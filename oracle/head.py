@@ -77,7 +77,9 @@ def bounds(o: Head, x, w, rounding: float, T=1.0):
     """(loss, dx, dw): how far fp32 sums and one rounding of g and of each result may be off.
 
     A logit: every addition of its sum rounds by at most 2^-24 of the absolute terms, and parts of
-    fp32 operands leave out 2^-23 of them: e_z = (d + 2) 2^-24 s_z. A loss moves by two logits and by
+    fp32 operands leave out 2^-23 of them: e_z = (d + 2) 2^-24 s_z. Parts under bf16's least normal value
+    2^-126 may count as 0: an operand v = v0 + v1 + v2 is then off by |v1| + |v2| < 2^-125 at
+    most, and a product x w by 2^-125 (|x| + |w|), which e_z has as well. A loss moves by two logits and by
     2e-5 of its absolute terms (sums of exponentials of up to 2^17 terms joined in runs of at most
     256, and the logarithms). A value of g moves by 2 e_z / min(T, 1) of its absolute terms and by 3e-5 of
     them besides, and is rounded once (`rounding`, 0 where it is not). dx and dw add these up with their
@@ -87,6 +89,8 @@ def bounds(o: Head, x, w, rounding: float, T=1.0):
     vocab = w.shape[0]
     x, w = torch.where(o.used[:, None], x.double(), 0.0), w.double()
     e_z = (d + 2) * 2.0 ** -24 * o.s_z
+    if not rounding:
+        e_z = e_z + 2.0 ** -125 * (x.abs().sum(dim=1) + w.abs().sum(dim=1).max())
     loss = 2 * e_z * max(T, 1.0) + 2e-5 * o.s_loss
     e_g = (2 * e_z / min(T, 1.0) + 3e-5)[:, None] * o.s_g + max(rounding, 2.0 ** -23) * o.g.abs()
     top = (o.g.abs() + e_g)

@@ -151,6 +151,19 @@ def test_far_logits(api):
         check(api, x, w, labels, t, ids, r, 1.0, 0.5)
 
 
+@pytest.mark.parametrize("rows", [5, 200])
+def test_largest_fp32_values(api, rows):
+    """Features at the end of fp32's range (they round to infinity in bf16) against words that are 0 or tiny there."""
+    x, w, labels, _, _, r = draw(rows, 64, 500, F32)
+    big = torch.finfo(F32).max
+    x[:, 3] = big * torch.where(torch.arange(rows, device="cuda") % 2 == 0, 1.0, -1.0)
+    w[:, 3] = torch.where(torch.arange(500, device="cuda") % 3 == 0, 0.0, 1e-38)
+    o = H.head(x, w, labels, None, None, r)
+    loss, dx, dw = api.head_loss_step(x, w, labels, row_weight=r)
+    near(loss, o.loss, H.bounds(o, x, w, 0.0)[0], "loss")
+    near(dx, o.dx, H.bounds(o, x, w, 0.0)[1], "dx")
+
+
 def test_rows_apart_and_unaligned(api):
     """Rows of x that lie apart or off 16-byte boundaries (a position of every sequence)."""
     for dtype in (F32, BF16):
