@@ -439,8 +439,9 @@ int monarch_distill_step(const void* logits, int64_t ld, const void* teacher, co
  *   one sum). Nothing else is of size rows * vocab, but that a step of at most 32 rows
  *   holds their logits until it is done (128 bytes a word, where it would read the head again).
  * Logits and all sums are fp32 (fp32 operands are multiplied as three bf16 parts each, exact to
- * 2^-23 of a product; parts under 2^-126 count as 0). In bf16 the gradient of the logits is
- * rounded to bf16 between its products; dx and dw are rounded once. Sums run in a fixed order.
+ * 2^-23 of a product; parts under 2^-126 count as 0). In bf16 the gradient of the logits,
+ * over the largest weight (dloss) of a row, is rounded to bf16 between its products (up to 64 rows: to two
+ * bf16 parts); dx and dw are rounded once. Sums run in a fixed order.
  *
  * monarch_head_bwd: dx and dw from dloss (fp32 [rows]) and the forward's inputs and
  * stats. monarch_head_step: loss, dx and dw for row_weight (fp32 [rows], NULL: 1) in dloss's

@@ -189,9 +189,18 @@ struct PipeShape {
   static constexpr int LDS = STAGE * NST;
 };
 
+// Sets a workgroup's sums to 0.
+template <class S>
+__device__ __forceinline__ void pipe_clear(f32x4 (&acc)[S::FM][S::FN]) {
+#pragma unroll
+  for (int mi = 0; mi < S::FM; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < S::FN; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
 // acc[mi][ni], lane l: rows m0 + (wm*FM + mi)*16 + 4*(l/16) + v, column n0 + (wn*FN + ni)*16 + l%16.
-// Sums k in [kb, ke) (kb a multiple of 64). Only a's k may end inside the last tile. Ends with a
-// barrier: `lds` is free.
+// Adds the products of k in [kb, ke) (kb a multiple of 64) to acc. Only a's k may end inside the last
+// tile. Ends with a barrier: `lds` is free.
 template <class S, bool AKM, bool BKM>
 __device__ __forceinline__ void pipe_product_bf16(const PipeProduct& p, int64_t m0, int64_t n0, int64_t kb, int64_t ke,
                                              char* lds, f32x4 (&acc)[S::FM][S::FN]) {
@@ -200,10 +209,6 @@ __device__ __forceinline__ void pipe_product_bf16(const PipeProduct& p, int64_t 
   constexpr int NI = TA::PER + TB::PER, FM = S::FM, FN = S::FN, NST = S::NST;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
-#pragma unroll
-  for (int mi = 0; mi < FM; ++mi)
-#pragma unroll
-    for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int ntiles = ke > kb ? static_cast<int>((ke - kb + kPipeK - 1) / kPipeK) : 0;
   if (ntiles == 0) return;
   TA a;
@@ -325,10 +330,6 @@ __device__ __forceinline__ void pipe_product_f32(const PipeProduct& p, int64_t m
   static_assert(2 * (TA::BYTES + TB::BYTES) <= S::LDS, "two tiles of each operand");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
-#pragma unroll
-  for (int mi = 0; mi < FM; ++mi)
-#pragma unroll
-    for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int ktiles = ke > kb ? static_cast<int>((ke - kb + kPipeK - 1) / kPipeK) : 0;
   if (ktiles == 0) return;
   TA a;

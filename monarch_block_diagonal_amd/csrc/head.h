@@ -62,11 +62,12 @@ struct HeadLogits {
   const HeadRow* row;
   uint16_t* g;
   int64_t vp, g_plane;
+  int fold;                   // bf16, few rows: g has two parts, the second one's rows `fold` behind the first's; or 0
 };
 
 struct HeadDx {
   PipeProduct pr;             // A: the head's words [v][d], B: g [n][v]
-  const int* count;
+  const int* count;           // rows of g in use
   int f32;
   int64_t d, dp, np;
   int64_t k, chunk;           // words of this piece, words a split
@@ -80,6 +81,7 @@ struct HeadDw {
   PipeProduct pr;             // A: the rows [n][d], B: g [n][v]
   const int* count;
   int f32;
+  const float* scale;         // what g was divided by (bf16)
   int64_t d, dp, cols;        // cols: words of this piece
   int splits;
   float* part;                // [splits][cols][dp], or null:

@@ -15,6 +15,13 @@
 // the rows that do are first copied side by side, with their columns padded to whole K
 // tiles; what a row left out holds (NaN too) reaches nothing.
 //
+// In bf16 g is divided by the largest weight of a row and multiplied back in its products' fp32 sums: the
+// labels' elements, nearly all of g, are then 1 - s[c] or a little less, whose rounding to bf16 is
+// half of that of a value just over a power of two (as 1 / rows may be, alike for every row). Up to 64 rows, where
+// single roundings do not average out, g is held in two bf16 parts: the second one's rows lie behind the first's
+// (32 or 64 of them), x's rows are copied twice, and the products take them as that many more rows: dw's K tiles and dx's
+// output tiles have the room, and the head is read no more often.
+//
 // The teacher's columns of g are few: their logits are taken from products of their
 // own in the forward pass (a wave an entry), and each is written again behind the piece's
 // epilogue with its share of p, once, in fp32 up to its one rounding.
@@ -44,6 +51,9 @@ struct Rows {
   int* label;    // [np] label, -1 without one
   int* has;      // [np] whether the row has a valid entry
   int* flag;     // [rows] whether it has (before the rows are counted)
+  float* scale;  // what g is divided by
+  int* g_rows;   // rows of g in use
+  int fold;      // 0, or the rows of one of g's two parts
 };
 
 struct Call {
@@ -105,6 +115,7 @@ __global__ __launch_bounds__(1024) void head_rows_kernel(Call c, Rows r, uint32_
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (threadIdx.x < 4) zeros[threadIdx.x] = 0;
   int base = 0;
+  float most = 0.f;   // weight of a row in use
   for (int64_t first = 0; first < c.rows; first += 1024 * PER) {
     int label[PER], has[PER], mine = 0;
 #pragma unroll
@@ -142,6 +153,8 @@ __global__ __launch_bounds__(1024) void head_rows_kernel(Call c, Rows r, uint32_
       const bool used = label[e] >= 0 || has[e];
       r.pos[i] = used ? at : -1;
       if (used) {
+        const float w = c.weight ? fabsf(c.weight[i]) : 1.f;
+        if (isfinite(w)) most = fmaxf(most, w);
         r.idx[at] = static_cast<int>(i), r.label[at] = label[e], r.has[at] = has[e];
         ++at;
       } else if (c.loss) {
@@ -154,11 +167,24 @@ __global__ __launch_bounds__(1024) void head_rows_kernel(Call c, Rows r, uint32_
   // the last tile's other rows
   const int end = (base + static_cast<int>(kHeadRows) - 1) / static_cast<int>(kHeadRows) * static_cast<int>(kHeadRows);
   for (int k = base + threadIdx.x; k < end; k += 1024) r.idx[k] = 0, r.label[k] = -1, r.has[k] = 0;
-  if (threadIdx.x == 0) *r.count = base;
+  most = lanes_reduce<MaxOp, 64>(most);
+  __shared__ float s_most[16];
+  if (lane == 0) s_most[wave] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    *r.count = base;
+    *r.g_rows = r.fold && base > 0 ? 2 * r.fold : base;
+    for (int w = 0; w < 16; ++w) most = fmaxf(most, s_most[w]);
+    most *= fmaxf(c.told ? 1.0f - c.mix : 0.f, c.taught ? c.mix * c.temperature : 0.f);
+    *r.scale = c.bf16 && most > 1e-30f && most < 1e30f ? most : 1.f;
+  }
   if (xc) {
     __syncthreads();
-    // a wave a row at a time; 64 rows are a K tile of dw's
-    for (int k = wave; k < kPipeK; k += 16) copy_row<64>(static_cast<const uint16_t*>(c.x) + (k < base ? r.idx[k] : 0) * c.ldx, k >= base, c.d, dp, xc + k * dp, lane);
+    // a wave a row at a time, both parts' rows of g
+    for (int k = wave; k < 2 * r.fold; k += 16) {
+      const int from = k % r.fold;
+      copy_row<64>(static_cast<const uint16_t*>(c.x) + (from < base ? r.idx[from] : 0) * c.ldx, from >= base, c.d, dp, xc + k * dp, lane);
+    }
   }
 }
 
@@ -170,24 +196,24 @@ __device__ __forceinline__ uint16_t next_part(float& v) {
 }
 
 // Rows of d elements copied to rows of dp, zeros behind them; fp32 as three bf16 planes.
-// With idx the rows are idx[k] for k < *count, then zeros up to the next whole tile;
-// without, k for k < rows, zeros behind. A workgroup a row.
+// With idx the rows are idx[k] for k < *count, then zeros up to the next whole tile (with
+// fold, the first `fold` of these twice); without, k for k < rows, zeros behind. A workgroup a row.
 template <typename T>
 __global__ __launch_bounds__(256) void head_copy_kernel(const T* __restrict__ src, int64_t ld, const int* idx,
-                                                        const int* count, int64_t rows, int64_t d, int64_t dp,
+                                                        const int* count, int fold, int64_t rows, int64_t d, int64_t dp,
                                                         uint16_t* __restrict__ dst, int64_t plane) {
   constexpr bool F32 = sizeof(T) == 4;
-  const int64_t k = blockIdx.x;
+  const int64_t to = blockIdx.x, k = fold && to < 2 * fold ? to % fold : to;
   bool zero = k >= rows;
   int64_t row = zero ? 0 : k;
   if (idx) {
     const int n = *count;
-    if (k >= (n + kHeadRows - 1) / kHeadRows * kHeadRows) return;
+    if (to >= (n + kHeadRows - 1) / kHeadRows * kHeadRows) return;
     zero = k >= n;
     row = zero ? 0 : idx[k];
   }
   const T* s = src + row * ld;
-  uint16_t* o = dst + k * dp;
+  uint16_t* o = dst + to * dp;
   if constexpr (F32) {
     const bool whole = ((reinterpret_cast<uintptr_t>(s) & 15) == 0) && d % 4 == 0;
     for (int64_t e = threadIdx.x * 4; e < dp; e += 1024) {
@@ -284,7 +310,7 @@ __device__ __forceinline__ void teacher_sums(const Call& c, int64_t i, int lane,
 __device__ __forceinline__ void row_factors(const Call& c, const Rows& r, int64_t k, int64_t i, float m, float st, float s1,
                                             HeadRow* out, float* taught) {
   HeadRow o;
-  const float w = c.weight ? c.weight[i] : 1.0f;
+  const float w = (c.weight ? c.weight[i] : 1.0f) / *r.scale;
   const float a = r.has[k] ? c.mix * c.temperature * w : 0.f;
   o.m = m;
   o.off = r.label[k] >= 0 ? (1.0f - c.mix) * w : 0.f;
@@ -386,12 +412,12 @@ __global__ __launch_bounds__(256) void head_factors_kernel(Call c, Rows r, HeadR
 }
 
 // g of few rows (HEAD_THIN) from their logits, which a step keeps for its length: they are smaller than
-// the head, which would be read again for them. Four words a thread, the 64 rows of a K tile of dw's.
+// the head, which would be read again for them. Four words a thread, all rows of a K tile of dw's.
 __global__ __launch_bounds__(256) void head_few_kernel(Call c, Rows r, const HeadRow* __restrict__ rows,
                                                        const float* __restrict__ z, int64_t zp, uint16_t* __restrict__ g,
                                                        int64_t vp, int64_t plane) {
   const int64_t v = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  const int n = blockIdx.y, planes = c.bf16 ? 1 : 3;
+  const int n = blockIdx.y, planes = c.bf16 ? 2 : 3;
   if (v >= vp) return;
   float o[4] = {0.f, 0.f, 0.f, 0.f};
   if (n < *r.count) {
@@ -460,11 +486,11 @@ __global__ __launch_bounds__(64) void head_taught_kernel(Call c, Rows r, const H
 }
 
 // dx of every row from the splits' sums; rows left out get 0. Four columns a thread, SL threads
-// that share the splits (many of them, where rows are few: 64 splits of 8 x 768 11 -> @@ us).
+// that share the splits (many of them, where rows are few: 64 splits of 8 x 768 11 us with one thread, 5 with 16).
 template <typename T, int SL>
 __global__ __launch_bounds__(256) void head_dx_out_kernel(const float* __restrict__ part, const int* __restrict__ pos,
                                                           int64_t rows, int64_t np, int64_t d, int64_t dp, int splits,
-                                                          T* __restrict__ dx) {
+                                                          int fold, const float* __restrict__ scale, T* __restrict__ dx) {
   constexpr int OUT = 256 / SL;
   const int64_t per = (d + 3) / 4, at = static_cast<int64_t>(blockIdx.x) * OUT + threadIdx.x % OUT;
   const int slice = threadIdx.x / OUT;
@@ -475,7 +501,10 @@ __global__ __launch_bounds__(256) void head_dx_out_kernel(const float* __restric
     i = at / per, e = (at - i * per) * 4;
     const int64_t k = pos[i];
     if (k >= 0)
-      for (int s = slice; s < splits; s += SL) v += *reinterpret_cast<const f32x4*>(part + (s * np + k) * dp + e);
+      for (int s = slice; s < splits; s += SL) {
+        v += *reinterpret_cast<const f32x4*>(part + (s * np + k) * dp + e);
+        if (fold) v += *reinterpret_cast<const f32x4*>(part + (s * np + k + fold) * dp + e);
+      }
   }
   if constexpr (SL > 1) {
     __shared__ f32x4 sums[256];
@@ -486,6 +515,7 @@ __global__ __launch_bounds__(256) void head_dx_out_kernel(const float* __restric
     for (int s = 1; s < SL; ++s) v += sums[s * OUT + threadIdx.x];
   }
   if (!in) return;
+  v *= *scale;
   T* o = dx + i * d + e;
   if (d % 4 == 0) {
     if constexpr (sizeof(T) == 2)
@@ -502,12 +532,14 @@ __global__ __launch_bounds__(256) void head_dx_out_kernel(const float* __restric
 // A piece's dw from the splits' sums.
 template <typename T>
 __global__ __launch_bounds__(256) void head_dw_out_kernel(const float* __restrict__ part, int64_t cols, int64_t d,
-                                                          int64_t dp, int splits, T* __restrict__ dw) {
+                                                          int64_t dp, int splits, const float* __restrict__ scale,
+                                                          T* __restrict__ dw) {
   const int64_t per = (d + 3) / 4, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (at >= cols * per) return;
   const int64_t v = at / per, e = (at - v * per) * 4;
   f32x4 a = {0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < splits; ++s) a += *reinterpret_cast<const f32x4*>(part + (s * cols + v) * dp + e);
+  a *= *scale;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     if (e + q < d) Io<T>::store(dw, v * d + e + q, a[q]);
@@ -522,6 +554,7 @@ int64_t tiles_of(int64_t v, int64_t tile) { return (v + tile - 1) / tile; }
 
 struct HeadPlan {
   int64_t d, dp, np, planes;
+  int fold;                    // bf16, few rows: rows of one of g's two parts
   bool copy_w;                 // the head is copied (fp32, or rows that are no whole pieces)
   HeadShape shape, products;   // of the logits, and of dx and dw
   int64_t tiles;               // of words, forward
@@ -551,6 +584,7 @@ double done_at(int64_t slots, int64_t first, double a, int64_t more, double b) {
 HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top, bool bf16) {
   HeadPlan p = {};
   p.d = d, p.dp = up(d, kPipeK), p.np = up(rows, kHeadRows), p.planes = bf16 ? 1 : 3;
+  p.fold = !bf16 || rows > 64 ? 0 : rows <= kThinRows ? static_cast<int>(kThinRows) : 64;
   p.copy_w = !bf16 || d % 8 != 0;
   // Rounds of 256 x 256 tiles (one a CU) against rounds of 128 x 128 tiles (two a CU), which take 0.6 of the
   // time: measured, 4096 x 768 x 50257 bf16 1368 us with the first and 1456 with the second (13 and 25
@@ -586,7 +620,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
     // (fp32 5370, 5999); 1000 x 625 x 10000 fp32 365 us, with 128 x 128 330
     const bool wide = rows > 128 && d > 128 && static_cast<double>(rows) * vocab * d >= 2e10;
     p.products = rows <= 32 ? HEAD_32 : wide ? HEAD_256 : HEAD_128;
-    const int64_t xm = head_tile_features(p.products), xn = head_tile_rows(p.products);
+    const int64_t xm = head_tile_features(p.products), xn = p.fold ? 128 : head_tile_rows(p.products);   // one tile of few rows
     const int64_t wm = wide ? 256 : 128;
     const int64_t slots = wide ? 256 : 512;
     const int64_t dx_tiles = tiles_of(d, xm) * tiles_of(rows, xn), dw_tiles = tiles_of(d, wm) * tiles_of(p.vp, wm);
@@ -639,25 +673,25 @@ bool off_elements(const void* p, int size) { return reinterpret_cast<uintptr_t>(
   } while (0)
 
 template <typename T>
-hipError_t copy_rows(const void* src, int64_t ld, const int* idx, const int* count, int64_t rows, int64_t grid, int64_t d,
+hipError_t copy_rows(const void* src, int64_t ld, const int* idx, const int* count, int fold, int64_t rows, int64_t grid, int64_t d,
                      int64_t dp, void* dst, int64_t plane, hipStream_t s) {
   hipLaunchKernelGGL(head_copy_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, static_cast<const T*>(src), ld,
-                     idx, count, rows, d, dp, static_cast<uint16_t*>(dst), plane);
+                     idx, count, fold, rows, d, dp, static_cast<uint16_t*>(dst), plane);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t dx_out(const Call& c, const HeadPlan& p, const float* part, const int* pos, hipStream_t s) {
+hipError_t dx_out(const Call& c, const HeadPlan& p, const float* part, const Rows& r, hipStream_t s) {
   const int64_t n = c.rows * ((p.d + 3) / 4);
   const int sl = p.dx_splits >= 16 ? 16 : 1;
   const int64_t grid = (n + 256 / sl - 1) / (256 / sl);
   if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
   if (sl == 16)
-    hipLaunchKernelGGL((head_dx_out_kernel<T, 16>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, pos, c.rows, p.np,
-                       p.d, p.dp, p.dx_splits, static_cast<T*>(c.dx));
+    hipLaunchKernelGGL((head_dx_out_kernel<T, 16>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, r.pos, c.rows, p.np,
+                       p.d, p.dp, p.dx_splits, r.fold, r.scale, static_cast<T*>(c.dx));
   else
-    hipLaunchKernelGGL((head_dx_out_kernel<T, 1>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, pos, c.rows, p.np,
-                       p.d, p.dp, p.dx_splits, static_cast<T*>(c.dx));
+    hipLaunchKernelGGL((head_dx_out_kernel<T, 1>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, r.pos, c.rows, p.np,
+                       p.d, p.dp, p.dx_splits, r.fold, r.scale, static_cast<T*>(c.dx));
   return hipGetLastError();
 }
 
@@ -666,6 +700,9 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
   Rows r;
   uint32_t* head = reinterpret_cast<uint32_t*>(ws + p.rows);   // 16 bytes of zeros, the count
   r.count = reinterpret_cast<int*>(head + 4);
+  r.scale = reinterpret_cast<float*>(head + 5);
+  r.g_rows = reinterpret_cast<int*>(head + 6);
+  r.fold = p.fold;
   r.idx = reinterpret_cast<int*>(head + 64);
   r.label = r.idx + p.np;
   r.has = r.label + p.np;
@@ -681,13 +718,13 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
   HEAD_TRY(hipGetLastError());
   const int64_t xplane = p.np * p.dp, wplane = (c.vocab + kPipeK) * p.dp;
   if (!few)
-    HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.x, c.ldx, r.idx, r.count, c.rows, p.np, p.d, p.dp, xc, xplane, s)
-                  : copy_rows<float>(c.x, c.ldx, r.idx, r.count, c.rows, p.np, p.d, p.dp, xc, xplane, s));
+    HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.x, c.ldx, r.idx, r.count, r.fold, c.rows, p.np, p.d, p.dp, xc, xplane, s)
+                  : copy_rows<float>(c.x, c.ldx, r.idx, r.count, r.fold, c.rows, p.np, p.d, p.dp, xc, xplane, s));
   const uint16_t* w = static_cast<const uint16_t*>(c.w);
   int64_t ldw = p.d;
   if (p.copy_w) {
-    HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.w, p.d, nullptr, nullptr, c.vocab, c.vocab + kPipeK, p.d, p.dp, ws + p.w, wplane, s)
-                    : copy_rows<float>(c.w, p.d, nullptr, nullptr, c.vocab, c.vocab + kPipeK, p.d, p.dp, ws + p.w, wplane, s));
+    HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.w, p.d, nullptr, nullptr, 0, c.vocab, c.vocab + kPipeK, p.d, p.dp, ws + p.w, wplane, s)
+                    : copy_rows<float>(c.w, p.d, nullptr, nullptr, 0, c.vocab, c.vocab + kPipeK, p.d, p.dp, ws + p.w, wplane, s));
     w = reinterpret_cast<const uint16_t*>(ws + p.w);
     ldw = p.dp;
   }
@@ -727,24 +764,24 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
     HEAD_TRY(hipGetLastError());
   }
   uint16_t* g = reinterpret_cast<uint16_t*>(ws + p.g);
-  l.row = factors, l.g = g, l.vp = p.vp, l.g_plane = p.np * p.vp;
+  l.row = factors, l.g = g, l.vp = p.vp, l.g_plane = (p.fold ? p.fold : p.np) * p.vp, l.fold = p.fold;
   HeadDx x = {};
   x.pr.zeros = l.pr.zeros, x.f32 = l.f32;
   x.pr.b.p = g, x.pr.b.ld = p.vp, x.pr.b.plane = l.g_plane, x.pr.b.rows = p.np;
-  x.count = r.count, x.d = p.d, x.dp = p.dp, x.np = p.np, x.chunk = p.dx_chunk, x.splits = p.dx_splits;
+  x.count = r.g_rows, x.d = p.d, x.dp = p.dp, x.np = p.np, x.chunk = p.dx_chunk, x.splits = p.dx_splits;
   x.part = reinterpret_cast<float*>(ws + p.dx);
   HeadDw y = {};
-  y.pr.zeros = l.pr.zeros, y.f32 = l.f32;
+  y.pr.zeros = l.pr.zeros, y.f32 = l.f32, y.scale = r.scale;
   y.pr.a.p = xc, y.pr.a.ld = p.dp, y.pr.a.plane = xplane, y.pr.a.rows = p.dp, y.pr.a.kvalid = p.np;
   y.pr.b.p = g, y.pr.b.ld = p.vp, y.pr.b.plane = l.g_plane, y.pr.b.rows = p.vp, y.pr.b.kvalid = p.np;
-  y.count = r.count, y.d = p.d, y.dp = p.dp, y.splits = p.dw_splits;
+  y.count = r.g_rows, y.d = p.d, y.dp = p.dp, y.splits = p.dw_splits;
   y.part = p.dw_splits > 1 ? reinterpret_cast<float*>(ws + p.dw) : nullptr;
   const int64_t es = c.bf16 ? 2 : 4;
   for (int64_t v0 = 0; v0 < c.vocab; v0 += p.vp) {
     const int64_t v1 = v0 + p.vp < c.vocab ? v0 + p.vp : c.vocab;
     l.v0 = v0, l.v1 = v1;
     if (p.keep) {
-      hipLaunchKernelGGL(head_few_kernel, dim3(static_cast<unsigned>((p.vp / 4 + 255) / 256), kPipeK), dim3(256), 0, s, c, r, factors,
+      hipLaunchKernelGGL(head_few_kernel, dim3(static_cast<unsigned>((p.vp / 4 + 255) / 256), c.bf16 ? kThinRows : kPipeK), dim3(256), 0, s, c, r, factors,
                          l.z, p.vp, g, p.vp, l.g_plane);
       HEAD_TRY(hipGetLastError());
     } else {
@@ -752,7 +789,7 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
     }
     if (c.taught) {
       hipLaunchKernelGGL(head_taught_kernel, dim3(static_cast<unsigned>(c.rows)), dim3(64), static_cast<size_t>(c.top) * 8, s, c,
-                         r, factors, taught, g, p.vp, l.g_plane, static_cast<int>(p.planes), v0, v1);
+                         r, factors, taught, g, p.vp, l.g_plane, p.fold ? 2 : static_cast<int>(p.planes), v0, v1);
       HEAD_TRY(hipGetLastError());
     }
     x.k = up(v1 - v0, kPipeK);
@@ -765,14 +802,14 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
       const unsigned n = static_cast<unsigned>((y.cols * ((p.d + 3) / 4) + 255) / 256);
       if (c.bf16)
         hipLaunchKernelGGL(head_dw_out_kernel<uint16_t>, dim3(n), dim3(256), 0, s, y.part, y.cols, p.d, p.dp, p.dw_splits,
-                           static_cast<uint16_t*>(y.dw));
+                           r.scale, static_cast<uint16_t*>(y.dw));
       else
         hipLaunchKernelGGL(head_dw_out_kernel<float>, dim3(n), dim3(256), 0, s, y.part, y.cols, p.d, p.dp, p.dw_splits,
-                           static_cast<float*>(y.dw));
+                           r.scale, static_cast<float*>(y.dw));
       HEAD_TRY(hipGetLastError());
     }
   }
-  return record_hip(c.bf16 ? dx_out<uint16_t>(c, p, x.part, r.pos, s) : dx_out<float>(c, p, x.part, r.pos, s));
+  return record_hip(c.bf16 ? dx_out<uint16_t>(c, p, x.part, r, s) : dx_out<float>(c, p, x.part, r, s));
 }
 
 int call(Call c, int what, const void* stats_in, int64_t top, float temperature, float mix, int dtype, void* workspace,

@@ -23,6 +23,7 @@ constexpr float kLowest = -3.402823466e38f;
 using Shape256 = PipeShape<2, 4, 8, 4, 2>;
 using Shape128 = PipeShape<2, 2, 4, 4, 2>;
 using Shape32 = PipeShape<4, 1, 2, 2, 4>;
+using Shape64 = PipeShape<4, 1, 2, 4, 3>;   // dx of few rows in bf16
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -63,6 +64,7 @@ __global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t 
   const int64_t v0 = p.v0 + tv * S::BM, n0 = tn * S::BN;
   if (n0 >= *p.count) return;
   f32x4 acc[S::FM][S::FN];
+  pipe_clear<S>(acc);
   pipe_product<S, false, false, F32>(p.pr, v0, n0, 0, p.d, lds, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -167,6 +169,7 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
   const int64_t v0 = p.v0 + tv * S::BM, n0 = tn * S::BN;
   if (n0 >= *p.count) return;
   f32x4 acc[S::FM][S::FN];
+  pipe_clear<S>(acc);
   pipe_product<S, false, false, F32>(p.pr, v0, n0, 0, p.d, lds, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -198,14 +201,14 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
       acc[mi][ni] = g;
     }
   }
-  constexpr int planes = F32 ? 3 : 1;
+  const int planes = F32 ? 3 : p.fold ? 2 : 1;
   for (int k = 0; k < planes; ++k) {
     if (k > 0) __syncthreads();
 #pragma unroll
     for (int ni = 0; ni < S::FN; ++ni)
 #pragma unroll
       for (int mi = 0; mi < S::FM; ++mi) {
-        const u32x2 w = F32 ? next_plane(acc[mi][ni]) : rounded(acc[mi][ni]);
+        const u32x2 w = F32 || planes > 1 ? next_plane(acc[mi][ni]) : rounded(acc[mi][ni]);
         *reinterpret_cast<u32x2*>(lds + staged<S::BM>((wn * S::FN + ni) * 16 + l15, (wm * S::FM + mi) * 16 + 4 * lh)) = w;
       }
     __syncthreads();
@@ -213,9 +216,10 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
     uint16_t* out = p.g + k * p.g_plane + n0 * p.vp + tv * S::BM;
     for (int c = threadIdx.x; c < S::BN * CH; c += S::NT) {
       const int row = c / CH, e = (c % CH) * 8;
+      if (!F32 && p.fold && n0 + row >= p.fold) continue;   // there the second part's rows lie
       *reinterpret_cast<u32x4*>(out + row * p.vp + e) = *reinterpret_cast<const u32x4*>(lds + staged<S::BM>(row, e));
       // a K tile of dw's is 64 rows: the other ones are 0
-      if constexpr (S::BN < kPipeK) *reinterpret_cast<u32x4*>(out + (S::BN + row) * p.vp + e) = u32x4{0, 0, 0, 0};
+      if constexpr (F32 && S::BN < kPipeK) *reinterpret_cast<u32x4*>(out + (S::BN + row) * p.vp + e) = u32x4{0, 0, 0, 0};
     }
   }
 }
@@ -371,11 +375,11 @@ __global__ __launch_bounds__(256) void head_thin_kernel(HeadLogits p, int64_t ru
         // a gradient's runs are whole tiles, as K tiles of dx's are (behind the last word g has room)
         uint16_t* o = p.g + n * p.vp + (vw - p.v0);
 #pragma unroll
-        for (int q = 0; q < (F32 ? 3 : 1); ++q) {
-          *reinterpret_cast<u32x2*>(o) = F32 ? next_plane(g) : rounded(g);
-          // a K tile of dw's is 64 rows: the other ones are 0
+        for (int q = 0; q < (F32 ? 3 : 2); ++q) {
+          *reinterpret_cast<u32x2*>(o) = next_plane(g);
+          // the other rows of a K tile of dw's (bf16: of the part's half of it) are 0
 #pragma unroll
-          for (int z = 16 * NB; z < kPipeK; z += 16 * NB) *reinterpret_cast<u32x2*>(o + z * p.vp) = u32x2{0, 0};
+          for (int z = 16 * NB; z < (F32 ? kPipeK : kThinRows); z += 16 * NB) *reinterpret_cast<u32x2*>(o + z * p.vp) = u32x2{0, 0};
           o += p.g_plane;
         }
       } else {
@@ -438,6 +442,7 @@ __device__ __forceinline__ void dx_tile(const HeadDx& p, int64_t at, char* lds) 
   if (n0 >= *p.count) return;
   const int64_t kb = split * p.chunk, ke = kb + p.chunk < p.k ? kb + p.chunk : p.k;
   f32x4 acc[S::FM][S::FN];
+  pipe_clear<S>(acc);
   pipe_product<S, true, false, F32>(p.pr, d0, n0, kb, ke, lds, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -468,7 +473,15 @@ __device__ __forceinline__ void dw_tile(const HeadDw& p, int64_t at, char* lds) 
   const int64_t steps = (count + kPipeK - 1) / kPipeK, per = (steps + p.splits - 1) / p.splits;
   const int64_t kb = split * per * kPipeK, end = (split + 1) * per < steps ? (split + 1) * per : steps;
   f32x4 acc[S::FM][S::FN];
+  pipe_clear<S>(acc);
   pipe_product<S, true, true, F32>(p.pr, d0, v0, kb, end * kPipeK, lds, acc);
+  if (!F32 && !p.part) {
+    const float scale = *p.scale;
+#pragma unroll
+    for (int mi = 0; mi < S::FM; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < S::FN; ++ni) acc[mi][ni] *= scale;
+  }
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / S::WN, wn = wave % S::WN, l15 = lane & 15, lh = lane >> 4;
@@ -586,16 +599,13 @@ hipError_t logits(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream
                          : logits<Shape32, GRAD>(a, second, st);
 }
 
-template <class SX, class SW>
+template <class SX, class SW, bool F32>
 hipError_t products(HeadDx x, HeadDw w, hipStream_t st) {
   x.dt = tiles(x.d, SX::BM), x.nt = tiles(x.np, SX::BN);
   w.dt = tiles(w.d, SW::BM), w.vt = tiles(w.cols, SW::BN);
   const int64_t dw_tiles = w.dt * w.vt * w.splits, n = dw_tiles + x.dt * x.nt * x.splits;
   if (hipError_t e = check_grid(n)) return e;
-  if (x.f32)
-    hipLaunchKernelGGL((head_products_kernel<SX, SW, true>), dim3(static_cast<unsigned>(n)), dim3(SX::NT), 0, st, x, w, dw_tiles);
-  else
-    hipLaunchKernelGGL((head_products_kernel<SX, SW, false>), dim3(static_cast<unsigned>(n)), dim3(SX::NT), 0, st, x, w, dw_tiles);
+  hipLaunchKernelGGL((head_products_kernel<SX, SW, F32>), dim3(static_cast<unsigned>(n)), dim3(SX::NT), 0, st, x, w, dw_tiles);
   return hipGetLastError();
 }
 
@@ -612,9 +622,13 @@ hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, HeadSecond second,
   return logits<true>(a, s, second, st);
 }
 hipError_t head_launch_products(const HeadDx& x, const HeadDw& w, HeadShape s, hipStream_t st) {
-  return s == HEAD_256   ? products<Shape256, Shape256>(x, w, st)
-         : s == HEAD_128 ? products<Shape128, Shape128>(x, w, st)
-                         : products<Shape32, Shape128>(x, w, st);
+  if (x.f32)
+    return s == HEAD_256   ? products<Shape256, Shape256, true>(x, w, st)
+           : s == HEAD_128 ? products<Shape128, Shape128, true>(x, w, st)
+                           : products<Shape32, Shape128, true>(x, w, st);
+  return s == HEAD_256   ? products<Shape256, Shape256, false>(x, w, st)
+         : s == HEAD_128 ? products<Shape128, Shape128, false>(x, w, st)
+                         : products<Shape64, Shape128, false>(x, w, st);
 }
 
 }  // namespace monarch
