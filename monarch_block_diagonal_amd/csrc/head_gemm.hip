@@ -5,7 +5,7 @@
 //            maximum and sum of exponentials are taken in registers, four lanes
 //            meet by two swaps, and only (maximum, sums) of a tile leave the chip;
 //            or, for the gradient, g = a q + b s - off [v = label], rounded to
-//            bf16 (fp32: three bf16 planes, exact), [n][v] through LDS.
+//            bf16 (up to 64 rows two bf16 parts; fp32: three, exact), [n][v] through LDS.
 //   dx       [d, n] = sum_v w[v, d] g[n, v]       split over the words
 //   dw       [d, v] = sum_n x[n, d] g[n, v]
 //
