@@ -61,6 +61,7 @@ struct HeadLogits {
   // gradient: g [planes][np][vp]
   const HeadRow* row;
   uint16_t* g;
+  float* few;                 // fp32, few rows: g as it is, [kThinRows][vp]
   int64_t vp, g_plane;
   int fold;                   // bf16, few rows: g has two parts, the second one's rows `fold` behind the first's; or 0
 };
@@ -96,5 +97,22 @@ hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, HeadSecond second,
 hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st);
 // dx and dw of a piece (HEAD_32: dx's tiles, dw's are HEAD_128's)
 hipError_t head_launch_products(const HeadDx& x, const HeadDw& w, HeadShape s, hipStream_t st);
+
+// Both products of at most kThinRows rows in fp32.
+struct HeadFew {
+  const float* g;             // [kThinRows][vp]
+  int64_t vp;
+  const float* x;             // rows idx[k] for k < *count
+  int64_t ldx;
+  const int *idx, *count;
+  const float* w;             // the piece's words
+  float *dw, *part;           // part [splits][head_few_rows][dp]
+  int64_t d, dp, words;
+  bool add;                   // part already holds other pieces' sums
+};
+int64_t head_few_rows(int64_t rows);
+// words of a split for a piece of `words`
+int64_t head_few_run(int64_t rows, int64_t d, int64_t words);
+hipError_t head_launch_few(const HeadFew& a, int64_t rows, int64_t run, int64_t splits, hipStream_t st);
 
 }  // namespace monarch

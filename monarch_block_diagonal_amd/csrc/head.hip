@@ -424,17 +424,17 @@ __global__ __launch_bounds__(256) void head_factors_kernel(Call c, Rows r, HeadR
 }
 
 // g of few rows (HEAD_THIN) from their logits, which a step keeps for its length: they are smaller than
-// the head, which would be read again for them. Four words a thread, all rows of a K tile of dw's.
+// the head, which would be read again for them. Four words a thread, kThinRows rows.
 __global__ __launch_bounds__(256) void head_few_kernel(Call c, Rows r, const HeadRow* __restrict__ rows,
-                                                       const float* __restrict__ z, int64_t zp, uint16_t* __restrict__ g,
+                                                       const float* __restrict__ z, uint16_t* __restrict__ g, float* __restrict__ gf,
                                                        int64_t vp, int64_t plane) {
   const int64_t v = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  const int n = blockIdx.y, planes = c.bf16 ? 2 : 3;
+  const int n = blockIdx.y;
   if (v >= vp) return;
   float o[4] = {0.f, 0.f, 0.f, 0.f};
   if (n < *r.count) {
     const HeadRow h = rows[n];
-    const f32x4 l = *reinterpret_cast<const f32x4*>(z + n * zp + v);
+    const f32x4 l = *reinterpret_cast<const f32x4*>(z + n * vp + v);
     const float ct = kLog2e / c.temperature;
     const int64_t own = r.label[n] - v;
 #pragma unroll
@@ -445,8 +445,12 @@ __global__ __launch_bounds__(256) void head_few_kernel(Call c, Rows r, const Hea
       if (v + i >= c.vocab) o[i] = 0.f;
     }
   }
+  if (gf) {
+    *reinterpret_cast<f32x4*>(gf + n * vp + v) = f32x4{o[0], o[1], o[2], o[3]};
+    return;
+  }
   uint16_t* to = g + n * vp + v;
-  for (int q = 0; q < planes; ++q, to += plane) {
+  for (int q = 0; q < 2; ++q, to += plane) {
     uint16_t part[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) part[i] = next_part(o[i]);
@@ -457,7 +461,7 @@ __global__ __launch_bounds__(256) void head_few_kernel(Call c, Rows r, const Hea
 // The teacher's columns of a piece of g: a wave a row.
 __global__ __launch_bounds__(64) void head_taught_kernel(Call c, Rows r, const HeadRow* __restrict__ rows,
                                                          const float* __restrict__ taught, uint16_t* __restrict__ g,
-                                                         int64_t vp, int64_t plane, int planes, int64_t v0, int64_t v1) {
+                                                         float* __restrict__ gf, int64_t vp, int64_t plane, int planes, int64_t v0, int64_t v1) {
   extern __shared__ __align__(16) int s_id[];
   float* s_p = reinterpret_cast<float*>(s_id + c.top);
   const int64_t k = blockIdx.x;
@@ -492,6 +496,10 @@ __global__ __launch_bounds__(64) void head_taught_kernel(Call c, Rows r, const H
     const float z = c.stats[c.rows * 4 + i * c.top + j] - h.m;
     float v = h.a * exp2_of(z * ct) + (c.second != HEAD_ONE ? h.b * exp2_of(z * kLog2e) : 0.f) - taught[k] * p;
     if (id == label) v -= h.off;
+    if (gf) {
+      gf[k * vp + (id - v0)] = v;
+      continue;
+    }
     uint16_t* o = g + k * vp + (id - v0);
     for (int q = 0; q < planes; ++q) o[q * plane] = next_part(v);
   }
@@ -501,7 +509,7 @@ __global__ __launch_bounds__(64) void head_taught_kernel(Call c, Rows r, const H
 // that share the splits (many of them, where rows are few: 64 splits of 8 x 768 11 us with one thread, 5 with 16).
 template <typename T, int SL>
 __global__ __launch_bounds__(256) void head_dx_out_kernel(const float* __restrict__ part, const int* __restrict__ pos,
-                                                          int64_t rows, int64_t np, int64_t d, int64_t dp, int splits,
+                                                          int64_t rows, int64_t np, int64_t d, int64_t dp, int splits,   // part [splits][np][dp]
                                                           int fold, const float* __restrict__ scale, T* __restrict__ dx) {
   constexpr int OUT = 256 / SL;
   const int64_t per = (d + 3) / 4, at = static_cast<int64_t>(blockIdx.x) * OUT + threadIdx.x % OUT;
@@ -568,11 +576,12 @@ struct HeadPlan {
   int64_t d, dp, np, planes;
   int fold;                    // bf16, few rows: rows of one of g's two parts
   bool copy_w;                 // the head is copied (fp32, or rows that are no whole pieces)
+  bool direct;                 // fp32, few rows: dx and dw by head_launch_few
   HeadShape shape, products;   // of the logits, and of dx and dw
   int64_t tiles;               // of words, forward
   int64_t vp, pieces;          // words of a piece
   int dx_splits, dw_splits;
-  int64_t dx_chunk;
+  int64_t dx_chunk, dx_rows;
   // byte offsets in the workspace
   bool keep;                   // a step of few rows keeps their logits
   size_t rows, x, w, part, z_label, stats, factors, taught, g, z, dx, dw, total;
@@ -614,7 +623,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
   };
   p.rows = take(256 + (p.np * 3 + rows * 2) * 4);
   p.x = take(p.planes * p.np * p.dp * 2);
-  p.copy_w = p.copy_w && !(what == FWD && !bf16 && p.shape == HEAD_THIN);   // which takes the head as it is
+  p.copy_w = p.copy_w && (bf16 || p.shape != HEAD_THIN);   // which takes an fp32 head as it is
   p.w = p.copy_w ? take(p.planes * (vocab + kPipeK) * p.dp * 2) : 0;   // zeros behind: whole K tiles of words
   if (what != BWD) {
     p.part = take(p.tiles * 3 * p.np * 4);
@@ -622,6 +631,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
   }
   if (what == STEP) p.stats = take(rows * (4 + top) * 4);
   if (what != FWD) {
+    p.direct = !bf16 && rows <= kThinRows;
     int64_t vp = up(kPieceBytes / (p.planes * p.np * 2), kHeadRows) - kHeadRows;
     if (vp < kHeadRows) vp = kHeadRows;
     p.pieces = (vocab + vp - 1) / vp;
@@ -654,14 +664,16 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
                                     static_cast<double>(p.vp) / n + ends) + n * static_cast<double>(p.np * p.dp) * 4 / 2500.0;
       if (xs == 0 || t < best) best = t, xs = n;
     }
-    p.dx_chunk = up((p.vp + xs - 1) / xs, kPipeK);
+    p.dx_chunk = p.direct ? head_few_run(rows, d, p.vp) : up((p.vp + xs - 1) / xs, kPipeK);
     p.dx_splits = static_cast<int>((p.vp + p.dx_chunk - 1) / p.dx_chunk);
+    p.dx_rows = p.direct ? head_few_rows(rows) : p.np;
+    if (p.direct) p.dw_splits = 1;
     p.factors = take(p.np * static_cast<int64_t>(sizeof(HeadRow)));
     p.taught = take(p.np * 4);
-    p.g = take(p.planes * p.np * p.vp * 2);
+    p.g = take(p.direct ? kThinRows * p.vp * 4 : p.planes * p.np * p.vp * 2);
     p.keep = what == STEP && p.shape == HEAD_THIN && p.pieces == 1;
     p.z = p.keep ? take(kThinRows * p.vp * 4) : 0;
-    p.dx = take(p.dx_splits * p.np * p.dp * 4);
+    p.dx = take(p.dx_splits * p.dx_rows * p.dp * 4);
     p.dw = p.dw_splits > 1 ? take(p.dw_splits * p.vp * p.dp * 4) : 0;
   }
   p.total = at;
@@ -699,10 +711,10 @@ hipError_t dx_out(const Call& c, const HeadPlan& p, const float* part, const Row
   const int64_t grid = (n + 256 / sl - 1) / (256 / sl);
   if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
   if (sl == 16)
-    hipLaunchKernelGGL((head_dx_out_kernel<T, 16>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, r.pos, c.rows, p.np,
+    hipLaunchKernelGGL((head_dx_out_kernel<T, 16>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, r.pos, c.rows, p.dx_rows,
                        p.d, p.dp, p.dx_splits, r.fold, r.scale, static_cast<T*>(c.dx));
   else
-    hipLaunchKernelGGL((head_dx_out_kernel<T, 1>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, r.pos, c.rows, p.np,
+    hipLaunchKernelGGL((head_dx_out_kernel<T, 1>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, r.pos, c.rows, p.dx_rows,
                        p.d, p.dp, p.dx_splits, r.fold, r.scale, static_cast<T*>(c.dx));
   return hipGetLastError();
 }
@@ -776,7 +788,8 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
     HEAD_TRY(hipGetLastError());
   }
   uint16_t* g = reinterpret_cast<uint16_t*>(ws + p.g);
-  l.row = factors, l.g = g, l.vp = p.vp, l.g_plane = (p.fold ? p.fold : p.np) * p.vp, l.fold = p.fold;
+  float* gf = p.direct ? reinterpret_cast<float*>(ws + p.g) : nullptr;
+  l.row = factors, l.g = g, l.few = gf, l.vp = p.vp, l.g_plane = (p.fold ? p.fold : p.np) * p.vp, l.fold = p.fold;
   HeadDx x = {};
   x.pr.zeros = l.pr.zeros, x.f32 = l.f32;
   x.pr.b.p = g, x.pr.b.ld = p.vp, x.pr.b.plane = l.g_plane, x.pr.b.rows = p.np;
@@ -793,16 +806,24 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
     const int64_t v1 = v0 + p.vp < c.vocab ? v0 + p.vp : c.vocab;
     l.v0 = v0, l.v1 = v1;
     if (p.keep) {
-      hipLaunchKernelGGL(head_few_kernel, dim3(static_cast<unsigned>((p.vp / 4 + 255) / 256), c.bf16 ? kThinRows : kPipeK), dim3(256), 0, s, c, r, factors,
-                         l.z, p.vp, g, p.vp, l.g_plane);
+      hipLaunchKernelGGL(head_few_kernel, dim3(static_cast<unsigned>((p.vp / 4 + 255) / 256), kThinRows), dim3(256), 0, s, c, r, factors, l.z,
+                         g, gf, p.vp, l.g_plane);
       HEAD_TRY(hipGetLastError());
     } else {
       HEAD_TRY(head_launch_grad(l, p.shape, c.second, s));
     }
     if (c.taught) {
       hipLaunchKernelGGL(head_taught_kernel, dim3(static_cast<unsigned>(c.rows)), dim3(64), static_cast<size_t>(c.top) * 8, s, c,
-                         r, factors, taught, g, p.vp, l.g_plane, p.fold ? 2 : static_cast<int>(p.planes), v0, v1);
+                         r, factors, taught, g, gf, p.vp, l.g_plane, p.fold ? 2 : static_cast<int>(p.planes), v0, v1);
       HEAD_TRY(hipGetLastError());
+    }
+    if (p.direct) {
+      HeadFew f = {};
+      f.g = gf, f.vp = p.vp, f.x = static_cast<const float*>(c.x), f.ldx = c.ldx, f.idx = r.idx, f.count = r.count;
+      f.w = static_cast<const float*>(c.w) + v0 * p.d, f.dw = static_cast<float*>(c.dw) + v0 * p.d, f.part = x.part;
+      f.d = p.d, f.dp = p.dp, f.words = v1 - v0, f.add = v0 > 0;
+      HEAD_TRY(head_launch_few(f, c.rows, p.dx_chunk, p.dx_splits, s));
+      continue;
     }
     x.k = up(v1 - v0, kPipeK);
     x.pr.a.p = w + v0 * ldw, x.pr.a.ld = ldw, x.pr.a.plane = wplane, x.pr.a.rows = ldw, x.pr.a.kvalid = p.copy_w ? x.k : v1 - v0;

@@ -23,7 +23,7 @@ constexpr float kLowest = -3.402823466e38f;
 using Shape256 = PipeShape<2, 4, 8, 4, 2>;
 using Shape128 = PipeShape<2, 2, 4, 4, 2>;
 using Shape32 = PipeShape<4, 1, 2, 2, 4>;
-using Shape64 = PipeShape<4, 1, 2, 4, 3>;   // dx of few rows in bf16
+using Shape64 = PipeShape<4, 1, 2, 4, 3>;   // dx of few rows
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -162,7 +162,6 @@ __device__ __forceinline__ int staged(int r, int e) {
 template <class S, HeadSecond SECOND, bool F32>
 __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t vt, int64_t nt) {
   static_assert(S::BM * S::BN * 2 <= S::LDS, "a tile of g is staged in LDS");
-  static_assert(S::BN % kPipeK == 0 || 2 * S::BN == kPipeK, "with the 0s, whole K tiles of rows");
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
   int64_t tv, tn;
   panel_tile(xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
@@ -201,6 +200,14 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
       acc[mi][ni] = g;
     }
   }
+  if constexpr (std::is_same<S, Shape32>::value) {   // one tile of rows
+#pragma unroll
+    for (int ni = 0; ni < S::FN; ++ni)
+#pragma unroll
+      for (int mi = 0; mi < S::FM; ++mi)
+        *reinterpret_cast<f32x4*>(p.few + ((wn * S::FN + ni) * 16 + l15) * p.vp + (vw - p.v0) + mi * 16) = acc[mi][ni];
+    return;
+  }
   const int planes = F32 ? 3 : p.fold ? 2 : 1;
   for (int k = 0; k < planes; ++k) {
     if (k > 0) __syncthreads();
@@ -218,8 +225,6 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
       const int row = c / CH, e = (c % CH) * 8;
       if (!F32 && p.fold && n0 + row >= p.fold) continue;   // there the second part's rows lie
       *reinterpret_cast<u32x4*>(out + row * p.vp + e) = *reinterpret_cast<const u32x4*>(lds + staged<S::BM>(row, e));
-      // a K tile of dw's is 64 rows: the other ones are 0
-      if constexpr (F32 && S::BN < kPipeK) *reinterpret_cast<u32x4*>(out + (S::BN + row) * p.vp + e) = u32x4{0, 0, 0, 0};
     }
   }
 }
@@ -373,14 +378,16 @@ __global__ __launch_bounds__(256) void head_thin_kernel(HeadLogits p, int64_t ru
           if (vw + v >= end) g[v] = 0.f;
         }
         // a gradient's runs are whole tiles, as K tiles of dx's are (behind the last word g has room)
-        uint16_t* o = p.g + n * p.vp + (vw - p.v0);
+        if constexpr (F32) {
+          *reinterpret_cast<f32x4*>(p.few + n * p.vp + (vw - p.v0)) = g;
+        } else {
+          uint16_t* o = p.g + n * p.vp + (vw - p.v0);
 #pragma unroll
-        for (int q = 0; q < (F32 ? 3 : 2); ++q) {
-          *reinterpret_cast<u32x2*>(o) = next_plane(g);
-          // the other rows of a K tile of dw's (bf16: of the part's half of it) are 0
-#pragma unroll
-          for (int z = 16 * NB; z < (F32 ? kPipeK : kThinRows); z += 16 * NB) *reinterpret_cast<u32x2*>(o + z * p.vp) = u32x2{0, 0};
-          o += p.g_plane;
+          for (int q = 0; q < 2; ++q, o += p.g_plane) {
+            *reinterpret_cast<u32x2*>(o) = next_plane(g);
+            // the other rows of the part's half of a K tile of dw's are 0
+            if constexpr (NB == 1) *reinterpret_cast<u32x2*>(o + 16 * p.vp) = u32x2{0, 0};
+          }
         }
       } else {
 #pragma unroll
@@ -549,6 +556,104 @@ __global__ __launch_bounds__(SX::NT) void head_products_kernel(HeadDx x, HeadDw 
     dx_tile<SX, F32>(x, at - dw_tiles, lds);
 }
 
+// dx and dw of at most R rows in fp32: a wave takes 64 C columns and a run of words. Their rows of x and of dx's
+// sums stay in its registers, each word's columns are read once, and written as dw's; g comes through scalar
+// registers, four words of a row at a time. Bound by reading w and writing dw up to 16 rows (at
+// 32 the fp32 units' rate is as near). By bf16 parts and matrix instructions the head was first copied as
+// three planes and g's K tiles were mostly zeros: step of 8 x 768 x 50257 278 -> 159 us.
+template <int R, int C, bool WHOLE>
+__global__ __launch_bounds__(64) void head_few_products_kernel(const float* __restrict__ g, int64_t vp, const float* __restrict__ x,
+                                                               int64_t ldx, const int* __restrict__ idx,
+                                                               const int* __restrict__ count, const float* __restrict__ w,
+                                                               float* __restrict__ dw, float* __restrict__ part, int64_t d,
+                                                               int64_t dp, int64_t words, int64_t run, bool add) {
+  constexpr int U = 4;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (64 * C) + (WHOLE ? threadIdx.x * C : threadIdx.x);
+  // columns c0 + i, or c0 + 64 i where rows are no whole pieces
+  auto column = [&](int i) { return c0 + (WHOLE ? i : 64 * i); };
+  const int64_t first = blockIdx.x * run, end = first + run < words ? first + run : words;
+  const int rows = *count;
+  float xs[R][C], dx[R][C];
+#pragma unroll
+  for (int n = 0; n < R; ++n) {
+    const float* row = x + (n < rows ? idx[n] : 0) * ldx;
+#pragma unroll
+    for (int i = 0; i < C; ++i) xs[n][i] = n < rows && column(i) < d ? row[column(i)] : 0.f, dx[n][i] = 0.f;
+  }
+  auto load = [&](int64_t v, float (&o)[C]) {
+    const float* at = w + v * d;
+    if constexpr (WHOLE) {
+      if (c0 < d) __builtin_memcpy(o, __builtin_assume_aligned(at + c0, 4 * C), 4 * C);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (column(i) < d) o[i] = at[column(i)];
+    }
+  };
+  auto store = [&](int64_t v, const float (&o)[C]) {
+    float* at = dw + v * d;
+    if constexpr (WHOLE) {
+      typedef float piece __attribute__((ext_vector_type(C)));
+      piece q;
+      __builtin_memcpy(&q, o, 4 * C);
+      if (c0 < d) __builtin_nontemporal_store(q, reinterpret_cast<piece*>(at + c0));
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (column(i) < d) at[column(i)] = o[i];
+    }
+  };
+  if (rows > 0) {
+    float next[U][C] = {};
+    auto fetch = [&](int64_t v) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v + u < end) load(v + u, next[u]);
+    };
+    fetch(first);
+    for (int64_t v = first; v < end; v += U) {
+      float now[U][C], s[U][C] = {};
+      __builtin_memcpy(now, next, sizeof(now));
+      fetch(v + U);
+#pragma unroll
+      for (int n = 0; n < R; ++n) {
+        // behind the last word g is 0 up to vp, a multiple of 256
+        const f32x4 q = *reinterpret_cast<const f32x4*>(g + n * vp + v);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < C; ++i) {
+            s[u][i] = fmaf(q[u], xs[n][i], s[u][i]);
+            // what lies behind the run's last word is another's
+            if (u == 0 || v + u < end) dx[n][i] = fmaf(q[u], now[u][i], dx[n][i]);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v + u < end) store(v + u, s[u]);
+    }
+  } else {
+    const float none[C] = {};
+    for (int64_t v = first; v < end; ++v) store(v, none);
+  }
+#pragma unroll
+  for (int n = 0; n < R; ++n) {
+    float* o = part + (blockIdx.x * static_cast<int64_t>(R) + n) * dp;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (column(i) < d) o[column(i)] = add ? o[column(i)] + dx[n][i] : dx[n][i];
+  }
+}
+
+template <int R, int C>
+hipError_t few(const HeadFew& a, int64_t run, int64_t splits, hipStream_t st) {
+  const int64_t cols = (a.d + 64 * C - 1) / (64 * C);
+  auto kernel = a.d % 4 == 0 ? head_few_products_kernel<R, C, true> : head_few_products_kernel<R, C, false>;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(splits), static_cast<unsigned>(cols)), dim3(64), 0, st, a.g, a.vp, a.x,
+                     a.ldx, a.idx, a.count, a.w, a.dw, a.part, a.d, a.dp, a.words, run, a.add);
+  return hipGetLastError();
+}
+
 int64_t tiles(int64_t n, int64_t by) { return (n + by - 1) / by; }
 
 hipError_t check_grid(int64_t grid) { return grid > 0x7fffffffLL ? hipErrorInvalidConfiguration : hipSuccess; }
@@ -594,9 +699,11 @@ hipError_t logits(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream
     if (a.f32) return a.rows <= 16 ? thin<GRAD, 1, true>(a, second, st) : thin<GRAD, 2, true>(a, second, st);
     return a.rows <= 16 ? thin<GRAD, 1, false>(a, second, st) : thin<GRAD, 2, false>(a, second, st);
   }
-  return s == HEAD_256   ? logits<Shape256, GRAD>(a, second, st)
-         : s == HEAD_128 ? logits<Shape128, GRAD>(a, second, st)
-                         : logits<Shape32, GRAD>(a, second, st);
+  if (s == HEAD_32)
+    return second == HEAD_ONE   ? logits<Shape32, GRAD, HEAD_ONE, true>(a, st)
+           : second == HEAD_OWN ? logits<Shape32, GRAD, HEAD_OWN, true>(a, st)
+                                : logits<Shape32, GRAD, HEAD_SQUARE, true>(a, st);
+  return s == HEAD_256 ? logits<Shape256, GRAD>(a, second, st) : logits<Shape128, GRAD>(a, second, st);
 }
 
 template <class SX, class SW, bool F32>
@@ -622,13 +729,20 @@ hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, HeadSecond second,
   return logits<true>(a, s, second, st);
 }
 hipError_t head_launch_products(const HeadDx& x, const HeadDw& w, HeadShape s, hipStream_t st) {
-  if (x.f32)
-    return s == HEAD_256   ? products<Shape256, Shape256, true>(x, w, st)
-           : s == HEAD_128 ? products<Shape128, Shape128, true>(x, w, st)
-                           : products<Shape32, Shape128, true>(x, w, st);
+  if (x.f32) return s == HEAD_256 ? products<Shape256, Shape256, true>(x, w, st) : products<Shape128, Shape128, true>(x, w, st);
   return s == HEAD_256   ? products<Shape256, Shape256, false>(x, w, st)
          : s == HEAD_128 ? products<Shape128, Shape128, false>(x, w, st)
                          : products<Shape64, Shape128, false>(x, w, st);
+}
+
+int64_t head_few_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// two waves a SIMD, of 16 words at least
+int64_t head_few_run(int64_t rows, int64_t d, int64_t words) {
+  const int64_t cols = tiles(d, rows <= 16 ? 256 : 128), run = tiles(tiles(words * cols, 2048), 4) * 4;
+  return run < 16 ? 16 : run;
+}
+hipError_t head_launch_few(const HeadFew& a, int64_t rows, int64_t run, int64_t splits, hipStream_t st) {
+  return rows <= 8 ? few<8, 4>(a, run, splits, st) : rows <= 16 ? few<16, 4>(a, run, splits, st) : few<32, 2>(a, run, splits, st);
 }
 
 }  // namespace monarch
