@@ -560,7 +560,7 @@ __global__ __launch_bounds__(SX::NT) void head_products_kernel(HeadDx x, HeadDw 
 // sums stay in its registers, each word's columns are read once, and written as dw's; g comes through scalar
 // registers, four words of a row at a time. Bound by reading w and writing dw up to 16 rows (at
 // 32 the fp32 units' rate is as near). By bf16 parts and matrix instructions the head was first copied as
-// three planes and g's K tiles were mostly zeros: step of 8 x 768 x 50257 278 -> 159 us.
+// three planes and g's K tiles were mostly zeros: step of 8 x 768 x 50257 278 -> 157 us.
 template <int R, int C, bool WHOLE>
 __global__ __launch_bounds__(64) void head_few_products_kernel(const float* __restrict__ g, int64_t vp, const float* __restrict__ x,
                                                                int64_t ldx, const int* __restrict__ idx,
