@@ -92,6 +92,52 @@ def test_few_rows(api, rows, d, vocab, top, dtype):
         check(api, x, w, labels, t, ids, r, T, mix)
 
 
+@pytest.mark.parametrize("rows,d,vocab,top", [(1, 64, 700, 0), (16, 40, 5000, 3), (17, 129, 2000, 0), (32, 264, 3001, 2), (33, 72, 4000, 0), (64, 256, 2500, 5)])
+def test_few_rows_round_g_twice(api, rows, d, vocab, top):
+    """Up to 64 rows g has two bf16 parts: off by 2^-8 of 2^-8, before dx and dw are rounded by 2^-8. Row weights
+    lie 10^6 apart, and rows are left out."""
+    x, w, labels, t, ids, r = draw(rows, d, vocab, BF16, top, holes=rows > 1, seed=rows)
+    r = r * 10.0 ** torch.linspace(-3, 3, rows, device="cuda")
+    how = dict(temperature=2.0, mix=0.5 if top else 0.0)
+    o = H.head(x, w, labels, t, ids, r, 2.0, how["mix"])
+    _, dx, dw = H.bounds(o, x, w, 2.0 ** -16, 2.0)
+    got = api.head_loss_step(x, w, labels, t, ids, r, **how)
+    near(got[1], o.dx, dx + 2.0 ** -8 * (o.dx.abs() + dx), "dx")
+    near(got[2], o.dw, dw + 2.0 ** -8 * (o.dw.abs() + dw), "dw")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,d,vocab", [(8, 64, 300), (30, 37, 1001), (32, 264, 515), (50, 96, 700), (64, 33, 257), (90, 72, 400)])
+def test_none_or_one_of_few_rows_counts(api, rows, d, vocab, dtype):
+    x, w, labels, _, _, r = draw(rows, d, vocab, dtype, seed=9)
+    for only in (None, rows - 1):
+        few = torch.full_like(labels, -1)
+        if only is not None:
+            few[only] = labels[only]
+        # memory that a workspace may get holds NaN
+        for n in (1 << 20, 1 << 22, 1 << 24):
+            torch.full((n,), float("nan"), device="cuda")
+        check(api, x, w, few, None, None, r, 1.0, 0.0)
+
+
+@pytest.mark.parametrize("rows,d,vocab,dtype", [(5, 8, 3000001, F32), (3, 6, 1500007, F32), (20, 8, 4300003, BF16)])
+def test_pieces_of_few_rows(api, rows, d, vocab, dtype):
+    """More words than a piece of g has. In fp32 a wave adds one 2048th of a piece's words in turn, 128 of
+    these sums a thread, 16 threads and two pieces: fewer than 2^11 additions in sequence for dx, where bounds() counts one a
+    word."""
+    x, w, labels, _, _, r = draw(rows, d, vocab, dtype, seed=5)
+    labels[0], labels[-1] = 1, vocab - 1
+    o = H.head(x, w, labels, None, None, r)
+    b_loss, b_dx, b_dw = H.bounds(o, x, w, U[dtype])
+    loss, dx, dw = api.head_loss_step(x, w, labels, row_weight=r)
+    near(loss, o.loss, b_loss, "loss")
+    if dtype == F32:
+        assert vocab / 2048 + 4 + 128 + 16 + 2 < 2 ** 11
+        b_dx = b_dx - (vocab - 2 ** 11) * 2.0 ** -24 * (o.g.abs() @ w.double().abs())
+    near(dx, o.dx, b_dx, "dx")
+    near(dw, o.dw, b_dw, "dw")
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_wide_tiles(api, dtype):
     """Enough tiles for the 256 x 256 products; words and rows that end inside a tile, a third of the rows left out."""
