@@ -42,7 +42,8 @@ __device__ __forceinline__ float head_g(const HeadRow& r, float logit, float ct,
   return label ? g - r.off : g;
 }
 
-enum HeadShape { HEAD_256 = 0, HEAD_128 = 1, HEAD_32 = 2, HEAD_THIN = 3 };   // HEAD_THIN: logits of at most 32 rows
+// HEAD_THIN: logits of at most 32 rows; HEAD_32: these in fp32 where words are no whole pieces, and dx in bf16
+enum HeadShape { HEAD_256 = 0, HEAD_128 = 1, HEAD_32 = 2, HEAD_THIN = 3 };
 
 struct HeadLogits {
   PipeProduct pr;             // A: the head's words, B: the rows
@@ -95,7 +96,7 @@ int64_t head_tile_rows(HeadShape s);     // rows of a logits and a dx tile
 int64_t head_tile_features(HeadShape s); // features of a dx tile
 hipError_t head_launch_sums(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st);
 hipError_t head_launch_grad(const HeadLogits& a, HeadShape s, HeadSecond second, hipStream_t st);
-// dx and dw of a piece (HEAD_32: dx's tiles, dw's are HEAD_128's)
+// dx and dw of a piece (HEAD_32: dx's tiles have 64 rows of g, dw's are HEAD_128's)
 hipError_t head_launch_products(const HeadDx& x, const HeadDw& w, HeadShape s, hipStream_t st);
 
 // Both products of at most kThinRows rows in fp32.

@@ -233,7 +233,7 @@ __global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t 
 // words, 64 at a time, 16 a wave, and a head's row comes in pieces of 512 bytes: K tiles of 256 (fp32:
 // 128) go straight into LDS, three in flight, one after another over the run's words, so that
 // loads never pause. A row's maximum and sums run on in registers over the run; lanes meet at its end.
-// Read in pieces of 128 bytes (HEAD_32's tiles), the forward pass of 32 x 4096 x 131072 bf16 takes
+// Read in pieces of 128 bytes (tiles of 128 words and 32 rows), the forward pass of 32 x 4096 x 131072 bf16 takes
 // 400 us, this way 267 (4.0 TB/s). In fp32 the head is taken as it is and cut into its three bf16 parts
 // in registers, where the wider tiles read a copy of planes.
 //
