@@ -890,20 +890,47 @@ class DropoutFunction(torch.autograd.Function):
 
 
 class Dropout(torch.nn.Module):
-    """residual + dropout(x) in training, residual + x otherwise. Every call draws anew: call k of a
-    module has offset k. The seed is drawn from torch's generator unless given. A captured graph would
-    replay one offset: pass a `state` then (dropout_forward)."""
+    """residual + dropout(x) in training, residual + x otherwise. Every call draws anew: under a seed
+    that it takes from torch's generator on the CPU, as torch's own dropout takes its numbers. So a copy of the
+    module drops elements of its own, a run goes on where the generator's state is restored, and a
+    forward pass that is computed again under activation checkpointing, which restores that
+    state, drops what the first one dropped.
+
+    With a `seed` of the module's own, call k has offset k (in every module of that seed: a copy drops the
+    same elements); the number of calls is kept in the state_dict. A forward pass that is computed
+    again would be another call, so one inside a backward pass raises.
+
+    A captured graph would replay one draw: pass a `state` then (dropout_forward), which takes the place of
+    both and is not moved on here."""
 
     def __init__(self, p: float = 0.1, seed: Optional[int] = None):
         super().__init__()
         if not 0.0 <= p <= 1.0:
             raise ValueError(f"p must be in [0, 1], got {p}")
         self.p = p
-        self.seed = int(torch.randint(0, (1 << 63) - 1, ())) if seed is None else seed
+        self.seed = seed
         self.calls = 0
+
+    def _save_to_state_dict(self, destination, prefix, keep_vars):
+        super()._save_to_state_dict(destination, prefix, keep_vars)
+        if self.seed is not None:
+            destination[prefix + "calls"] = torch.tensor(self.calls, device="cpu")
+
+    def _load_from_state_dict(self, state_dict, prefix, *rest):
+        # weights saved without a count leave it as it is
+        calls = state_dict.pop(prefix + "calls", None)
+        if calls is not None and self.seed is not None:
+            self.calls = int(calls)
+        super()._load_from_state_dict(state_dict, prefix, *rest)
 
     def forward(self, x, residual=None, state=None):
         if not self.training or self.p == 0.0:
             return x if residual is None else residual + x
-        offset, self.calls = self.calls, self.calls + 1
-        return DropoutFunction.apply(x, self.p, self.seed, offset, residual, state)
+        seed, offset = self.seed, self.calls
+        if state is None and seed is None:
+            seed, offset = int(torch.randint(0, (1 << 63) - 1, (), device="cpu")), 0
+        elif state is None and torch._C._current_graph_task_id() != -1:
+            raise RuntimeError("Dropout with a seed counts its calls, so a forward pass that is computed again in the backward "
+                               "pass (activation checkpointing) would drop other elements: leave the seed out, or pass a state")
+        self.calls += 1
+        return DropoutFunction.apply(x, self.p, seed, offset, residual, state)
