@@ -477,7 +477,8 @@ int monarch_head_step(const void* x, int64_t ldx, const void* w, const void* lab
  * offset. A call with an offset of its own draws its own numbers.
  * state (NULL, or two uint64 in device memory, 8-byte aligned): seed and offset are read there when the
  * kernel runs instead of taken from the arguments, so that replays of a captured
- * graph can draw anew.
+ * graph can draw anew. Calls with the same seed and offset drop the same elements, from a
+ * state too: each call of a step takes one of its own.
  * 0 <= p <= 1 or MONARCH_ERR_VALUE, n <= 2^41; y may be x or residual. What is dropped
  * may hold anything (NaN too). n == 0 returns MONARCH_OK; otherwise errors as for monarch_fwd. */
 int monarch_dropout(const void* x, const void* residual, void* y, int64_t n, double p,

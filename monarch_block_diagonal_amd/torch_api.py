@@ -853,7 +853,9 @@ def dropout_forward(x, p: float, seed: Optional[int] = None, offset: int = 0, re
     r: 16 bits for each element, drawn from (seed, offset) and its place alone, so no mask is kept and
     the backward pass draws them again; give every call an offset of its own. state (int64 [2] on the
     GPU: seed and offset) takes their place where a captured graph draws anew at each replay: the
-    program then changes it between replays, and behind the backward pass that draws from it."""
+    program then changes it between replays, and behind the backward pass that draws from it. Calls
+    that share a state's value drop the same elements: every call of a step needs a state of its own, for
+    instance a row of one [calls, 2] tensor."""
     if stream is not None:
         return _on_stream(stream, dropout_forward, x, p, seed, offset, residual, state=state)
     device = B.current_device()
@@ -900,8 +902,8 @@ class Dropout(torch.nn.Module):
     same elements); the number of calls is kept in the state_dict. A forward pass that is computed
     again would be another call, so one inside a backward pass raises.
 
-    A captured graph would replay one draw: pass a `state` then (dropout_forward), which takes the place of
-    both and is not moved on here."""
+    A captured graph would replay one draw: pass a `state` then (dropout_forward), one for every call of a
+    step. It takes the place of seed and count, and is not moved on here."""
 
     def __init__(self, p: float = 0.1, seed: Optional[int] = None):
         super().__init__()

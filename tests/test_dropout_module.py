@@ -128,3 +128,14 @@ def test_a_default_device_of_its_own(device):
     with torch.device("meta"):
         got = drop(x)
     assert torch.equal(got, want)
+
+
+def test_states_of_calls(device):
+    """Calls that share a state drop the same elements; the rows of one tensor are states of their own."""
+    _, x = layer(device)
+    drops = [T.Dropout(0.5), T.Dropout(0.5, seed=3)]
+    state = torch.tensor([[7, 8], [7, 9]], dtype=torch.int64, device=device)
+    one, two = (d(x, state=state[0]) for d in drops)
+    assert torch.equal(one, two) and torch.equal(one, T.dropout_forward(x, 0.5, 7, 8))
+    one, two = (d(x, state=s) for d, s in zip(drops, state))
+    assert not torch.equal(one, two) and torch.equal(two, T.dropout_forward(x, 0.5, 7, 9))
