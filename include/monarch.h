@@ -424,8 +424,8 @@ int monarch_distill_step(const void* logits, int64_t ld, const void* teacher, co
  * head w [vocab, features]; with T = temperature, q = softmax(z / T), s = softmax(z), and p, entries
  * and labels as for monarch_distill_*:
  *   loss[i] = mix * T^2 * sum_k p_k (log p_k - log q[id_k]) - (1 - mix) * log s[label]
- * top 0 or mix 0 leaves the cross entropy alone (temperature is then not used), labels
- * NULL or mix 1 the teacher's term alone. A row without a label and a valid entry (of a
+ * top 0 is mix 0, whatever mix is given: the cross entropy alone (mix and temperature are
+ * checked all the same); labels NULL or mix 1 is the teacher's term alone. A row without a label and a valid entry (of a
  * term that counts) has loss 0 and gradient 0 and adds nothing to dw, whatever it
  * holds, and costs no product: padded tokens, prompts.
  *   x [rows, ldx]: row i's features start at i*ldx (ldx >= features, in elements), aligned

@@ -849,6 +849,7 @@ int call(Call c, int what, const void* stats_in, int64_t top, float temperature,
   if (st) return st;
   if (!(temperature >= 1e-6f) || !(temperature <= 1e6f) || !(mix >= 0.0f) || !(mix <= 1.0f)) return MONARCH_ERR_VALUE;
   c.bf16 = dtype == MONARCH_BF16;
+  if (top == 0) mix = 0.0f;   // the cross entropy, unweighted
   c.top = static_cast<int>(top), c.mix = mix;
   c.told = c.labels && mix < 1.0f;
   c.taught = top > 0 && mix > 0.0f;

@@ -746,8 +746,8 @@ def head_loss_forward(x, w, labels=None, teacher=None, ids=None, *, temperature:
 
         loss = mix * temperature^2 * KL(p || softmax(z / temperature)) + (1 - mix) * CE(labels)
 
-    with labels, teacher and ids as for distill_forward; without a teacher, or with mix 0 (the
-    default), it is the softmax cross entropy. Rows without a label and a valid entry have loss 0 and cost nothing. stats goes to
+    with labels, teacher and ids as for distill_forward; without a teacher (or one of no columns), or with
+    mix 0 (the default), it is the softmax cross entropy. Rows without a label and a valid entry have loss 0 and cost nothing. stats goes to
     head_loss_backward."""
     if stream is not None:
         return _on_stream(stream, head_loss_forward, x, w, labels, teacher, ids,

@@ -6,7 +6,7 @@ points compute, in torch on whatever device its inputs are. TEST INFRASTRUCTURE 
     loss = mix T^2 sum_k p_k (log p_k - log q[id_k]) - (1 - mix) log s[c]
     g = r (mix T (q - p spread) + (1 - mix) (s - onehot(c))), dx = g w, dw = g^T x
 
-A row without a label (mix < 1) and without a valid entry (mix > 0) gives 0 and adds
+Without a teacher's columns mix is 0. A row without a label (mix < 1) and without a valid entry (mix > 0) gives 0 and adds
 nothing to dw, whatever it holds.
 """
 from __future__ import annotations
@@ -30,6 +30,8 @@ class Head(NamedTuple):
 def head(x, w, labels=None, teacher=None, ids=None, weight=None, T=1.0, mix=0.0) -> Head:
     x, w = x.double(), w.double()
     rows, vocab, dev = x.shape[0], w.shape[0], x.device
+    if teacher is None or not teacher.shape[1]:
+        mix = 0.0
     zero = torch.zeros((rows,), dtype=torch.float64, device=dev)
     told = torch.zeros((rows,), dtype=torch.bool, device=dev)
     some = told.clone()
