@@ -735,20 +735,31 @@ def _head_shapes(x, w, labels, teacher, ids, per_row, name):
     return rows, d, vocab, top, _rows_apart(x, rows, d, "x"), device
 
 
+def _teachers_share(mix, teacher):
+    """mix, which is 0 without a teacher; with one it has to be given (distill_* take it whole then, a loss of
+    labels none of it)."""
+    if mix is not None:
+        return mix
+    if teacher is not None and teacher.numel():
+        raise ValueError("a teacher needs mix: its share of the loss, 1 for all of it")
+    return 0.0
+
+
 # a function of the sizes alone: asked for once for each of them
 _head_workspace = functools.lru_cache(maxsize=256)(B.monarch_head_workspace_bytes)
 
 
 def head_loss_forward(x, w, labels=None, teacher=None, ids=None, *, temperature: float = 1.0,
-                      mix: float = 0.0, stream=None):
+                      mix: Optional[float] = None, stream=None):
     """(loss [rows], stats) of rows x [rows, features] under a dense head w [vocab, features], whose
     logits z = x wᵀ are not kept:
 
         loss = mix * temperature^2 * KL(p || softmax(z / temperature)) + (1 - mix) * CE(labels)
 
     with labels, teacher and ids as for distill_forward; without a teacher (or one of no columns), or with
-    mix 0 (the default), it is the softmax cross entropy. Rows without a label and a valid entry have loss 0 and cost nothing. stats goes to
-    head_loss_backward."""
+    mix 0, it is the softmax cross entropy. mix has to be given where there is a teacher. Rows without a
+    label and a valid entry have loss 0 and cost nothing. stats goes to head_loss_backward."""
+    mix = _teachers_share(mix, teacher)
     if stream is not None:
         return _on_stream(stream, head_loss_forward, x, w, labels, teacher, ids,
                           temperature=temperature, mix=mix)
@@ -764,8 +775,9 @@ def head_loss_forward(x, w, labels=None, teacher=None, ids=None, *, temperature:
 
 
 def head_loss_backward(dloss, x, w, labels, teacher, ids, stats, *, temperature: float = 1.0,
-                       mix: float = 0.0, stream=None):
+                       mix: Optional[float] = None, stream=None):
     """(dx, dw) for dloss [rows]; stats is the forward's. The logits are computed again."""
+    mix = _teachers_share(mix, teacher)
     if stream is not None:
         return _on_stream(stream, head_loss_backward, dloss, x, w, labels, teacher, ids, stats,
                           temperature=temperature, mix=mix)
@@ -782,9 +794,10 @@ def head_loss_backward(dloss, x, w, labels, teacher, ids, stats, *, temperature:
 
 
 def head_loss_step(x, w, labels=None, teacher=None, ids=None, row_weight=None, *,
-                   temperature: float = 1.0, mix: float = 0.0, stream=None):
+                   temperature: float = 1.0, mix: Optional[float] = None, stream=None):
     """(loss [rows], dx, dw) in one call: the gradients of sum(row_weight * loss) (row_weight
     None: 1 for every row)."""
+    mix = _teachers_share(mix, teacher)
     if stream is not None:
         return _on_stream(stream, head_loss_step, x, w, labels, teacher, ids, row_weight,
                           temperature=temperature, mix=mix)
@@ -807,7 +820,7 @@ class HeadLossFunction(torch.autograd.Function):
     the backward pass behind those of the forward pass in one call."""
 
     @staticmethod
-    def forward(ctx, x, w, labels, teacher, ids, temperature: float = 1.0, mix: float = 0.0):
+    def forward(ctx, x, w, labels, teacher, ids, temperature: float = 1.0, mix: Optional[float] = None):
         lead = x.shape[:-1]
         _expect(labels, lead, "labels")
         if teacher is not None and ids is not None:
@@ -820,7 +833,7 @@ class HeadLossFunction(torch.autograd.Function):
         whole = lambda t: None if t is None else t.contiguous()  # noqa: E731
         saved = (rows, _whole(w), whole(None if labels is None else labels.reshape(lead.numel())),
                  whole(flat(teacher)), whole(flat(ids)))
-        ctx.how, ctx.lead = dict(temperature=temperature, mix=mix), lead
+        ctx.how, ctx.lead = dict(temperature=temperature, mix=_teachers_share(mix, teacher)), lead
         loss, stats = head_loss_forward(*saved, **ctx.how)
         ctx.save_for_backward(*saved, stats)
         return loss.view(lead)

@@ -45,3 +45,16 @@ def test_calls(mix, rows, dtype):
         assert torch.equal(loss, want[0])
         for a, b in zip(T.head_loss_backward(r, x, w, labels, t, ids, stats, **how), want[1:]):
             assert torch.equal(a, b)
+
+
+def test_a_teacher_needs_its_share():
+    """Not given, it is 0 where there is no teacher, and nothing leaves a teacher out silently."""
+    from monarch_block_diagonal_amd import torch_api as T
+    x, w, labels, r = inputs(9, 40, 33, "cpu")
+    t, ids = torch.zeros((9, 2)), torch.zeros((9, 2), dtype=torch.int64)
+    for call in (lambda: T.head_loss_forward(x, w, labels, t, ids), lambda: T.head_loss_step(x, w, labels, t, ids, r),
+                 lambda: T.head_loss_backward(r, x, w, labels, t, ids, None), lambda: T.HeadLossFunction.apply(x, w, labels, t, ids, 2.0)):
+        with pytest.raises(ValueError, match="mix"):
+            call()
+    assert T._teachers_share(None, None) == T._teachers_share(None, no_entries(9, "cpu")[0]) == 0.0
+    assert T._teachers_share(0.5, None) == 0.5 and T._teachers_share(0.0, t) == 0.0
