@@ -12,6 +12,21 @@ namespace monarch {
 constexpr int64_t kThinRows = 32;    // rows that HEAD_THIN takes
 constexpr int64_t kHeadRows = 256;   // rows of the workspace's copies are a multiple of this, and so are a piece's columns
 
+// Workgroups of a launch, so that it has fewer than 2^32 threads (workgroups have 512 at most), which is all that
+// a launch can have. Calls of more rows or words than that launch a kernel several times.
+constexpr int64_t kLaunchGroups = int64_t(1) << 22;
+
+// f(first, grid) launches the workgroups [first, first + grid).
+template <class F>
+hipError_t launch_groups(int64_t groups, F f) {
+  for (int64_t first = 0; first < groups; first += kLaunchGroups) {
+    const int64_t n = groups - first < kLaunchGroups ? groups - first : kLaunchGroups;
+    f(first, dim3(static_cast<unsigned>(n)));
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
+}
+
 // What the products' epilogues take of a row: its largest logit and the factors of
 // its exponentials; the label's share is taken off at the label.
 struct HeadRow {

@@ -96,9 +96,9 @@ __device__ __forceinline__ void copy_row(const uint16_t* s, bool zero, int64_t d
   }
 }
 
-// A wave a row: does it have an entry?
-__global__ __launch_bounds__(256) void head_flag_kernel(Call c, Rows r) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+// A wave a row: does it have an entry? (`group`, here and below: this launch's first workgroup.)
+__global__ __launch_bounds__(256) void head_flag_kernel(Call c, Rows r, int64_t group) {
+  const int64_t i = (group + blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (i >= c.rows) return;
   bool any = false;
   for (int k = threadIdx.x & 63; k < c.top; k += 64)
@@ -201,9 +201,9 @@ __device__ __forceinline__ uint16_t next_part(float& v) {
 template <typename T>
 __global__ __launch_bounds__(256) void head_copy_kernel(const T* __restrict__ src, int64_t ld, const int* idx,
                                                         const int* count, int fold, int64_t rows, int64_t d, int64_t dp,
-                                                        uint16_t* __restrict__ dst, int64_t plane) {
+                                                        uint16_t* __restrict__ dst, int64_t plane, int64_t group) {
   constexpr bool F32 = sizeof(T) == 4;
-  const int64_t to = blockIdx.x, k = fold && to < 2 * fold ? to % fold : to;
+  const int64_t to = group + blockIdx.x, k = fold && to < 2 * fold ? to % fold : to;
   bool zero = k >= rows;
   int64_t row = zero ? 0 : k;
   if (idx) {
@@ -246,11 +246,12 @@ __global__ __launch_bounds__(256) void head_copy_kernel(const T* __restrict__ sr
 // of x behind the statistics; 0 for an entry that is not valid.
 template <typename T>
 __global__ __launch_bounds__(256) void head_entries_kernel(Call c, Rows r, const T* __restrict__ xs, int64_t ldx,
-                                                           bool by_row, const T* __restrict__ ws, int64_t ldw) {
-  const int k = blockIdx.x;
+                                                           bool by_row, const T* __restrict__ ws, int64_t ldw,
+                                                           int64_t group) {
+  const int64_t k = group + blockIdx.x;
   if (k >= *r.count || !r.has[k]) return;
   const int64_t i = r.idx[k];
-  const T* x = xs + (by_row ? i : static_cast<int64_t>(k)) * ldx;
+  const T* x = xs + (by_row ? i : k) * ldx;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float* out = c.stats + c.rows * 4 + i * c.top;
   for (int j0 = wave * 4; j0 < c.top; j0 += 16) {
@@ -339,10 +340,10 @@ __device__ __forceinline__ void row_factors(const Call& c, const Rows& r, int64_
 template <int RW>
 __global__ __launch_bounds__(256) void head_loss_kernel(Call c, Rows r, const float* __restrict__ part, int64_t np,
                                                         int tiles, const float* __restrict__ z_label, HeadRow* factors,
-                                                        float* taught) {
+                                                        float* taught, int64_t group) {
   constexpr int SL = 256 / RW;
   __shared__ float s[3][256];
-  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * RW;
+  const int64_t k0 = (group + blockIdx.x) * RW;
   const int count = *r.count;
   if (k0 >= count) {
     if (factors && k0 < (count + kHeadRows - 1) / kHeadRows * kHeadRows && threadIdx.x < RW)
@@ -461,10 +462,11 @@ __global__ __launch_bounds__(256) void head_few_kernel(Call c, Rows r, const Hea
 // The teacher's columns of a piece of g: a wave a row.
 __global__ __launch_bounds__(64) void head_taught_kernel(Call c, Rows r, const HeadRow* __restrict__ rows,
                                                          const float* __restrict__ taught, uint16_t* __restrict__ g,
-                                                         float* __restrict__ gf, int64_t vp, int64_t plane, int planes, int64_t v0, int64_t v1) {
+                                                         float* __restrict__ gf, int64_t vp, int64_t plane, int planes, int64_t v0, int64_t v1,
+                                                         int64_t group) {
   extern __shared__ __align__(16) int s_id[];
   float* s_p = reinterpret_cast<float*>(s_id + c.top);
-  const int64_t k = blockIdx.x;
+  const int64_t k = group + blockIdx.x;
   if (k >= *r.count || !r.has[k]) return;
   const int64_t i = r.idx[k];
   const int lane = threadIdx.x;
@@ -510,9 +512,10 @@ __global__ __launch_bounds__(64) void head_taught_kernel(Call c, Rows r, const H
 template <typename T, int SL>
 __global__ __launch_bounds__(256) void head_dx_out_kernel(const float* __restrict__ part, const int* __restrict__ pos,
                                                           int64_t rows, int64_t np, int64_t d, int64_t dp, int splits,   // part [splits][np][dp]
-                                                          int fold, const float* __restrict__ scale, T* __restrict__ dx) {
+                                                          int fold, const float* __restrict__ scale, T* __restrict__ dx,
+                                                          int64_t group) {
   constexpr int OUT = 256 / SL;
-  const int64_t per = (d + 3) / 4, at = static_cast<int64_t>(blockIdx.x) * OUT + threadIdx.x % OUT;
+  const int64_t per = (d + 3) / 4, at = (group + blockIdx.x) * OUT + threadIdx.x % OUT;
   const int slice = threadIdx.x / OUT;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   int64_t i = 0, e = 0;
@@ -699,9 +702,10 @@ bool off_elements(const void* p, int size) { return reinterpret_cast<uintptr_t>(
 template <typename T>
 hipError_t copy_rows(const void* src, int64_t ld, const int* idx, const int* count, int fold, int64_t rows, int64_t grid, int64_t d,
                      int64_t dp, void* dst, int64_t plane, hipStream_t s) {
-  hipLaunchKernelGGL(head_copy_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, static_cast<const T*>(src), ld,
-                     idx, count, fold, rows, d, dp, static_cast<uint16_t*>(dst), plane);
-  return hipGetLastError();
+  return launch_groups(grid, [&](int64_t first, dim3 g) {
+    hipLaunchKernelGGL(head_copy_kernel<T>, g, dim3(256), 0, s, static_cast<const T*>(src), ld, idx, count, fold, rows, d, dp,
+                       static_cast<uint16_t*>(dst), plane, first);
+  });
 }
 
 template <typename T>
@@ -709,12 +713,11 @@ hipError_t dx_out(const Call& c, const HeadPlan& p, const float* part, const Row
   const int64_t n = c.rows * ((p.d + 3) / 4);
   // 128 threads for few columns of many splits: step of 1 x 768 x 50257 fp32 156 -> 146 us, but 32 rows 236 -> 252
   const int sl = p.dx_splits >= 256 && n <= 2048 ? 128 : p.dx_splits >= 16 ? 16 : 1;
-  const int64_t grid = (n + 256 / sl - 1) / (256 / sl);
-  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
   auto kernel = sl == 128 ? head_dx_out_kernel<T, 128> : sl == 16 ? head_dx_out_kernel<T, 16> : head_dx_out_kernel<T, 1>;
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, part, r.pos, c.rows, p.dx_rows, p.d, p.dp,
-                     p.dx_splits, r.fold, r.scale, static_cast<T*>(c.dx));
-  return hipGetLastError();
+  return launch_groups(tiles_of(n, 256 / sl), [&](int64_t first, dim3 g) {
+    hipLaunchKernelGGL(kernel, g, dim3(256), 0, s, part, r.pos, c.rows, p.dx_rows, p.d, p.dp, p.dx_splits, r.fold, r.scale,
+                       static_cast<T*>(c.dx), first);
+  });
 }
 
 // One call of the three: checks are done.
@@ -731,10 +734,10 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
   r.pos = r.has + p.np;
   r.flag = r.pos + c.rows;
   uint16_t* xc = reinterpret_cast<uint16_t*>(ws + p.x);
-  if (c.taught) {
-    hipLaunchKernelGGL(head_flag_kernel, dim3(static_cast<unsigned>((c.rows + 3) / 4)), dim3(256), 0, s, c, r);
-    HEAD_TRY(hipGetLastError());
-  }
+  if (c.taught)
+    HEAD_TRY(launch_groups(tiles_of(c.rows, 4), [&](int64_t first, dim3 g) {
+      hipLaunchKernelGGL(head_flag_kernel, g, dim3(256), 0, s, c, r, first);
+    }));
   const bool few = c.bf16 && c.rows <= kThinRows && c.d <= 4096;   // one workgroup's copy
   hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, s, c, r, head, few ? xc : nullptr, p.dp);
   HEAD_TRY(hipGetLastError());
@@ -759,15 +762,15 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
   HeadRow* factors = what == FWD ? nullptr : reinterpret_cast<HeadRow*>(ws + p.factors);
   float* taught = what == FWD ? nullptr : reinterpret_cast<float*>(ws + p.taught);
   if (what != BWD) {
-    if (c.taught) {
-      const dim3 g(static_cast<unsigned>(c.rows));
-      if (c.bf16)
-        hipLaunchKernelGGL(head_entries_kernel<uint16_t>, g, dim3(256), 0, s, c, r, static_cast<const uint16_t*>(xc), p.dp, false, w, ldw);
-      else
-        hipLaunchKernelGGL(head_entries_kernel<float>, g, dim3(256), 0, s, c, r, static_cast<const float*>(c.x), c.ldx, true,
-                           static_cast<const float*>(c.w), p.d);
-      HEAD_TRY(hipGetLastError());
-    }
+    if (c.taught)
+      HEAD_TRY(launch_groups(c.rows, [&](int64_t first, dim3 g) {
+        if (c.bf16)
+          hipLaunchKernelGGL(head_entries_kernel<uint16_t>, g, dim3(256), 0, s, c, r, static_cast<const uint16_t*>(xc), p.dp, false,
+                             w, ldw, first);
+        else
+          hipLaunchKernelGGL(head_entries_kernel<float>, g, dim3(256), 0, s, c, r, static_cast<const float*>(c.x), c.ldx, true,
+                             static_cast<const float*>(c.w), p.d, first);
+      }));
     l.v0 = 0, l.v1 = c.vocab;
     l.z = p.keep ? reinterpret_cast<float*>(ws + p.z) : nullptr, l.vp = p.vp;
     l.part = reinterpret_cast<float*>(ws + p.part), l.z_label = reinterpret_cast<float*>(ws + p.z_label);
@@ -776,9 +779,9 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
     // 50257 6.6 and 11.7 us, 4096 rows with 64 entries 18.0 and 15.4)
     const int rw = c.rows <= 256 ? 1 : c.rows <= 2048 ? 4 : 16;
     auto loss = rw == 1 ? head_loss_kernel<1> : rw == 4 ? head_loss_kernel<4> : head_loss_kernel<16>;
-    hipLaunchKernelGGL(loss, dim3(static_cast<unsigned>(p.np / rw)), dim3(256), 0, s, c, r, l.part, p.np,
-                       static_cast<int>(p.tiles), l.z_label, factors, taught);
-    HEAD_TRY(hipGetLastError());
+    HEAD_TRY(launch_groups(p.np / rw, [&](int64_t first, dim3 g) {
+      hipLaunchKernelGGL(loss, g, dim3(256), 0, s, c, r, l.part, p.np, static_cast<int>(p.tiles), l.z_label, factors, taught, first);
+    }));
   }
   if (what == FWD) return MONARCH_OK;
   if (what == BWD) {
@@ -810,11 +813,11 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
     } else {
       HEAD_TRY(head_launch_grad(l, p.shape, c.second, s));
     }
-    if (c.taught) {
-      hipLaunchKernelGGL(head_taught_kernel, dim3(static_cast<unsigned>(c.rows)), dim3(64), static_cast<size_t>(c.top) * 8, s, c,
-                         r, factors, taught, g, gf, p.vp, l.g_plane, p.fold ? 2 : static_cast<int>(p.planes), v0, v1);
-      HEAD_TRY(hipGetLastError());
-    }
+    if (c.taught)
+      HEAD_TRY(launch_groups(c.rows, [&](int64_t first, dim3 grid) {
+        hipLaunchKernelGGL(head_taught_kernel, grid, dim3(64), static_cast<size_t>(c.top) * 8, s, c, r, factors, taught, g, gf, p.vp,
+                           l.g_plane, p.fold ? 2 : static_cast<int>(p.planes), v0, v1, first);
+      }));
     if (p.direct) {
       HeadFew f = {};
       f.g = gf, f.vp = p.vp, f.x = static_cast<const float*>(c.x), f.ldx = c.ldx, f.idx = r.idx, f.count = r.count;

@@ -57,10 +57,10 @@ __device__ __forceinline__ void panel_tile(int64_t t, int64_t outer, int64_t inn
 }
 
 template <class S, HeadSecond SECOND, bool F32>
-__global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t vt, int64_t nt) {
+__global__ __launch_bounds__(S::NT) void head_sums_kernel(HeadLogits p, int64_t vt, int64_t nt, int64_t group) {
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
   int64_t tv, tn;
-  panel_tile(xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
+  panel_tile(group + xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
   const int64_t v0 = p.v0 + tv * S::BM, n0 = tn * S::BN;
   if (n0 >= *p.count) return;
   f32x4 acc[S::FM][S::FN];
@@ -160,11 +160,11 @@ __device__ __forceinline__ int staged(int r, int e) {
 }
 
 template <class S, HeadSecond SECOND, bool F32>
-__global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t vt, int64_t nt) {
+__global__ __launch_bounds__(S::NT) void head_grad_kernel(HeadLogits p, int64_t vt, int64_t nt, int64_t group) {
   static_assert(S::BM * S::BN * 2 <= S::LDS, "a tile of g is staged in LDS");
   __shared__ __attribute__((aligned(16))) char lds[S::LDS];
   int64_t tv, tn;
-  panel_tile(xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
+  panel_tile(group + xcd_tile(blockIdx.x, gridDim.x), vt, nt, &tv, &tn);
   const int64_t v0 = p.v0 + tv * S::BM, n0 = tn * S::BN;
   if (n0 >= *p.count) return;
   f32x4 acc[S::FM][S::FN];
@@ -656,18 +656,15 @@ hipError_t few(const HeadFew& a, int64_t run, int64_t splits, hipStream_t st) {
 
 int64_t tiles(int64_t n, int64_t by) { return (n + by - 1) / by; }
 
-hipError_t check_grid(int64_t grid) { return grid > 0x7fffffffLL ? hipErrorInvalidConfiguration : hipSuccess; }
-
 template <class S, bool GRAD, HeadSecond SECOND, bool F32>
 hipError_t logits(const HeadLogits& a, hipStream_t st) {
   const int64_t vt = tiles(a.v1 - a.v0, S::BM), nt = tiles(a.np, S::BN);
-  if (hipError_t e = check_grid(vt * nt)) return e;
-  const dim3 g(static_cast<unsigned>(vt * nt));
-  if constexpr (GRAD)
-    hipLaunchKernelGGL((head_grad_kernel<S, SECOND, F32>), g, dim3(S::NT), 0, st, a, vt, nt);
-  else
-    hipLaunchKernelGGL((head_sums_kernel<S, SECOND, F32>), g, dim3(S::NT), 0, st, a, vt, nt);
-  return hipGetLastError();
+  return launch_groups(vt * nt, [&](int64_t first, dim3 g) {
+    if constexpr (GRAD)
+      hipLaunchKernelGGL((head_grad_kernel<S, SECOND, F32>), g, dim3(S::NT), 0, st, a, vt, nt, first);
+    else
+      hipLaunchKernelGGL((head_sums_kernel<S, SECOND, F32>), g, dim3(S::NT), 0, st, a, vt, nt, first);
+  });
 }
 
 template <class S, bool GRAD>
@@ -711,7 +708,8 @@ hipError_t products(HeadDx x, HeadDw w, hipStream_t st) {
   x.dt = tiles(x.d, SX::BM), x.nt = tiles(x.np, SX::BN);
   w.dt = tiles(w.d, SW::BM), w.vt = tiles(w.cols, SW::BN);
   const int64_t dw_tiles = w.dt * w.vt * w.splits, n = dw_tiles + x.dt * x.nt * x.splits;
-  if (hipError_t e = check_grid(n)) return e;
+  // memory ends first: a tile stands for 128 rows or words of 64 padded columns at least
+  if (n * SX::NT >= int64_t(1) << 32) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((head_products_kernel<SX, SW, F32>), dim3(static_cast<unsigned>(n)), dim3(SX::NT), 0, st, x, w, dw_tiles);
   return hipGetLastError();
 }
