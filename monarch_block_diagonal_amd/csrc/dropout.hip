@@ -53,13 +53,13 @@ __device__ __forceinline__ void philox(uint64_t at, uint64_t offset, uint64_t se
   }
 }
 
-// U pieces a thread, 256 pieces apart.
+// U pieces a thread, 256 pieces apart; `group`: this launch's first workgroup.
 template <typename T, bool RES, int U>
-__global__ __launch_bounds__(256) void dropout_kernel(Dropout a) {
+__global__ __launch_bounds__(256) void dropout_kernel(Dropout a, int64_t group) {
   constexpr int N = PieceOf<T>::N;
   uint64_t seed = a.seed, offset = a.offset;
   if (a.state) seed = a.state[0], offset = a.state[1];
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * U) + threadIdx.x;
+  const int64_t first = (group + blockIdx.x) * (256 * U) + threadIdx.x;
   const int64_t whole = a.n / N;
   const u32x4* x = static_cast<const u32x4*>(a.x);
   const u32x4* res = static_cast<const u32x4*>(a.residual);
@@ -113,12 +113,20 @@ hipError_t launch(const Dropout& a, hipStream_t s) {
   constexpr int U = 4;
   const int64_t pieces = (a.n + PieceOf<T>::N - 1) / PieceOf<T>::N;
   // few pieces: one a thread, so that every CU has some
-  if (pieces <= 256 * 1024)
-    hipLaunchKernelGGL((dropout_kernel<T, RES, 1>), dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((dropout_kernel<T, RES, U>), dim3(static_cast<unsigned>((pieces + 256 * U - 1) / (256 * U))), dim3(256),
-                       0, s, a);
-  return hipGetLastError();
+  if (pieces <= 256 * 1024) {
+    hipLaunchKernelGGL((dropout_kernel<T, RES, 1>), dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, s, a,
+                       int64_t(0));
+    return hipGetLastError();
+  }
+  // A launch has fewer than 2^32 threads; 2^21 workgroups are 32 GiB of a tensor.
+  constexpr int64_t kMost = int64_t(1) << 21;
+  const int64_t groups = (pieces + 256 * U - 1) / (256 * U);
+  for (int64_t first = 0; first < groups; first += kMost) {
+    const int64_t n = groups - first < kMost ? groups - first : kMost;
+    hipLaunchKernelGGL((dropout_kernel<T, RES, U>), dim3(static_cast<unsigned>(n)), dim3(256), 0, s, a, first);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
