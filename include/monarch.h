@@ -56,7 +56,7 @@
 extern "C" {
 #endif
 
-#define MONARCH_ABI_VERSION 7
+#define MONARCH_ABI_VERSION 8
 
 typedef enum {
   MONARCH_OK = 0,
@@ -466,6 +466,12 @@ int monarch_head_step(const void* x, int64_t ldx, const void* w, const void* lab
                       void* dx, void* dw, void* workspace, size_t workspace_bytes, int64_t rows,
                       int64_t features, int64_t vocab, int64_t top, float temperature, float mix,
                       int dtype, void* stream, void* const* events, int n_events);
+
+/* Kernels of a call (0 forward, 1 backward, 2 step) whose terms all count (those of entries where
+ * top > 0), in their order, with the tiles of those that have several ("head_sums_256": 256 x 256); a piece of
+ * the vocabulary's kernels are named once, with "*n" behind them for n > 1 pieces. */
+int monarch_head_describe(int call, int64_t rows, int64_t features, int64_t vocab, int64_t top, int dtype,
+                          char* buf, size_t buf_len);
 
 /* ---------------------------------------------------------------------------
  * Dropout joined to a residual:

@@ -18,6 +18,6 @@ from .binding import (  # noqa: F401
     monarch_bwd_noalloc, monarch_stream_copy, NORM_NONE, NORM_RMS, NORM_LAYER,
     monarch_sandwich_fwd, monarch_sandwich_stats_bytes, monarch_sandwich_bwd_workspace_bytes,
     monarch_sandwich_bwd, monarch_sandwich_describe, monarch_distill_fwd, monarch_distill_bwd, monarch_distill_step,
-    DISTILL_MAX_TOP, monarch_head_workspace_bytes, monarch_head_stats_bytes, monarch_head_fwd,
+    DISTILL_MAX_TOP, monarch_head_workspace_bytes, monarch_head_stats_bytes, monarch_head_describe, monarch_head_fwd,
     monarch_head_bwd, monarch_head_step, monarch_dropout,
 )

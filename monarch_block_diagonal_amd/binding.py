@@ -50,7 +50,7 @@ EXPORTED = (
     "monarch_sandwich_fwd", "monarch_sandwich_stats_bytes", "monarch_sandwich_bwd_workspace_bytes",
     "monarch_sandwich_bwd", "monarch_sandwich_describe", "monarch_distill_fwd", "monarch_distill_bwd",
     "monarch_distill_step", "monarch_head_workspace_bytes", "monarch_head_stats_bytes",
-    "monarch_head_fwd", "monarch_head_bwd", "monarch_head_step", "monarch_dropout",
+    "monarch_head_describe", "monarch_head_fwd", "monarch_head_bwd", "monarch_head_step", "monarch_dropout",
 )
 
 _lib = None
@@ -136,6 +136,8 @@ def load_library():
     lib.monarch_head_workspace_bytes.restype = sz
     lib.monarch_head_stats_bytes.argtypes = [i64] * 2
     lib.monarch_head_stats_bytes.restype = sz
+    lib.monarch_head_describe.argtypes = [c_int] + [i64] * 4 + [c_int, ctypes.c_char_p, sz]
+    lib.monarch_head_describe.restype = c_int
     head = [sz] + [i64] * 4 + [c_float] * 2 + [c_int, vp] + ev
     lib.monarch_head_fwd.argtypes = [vp, i64] + [vp] * 7 + head
     lib.monarch_head_fwd.restype = c_int
@@ -512,6 +514,16 @@ def monarch_head_workspace_bytes(call, rows, features, vocab, top, dtype) -> int
 
 def monarch_head_stats_bytes(rows, top) -> int:
     return load_library().monarch_head_stats_bytes(rows, top)
+
+
+def monarch_head_describe(call, rows, features, vocab, top, dtype):
+    """Kernel names of a forward call (HEAD_FWD), a backward call (HEAD_BWD) or a step (HEAD_STEP)."""
+    lib = load_library()
+    buf = ctypes.create_string_buffer(1024)
+    n = lib.monarch_head_describe(call, rows, features, vocab, top, dtype, buf, len(buf))
+    if n < 0:
+        raise MonarchError(n, monarch_status_string(n))
+    return buf.value.decode().split(";") if n else []
 
 
 def monarch_head_fwd(x, ldx, w, labels, teacher, ids, loss, stats, workspace, workspace_bytes, rows,

@@ -26,6 +26,7 @@
 // own in the forward pass (a wave an entry), and each is written again behind the piece's
 // epilogue with its share of p, once, in fp32 up to its one rounding.
 #include <math.h>
+#include <stdio.h>
 
 #include "api_internal.h"
 #include "head.h"
@@ -578,6 +579,7 @@ int64_t tiles_of(int64_t v, int64_t tile) { return (v + tile - 1) / tile; }
 struct HeadPlan {
   int64_t d, dp, np, planes;
   int fold;                    // bf16, few rows: rows of one of g's two parts
+  bool few;                    // bf16, few rows: head_rows_kernel copies them
   bool copy_w;                 // the head is copied (fp32, or rows that are no whole pieces)
   bool direct;                 // fp32, few rows: dx and dw by head_launch_few
   HeadShape shape, products;   // of the logits, and of dx and dw
@@ -609,6 +611,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
   HeadPlan p = {};
   p.d = d, p.dp = up(d, kPipeK), p.np = up(rows, kHeadRows), p.planes = bf16 ? 1 : 3;
   p.fold = !bf16 || rows > 64 ? 0 : rows <= kThinRows ? static_cast<int>(kThinRows) : 64;
+  p.few = bf16 && rows <= kThinRows && d <= 4096;   // one workgroup's copy
   p.copy_w = !bf16 || d % 8 != 0;
   // Rounds of 256 x 256 tiles (one a CU) against rounds of 128 x 128 tiles (two a CU), which take 0.6 of the
   // time: measured, 4096 x 768 x 50257 bf16 1368 us with the first and 1456 with the second (13 and 25
@@ -738,11 +741,10 @@ int run(const Call& c, const HeadPlan& p, int what, char* ws, hipStream_t s) {
     HEAD_TRY(launch_groups(tiles_of(c.rows, 4), [&](int64_t first, dim3 g) {
       hipLaunchKernelGGL(head_flag_kernel, g, dim3(256), 0, s, c, r, first);
     }));
-  const bool few = c.bf16 && c.rows <= kThinRows && c.d <= 4096;   // one workgroup's copy
-  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, s, c, r, head, few ? xc : nullptr, p.dp);
+  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, s, c, r, head, p.few ? xc : nullptr, p.dp);
   HEAD_TRY(hipGetLastError());
   const int64_t xplane = p.np * p.dp, wplane = (c.vocab + kPipeK) * p.dp;
-  if (!few)
+  if (!p.few)
     HEAD_TRY(c.bf16 ? copy_rows<uint16_t>(c.x, c.ldx, r.idx, r.count, r.fold, c.rows, p.np, p.d, p.dp, xc, xplane, s)
                   : copy_rows<float>(c.x, c.ldx, r.idx, r.count, r.fold, c.rows, p.np, p.d, p.dp, xc, xplane, s));
   const uint16_t* w = static_cast<const uint16_t*>(c.w);
@@ -904,6 +906,54 @@ size_t monarch_head_workspace_bytes(int call, int64_t rows, int64_t features, in
 size_t monarch_head_stats_bytes(int64_t rows, int64_t top) {
   if (rows < 0 || rows >= kLimit - kHeadRows || top < 0 || top > MONARCH_DISTILL_MAX_TOP) return 0;
   return static_cast<size_t>(rows) * (4 + top) * sizeof(float);
+}
+
+int monarch_head_describe(int call, int64_t rows, int64_t features, int64_t vocab, int64_t top, int dtype, char* buf,
+                          size_t buf_len) {
+  const int st = check_sizes(rows, features, vocab, features, top, dtype);
+  if (st) return st;
+  if (call < 0 || call > 2) return MONARCH_ERR_DTYPE;
+  static const char* const zero = "zero_dw";
+  if (rows == 0) return write_names(&zero, call == FWD ? 0 : 1, buf, buf_len);
+  const HeadPlan p = head_plan(call, rows, features, vocab, top, dtype == MONARCH_BF16);
+  static const char* const tile[] = {"_256", "_128", "_32", ""};   // by HeadShape
+  char text[16][48];
+  const char* names[16];
+  int n = 0;
+  auto add = [&](const char* name, const char* of, int64_t pieces) {
+    if (pieces > 1)
+      snprintf(text[n], sizeof text[n], "%s%s*%lld", name, of, static_cast<long long>(pieces));
+    else
+      snprintf(text[n], sizeof text[n], "%s%s", name, of);
+    names[n] = text[n];
+    ++n;
+  };
+  const char* logits = p.shape == HEAD_THIN ? "head_thin" : "head_sums";
+  const char* again = p.shape == HEAD_THIN ? "head_thin_grad" : "head_grad";
+  if (top > 0) add("head_flag", "", 1);
+  add("head_rows", "", 1);
+  if (!p.few) add("head_copy_x", "", 1);
+  if (p.copy_w) add("head_copy_w", "", 1);
+  if (call != BWD) {
+    if (top > 0) add("head_entries", "", 1);
+    add(logits, tile[p.shape], 1);
+    add("head_loss", "", 1);
+  }
+  if (call != FWD) {
+    if (call == BWD) add("head_factors", "", 1);
+    if (p.keep)
+      add("head_few", "", 1);
+    else
+      add(again, tile[p.shape], p.pieces);
+    if (top > 0) add("head_taught", "", p.pieces);
+    if (p.direct)
+      add("head_few_products", "", p.pieces);
+    else
+      add("head_products", tile[p.products], p.pieces);
+    if (p.dw_splits > 1) add("head_dw_out", "", p.pieces);
+    add("head_dx_out", "", 1);
+  }
+  return write_names(names, n, buf, buf_len);
 }
 
 int monarch_head_fwd(const void* x, int64_t ldx, const void* w, const void* labels, const void* teacher, const void* ids,
