@@ -435,7 +435,7 @@ int monarch_distill_step(const void* logits, int64_t ld, const void* teacher, co
  *   stats: monarch_head_stats_bytes, written by the forward pass for the backward pass.
  *   workspace: monarch_head_workspace_bytes of the call (0 forward, 1 backward, 2 step): a
  *   copy of x, in fp32 (but up to 32 rows with features % 4 == 0) or with features % 8 != 0 one of w, a piece of the vocabulary's gradient of
- *   the logits (at most 2 GiB, or 256 words of it) and partial sums (at most 1 GiB each, or
+ *   the logits (at most 1 GiB, or 256 words of it) and partial sums (at most 1 GiB each, or
  *   one sum). Nothing else is of size rows * vocab, but that a step of at most 32 rows
  *   holds their logits until it is done (128 bytes a word, where it would read the head again).
  * Logits and all sums are fp32 (fp32 operands are multiplied as three bf16 parts each, exact to

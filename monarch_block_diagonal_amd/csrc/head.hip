@@ -40,7 +40,10 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int64_t kLimit = int64_t(1) << 31;
 constexpr int64_t kMaxFeatures = int64_t(1) << 20;
-constexpr int64_t kPieceBytes = int64_t(1) << 31;   // of g
+// Of g. Steps with pieces of at most 2 GiB, 1 GiB, 512 and 256 MiB, ms: 16384 x 768 x 50257 bf16 5.36, 5.26, 5.56, 5.66;
+// 4096 x 4096 x 131072 14.75, 14.66, 14.91, 15.31; 65536 x 1024 x 131072 68.5, 68.0, 71.1, 75.9; 4096 x 768 x 50257 fp32
+// 5.54, 5.63, 5.75, 5.89.
+constexpr int64_t kPieceBytes = int64_t(1) << 30;
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -638,7 +641,8 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
   if (what == STEP) p.stats = take(rows * (4 + top) * 4);
   if (what != FWD) {
     p.direct = !bf16 && rows <= kThinRows;
-    int64_t vp = up(kPieceBytes / (p.planes * p.np * 2), kHeadRows) - kHeadRows;
+    // np rows of each plane, but few rows hold half of that at most (as below)
+    int64_t vp = up((p.fold || p.direct ? 2 : 1) * kPieceBytes / (p.planes * p.np * 2), kHeadRows) - kHeadRows;
     if (vp < kHeadRows) vp = kHeadRows;
     p.pieces = (vocab + vp - 1) / vp;
     p.vp = up((vocab + p.pieces - 1) / p.pieces, kHeadRows);
@@ -676,7 +680,7 @@ HeadPlan head_plan(int what, int64_t rows, int64_t d, int64_t vocab, int64_t top
     if (p.direct) p.dw_splits = 1;
     p.factors = take(p.np * static_cast<int64_t>(sizeof(HeadRow)));
     p.taught = take(p.np * 4);
-    p.g = take(p.direct ? kThinRows * p.vp * 4 : p.planes * p.np * p.vp * 2);
+    p.g = take(p.direct ? kThinRows * p.vp * 4 : p.fold ? 2 * p.fold * p.vp * 2 : p.planes * p.np * p.vp * 2);
     p.keep = what == STEP && p.shape == HEAD_THIN && p.pieces == 1;
     p.z = p.keep ? take(kThinRows * p.vp * 4) : 0;
     p.dx = take(p.dx_splits * p.dx_rows * p.dp * 4);

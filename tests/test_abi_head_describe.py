@@ -13,8 +13,8 @@ def test_kernels_of_a_call():
         "head_rows", "head_copy_x", "head_factors", "head_thin_grad", "head_few_products", "head_dx_out"]
     assert M.monarch_head_describe(B.HEAD_STEP, 8, 6, 500, 0, B.F32)[:4] == ["head_rows", "head_copy_x", "head_copy_w", "head_sums_32"]
     assert M.monarch_head_describe(B.HEAD_STEP, 16384, 768, 50257, 0, B.BF16) == [
-        "head_rows", "head_copy_x", "head_sums_256", "head_loss", "head_grad_256", "head_products_256", "head_dx_out"]
-    assert M.monarch_head_describe(B.HEAD_STEP, 65536, 1024, 131072, 0, B.BF16)[4:6] == ["head_grad_256*9", "head_products_256*9"]
+        "head_rows", "head_copy_x", "head_sums_256", "head_loss", "head_grad_256*2", "head_products_256*2", "head_dx_out"]
+    assert M.monarch_head_describe(B.HEAD_STEP, 65536, 1024, 131072, 0, B.BF16)[4:6] == ["head_grad_256*17", "head_products_256*17"]
 
 
 @pytest.mark.parametrize("dt", [B.F32, B.BF16])
@@ -33,3 +33,11 @@ def test_no_rows_and_refusals():
                 (0, 4, 8, 9, 0, 2)):
         with pytest.raises(M.MonarchError):
             M.monarch_head_describe(*bad)
+
+
+def test_memory():
+    """A step takes less than the logits would in the call's own type, from 1 GiB of them on; few rows take what they have."""
+    for rows, d, vocab in ((16384, 768, 50257), (4096, 4096, 131072), (65536, 1024, 131072)):
+        assert M.monarch_head_workspace_bytes(B.HEAD_STEP, rows, d, vocab, 0, B.BF16) < 0.62 * rows * vocab * 2
+    # two parts of g of 32 rows each in bf16, the logits, a copy of the rows and partial sums
+    assert M.monarch_head_workspace_bytes(B.HEAD_STEP, 8, 768, 50257, 0, B.BF16) < (64 * 2 + 32 * 4) * 50688 + (32 << 20)

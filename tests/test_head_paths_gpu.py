@@ -51,12 +51,12 @@ def test_small_tiles_with_many_steps(api, rows, d, vocab, T, mix, dtype):  # noq
 @pytest.mark.parametrize("rows,vocab,dtype", [(5200, 70001, F32), (16400, 70001, BF16)], ids=["f32", "bf16"])
 @pytest.mark.parametrize("T,mix", [(2.0, 0.5), (1.3, 0.7)])
 def test_pieces_with_entries(api, rows, vocab, dtype, T, mix):  # noqa: F811
-    """Two pieces of the vocabulary in large tiles: the second one's sums for dx are added to the first one's, and
-    entries and labels lie in either, also at the border between the two."""
+    """Three pieces of the vocabulary in large tiles: later ones' sums for dx are added to the first one's, and
+    entries and labels lie in each, also at the borders between them."""
     x, w, labels, t, ids, r = draw(rows, 136, vocab, dtype, top=5, holes=True, seed=35)
-    takes(x, w, 5, "head_grad_256*2", "head_taught*2", "head_products_256*2")
-    half = (vocab // 2 + 255) // 256 * 256
-    for k, at in enumerate((half - 2, half - 1, half, half + 1, vocab - 1)):
+    takes(x, w, 5, "head_grad_256*3", "head_taught*3", "head_products_256*3")
+    third = (vocab // 3 + 256) // 256 * 256
+    for k, at in enumerate((third - 1, third, 2 * third - 1, 2 * third, vocab - 1)):
         labels[k], ids[100 + k, 0], ids[100 + k, 2] = at, at, at
     check(api, x, w, labels, t, ids, r, T, mix)
     torch.cuda.empty_cache()
