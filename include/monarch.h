@@ -439,7 +439,7 @@ int monarch_distill_step(const void* logits, int64_t ld, const void* teacher, co
  *   one sum). Nothing else is of size rows * vocab, but that a step of at most 32 rows
  *   holds their logits until it is done (128 bytes a word, where it would read the head again).
  * Logits and all sums are fp32 (fp32 operands are multiplied as three bf16 parts each, exact to
- * 2^-23 of a product; parts under 2^-126 count as 0). In bf16 the gradient of the logits,
+ * 2^-23 of a product; parts under 2^-126 count as 0, and an infinity among them makes its logits NaN). In bf16 the gradient of the logits,
  * over the largest weight (dloss) of a row, is rounded to bf16 between its products (up to 64 rows: to two
  * bf16 parts); dx and dw are rounded once. Sums run in a fixed order.
  *
