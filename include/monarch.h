@@ -425,19 +425,21 @@ int monarch_distill_step(const void* logits, int64_t ld, const void* teacher, co
  * and labels as for monarch_distill_*:
  *   loss[i] = mix * T^2 * sum_k p_k (log p_k - log q[id_k]) - (1 - mix) * log s[label]
  * top 0 is mix 0, whatever mix is given: the cross entropy alone (mix and temperature are
- * checked all the same); labels NULL or mix 1 is the teacher's term alone. A row without a label and a valid entry (of a
- * term that counts) has loss 0 and gradient 0 and adds nothing to dw, whatever it
- * holds, and costs no product: padded tokens, prompts.
+ * checked all the same); labels NULL or mix 1 is the teacher's term alone. A row without a
+ * label and a valid entry (of a term that counts) has loss 0 and gradient 0 and adds nothing
+ * to dw, whatever it holds, and costs no product: padded tokens, prompts.
  *   x [rows, ldx]: row i's features start at i*ldx (ldx >= features, in elements), aligned
  *   to their element size only; w and dw [vocab, features], dx [rows, features] contiguous.
  *   features <= 2^20, vocab <= 2^30, top <= MONARCH_DISTILL_MAX_TOP.
  *   loss fp32 [rows]; labels int64 [rows]; teacher fp32, ids int64 [rows, top];
  *   stats: monarch_head_stats_bytes, written by the forward pass for the backward pass.
  *   workspace: monarch_head_workspace_bytes of the call (0 forward, 1 backward, 2 step): a
- *   copy of x, in fp32 (but up to 32 rows with features % 4 == 0) or with features % 8 != 0 one of w, a piece of the vocabulary's gradient of
- *   the logits (at most 1 GiB, or 256 words of it) and partial sums (at most 1 GiB each, or
- *   one sum). Nothing else is of size rows * vocab, but that a step of at most 32 rows
- *   holds their logits until it is done (128 bytes a word, where it would read the head again).
+ *   copy of x, in fp32 (but up to 32 rows with features % 4 == 0) or with features % 8 != 0
+ *   one of w, a piece of the vocabulary's gradient of the logits (2 bytes a value, in fp32 6; at
+ *   most 1 GiB, or 256 words of it, and whole where that holds it) and partial sums of dx and
+ *   dw (at most 1 GiB each, or one sum). What grows with rows * vocab: 12 bytes for every row and
+ *   256 (few rows: 128) words in a forward pass or step, and in a step of at most 32 rows their logits
+ *   (128 bytes a word, where it would read the head again).
  * Logits and all sums are fp32 (fp32 operands are multiplied as three bf16 parts each, exact to
  * 2^-23 of a product; parts under 2^-126 count as 0, and an infinity among them makes its logits NaN). In bf16 the gradient of the logits,
  * over the largest weight (dloss) of a row, is rounded to bf16 between its products (up to 64 rows: to two

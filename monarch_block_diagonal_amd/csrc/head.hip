@@ -1,5 +1,6 @@
 // Head loss: the loss of rows x [n][d] under a dense head w [vocab][d] and its
-// gradients by both, in pieces of the vocabulary; the logits z = x w^T are never kept.
+// gradients by both, in pieces of the vocabulary; the logits z = x w^T are not kept (but those of
+// up to 32 rows for the length of a step).
 //
 // With q = softmax(z / T), s = softmax(z), p = softmax(t / T) over a row's valid teacher
 // entries (id_k, t_k), label c and row weight r:

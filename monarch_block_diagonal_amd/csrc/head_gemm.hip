@@ -9,8 +9,7 @@
 //   dx       [d, n] = sum_v w[v, d] g[n, v]       split over the words
 //   dw       [d, v] = sum_n x[n, d] g[n, v]
 //
-// g is one piece of the vocabulary: it stays in a workspace that does not grow with
-// the vocabulary.
+// g is one piece of the vocabulary, in the workspace: at most 1 GiB, or 256 words of it.
 #include "head.h"
 #include "kernels.h"
 

@@ -796,7 +796,9 @@ def head_loss_backward(dloss, x, w, labels, teacher, ids, stats, *, temperature:
 def head_loss_step(x, w, labels=None, teacher=None, ids=None, row_weight=None, *,
                    temperature: float = 1.0, mix: Optional[float] = None, stream=None):
     """(loss [rows], dx, dw) in one call: the gradients of sum(row_weight * loss) (row_weight
-    None: 1 for every row)."""
+    None: 1 for every row). The logits' gradient is held a piece of at most 1 GiB at a time and the logits are
+    computed twice: bf16 steps of thousands of rows whose logits fit in memory are a fifth to two fifths slower than
+    with the logits kept (a product, distill_step in their place, two products)."""
     mix = _teachers_share(mix, teacher)
     if stream is not None:
         return _on_stream(stream, head_loss_step, x, w, labels, teacher, ids, row_weight,
