@@ -819,7 +819,8 @@ class HeadLossFunction(torch.autograd.Function):
     """head_loss_forward's loss with its gradients by x and w, for x [..., features], labels [...],
     teacher and ids [..., top]: one loss a row, [...]. What does not lie as the library takes it is
     copied. Where the rows' weights are known before the loss, head_loss_step computes the logits of
-    the backward pass behind those of the forward pass in one call."""
+    the backward pass behind those of the forward pass in one call. Both gradients are computed, also
+    where only one of x and w needs its own."""
 
     @staticmethod
     def forward(ctx, x, w, labels, teacher, ids, temperature: float = 1.0, mix: Optional[float] = None):
